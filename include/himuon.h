@@ -319,6 +319,184 @@ himuon_status_t himuon_pair_stats(const himuon_matrix_t* a, const himuon_matrix_
  * shapes of `a`; pointers are not read).  Host-side only. */
 himuon_status_t himuon_pair_stats_workspace(const himuon_matrix_t* a, int32_t n, size_t* bytes);
 
+/* ==========================================================================
+ * Operators around the optimiser step
+ *
+ * The matrices this library orthogonalises are the weights of language
+ * models.  The entry points below compute what such a training step needs
+ * next to it: the products of a mixture-of-experts layer (whose weight
+ * gradient is the G of himuon_muon_step), the loss of a student against a
+ * teacher's top logits, and the log probabilities of given tokens.  The
+ * conventions at the top of this file hold, with these additions:
+ * - X, Y, D (rows of tokens) and logits may have 0 rows; their pointer may
+ *   then be NULL.
+ * - dt is HIMUON_BF16 or HIMUON_FP32 (HIMUON_ERR_UNSUPPORTED otherwise).
+ *   bf16 products are accumulated in fp32 and rounded once; softmax
+ *   statistics, losses and log probabilities are fp32 for either type.
+ * - Arrays named as device arrays are contiguous and aligned to their
+ *   element.  Their contents are not validated on the host; the kernels clamp
+ *   or skip as stated, and never access memory outside the operands.
+ * - Results do not depend on scheduling: the same inputs give the same bits.
+ * ========================================================================== */
+
+/*
+ * himuon_grouped_mm - matrix products grouped by expert with ragged sizes.
+ *
+ *     Y[r, :] = X[r, :] W_e      for every row r of expert e
+ *
+ * X        : M x K, rows sorted by expert.
+ * W, n     : n >= 1 weight matrices, all of one shape: K x N, or N x K when
+ *            trans_w is not 0 (then Y = X W_e^T; with the weights of a forward
+ *            product and trans_w flipped this is its input gradient).
+ * ends     : device array of n int32, non-decreasing: expert e owns rows
+ *            [ends[e-1], ends[e]) with ends[-1] = 0.  An expert may own no
+ *            row.  Values are clamped to [0, M]; rows at or past ends[n-1]
+ *            belong to no expert and become zero.  (An array that decreases
+ *            gives unspecified values in Y, but no access outside it.)
+ * Y        : M x N, written; must not overlap X or any W.
+ * stream   : hipStream_t to enqueue on.
+ * One launch per 255 experts.  16-byte aligned rows with K (and N where the
+ * weights are K x N) a multiple of 8 take the fast path.
+ * Errors: HIMUON_ERR_INVALID_ARGUMENT (null pointer, n < 1, shapes that do not
+ * match), HIMUON_ERR_UNSUPPORTED (dtype), HIMUON_ERR_LAYOUT (alignment, a side
+ * above INT32_MAX, or more output tiles than a launch can hold),
+ * HIMUON_ERR_OVERLAP, HIMUON_ERR_HIP.
+ */
+himuon_status_t himuon_grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, int32_t n, int32_t trans_w,
+                                  const int32_t* ends, const himuon_matrix_t* Y, himuon_dtype_t dt, void* stream);
+
+/*
+ * himuon_grouped_wgrad - the weight gradients of himuon_grouped_mm.
+ *
+ *     G_e = X_e^T D_e,   X_e and D_e the rows of expert e
+ *
+ * X, D     : M x K and M x N, rows sorted by expert (D = dL/dY).
+ * G, n     : n >= 1 matrices of K x N, written (zero for an expert without
+ *            rows); they must not overlap each other, X or D.  For weights
+ *            stored N x K, pass D as X and X as D.
+ * ends     : as for himuon_grouped_mm; rows past ends[n-1] count nowhere.
+ * Errors as for himuon_grouped_mm.
+ */
+himuon_status_t himuon_grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D, const int32_t* ends,
+                                     const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* stream);
+
+/* Element type of a device array of vocabulary ids. */
+typedef enum himuon_index {
+    HIMUON_I32 = 0,
+    HIMUON_I64 = 1
+} himuon_index_t;
+
+/*
+ * himuon_distill - distillation from a teacher's top logits: the loss of each
+ * row and, optionally, its gradient in the same call.
+ *
+ * With s = Z / temperature and q = softmax(s) over the V columns of a row, and
+ * teacher entries (i_j, t_j), j = 1..k, of that row:
+ *     p_j  = softmax over the row's entries of t_j / temperature
+ *                                                   (normalize != 0), or
+ *     p_j  = exp(t_j)                               (normalize == 0; t_j are
+ *            log probabilities, taken as they stand)
+ *     loss = weight * sum_j p_j (log p_j - log q[i_j])
+ *     dZ_v = weight / temperature * (P q_v - sum_{j: i_j = v} p_j),  P = sum_j p_j
+ *
+ * Z        : N x V student logits.
+ * idx      : device array N x k of ids, of type it.  An id outside [0, V)
+ *            marks an absent entry.  An id may occur more than once in a row.
+ * T        : N x k fp32 teacher values (row stride T->ld).  -inf is p_j = 0.
+ * temperature : > 0, finite.
+ * weight   : device array of N fp32, or NULL (all 1).
+ * loss     : device array of N fp32, written.
+ * lse      : device array of N x 2 fp32, written, or NULL: log sum exp of s
+ *            rounded to fp32, and what that rounding lost (a row masked by the
+ *            type's lowest value would lose it all), for himuon_distill_grad.
+ * dZ       : N x V in dt, written, or NULL.  It may be Z itself (the same
+ *            pointer and ld); any other overlap is refused.
+ * workspace: device scratch of at least himuon_distill_workspace bytes,
+ *            16-byte aligned; may be NULL when that is 0.
+ * A row whose weight is 0, or that has no entry with p_j > 0, is not read: its
+ * loss, lse and gradient are 0 whatever it holds.  In the other rows a logit
+ * of -inf has q = 0 (an entry there gives the loss +inf); NaN or +inf logits
+ * make that row's results NaN.  k up to HIMUON_MAX_ENTRIES.
+ * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (dtype, index
+ * type, k above the maximum), HIMUON_ERR_LAYOUT, HIMUON_ERR_OVERLAP,
+ * HIMUON_ERR_WORKSPACE, HIMUON_ERR_HIP.
+ */
+#define HIMUON_MAX_ENTRIES 1024
+himuon_status_t himuon_distill(const himuon_matrix_t* Z, const void* idx, himuon_index_t it, const himuon_matrix_t* T,
+                               float temperature, int32_t normalize, const float* weight, float* loss, float* lse,
+                               const himuon_matrix_t* dZ, himuon_dtype_t dt, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Bytes of workspace himuon_distill needs for logits of this shape (the
+ * pointer is not read), with a gradient or without.  Host-side only. */
+himuon_status_t himuon_distill_workspace(const himuon_matrix_t* Z, himuon_dtype_t dt, int32_t with_grad,
+                                         size_t* bytes);
+
+/*
+ * himuon_distill_grad - the gradient alone, from the lse of a himuon_distill
+ * call on the same inputs.  g is the device array of N fp32 gradients of the
+ * unweighted row losses (dL/dloss_i, times the row's weight if one was used);
+ * it takes the place of weight above.  Rows with g = 0 or without entries get
+ * zeros and are not read.
+ */
+himuon_status_t himuon_distill_grad(const himuon_matrix_t* Z, const void* idx, himuon_index_t it,
+                                    const himuon_matrix_t* T, float temperature, int32_t normalize, const float* lse,
+                                    const float* g, const himuon_matrix_t* dZ, himuon_dtype_t dt, void* stream);
+
+/*
+ * himuon_token_logprobs - log probabilities of given tokens, with the entropy
+ * and the top alternatives of every row.
+ *
+ * With s = Z / temperature, lse = log sum_v exp(s_v), q = exp(s - lse):
+ *     logp    = s[token] - lse
+ *     entropy = -sum_v q_v log q_v            (a term with q_v = 0 is 0)
+ *     top_idx, top_logp: the ids of the `top` largest logits, largest first
+ *              and equal ones by the lowest id, and their log probabilities
+ *
+ * Z        : N x V logits.
+ * tokens   : device array of N ids of type it, or NULL (then logp must be
+ *            NULL).  A row whose token lies outside [0, V) is skipped: logp,
+ *            entropy and lse are 0, top_idx -1 and top_logp -inf.
+ * top      : 0 <= top <= min(V, HIMUON_MAX_TOP).
+ * logp, entropy : device arrays of N fp32, written; each may be NULL.
+ * lse      : device array of N x 2 fp32, written, or NULL (as for himuon_distill).
+ * top_idx, top_logp  : device arrays N x top of int32 and fp32, written; may
+ *            be NULL when top is 0.
+ * workspace: at least himuon_token_logprobs_workspace bytes, 16-byte aligned;
+ *            may be NULL when that is 0.
+ * A logit of -inf has q = 0 and log probability -inf (so does every id of a
+ * row that holds nothing else; its lse is -inf and its entropy 0).  A NaN or
+ * +inf makes the row's values NaN; NaN ranks with -inf among the alternatives.
+ * Errors as for himuon_distill.
+ */
+#define HIMUON_MAX_TOP 64
+himuon_status_t himuon_token_logprobs(const himuon_matrix_t* Z, const void* tokens, himuon_index_t it,
+                                      float temperature, int32_t top, float* logp, float* entropy, float* lse,
+                                      int32_t* top_idx, float* top_logp, himuon_dtype_t dt, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace himuon_token_logprobs needs for logits of this shape (the
+ * pointer is not read).  Host-side only. */
+himuon_status_t himuon_token_logprobs_workspace(const himuon_matrix_t* Z, int32_t top, himuon_dtype_t dt,
+                                                size_t* bytes);
+
+/*
+ * himuon_token_logprobs_grad - the gradient of the logits through logp and
+ * entropy:
+ *     dZ_v = (g_logp ([v = token] - q_v) - g_entropy q_v (log q_v + entropy)) / temperature
+ *
+ * lse, entropy : device arrays of N x 2 and N fp32 from himuon_token_logprobs
+ *            on the same inputs (entropy may be NULL when g_entropy is).
+ * g_logp, g_entropy : device arrays of N fp32, either may be NULL (zero).
+ *            tokens may be NULL when g_logp is.
+ * dZ       : N x V in dt, written; may be Z itself.
+ * A skipped row, and one whose two gradients are 0, gets zeros and is not read.
+ */
+himuon_status_t himuon_token_logprobs_grad(const himuon_matrix_t* Z, const void* tokens, himuon_index_t it,
+                                           float temperature, const float* lse, const float* entropy,
+                                           const float* g_logp, const float* g_entropy, const himuon_matrix_t* dZ,
+                                           himuon_dtype_t dt, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* himuon_status_string(himuon_status_t s);
 

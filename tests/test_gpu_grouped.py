@@ -1,0 +1,255 @@
+"""The experts' products on the GPU against fp64.
+
+Tolerance, elementwise: the products of bf16 or fp32 inputs are accumulated in
+fp32 over L terms in some order, so the error is at most 2 L 2^-24 sum |a b|
+(one rounding of up to 2^-23 for each addition of a partial sum that stays
+below sum |a b|), and the result is rounded once: 2^-8 |y| bounds half a unit
+in bf16, 2^-23 |y| in fp32.
+"""
+import pytest
+import torch
+
+import tiled_newton_schulz_amd as H
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+ROUND = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -23}
+
+
+def randn(shape, dt, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(TYPES[dt]).cuda()
+
+
+def ends_of(counts):
+    return torch.tensor(counts).cumsum(0).to(torch.int32).cuda()
+
+
+def product(a, b, dt):
+    """(a @ b, its bound) in fp64 on the host."""
+    a, b = a.double().cpu(), b.double().cpu()
+    y = a @ b
+    return y, 2 * a.shape[1] * 2.0 ** -24 * (a.abs() @ b.abs()) + ROUND[dt] * y.abs()
+
+
+def close(got, want, bound):
+    d = (got.double().cpu() - want).abs()
+    assert torch.all(d <= bound), float((d - bound).max())
+
+
+def check_mm(x, w, counts, dt, out=None):
+    y = H.himuon_grouped_mm(x, w, ends_of(counts), out=out)
+    torch.cuda.synchronize()
+    r = 0
+    for e, c in enumerate(counts):
+        if c:
+            close(y[r:r + c], *product(x[r:r + c], w[e], dt))
+        r += c
+    assert torch.all(y[r:] == 0)
+    return y
+
+
+def check_wgrad(x, d, counts, dt, out=None):
+    g = H.himuon_grouped_wgrad(x, d, ends_of(counts), out=out)
+    torch.cuda.synchronize()
+    r = 0
+    for e, c in enumerate(counts):
+        if c:
+            close(g[e], *product(x[r:r + c].t(), d[r:r + c], dt))
+        else:
+            assert torch.all(g[e] == 0)
+        r += c
+    return g
+
+
+# rows of each expert, K, N
+CASES = [
+    ([1], 1, 1),
+    ([5], 8, 8),
+    ([0, 3, 0], 16, 40),
+    ([7, 0, 1, 64, 65], 24, 136),
+    ([130, 1, 0, 63], 100, 96),
+    ([256, 257, 31], 192, 264),
+    ([3, 300, 0, 17], 515, 261),
+    ([1, 2, 0, 1, 1, 0, 3, 1], 512, 256),
+    ([600, 20], 1031, 72),
+    ([33, 90, 200], 320, 704),
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("stored", ["kn", "nk"])
+@pytest.mark.parametrize("counts,K,N", CASES)
+def test_product(cuda, counts, K, N, stored, dt):
+    print(f"product {counts} {K}x{N} {stored} {dt}", flush=True)
+    M, n = sum(counts), len(counts)
+    x = randn((M, K), dt, 1)
+    w = randn((n, K, N), dt, 2) if stored == "kn" else randn((n, N, K), dt, 2).transpose(1, 2)
+    check_mm(x, w, counts, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("counts,K,N", CASES)
+def test_weight_gradient(cuda, counts, K, N, dt):
+    print(f"weight gradient {counts} {K}x{N} {dt}", flush=True)
+    M = sum(counts)
+    check_wgrad(randn((M, K), dt, 3), randn((M, N), dt, 4), counts, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("pad,shift", [(8, 0), (3, 1), (24, 8)])
+def test_strides_and_padding(cuda, dt, pad, shift):
+    """Column blocks of wider tensors whose other columns hold NaN, outputs
+    into the middle of a wider tensor whose other columns stay as they were,
+    a list of separate weights and of transposed ones."""
+    counts, K, N = [70, 0, 130, 9], 144, 168
+    M, n = sum(counts), len(counts)
+
+    def wide(rows, cols, seed):
+        t = torch.full((rows, cols + pad + shift), float("nan"), dtype=TYPES[dt], device=cuda)
+        v = t[:, shift:shift + cols]
+        v.copy_(randn((rows, cols), dt, seed))
+        return v
+
+    print(f"strides pad {pad} shift {shift} {dt}", flush=True)
+    x, d = wide(M, K, 5), wide(M, N, 6)
+    w = [wide(K, N, 10 + e) for e in range(n)]
+    wt = [wide(N, K, 20 + e).t() for e in range(n)]
+    for weights in (w, wt):
+        store = torch.full((M, N + pad + shift), 7.0, dtype=TYPES[dt], device=cuda)
+        check_mm(x, weights, counts, dt, out=store[:, shift:shift + N])
+        assert torch.all(store[:, :shift] == 7.0) and torch.all(store[:, shift + N:] == 7.0)
+    for tr in (False, True):
+        stores = [torch.full((N, K + pad + shift) if tr else (K, N + pad + shift), 7.0, dtype=TYPES[dt], device=cuda)
+                  for _ in range(n)]
+        g = [s[:, shift:shift + (K if tr else N)] for s in stores]
+        check_wgrad(x, d, counts, dt, out=[v.t() for v in g] if tr else g)
+        for s in stores:
+            assert torch.all(s[:, :shift] == 7.0) and torch.all(s[:, shift + (K if tr else N):] == 7.0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("K,N", [(72, 88), (200, 264), (131, 77)])
+def test_nan_stays_with_its_expert(cuda, dt, K, N):
+    """NaN in the rows or weights of one expert, in rows of no expert and in
+    the weights of an expert without rows reaches nobody else."""
+    counts = [30, 1, 0, 100, 65]
+    M, n = sum(counts), len(counts)
+    x, d, w = randn((M + 20, K), dt, 7), randn((M + 20, N), dt, 8), randn((n, K, N), dt, 9)
+    bad = slice(31, 131)
+    for t in (x, d):
+        t[bad] = float("nan")
+        t[M:] = float("nan")
+    w[2:4] = float("nan")
+    print(f"nan {K}x{N} {dt}", flush=True)
+    for stored in (w, w.transpose(1, 2).contiguous().transpose(1, 2)):
+        y = H.himuon_grouped_mm(x, stored, ends_of(counts))
+        assert torch.isnan(y[bad]).all() and torch.all(y[M:] == 0)
+        for e, r in ((0, slice(0, 30)), (1, slice(30, 31)), (4, slice(131, M))):
+            close(y[r], *product(x[r], w[e], dt))
+    g = H.himuon_grouped_wgrad(x, d, ends_of(counts))
+    assert torch.isnan(g[3]).all() and torch.all(g[2] == 0)
+    for e, r in ((0, slice(0, 30)), (1, slice(30, 31)), (4, slice(131, M))):
+        close(g[e], *product(x[r].t(), d[r], dt))
+
+
+def test_many_experts_and_no_rows(cuda):
+    """More experts than one launch holds, and calls without a row."""
+    n, K, N = 600, 40, 24
+    g = torch.Generator().manual_seed(11)
+    counts = torch.randint(0, 5, (n,), generator=g).tolist()
+    counts[254:258] = [0, 70, 0, 3]
+    M = sum(counts)
+    print("600 experts", flush=True)
+    x, d, w = randn((M + 9, K), "bf16", 12), randn((M + 9, N), "bf16", 13), randn((n, K, N), "bf16", 14)
+    check_mm(x, w, counts, "bf16")
+    check_wgrad(x, d, counts, "bf16")
+    none = [0] * 3
+    assert H.himuon_grouped_mm(x[:0], w[:3], ends_of(none)).shape == (0, N)
+    assert torch.all(H.himuon_grouped_wgrad(x[:0], d[:0], ends_of(none)) == 0)
+    assert torch.all(H.himuon_grouped_mm(x, w[:3], ends_of(none)) == 0)
+    assert torch.all(H.himuon_grouped_wgrad(x, d, ends_of(none)) == 0)
+
+
+def test_ends_are_clamped(cuda):
+    """End rows outside [0, M] are clamped to it."""
+    x, w = randn((50, 32), "bf16", 15), randn((3, 32, 16), "bf16", 16)
+    ends = torch.tensor([-5, 20, 1 << 30], dtype=torch.int32, device=cuda)
+    y = H.himuon_grouped_mm(x, w, ends)
+    close(y[:20], *product(x[:20], w[1], "bf16"))
+    close(y[20:], *product(x[20:], w[2], "bf16"))
+    g = H.himuon_grouped_wgrad(x, x, ends)
+    assert torch.all(g[0] == 0)
+    close(g[2], *product(x[20:].t(), x[20:], "bf16"))
+
+
+def test_same_bits_and_other_streams(cuda):
+    """The same call gives the same bits again, on a stream of the caller's
+    choice, and from a captured graph replayed between eager calls."""
+    counts = [100, 3, 0, 290, 41]
+    x, d = randn((sum(counts), 256), "bf16", 17), randn((sum(counts), 136), "bf16", 18)
+    w, ends = H.matrices(randn((5, 256, 136), "bf16", 19)), ends_of(counts)
+    y0, g0 = H.himuon_grouped_mm(x, w, ends), H.himuon_grouped_wgrad(x, d, ends)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y1 = H.himuon_grouped_mm(x, w, ends, stream=side)
+    g1 = H.himuon_grouped_wgrad(x, d, ends, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(g0, g1)
+    y2, g2 = torch.empty_like(y0), torch.empty_like(g0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        H.himuon_grouped_mm(x, w, ends, out=y2)
+        H.himuon_grouped_wgrad(x, d, ends, out=g2)
+    for k in range(3):
+        x.copy_(randn(tuple(x.shape), "bf16", 30 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y2, H.himuon_grouped_mm(x, w, ends))
+        assert torch.equal(g2, H.himuon_grouped_wgrad(x, d, ends))
+
+
+def test_gradients_against_differences(cuda):
+    """L = <Y, R>: its difference along a direction of X and of W against the
+    input and weight gradients.  L is linear in each, so the difference is
+    exact up to the rounding of the two products: for entries of size about 1
+    it is sqrt(M N) K 2^-23 of their norm, taken ten times over."""
+    counts, K, N = [40, 0, 77], 48, 56
+    M = sum(counts)
+    x, w, R = randn((M, K), "fp32", 20), randn((3, K, N), "fp32", 21), randn((M, N), "fp32", 22)
+    u, v = randn((M, K), "fp32", 23), randn((3, K, N), "fp32", 24)
+    ends = ends_of(counts)
+
+    def loss(x, w):
+        return float((H.himuon_grouped_mm(x, w, ends).double() * R.double()).sum())
+
+    dx = H.himuon_grouped_mm(R, w.transpose(1, 2), ends)
+    dw = H.himuon_grouped_wgrad(x, R, ends)
+    tol = 10 * M * N * K * 2.0 ** -23
+    assert abs((loss(x + u, w) - loss(x - u, w)) / 2 - float((dx.double() * u.double()).sum())) <= tol
+    assert abs((loss(x, w + v) - loss(x, w - v)) / 2 - float((dw.double() * v.double()).sum())) <= tol
+
+
+def test_large_products(cuda):
+    """Column and row tiles at full size, against fp64 on sampled rows and columns."""
+    counts, K, N = [700, 0, 1, 1100, 255], 1408, 2048
+    M = sum(counts)
+    print("large products", flush=True)
+    x, d = randn((M, K), "bf16", 25), randn((M, N), "bf16", 26)
+    w = randn((5, K, N), "bf16", 27)
+    ends = ends_of(counts)
+    rows = torch.tensor([0, 255, 256, 699, 700, 701, 956, 957, 1800, 1801, M - 1])
+    for weights in (w, w.transpose(1, 2).contiguous().transpose(1, 2)):
+        y = H.himuon_grouped_mm(x, weights, ends)
+        for r in rows.tolist():
+            e = int((ends.cpu() <= r).sum())
+            close(y[r:r + 1], *product(x[r:r + 1], w[e], "bf16"))
+    g = H.himuon_grouped_wgrad(x, d, ends)
+    r = 0
+    for e, c in enumerate(counts):
+        for i in (0, 127, 128, 255, 256, 1279, 1280, 1407):
+            if c:
+                close(g[e][i:i + 1], *product(x[r:r + c, i:i + 1].t(), d[r:r + c], "bf16"))
+        r += c
+    assert torch.all(g[1] == 0)

@@ -1,0 +1,419 @@
+"""Distillation and token log probabilities on the GPU against fp64.
+
+Bounds.  With A the largest finite |s| of a row, s = z / temperature: s itself
+carries a relative error of 2^-22 (the reciprocal of the temperature and one
+product), an exponential of |x| <= 2 A + 8 a relative error of 2^-22 (2 A + 8)
+(its argument's rounding and a few units of the instruction), and a sum of V
+terms in parts of at most V / 64 + 64 additions (V / 64 + 64) 2^-24.  So log q
+is off by at most
+
+    d = 2^-20 (A + 8) + (V / 64 + 64) 2^-24,
+
+q by d relative to itself, the entropy by d (2 A + 8 + log V), and likewise
+with A_t, k for the teacher's p (d_p).  The loss is off by at most
+P (d + d_p (1 + max |log p - log q|)), the gradient by
+c (P q (d + d_p) + p d_p), c = |weight| / temperature, before it is rounded to
+its type: 2^-8 (bf16), 2^-22 (fp32) of itself.
+"""
+import math
+
+import pytest
+import torch
+
+import tiled_newton_schulz_amd as H
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+ROUND = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -22}
+INF = float("inf")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def logits(N, V, dt, seed, scale=3.0, mask=0.0):
+    z = torch.randn((N, V), generator=gen(seed)) * scale
+    if mask:
+        z[torch.rand((N, V), generator=gen(seed + 1)) < mask] = -INF
+        z[:, 0] = 1.0
+    return z.to(TYPES[dt])
+
+
+def strided(z, pad, shift):
+    """The same values on the GPU inside a wider tensor of NaN."""
+    t = torch.full((z.shape[0], z.shape[1] + pad + shift), float("nan"), dtype=z.dtype, device="cuda")
+    v = t[:, shift:shift + z.shape[1]]
+    v.copy_(z)
+    return v
+
+
+def row_bound(s, V):
+    A = torch.where(torch.isfinite(s), s.abs(), 0.0).amax(1)
+    return A, 2.0 ** -20 * (A + 8) + (V / 64 + 64) * 2.0 ** -24
+
+
+def softmax64(z, tau):
+    s = z.double() / tau
+    lse = torch.logsumexp(s, 1)
+    lq = s - lse[:, None]
+    return s, lse, lq, torch.exp(lq)
+
+
+def near(got, want, bound, what):
+    got = got.double().cpu()
+    same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+    ok = same | ((got - want).abs() <= bound)
+    assert torch.all(ok), (what, float(torch.where(ok, 0.0, (got - want).abs() - bound).nan_to_num(9e99).max()))
+
+
+# ---- token log probabilities -----------------------------------------------------
+
+def check_logprobs(z, zg, tokens, top, tau, dt, r=None):
+    N, V = z.shape
+    if r is None:
+        r = H.himuon_token_logprobs(zg, tokens.cuda(), top=top, temperature=tau)
+    torch.cuda.synchronize()
+    live = (tokens >= 0) & (tokens < V)
+    s, lse, lq, q = softmax64(z, tau)
+    A, d = row_bound(s, V)
+    want = torch.where(live, lq.gather(1, tokens.long().clamp(0, V - 1)[:, None])[:, 0], 0.0)
+    near(r.logp, want, d, "logp")
+    H_ = -torch.where(q > 0, q * lq, 0.0).sum(1)
+    near(r.entropy, torch.where(live, H_, 0.0), d * (2 * A + 8 + math.log(V)), "entropy")
+    near(r.lse.double().sum(1), torch.where(live, lse, 0.0), d, "lse")
+    if top:
+        order = torch.sort(z.double(), dim=1, descending=True, stable=True)[1][:, :top]
+        assert torch.equal(r.top_idx.cpu().long()[live], order[live])
+        assert torch.all(r.top_idx.cpu()[~live] == -1) and torch.all(r.top_logp.cpu()[~live] == -INF)
+        near(r.top_logp[live.cuda()], lq.gather(1, order)[live], d[live][:, None], "top_logp")
+    return r, (s, lse, lq, q, H_, live, A, d)
+
+
+def check_logprobs_grad(z, zg, tokens, tau, dt, r, ref, gl, gh, out=None):
+    V = z.shape[1]
+    s, lse, lq, q, H_, live, A, d = ref
+    g = H.himuon_token_logprobs_grad(zg, tokens.cuda(), r.lse, r.entropy, None if gl is None else gl.cuda(),
+                                     None if gh is None else gh.cuda(), temperature=tau, out=out)
+    torch.cuda.synchronize()
+    a = torch.zeros(z.shape[0]).double() if gl is None else gl.double()
+    b = torch.zeros(z.shape[0]).double() if gh is None else gh.double()
+    hot = torch.zeros_like(q)
+    hot[torch.arange(z.shape[0]), tokens.long().clamp(0, V - 1)] = 1.0
+    qlq = torch.where(q > 0, q * lq, 0.0)
+    want = (a[:, None] * (hot - q) - b[:, None] * (qlq + q * H_[:, None])) / tau
+    dH = d * (2 * A + 8 + math.log(V))
+    # terms cancel: each carries its own rounding
+    err = (a.abs()[:, None] * (q * d[:, None] + 2.0 ** -22 * (hot + q))
+           + b.abs()[:, None] * (q * (d + dH)[:, None] + (qlq.abs() + q * H_[:, None].abs()) * (d[:, None] + 2.0 ** -21))) / tau
+    want = torch.where(live[:, None], want, 0.0)
+    near(g, want, err + ROUND[dt] * want.abs() + 1e-38, "grad")
+    return g
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,V,top", [(1, 1, 1), (3, 2, 2), (2, 64, 64), (5, 63, 5), (37, 1000, 20), (7, 5003, 3),
+                                     (4, 32000, 64), (1, 131072, 20), (3, 131073, 1), (300, 257, 8), (2, 200001, 10)])
+def test_logprobs(cuda, N, V, top, dt):
+    print(f"logprobs {N}x{V} top {top} {dt}", flush=True)
+    z = logits(N, V, dt, N + V, mask=0.1 if V > 2 else 0.0)
+    tokens = torch.randint(0, V, (N,), generator=gen(1), dtype=torch.int64 if N % 2 else torch.int32)
+    tau = [1.0, 0.7, 2.0][V % 3]
+    zg = z.cuda()
+    r, ref = check_logprobs(z, zg, tokens, top, tau, dt)
+    gl, gh = torch.randn(N, generator=gen(2)), torch.randn(N, generator=gen(3))
+    check_logprobs_grad(z, zg, tokens, tau, dt, r, ref, gl, gh)
+    check_logprobs_grad(z, zg, tokens, tau, dt, r, ref, gl, None)
+    check_logprobs_grad(z, zg, tokens, tau, dt, r, ref, None, gh)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("pad,shift", [(8, 0), (5, 1), (16, 8)])
+def test_logprobs_strides_in_place(cuda, dt, pad, shift):
+    """Rows inside a wider tensor of NaN; the gradient in place of the logits
+    leaves the columns around them."""
+    N, V = 9, 4099
+    print(f"logprobs strides {pad} {shift} {dt}", flush=True)
+    z = logits(N, V, dt, 5)
+    zg = strided(z, pad, shift)
+    tokens = torch.randint(0, V, (N,), generator=gen(6))
+    tokens[3], tokens[4] = -100, V      # skipped rows
+    r, ref = check_logprobs(z, zg, tokens, 11, 1.3, dt)
+    gl, gh = torch.randn(N, generator=gen(7)), torch.randn(N, generator=gen(8))
+    want = check_logprobs_grad(z, zg, tokens, 1.3, dt, r, ref, gl, gh)
+    got = check_logprobs_grad(z, zg, tokens, 1.3, dt, r, ref, gl, gh, out=zg)
+    assert torch.equal(got, want)
+    base = zg._base
+    assert torch.isnan(base[:, :shift]).all() and torch.isnan(base[:, shift + V:]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [50, 2048, 40000])
+def test_alternatives_with_ties_and_masks(cuda, dt, V):
+    """Constant rows, rows of few distinct values, rows with fewer allowed ids
+    than alternatives, ascending and descending rows, the largest in one run."""
+    top = 40
+    z = torch.zeros((8, V))
+    z[1] = torch.randint(0, 3, (V,), generator=gen(1)).float()
+    z[2] = -INF
+    z[2, torch.randperm(V, generator=gen(2))[:7]] = torch.arange(7).float()
+    z[3] = torch.arange(V).float() / 64
+    z[4] = -torch.arange(V).float() / 64
+    z[5, V // 2:] = 1.0
+    z[6] = -INF                                             # nothing left
+    z[7] = torch.finfo(TYPES[dt]).min                       # masked by the lowest value
+    z[7, V // 3] = 2.0
+    z[0, ::2] = -0.0                                        # -0 ranks with +0
+    z = z.to(TYPES[dt])
+    tokens = torch.full((8,), V // 3)
+    print(f"ties {V} {dt}", flush=True)
+    live = [0, 1, 2, 3, 4, 5, 7]
+    r = H.himuon_token_logprobs(z.cuda(), tokens.cuda(), top=top)
+    sub = type(r)(*[x[live] for x in r])
+    check_logprobs(z[live], None, tokens[live], top, 1.0, dt, r=sub)
+    assert r.lse[6, 0].item() == -INF and r.logp[6].item() == -INF and r.entropy[6].item() == 0.0
+    assert r.top_idx[6].tolist() == list(range(top)) and torch.all(r.top_logp[6] == -INF)
+    g = H.himuon_token_logprobs_grad(z.cuda(), tokens.cuda(), r.lse, r.entropy, torch.ones(8).cuda(), torch.ones(8).cuda())
+    assert torch.isfinite(g).all()
+
+
+def test_logprobs_nan_and_inf_stay_in_their_row(cuda):
+    V = 3000
+    z = logits(6, V, "fp32", 9)
+    z[1, 17] = float("nan")
+    z[2, 40] = INF
+    z[3] = float("nan")
+    z[4, 5] = float("nan")
+    tokens = torch.tensor([4, 5, 6, 7, -1, 8])
+    r = H.himuon_token_logprobs(z.cuda(), tokens.cuda(), top=4)
+    for t in (r.logp, r.entropy, r.lse[:, 0]):
+        assert torch.isnan(t[1:4]).all() and t[4].item() == 0.0 and torch.isfinite(t[[0, 5]]).all()
+    keep = [0, 5]
+    check_logprobs(z[keep], None, tokens[keep], 4, 1.0, "fp32", r=type(r)(*[x[keep] for x in r]))
+    assert r.top_idx[2, 0].item() == 40
+    assert r.top_idx[3].tolist() == [0, 1, 2, 3]
+    g = H.himuon_token_logprobs_grad(z.cuda(), tokens.cuda(), r.lse, r.entropy, torch.ones(6).cuda())
+    assert torch.isnan(g[1:4]).all() and torch.all(g[4] == 0) and torch.isfinite(g[keep]).all()
+
+
+def test_logprobs_without_tokens_and_rows(cuda):
+    z = logits(5, 777, "bf16", 10)
+    r = H.himuon_token_logprobs(z.cuda(), top=3)
+    assert r.logp is None
+    full, _ = check_logprobs(z, z.cuda(), torch.zeros(5, dtype=torch.int64), 3, 1.0, "bf16")
+    for a, b in ((r.entropy, full.entropy), (r.lse, full.lse), (r.top_idx, full.top_idx), (r.top_logp, full.top_logp)):
+        assert torch.equal(a, b)
+    e = H.himuon_token_logprobs(z.cuda()[:0], torch.zeros(0, dtype=torch.int64, device="cuda"), top=3)
+    assert e.logp.shape == (0,) and e.top_idx.shape == (0, 3)
+    assert H.himuon_token_logprobs_grad(z.cuda()[:0], None, e.lse, e.entropy, None, e.entropy).shape == (0, 777)
+    # entropy alone
+    g = H.himuon_token_logprobs_grad(z.cuda(), None, r.lse, r.entropy, None, torch.ones(5).cuda())
+    h = H.himuon_token_logprobs_grad(z.cuda(), torch.zeros(5, dtype=torch.int64).cuda(), r.lse, r.entropy, None, torch.ones(5).cuda())
+    assert torch.equal(g, h)
+
+
+# ---- distillation --------------------------------------------------------------------
+
+def distill64(z, idx, t, tau, normalize, w):
+    """(loss, dz, their bounds) in fp64."""
+    V = z.shape[1]
+    there = (idx >= 0) & (idx < V)
+    u = torch.where(there, t.double() / tau if normalize else t.double(), -INF)
+    if normalize:
+        m = u.amax(1, keepdim=True)
+        l = torch.where(m == -INF, 0.0, torch.logsumexp(u, 1, keepdim=True))
+        lp = u - l
+    else:
+        lp = u
+    p = torch.exp(lp)
+    live = (w != 0) & ~(u == -INF).all(1)
+    s, lse, lq, q = softmax64(z, tau)
+    where = idx.long().clamp(0, V - 1)
+    pick = lq.gather(1, where)
+    term = torch.where(p > 0, p * (lp - pick), 0.0)
+    loss = torch.where(live, w.double() * term.sum(1), 0.0)
+    P = p.sum(1)
+    dense = torch.zeros_like(q).scatter_add_(1, where, torch.where(there, p, 0.0))
+    c = w.double() / tau
+    grad = torch.where(live[:, None], c[:, None] * (P[:, None] * q - dense), 0.0)
+    A, d = row_bound(s, V)
+    At = torch.where(torch.isfinite(u), u.abs(), 0.0).amax(1)
+    dp = 2.0 ** -20 * (At + 8) + (idx.shape[1] / 64 + 64) * 2.0 ** -24
+    gap = torch.where(p > 0, (lp.abs() + pick.abs()), 0.0).amax(1)
+    lb = w.double().abs() * P * (d + dp * (1 + gap))
+    gb = c.abs()[:, None] * (P[:, None] * q * (d + dp)[:, None] + dense * dp[:, None])
+    return loss, grad, torch.where(live, lse, 0.0), d, lb, gb
+
+
+def check_distill(z, zg, idx, t, tau, normalize, w, dt):
+    loss, grad, lse, d, lb, gb = distill64(z, idx, t, tau, normalize, w)
+    ig, tg, wg = idx.cuda(), t.cuda(), w.cuda()
+    kw = dict(temperature=tau, normalize=normalize)
+    fused = H.himuon_distill(zg, ig, tg, weight=wg, grad=True, **kw)
+    apart = H.himuon_distill(zg, ig, tg, weight=wg, **kw)
+    g2 = H.himuon_distill_grad(zg, ig, tg, apart.lse, wg, **kw)
+    torch.cuda.synchronize()
+    for r in (fused, apart):
+        near(r.loss, loss, lb, "loss")
+        near(r.lse.double().sum(1), lse, d, "lse")
+    for g in (fused.grad, g2):
+        near(g, grad, gb + ROUND[dt] * grad.abs() + 1e-38, "grad")
+    return fused
+
+
+def teacher(N, V, k, seed, kind=torch.int64):
+    idx = torch.stack([torch.randperm(V, generator=gen(seed + i))[:k] for i in range(N)]).to(kind)
+    return idx, torch.randn((N, k), generator=gen(seed + 999)) * 3
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,V,k", [(1, 1, 1), (2, 5, 5), (37, 1000, 8), (6, 5003, 64), (3, 32000, 100), (300, 263, 16),
+                                   (2, 131072, 64), (2, 131073, 1024), (1, 200001, 7)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_distill(cuda, N, V, k, normalize, dt):
+    print(f"distill {N}x{V} k {k} {normalize} {dt}", flush=True)
+    z = logits(N, V, dt, N + V)
+    idx, t = teacher(N, V, k, 50, torch.int64 if N % 2 else torch.int32)
+    if not normalize:
+        t = torch.log_softmax(t, 1) - 0.1
+    w = torch.rand(N, generator=gen(4)) + 0.5
+    check_distill(z, z.cuda(), idx, t, [1.0, 0.7, 2.0][V % 3], normalize, w, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("V,pad,shift", [(3000, 0, 0), (4099, 3, 1), (70000, 8, 8)])
+def test_distill_absent_repeated_masked(cuda, dt, V, pad, shift):
+    """Absent entries, rows without any, weight 0 over a row of NaN, ids given
+    more than once, p = 0, masked logits (some where the teacher has an entry),
+    a strided teacher, and the gradient in place."""
+    N, k = 8, 12
+    z = logits(N, V, dt, 70)
+    idx, t = teacher(N, V, k, 71)
+    wide = torch.full((N, k + 4), float("nan"))
+    wide[:, :k] = t
+    idx[0, 5:] = -1
+    idx[1] = V + 3
+    idx[2, 3:6] = idx[2, 0]
+    idx[3, :] = idx[3, 0]
+    t[4, 2:] = -INF
+    t[5] = -INF
+    wide[:, :k] = t
+    z[6, ::3] = -INF
+    z[6, idx[6, 1]] = 0.5
+    z[7] = float("nan")
+    w = torch.ones(N)
+    w[7] = 0.0
+    blocked = (z[6, idx[6]] == -INF)
+    idx[6, blocked] = -1
+    print(f"distill special {V} {dt}", flush=True)
+    zg = strided(z, pad, shift)
+    tg = wide.cuda()[:, :k]
+    for normalize in (True, False):
+        u = t if normalize else t - 3.0
+        zz = z.clone()
+        zz[7] = 0.0                       # the weight makes it count nothing; 0 * NaN would spread in the reference
+        loss, grad, lse, d, lb, gb = distill64(zz, idx, u, 1.5, normalize, w)
+        tt = tg if normalize else tg - 3.0
+        r = H.himuon_distill(zg, idx.cuda(), tt, 1.5, normalize, w.cuda(), grad=True)
+        near(r.loss, loss, lb, "loss")
+        near(r.grad, grad, gb + ROUND[dt] * grad.abs() + 1e-38, "grad")
+        assert r.loss[[1, 5, 7]].tolist() == [0.0, 0.0, 0.0] and torch.all(r.grad[[1, 5, 7]] == 0)
+        g2 = H.himuon_distill_grad(zg, idx.cuda(), tt, r.lse, w.cuda(), 1.5, normalize)
+        near(g2, grad, gb + ROUND[dt] * grad.abs() + 1e-38, "grad")
+    # in place, both ways
+    z1, z2 = strided(z, pad, shift), strided(z, pad, shift)
+    a = H.himuon_distill(z1, idx.cuda(), tg, 1.5, True, w.cuda(), grad=z1)
+    assert a.grad is z1
+    r = H.himuon_distill(zg, idx.cuda(), tg, 1.5, True, w.cuda(), grad=True)
+    assert torch.equal(z1, r.grad) and torch.equal(a.loss, r.loss)
+    H.himuon_distill_grad(z2, idx.cuda(), tg, r.lse, w.cuda(), 1.5, True, out=z2)
+    assert torch.equal(z2, H.himuon_distill_grad(zg, idx.cuda(), tg, r.lse, w.cuda(), 1.5, True))
+    for v in (z1, z2):
+        if v._base is not None:
+            assert torch.isnan(v._base[:, :shift]).all() and torch.isnan(v._base[:, shift + V:]).all()
+
+
+def test_distill_extremes(cuda):
+    """A masked logit under an entry gives the loss +inf and a finite gradient;
+    NaN and +inf make their own row NaN; a row of the lowest value is uniform."""
+    V = 2500
+    z = logits(5, V, "fp32", 80)
+    idx, t = teacher(5, V, 4, 81)
+    z[1, idx[1, 2]] = -INF
+    z[2, 9] = float("nan")
+    z[3, 9] = INF
+    z[4] = torch.finfo(torch.float32).min
+    r = H.himuon_distill(z.cuda(), idx.cuda(), t.cuda(), grad=True)
+    assert r.loss[1].item() == INF and torch.isfinite(r.grad[1]).all()
+    assert torch.isnan(r.loss[2:4]).all() and torch.isnan(r.grad[2:4]).all()
+    keep = [0, 4]
+    zz = z.clone()
+    zz[4] = 0.0
+    loss, grad, lse, d, lb, gb = distill64(zz, idx, t, 1.0, True, torch.ones(5))
+    near(r.loss[keep], loss[keep], lb[keep], "loss")
+    near(r.grad[keep], grad[keep], (gb + ROUND["fp32"] * grad.abs())[keep] + 1e-38, "grad")
+
+
+def test_distill_no_rows(cuda):
+    z = torch.zeros((0, 100), device="cuda")
+    r = H.himuon_distill(z, torch.zeros((0, 3), dtype=torch.int64, device="cuda"), torch.zeros((0, 3), device="cuda"), grad=True)
+    assert r.loss.shape == (0,) and r.grad.shape == (0, 100)
+
+
+def test_gradients_against_differences(cuda):
+    """Central differences of the forward results along a direction v of unit
+    entries: the third derivative of each is at most 8 times the sum of its
+    weights, so the difference is off by 8 h^2 and the rounding of the two
+    losses by 2 d / (2 h)."""
+    N, V, h = 4, 300, 2.0 ** -6
+    z = logits(N, V, "fp32", 90, scale=1.5)
+    v = torch.sign(torch.randn((N, V), generator=gen(91)))
+    idx, t = teacher(N, V, 6, 92)
+    tol = N * (8 * h * h + 2.0 ** -15 / h)
+    up, down = (z + h * v).cuda(), (z - h * v).cuda()
+
+    def loss(x):
+        return H.himuon_distill(x, idx.cuda(), t.cuda()).loss.double().sum()
+
+    g = H.himuon_distill(z.cuda(), idx.cuda(), t.cuda(), grad=True).grad
+    assert abs(float((loss(up) - loss(down)) / (2 * h)) - float((g.double().cpu() * v).sum())) <= tol
+    tokens = torch.tensor([5, 17, 0, 299])
+    one = torch.ones(N, device="cuda")
+    r = H.himuon_token_logprobs(z.cuda(), tokens.cuda())
+    for pick, args in (("logp", (one, None)), ("entropy", (None, one))):
+        f = lambda x: getattr(H.himuon_token_logprobs(x, tokens.cuda()), pick).double().sum()
+        g = H.himuon_token_logprobs_grad(z.cuda(), tokens.cuda(), r.lse, r.entropy, *args)
+        assert abs(float((f(up) - f(down)) / (2 * h)) - float((g.double().cpu() * v).sum())) <= tol
+
+
+@pytest.mark.parametrize("N,V", [(3, 100000), (600, 2048)])
+def test_same_bits_streams_graph(cuda, N, V):
+    z = logits(N, V, "bf16", 95).cuda()
+    idx, t = teacher(N, V, 9, 96)
+    idx, t = idx.cuda(), t.cuda()
+    tokens = torch.randint(0, V, (N,), generator=gen(97)).cuda()
+    w = torch.ones(N, device="cuda")
+
+    def calls(stream=None):
+        a = H.himuon_distill(z, idx, t, weight=w, grad=True, stream=stream)
+        b = H.himuon_token_logprobs(z, tokens, top=12, stream=stream)
+        c = H.himuon_token_logprobs_grad(z, tokens, b.lse, b.entropy, w, w, stream=stream)
+        e = H.himuon_distill_grad(z, idx, t, a.lse, w, stream=stream)
+        return [*a, *b, c, e]
+
+    ref = calls()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        got = calls(stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ref, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls()
+    for k in range(3):
+        z.copy_(logits(N, V, "bf16", 100 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(calls(), got))

@@ -1,0 +1,151 @@
+"""Refusals of the operators around the optimiser step: every bad argument is
+answered with its status before anything is launched (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import tiled_newton_schulz_amd as H
+from tiled_newton_schulz_amd import shape_descriptor as sd
+
+OK, INVALID, UNSUPPORTED, LAYOUT, OVERLAP, WORKSPACE = 0, 1, 2, 3, 4, 5
+P = 1 << 30
+
+
+def at(k):
+    return P + (k << 24)
+
+
+def ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def mats(ds):
+    return (H.himuon_matrix_t * len(ds))(*ds)
+
+
+def mm(x=sd(10, 64, ptr=at(0)), w=None, n=None, tr=0, ends=at(5), y=sd(10, 32, ptr=at(1)), dt=H.BF16):
+    w = [sd(64, 32, ptr=at(2)), sd(64, 32, ptr=at(3))] if w is None else w
+    return H.lib.himuon_grouped_mm(ref(x), mats(w) if w else None, len(w) if n is None else n, tr, ends, ref(y), dt, None)
+
+
+def wgrad(x=sd(10, 64, ptr=at(0)), d=sd(10, 32, ptr=at(1)), ends=at(5), g=None, n=None, dt=H.BF16):
+    g = [sd(64, 32, ptr=at(2)), sd(64, 32, ptr=at(3))] if g is None else g
+    return H.lib.himuon_grouped_wgrad(ref(x), ref(d), ends, mats(g) if g else None, len(g) if n is None else n, dt, None)
+
+
+def test_grouped_refusals():
+    assert mm(x=None) == mm(y=None) == mm(w=[]) == mm(ends=None) == mm(n=0) == mm(n=-1) == INVALID
+    assert mm(dt=7) == mm(dt=H.BF16_PRECISE) == UNSUPPORTED
+    assert mm(x=sd(10, 63, ptr=at(0))) == INVALID                       # inner sizes differ
+    assert mm(y=sd(11, 32, ptr=at(1))) == mm(y=sd(10, 31, ptr=at(1))) == INVALID
+    assert mm(tr=1) == INVALID                                          # stored N x K then
+    assert mm(w=[sd(64, 32, ptr=at(2)), sd(64, 33, ptr=at(3))]) == INVALID
+    assert mm(w=[sd(64, 32, ptr=at(2)), H.himuon_matrix_t(None, 64, 32, 32)]) == INVALID
+    assert mm(x=sd(10, 64, ld=63, ptr=at(0))) == INVALID
+    assert mm(x=sd(-1, 64, ptr=at(0))) == INVALID
+    assert mm(x=sd(10, 64, ptr=at(0) + 1)) == LAYOUT
+    assert mm(ends=at(5) + 2) == LAYOUT
+    assert mm(y=sd(10, 32, ptr=at(0))) == OVERLAP
+    assert mm(y=sd(10, 32, ptr=at(3) + 64)) == OVERLAP
+    assert mm(ends=at(1)) == OVERLAP
+    huge = 1 << 31
+    assert mm(x=sd(huge, 64, ptr=at(0)), y=sd(huge, 32, ptr=1 << 50)) == LAYOUT
+    big = (1 << 31) - 1
+    assert mm(x=sd(big, 64, ptr=1 << 40), w=[sd(64, 1 << 22, ptr=at(9))], y=sd(big, 1 << 22, ptr=1 << 58)) == LAYOUT
+    # no rows: nothing to do, pointers of the rows are not looked at
+    assert mm(x=H.himuon_matrix_t(None, 0, 64, 64), y=H.himuon_matrix_t(None, 0, 32, 32)) == OK
+    assert mm(x=H.himuon_matrix_t(None, 0, 64, 63), y=H.himuon_matrix_t(None, 0, 32, 32)) == INVALID
+
+
+def test_wgrad_refusals():
+    assert wgrad(x=None) == wgrad(d=None) == wgrad(g=[]) == wgrad(ends=None) == wgrad(n=0) == INVALID
+    assert wgrad(dt=H.BF16_PRECISE) == UNSUPPORTED
+    assert wgrad(d=sd(11, 32, ptr=at(1))) == wgrad(d=sd(10, 33, ptr=at(1))) == INVALID
+    assert wgrad(g=[sd(32, 64, ptr=at(2))]) == INVALID
+    assert wgrad(g=[sd(64, 32, ptr=at(2) + 1)]) == LAYOUT
+    assert wgrad(g=[sd(64, 32, ptr=at(2)), sd(64, 32, ptr=at(2) + 2048)]) == OVERLAP
+    assert wgrad(g=[sd(64, 32, ptr=at(0))]) == wgrad(g=[sd(64, 32, ptr=at(1))]) == wgrad(g=[sd(64, 32, ptr=at(5))]) == OVERLAP
+    # more output tiles than a launch can hold
+    wide = (1 << 24) - 8
+    assert wgrad(x=sd(1, wide, ptr=at(0)), d=sd(1, wide, ptr=at(9)), g=[sd(wide, wide, ptr=1 << 40)]) == LAYOUT
+
+
+Z = sd(6, 100, ptr=at(0))
+T = sd(6, 4, ptr=at(2))
+
+
+def distill(z=Z, idx=at(1), it=H.I32, t=T, tau=1.0, norm=1, weight=None, loss=at(3), lse=at(4), dz=None, dt=H.BF16,
+            ws=at(20), nb=1 << 20):
+    return H.lib.himuon_distill(ref(z), idx, it, ref(t), tau, norm, weight, loss, lse, ref(dz), dt, ws, nb, None)
+
+
+def distill_grad(z=Z, idx=at(1), it=H.I32, t=T, tau=1.0, lse=at(4), g=at(3), dz=sd(6, 100, ptr=at(6)), dt=H.BF16):
+    return H.lib.himuon_distill_grad(ref(z), idx, it, ref(t), tau, 1, lse, g, ref(dz), dt, None)
+
+
+def test_distill_refusals():
+    assert distill(z=None) == distill(t=None) == distill(idx=None) == distill(loss=None) == INVALID
+    for tau in (0.0, -1.0, float("inf"), float("nan"), 1e-45):
+        assert distill(tau=tau) == distill_grad(tau=tau) == INVALID
+    assert distill(dt=H.BF16_PRECISE) == distill(it=2) == distill_grad(it=-1) == UNSUPPORTED
+    assert distill(t=sd(6, H.MAX_ENTRIES + 1, ptr=at(2))) == UNSUPPORTED
+    assert distill(t=sd(5, 4, ptr=at(2))) == INVALID
+    assert distill(dz=sd(6, 99, ptr=at(6))) == distill(dz=sd(5, 100, ptr=at(6))) == INVALID
+    assert distill(idx=at(1) + 2) == distill(idx=at(1) + 4, it=H.I64) == distill(loss=at(3) + 1) == LAYOUT
+    assert distill(z=sd(6, 100, ptr=at(0) + 1)) == LAYOUT
+    assert distill(dz=sd(6, 100, ptr=at(0) + 200)) == OVERLAP          # shifted over Z
+    assert distill(dz=sd(6, 100, ld=104, ptr=at(0))) == OVERLAP        # Z at another stride
+    assert distill(dz=sd(6, 100, ptr=at(2))) == OVERLAP                # over the teacher's values
+    assert distill(loss=at(4)) == distill(loss=at(0)) == distill(weight=at(3)) == distill(lse=at(1)) == OVERLAP
+    assert distill_grad(dz=None) == distill_grad(lse=None) == distill_grad(g=None) == INVALID
+    assert distill_grad(dz=sd(6, 100, ptr=at(4))) == OVERLAP
+    e = lambda c: H.himuon_matrix_t(None, 0, c, c)
+    assert distill(z=e(100), t=e(4), idx=None, loss=None, lse=None) == OK
+    n = ctypes.c_size_t(7)
+    assert H.lib.himuon_distill_workspace(None, H.BF16, 1, ctypes.byref(n)) == INVALID
+    assert H.lib.himuon_distill_workspace(ref(Z), H.BF16, 1, None) == INVALID
+    assert H.lib.himuon_distill_workspace(ref(Z), H.BF16_PRECISE, 1, ctypes.byref(n)) == UNSUPPORTED
+    assert H.lib.himuon_distill_workspace(ref(Z), H.BF16, 1, ctypes.byref(n)) == OK
+
+
+def logprobs(z=Z, tok=at(1), it=H.I64, tau=1.0, top=3, logp=at(2), ent=at(3), lse=at(4), ti=at(5), tl=at(6), dt=H.BF16,
+             ws=at(20), nb=1 << 20):
+    return H.lib.himuon_token_logprobs(ref(z), tok, it, tau, top, logp, ent, lse, ti, tl, dt, ws, nb, None)
+
+
+def logprobs_grad(z=Z, tok=at(1), it=H.I64, tau=1.0, lse=at(4), ent=at(3), gl=at(5), gh=at(6), dz=sd(6, 100, ptr=at(7)),
+                  dt=H.BF16):
+    return H.lib.himuon_token_logprobs_grad(ref(z), tok, it, tau, lse, ent, gl, gh, ref(dz), dt, None)
+
+
+def test_logprobs_refusals():
+    assert logprobs(z=None) == logprobs(tok=None) == logprobs(top=-1) == logprobs(top=101) == INVALID
+    assert logprobs(ti=None) == logprobs(tl=None) == INVALID
+    assert logprobs(top=H.MAX_TOP + 1) == logprobs(dt=9) == logprobs(it=5) == UNSUPPORTED
+    assert logprobs(tok=at(1) + 4) == logprobs(lse=at(4) + 2) == LAYOUT
+    assert logprobs(logp=at(3)) == logprobs(lse=at(0)) == logprobs(ti=at(1)) == OVERLAP
+    assert logprobs(lse=at(3) + 8) == OVERLAP
+    assert logprobs(tau=0.0) == logprobs_grad(tau=float("nan")) == INVALID
+    assert logprobs_grad(dz=None) == logprobs_grad(lse=None) == logprobs_grad(tok=None) == logprobs_grad(ent=None) == INVALID
+    assert logprobs_grad(dz=sd(6, 100, ptr=at(5))) == OVERLAP
+    e = H.himuon_matrix_t(None, 0, 100, 100)
+    assert logprobs(z=e, ti=None, tl=None) == OK
+    n = ctypes.c_size_t(7)
+    assert H.lib.himuon_token_logprobs_workspace(ref(Z), 101, H.BF16, ctypes.byref(n)) == INVALID
+    assert H.lib.himuon_token_logprobs_workspace(ref(sd(6, 1000)), 65, H.BF16, ctypes.byref(n)) == UNSUPPORTED
+    assert H.lib.himuon_token_logprobs_workspace(ref(Z), 3, H.BF16, ctypes.byref(n)) == OK
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(4, 8), torch.zeros(2, 8, 8)
+    ends = torch.tensor([1, 4], dtype=torch.int32)
+    for call in (lambda: H.matrices(w), lambda: H.himuon_grouped_mm(x, w, ends),
+                 lambda: H.himuon_grouped_wgrad(x, x, ends),
+                 lambda: H.himuon_distill(x, ends, x), lambda: H.himuon_token_logprobs(x)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ValueError):
+        H.matrices([])
+    with pytest.raises(ValueError):
+        H.matrices(torch.zeros(2, 8, 8, 2)[..., 0].transpose(0, 1))

@@ -1,0 +1,36 @@
+// Internal declarations of the experts' products (api_model.cpp, grouped.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace himuon {
+
+// Experts of one launch.  With the rows that belong to no expert as one more
+// slot they fill four slots for each lane of a wave (find_tile in grouped.hip).
+constexpr int kExperts = 255;
+
+// One launch of Y = X W_e (or X W_e^T) or of G_e = X_e^T D_e.
+struct GroupedArgs {
+    const void* x;           // M x K
+    const void* d;           // weight gradient: M x N
+    void* y;                 // product: M x N
+    int64_t x_ld, d_ld, y_ld;
+    const int32_t* ends;     // device: end row of every expert of the call
+    int32_t rows;            // M
+    int32_t kdim, ndim;      // K, N
+    int32_t e0, n;           // experts [e0, e0 + n) of the call
+    int32_t last;            // product: this launch also zeroes the rows past the last expert
+    int32_t dtype;           // 0 bf16, 1 fp32
+    int32_t vec;             // rows and widths allow 16-byte chunks
+    void* w[kExperts];       // product: weights; weight gradient: results
+    int64_t w_ld[kExperts];
+};
+
+// Largest grid the launchers would use (checked against INT32_MAX before any launch).
+int64_t grouped_mm_grid(const GroupedArgs& a);
+int64_t grouped_wgrad_grid(const GroupedArgs& a);
+hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s);
+hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
+
+}  // namespace himuon
