@@ -38,7 +38,8 @@ himuon_status_t check_rows(const himuon_matrix_t& d, size_t es) {
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-bool chunked(const himuon_matrix_t& d) { return aligned(d.ptr, 16) && d.ld % 8 == 0; }
+// Rows of whole 16-byte chunks, and 256 of them within 32-bit byte offsets.
+bool chunked(const himuon_matrix_t& d) { return aligned(d.ptr, 16) && d.ld % 8 == 0 && d.ld <= (1 << 22); }
 
 // Byte range of a contiguous device array, as an extent of one row.
 Extent array_extent(const void* p, int64_t bytes) {

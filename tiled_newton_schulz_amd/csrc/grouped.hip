@@ -73,14 +73,15 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
     }
     int lo, hi;
     slot_rows(a, e, lo, hi);
-    t.e = e;
-    t.row0 = lo;
-    t.rows = hi - lo;
+    // the same in every lane: scalar registers
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    t.row0 = __builtin_amdgcn_readfirstlane(lo);
+    t.rows = __builtin_amdgcn_readfirstlane(hi - lo);
     const int64_t off = id - base * ntn;
     // always true where the end rows do not decrease; otherwise the tile is left out
     if (c <= 0 || off < 0 || off >= (int64_t)c * ntn) return false;
-    t.mt = (int)(off % c);
-    t.nt = (int)(off / c);
+    t.mt = __builtin_amdgcn_readfirstlane((int)off % c);
+    t.nt = __builtin_amdgcn_readfirstlane((int)off / c);
     return true;
 }
 
@@ -169,6 +170,7 @@ template <int DT>
 __global__ __launch_bounds__(256) void grouped_wgrad_kernel(const GroupedArgs a) {
     using T = typename Io<DT>::T;
     const int ntk = (a.kdim + 63) / 64, ntn = (a.ndim + 63) / 64;
+    if ((int)blockIdx.x >= a.n * ntk * ntn) return;
     const int e = blockIdx.x / (ntk * ntn), b = blockIdx.x % (ntk * ntn);
     const int i0 = (b % ntk) * 64, j0 = (b / ntk) * 64;
     int lo, hi;
@@ -181,21 +183,257 @@ __global__ __launch_bounds__(256) void grouped_wgrad_kernel(const GroupedArgs a)
     store64<DT>(reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], mi, nj, acc);
 }
 
+// ---------------------------------------------------------------------------
+// bf16 operands of 16-byte chunks: 256 x 256 tiles, k in steps of 64, eight
+// waves (2 along the rows, 4 along the columns), two LDS stages filled straight
+// from global memory.
+//
+// Ragged tiles: the 32 x 32 blocks of a wave interleave with the other waves'
+// (rows (2 i + wm) 32, columns (4 j + wn) 32), so a tile of r rows and c columns
+// costs FM = ceil(r / 64) by FN = ceil(c / 128) blocks in every wave, and the
+// loop is compiled for each FM and FN.
+//
+// An operand is stored in memory either along k (rows i of k) or along its
+// other side (rows k of i), and its LDS stage keeps that order:
+//   along k: 256 rows of 8 16-byte chunks, chunk c of row r at place c ^ (r & 7)
+//   along i: two sub-panels of 64 k rows of 128 elements, chunk c of row k at
+//            place c ^ (4 (k & 3)); read transposed (ds_read_tr16_b64)
+// The products run with the operands exchanged (columns as the MFMA's rows), so
+// that a lane ends with runs of four consecutive columns of one row.
+// ---------------------------------------------------------------------------
+constexpr int kBig = 256;             // tile edge
+constexpr int kBK = 64;
+constexpr int kStage = kBig * kBK;    // elements of one operand's stage
+constexpr int kLdc = kBig + 8;        // row stride of the result in LDS
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// Buffer descriptor of [p, p + bytes): loads past it give zeros.
+__device__ __forceinline__ i32x4 rsrc_words(const void* p, uint32_t bytes) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return i32x4{(int)(uint32_t)u, (int)(uint32_t)(u >> 32) & 0xffff, (int)bytes, 0x00020000};
+}
+// 64 lanes x 16 bytes from r + off to LDS byte address lds + 16 lane.  As
+// inline assembly, since the compiler makes every transposed LDS read wait for
+// all such loads it knows of; the waits are in stage_ready().  It has no
+// register result, so nothing can be read or reused too early.
+__device__ __forceinline__ void dma16(i32x4 r, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(off), "s"(r) : "memory");
+}
+// Every load of this wave has landed and its LDS reads are done; then the same
+// of all waves.
+__device__ __forceinline__ void stage_ready() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// One operand of a tile: up to 256 rows or columns (`side`) by k.
+template <bool ALONG_K>
+struct Panel {
+    const unsigned short* p;   // element (0, 0) of the tile at k = 0
+    int64_t ld;
+    int side;                  // rows (or columns) of the tile inside the operand
+    int kd;                    // length of k
+
+    // instructions a wave issues for B blocks of 32 * (waves along the side)
+    static constexpr int count(int units64) { return ALONG_K ? units64 : 2 * ((units64 + 1) / 2); }
+
+    // byte offset of instruction j of this wave from the step's first byte
+    __device__ __forceinline__ uint32_t offset(int j, int wave, int lane) const {
+        const int pos = (j * 8 + wave) * 64 + lane;
+        if (ALONG_K) {
+            const int r = pos >> 3, c = (pos & 7) ^ (r & 7);
+            // rows past the operand go past the buffer's end
+            return r < side ? (uint32_t)(r * (uint32_t)ld * 2u) + c * 16u : 0xffffff00u;
+        }
+        const int sub = pos >> 10, k = (pos & 1023) >> 4, c = (pos & 15) ^ ((k & 3) * 4);
+        const int i = sub * 128 + c * 8;
+        return i < side ? (uint32_t)(k * (uint32_t)ld * 2u) + i * 2u : 0xffffff00u;
+    }
+    // first k element of the chunk (stored along k)
+    static __device__ __forceinline__ int chunk_k(int j, int wave, int lane) {
+        const int pos = (j * 8 + wave) * 64 + lane, r = pos >> 3;
+        return ((pos & 7) ^ (r & 7)) * 8;
+    }
+    // the operand's bytes from step k0 on (the last row that counts ends them)
+    __device__ __forceinline__ i32x4 rsrc(int k0) const {
+        if (ALONG_K) return rsrc_words(p + k0, (uint32_t)(((side - 1) * ld + kd - k0) * 2));
+        const int rows = min(kBK, kd - k0);
+        return rsrc_words(p + k0 * ld, (uint32_t)(((rows - 1) * ld + side) * 2));
+    }
+    // MFMA operand of the 32-wide block at `first`, k sub-step kk
+    static __device__ __forceinline__ bf16x8 read(const unsigned short* st, int first, int kk, int lane) {
+        if (ALONG_K) {
+            const int r = first + (lane & 31), c = (kk * 2 + (lane >> 5)) ^ (r & 7);
+            return *reinterpret_cast<const bf16x8*>(&st[r * kBK + c * 8]);
+        }
+        const int i16 = lane & 15;
+        const int col = first + 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
+        const int k = kk * 16 + 8 * (lane >> 5) + (i16 >> 2);
+        const int cl = col & 127;
+        const unsigned short* q = &st[(col >> 7) * (kBK * 128) + k * 128 + (((cl >> 3) ^ ((k & 3) * 4)) * 8) + (cl & 7)];
+        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q));
+        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q + 4 * 128));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+template <bool AK, bool BK_, int FM, int FN>
+__device__ __forceinline__ void big_tile(const Panel<AK>& A, const Panel<BK_>& B, unsigned short* sbuf,
+                                         unsigned short* C, int64_t ldc) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    constexpr int NA = Panel<AK>::count(FM), NB = Panel<BK_>::count(2 * FN);
+    uint32_t oa[NA], ob[NB];
+#pragma unroll
+    for (int j = 0; j < NA; ++j) oa[j] = A.offset(j, wave, lane);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) ob[j] = B.offset(j, wave, lane);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS void*)sbuf;
+    const int nk = (A.kd + kBK - 1) / kBK;
+
+    auto issue = [&](int kt) __attribute__((always_inline)) {
+        const int k0 = kt * kBK;
+        const i32x4 ra = A.rsrc(k0), rb = B.rsrc(k0);
+        const uint32_t la = lds0 + (kt & 1) * (2 * kStage * 2) + wave * 1024, lb = la + kStage * 2;
+        // a last step that k does not fill: chunks past its end would read the
+        // next row, so they go past the buffer's end too
+        const int left = A.kd - k0;
+#pragma unroll
+        for (int j = 0; j < NA; ++j)
+            dma16(ra, AK && left < kBK && Panel<AK>::chunk_k(j, wave, lane) >= left ? 0xffffff00u : oa[j], la + j * 8192);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            dma16(rb, BK_ && left < kBK && Panel<BK_>::chunk_k(j, wave, lane) >= left ? 0xffffff00u : ob[j], lb + j * 8192);
+    };
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+
+    if (nk > 0) issue(0);
+    for (int kt = 0; kt < nk; ++kt) {
+        stage_ready();
+        if (kt + 1 < nk) issue(kt + 1);
+        const unsigned short* sa = sbuf + (kt & 1) * 2 * kStage;
+        const unsigned short* sb = sa + kStage;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk) {
+            bf16x8 av[FM], bv[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) av[i] = Panel<AK>::read(sa, (i * 2 + wm) * 32, kk, lane);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) bv[j] = Panel<BK_>::read(sb, (j * 4 + wn) * 32, kk, lane);
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    // result through LDS, then whole 16-byte chunks of rows
+    __syncthreads();
+    const int l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const u32x2 v = {pack2(acc[i][j][4 * m], acc[i][j][4 * m + 1]),
+                                 pack2(acc[i][j][4 * m + 2], acc[i][j][4 * m + 3])};
+                *reinterpret_cast<u32x2*>(&sbuf[((i * 2 + wm) * 32 + l32) * kLdc + (j * 4 + wn) * 32 + m * 8 + gl * 4]) = v;
+            }
+    __syncthreads();
+    constexpr int CH = FN * 16;   // chunks of a row
+#pragma unroll
+    for (int it = 0; it < FM * 64 * CH / 512; ++it) {
+        const int id = it * 512 + tid, r = id / CH, c = (id % CH) * 8;
+        if (r < A.side && c < B.side)
+            *reinterpret_cast<u32x4*>(C + r * ldc + c) = *reinterpret_cast<const u32x4*>(&sbuf[r * kLdc + c]);
+    }
+}
+
+template <bool AK, bool BK_>
+__device__ __forceinline__ void big_dispatch(const Panel<AK>& A, const Panel<BK_>& B, unsigned short* sbuf,
+                                             unsigned short* C, int64_t ldc) {
+    const int fm = (A.side + 63) / 64;
+    if (B.side > 128) {
+        if (fm == 4) big_tile<AK, BK_, 4, 2>(A, B, sbuf, C, ldc);
+        else if (fm == 3) big_tile<AK, BK_, 3, 2>(A, B, sbuf, C, ldc);
+        else if (fm == 2) big_tile<AK, BK_, 2, 2>(A, B, sbuf, C, ldc);
+        else big_tile<AK, BK_, 1, 2>(A, B, sbuf, C, ldc);
+    } else {
+        if (fm == 4) big_tile<AK, BK_, 4, 1>(A, B, sbuf, C, ldc);
+        else if (fm == 3) big_tile<AK, BK_, 3, 1>(A, B, sbuf, C, ldc);
+        else if (fm == 2) big_tile<AK, BK_, 2, 1>(A, B, sbuf, C, ldc);
+        else big_tile<AK, BK_, 1, 1>(A, B, sbuf, C, ldc);
+    }
+}
+
+template <bool WT>
+__global__ __launch_bounds__(512) void grouped_mm_big(const GroupedArgs a) {
+    __shared__ __attribute__((aligned(16))) unsigned short sbuf[kBig * kLdc];
+    GroupTile t;
+    if (!find_tile(a, kBig, (a.ndim + kBig - 1) / kBig, t)) return;
+    const int64_t m0 = t.row0 + t.mt * kBig;
+    const int n0 = t.nt * kBig;
+    Panel<true> A{reinterpret_cast<const unsigned short*>(a.x) + m0 * a.x_ld, a.x_ld,
+                  min(kBig, t.rows - t.mt * kBig), a.kdim};
+    Panel<WT> B{nullptr, 0, min(kBig, a.ndim - n0), a.kdim};
+    if (t.e < a.n) {
+        B.ld = a.w_ld[t.e];
+        B.p = reinterpret_cast<const unsigned short*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
+    } else {
+        A.kd = B.kd = 0;   // rows of no expert: zeros
+    }
+    big_dispatch<true, WT>(A, B, sbuf, reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
+}
+
+__global__ __launch_bounds__(512) void grouped_wgrad_big(const GroupedArgs a) {
+    __shared__ __attribute__((aligned(16))) unsigned short sbuf[kBig * kLdc];
+    const int ntk = (a.kdim + kBig - 1) / kBig, ntn = (a.ndim + kBig - 1) / kBig;
+    const int total = a.n * ntk * ntn, per = (total + 7) / 8;
+    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+    const int e = id / (ntk * ntn), b = id % (ntk * ntn);
+    const int i0 = (b % ntk) * kBig, j0 = (b / ntk) * kBig;
+    int lo, hi;
+    slot_rows(a, e, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    const int kd = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
+    const Panel<false> A{reinterpret_cast<const unsigned short*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(kBig, a.kdim - i0), kd};
+    const Panel<false> B{reinterpret_cast<const unsigned short*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(kBig, a.ndim - j0), kd};
+    big_dispatch<false, false>(A, B, sbuf, reinterpret_cast<unsigned short*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int tile_edge(const GroupedArgs& a) { return a.dtype == 0 && a.vec ? kBig : 64; }
 
 }  // namespace
 
 int64_t grouped_mm_grid(const GroupedArgs& a) {
     // every slot ends in at most one partial row tile
-    const int64_t row_tiles = a.rows / 64 + a.n + 1;
-    return cdiv(row_tiles * cdiv(a.ndim, 64), 8) * 8;
+    const int edge = tile_edge(a);
+    const int64_t row_tiles = a.rows / edge + a.n + 1;
+    return cdiv(row_tiles * cdiv(a.ndim, edge), 8) * 8;
 }
 
-int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(a.kdim, 64) * cdiv(a.ndim, 64) * a.n; }
+int64_t grouped_wgrad_grid(const GroupedArgs& a) {
+    const int edge = tile_edge(a);
+    return cdiv(cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n, 8) * 8;
+}
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
     const dim3 grid((uint32_t)grouped_mm_grid(a));
-    if (a.dtype == 0) {
+    if (a.dtype == 0 && a.vec) {
+        if (trans_w) hipLaunchKernelGGL((grouped_mm_big<true>), grid, dim3(512), 0, s, a);
+        else hipLaunchKernelGGL((grouped_mm_big<false>), grid, dim3(512), 0, s, a);
+    } else if (a.dtype == 0) {
         if (trans_w) hipLaunchKernelGGL((grouped_mm_kernel<0, true>), grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL((grouped_mm_kernel<0, false>), grid, dim3(256), 0, s, a);
     } else {
@@ -207,7 +445,8 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
     const dim3 grid((uint32_t)grouped_wgrad_grid(a));
-    if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_kernel<0>), grid, dim3(256), 0, s, a);
+    if (a.dtype == 0 && a.vec) hipLaunchKernelGGL(grouped_wgrad_big, grid, dim3(512), 0, s, a);
+    else if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_kernel<0>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((grouped_wgrad_kernel<1>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
