@@ -45,7 +45,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
         const int i = lane * 4 + k;
         int lo = 0, hi = 0;
         if (i < slots) slot_rows(a, i, lo, hi);
-        cnt[k] = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+        cnt[k] = hi > lo ? (hi - lo - 1) / BM + 1 : 0;
         sum += cnt[k];
     }
     int incl = sum;
@@ -185,229 +185,426 @@ __global__ __launch_bounds__(256) void grouped_wgrad_kernel(const GroupedArgs a)
 
 // ---------------------------------------------------------------------------
 // bf16 operands of 16-byte chunks: 256 x 256 tiles, k in steps of 64, eight
-// waves (2 along the rows, 4 along the columns), two LDS stages filled straight
-// from global memory.
+// waves (2 along the rows, 4 along the columns).
 //
-// Ragged tiles: the 32 x 32 blocks of a wave interleave with the other waves'
-// (rows (2 i + wm) 32, columns (4 j + wn) 32), so a tile of r rows and c columns
-// costs FM = ceil(r / 64) by FN = ceil(c / 128) blocks in every wave, and the
-// loop is compiled for each FM and FN.
+// LDS holds two steps of both operands (A0 A1 B0 B1, each half a panel: 128 rows
+// or columns by 64), filled straight from global memory.  The 32 x 32 blocks of
+// a wave interleave with the other waves' (rows (2 i + wm) 32, columns
+// (4 j + wn) 32), so every wave reads every half.  A step is four slots of a
+// wave, with a barrier after each:
+//     read    A0, B0, B1 into registers; A1 of the next step into LDS
+//     multiply A0 B0, A0 B1 (16 MFMAs)
+//     read    A1 into the registers of A0; A0, B0, B1 two steps on into LDS
+//     multiply A1 B0, A1 B1
+// Waves 4 - 7 run one slot behind waves 0 - 3, so that of the two waves on a
+// SIMD one always multiplies while the other reads, loads, stores a finished
+// tile or looks up the next one.  (With all waves in step, the reads between the
+// products as in a usual pipeline, the matrix units idled a third of the time
+// around the barriers.)
+// The loads run on into the next tile of the workgroup, and the result goes from
+// registers to memory, so neither the pipeline's start nor a tile's end drains it.
+//
+// Ragged tiles: halves of 128 rows or columns outside the tile are not
+// multiplied; their loads end past the buffer and give zeros.
 //
 // An operand is stored in memory either along k (rows i of k) or along its
-// other side (rows k of i), and its LDS stage keeps that order:
-//   along k: 256 rows of 8 16-byte chunks, chunk c of row r at place c ^ (r & 7)
-//   along i: two sub-panels of 64 k rows of 128 elements, chunk c of row k at
-//            place c ^ (4 (k & 3)); read transposed (ds_read_tr16_b64)
+// other side (rows k of i), and LDS keeps that order:
+//   along k: 16-byte chunk c of row i at place c ^ ((i / 2) & 7)
+//   along i: sub-panels of 128 elements; chunk c of row k at place
+//            c ^ (4 (k & 3)); read transposed (ds_read_tr16_b64)
+// Both leave the 16 lanes that read together on 64 different banks.
 // The products run with the operands exchanged (columns as the MFMA's rows), so
 // that a lane ends with runs of four consecutive columns of one row.
 // ---------------------------------------------------------------------------
-constexpr int kBig = 256;             // tile edge
-constexpr int kBK = 64;
-constexpr int kStage = kBig * kBK;    // elements of one operand's stage
-constexpr int kLdc = kBig + 8;        // row stride of the result in LDS
+constexpr int kBig = 256;                  // tile edge
+constexpr int kBK = 64;                    // k of a step
+constexpr int kPanel = kBig * kBK;         // elements of one operand's step
+constexpr uint32_t kNowhere = 0x80000000u; // byte offset past every buffer
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// Buffer descriptor of [p, p + bytes): loads past it give zeros.
-__device__ __forceinline__ i32x4 rsrc_words(const void* p, uint32_t bytes) {
+// Buffer descriptor of [p, p + bytes): loads past it give zeros, stores are dropped.
+__device__ __forceinline__ i32x4 rsrc_words(const void* p, int64_t bytes) {
     const uint64_t u = reinterpret_cast<uint64_t>(p);
-    return i32x4{(int)(uint32_t)u, (int)(uint32_t)(u >> 32) & 0xffff, (int)bytes, 0x00020000};
+    const int n = bytes < 0 ? 0 : bytes > 0x7fffff00 ? 0x7fffff00 : (int)bytes;
+    return i32x4{(int)(uint32_t)u, (int)((uint32_t)(u >> 32) & 0xffffu), n, 0x00020000};
 }
 // 64 lanes x 16 bytes from r + off to LDS byte address lds + 16 lane.  As
 // inline assembly, since the compiler makes every transposed LDS read wait for
-// all such loads it knows of; the waits are in stage_ready().  It has no
+// all such loads it knows of; the waits are in phase_gate().  It has no
 // register result, so nothing can be read or reused too early.
 __device__ __forceinline__ void dma16(i32x4 r, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(lds), "v"(off), "s"(r) : "memory");
 }
-// Every load of this wave has landed and its LDS reads are done; then the same
-// of all waves.
-__device__ __forceinline__ void stage_ready() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// Ends a reading slot: all but this wave's newest loads have landed and its LDS
+// reads are done; then the same of all waves.  A half is loaded one step before
+// this wait for it: four halves (8 loads of the wave) are newer.  In the step
+// after a tile's result, its 16 stores (always issued, see put_result) are too.
+constexpr int kStores = 16;
+__device__ __forceinline__ void end_read(int stores) {
+    asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lgate%=\n\ts_waitcnt vmcnt(8)\n"
+                 ".Lgate%=:\n\ts_waitcnt vmcnt(24) lgkmcnt(0)\n\ts_barrier" :: "s"(stores) : "memory", "scc");
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0) again, for the compiler's own count
+    __builtin_amdgcn_sched_barrier(0);
+}
+static_assert(8 + kStores == 24, "end_read");
+__device__ __forceinline__ void end_multiply() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
-// One operand of a tile: up to 256 rows or columns (`side`) by k.
-template <bool ALONG_K>
+// One operand of a tile, 256 rows (or columns) by k.
 struct Panel {
     const unsigned short* p;   // element (0, 0) of the tile at k = 0
     int64_t ld;
     int side;                  // rows (or columns) of the tile inside the operand
-    int kd;                    // length of k
+    int kd;                    // length of k (0: no operand, all zeros)
+};
 
-    // instructions a wave issues for B blocks of 32 * (waves along the side)
-    static constexpr int count(int units64) { return ALONG_K ? units64 : 2 * ((units64 + 1) / 2); }
+// The loads of one operand, step by step.  An instruction of the workgroup
+// fills 64 rows of 128 bytes (along k) or 32 rows of 256 bytes (along i); a half
+// takes two.
+template <bool ALONG_K>
+struct Feed {
+    uint64_t at;        // first byte of the step
+    int64_t rest;       // bytes from there to the operand's end (the end of the last row that counts)
+    int64_t move;       // bytes to the next step
+    int left;           // k from the step on
+    uint32_t v, first;  // this lane's byte offset in an instruction; first k element of its chunk
+    uint32_t off[2][2]; // byte offset of instruction j of half h
 
-    // byte offset of instruction j of this wave from the step's first byte
-    __device__ __forceinline__ uint32_t offset(int j, int wave, int lane) const {
-        const int pos = (j * 8 + wave) * 64 + lane;
-        if (ALONG_K) {
-            const int r = pos >> 3, c = (pos & 7) ^ (r & 7);
-            // rows past the operand go past the buffer's end
-            return r < side ? (uint32_t)(r * (uint32_t)ld * 2u) + c * 16u : 0xffffff00u;
+    __device__ __forceinline__ void start(const Panel& q, int wave, int lane) {
+        const uint32_t ld2 = 2u * (uint32_t)q.ld;
+        at = reinterpret_cast<uint64_t>(q.p);
+        left = q.kd;
+        if constexpr (ALONG_K) {
+            const uint32_t c = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
+            rest = 2 * ((int64_t)(q.side - 1) * q.ld + q.kd);
+            move = 2 * kBK;
+            v = (uint32_t)(8 * wave + (lane >> 3)) * ld2 + c * 16u;
+            first = c * 8;
+        } else {
+            rest = 2 * ((int64_t)(q.kd - 1) * q.ld + q.side);
+            move = (int64_t)kBK * ld2;
+            v = (uint32_t)(4 * wave + (lane >> 4)) * ld2 + (((lane & 15) ^ ((lane >> 4) * 4)) * 16u);
+            first = 0;
         }
-        const int sub = pos >> 10, k = (pos & 1023) >> 4, c = (pos & 15) ^ ((k & 3) * 4);
-        const int i = sub * 128 + c * 8;
-        return i < side ? (uint32_t)(k * (uint32_t)ld * 2u) + i * 2u : 0xffffff00u;
+        // rows past the operand start past its end; columns are left out by half
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                off[h][j] = ALONG_K ? (h * 128 + j * 64) * ld2
+                                    : h * 128 < q.side ? h * 256 + j * 32 * ld2 : kNowhere;
     }
-    // first k element of the chunk (stored along k)
-    static __device__ __forceinline__ int chunk_k(int j, int wave, int lane) {
-        const int pos = (j * 8 + wave) * 64 + lane, r = pos >> 3;
-        return ((pos & 7) ^ (r & 7)) * 8;
+    __device__ __forceinline__ void next() {
+        at += move;
+        rest -= move;
+        left -= kBK;
     }
-    // the operand's bytes from step k0 on (the last row that counts ends them)
-    __device__ __forceinline__ i32x4 rsrc(int k0) const {
-        if (ALONG_K) return rsrc_words(p + k0, (uint32_t)(((side - 1) * ld + kd - k0) * 2));
-        const int rows = min(kBK, kd - k0);
-        return rsrc_words(p + k0 * ld, (uint32_t)(((rows - 1) * ld + side) * 2));
-    }
-    // MFMA operand of the 32-wide block at `first`, k sub-step kk
-    static __device__ __forceinline__ bf16x8 read(const unsigned short* st, int first, int kk, int lane) {
-        if (ALONG_K) {
-            const int r = first + (lane & 31), c = (kk * 2 + (lane >> 5)) ^ (r & 7);
-            return *reinterpret_cast<const bf16x8*>(&st[r * kBK + c * 8]);
-        }
-        const int i16 = lane & 15;
-        const int col = first + 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
-        const int k = kk * 16 + 8 * (lane >> 5) + (i16 >> 2);
-        const int cl = col & 127;
-        const unsigned short* q = &st[(col >> 7) * (kBK * 128) + k * 128 + (((cl >> 3) ^ ((k & 3) * 4)) * 8) + (cl & 7)];
-        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q));
-        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q + 4 * 128));
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    // half h into LDS byte address lds (this wave's part)
+    __device__ __forceinline__ void load(int h, uint32_t lds) const {
+        const i32x4 r = rsrc_words(reinterpret_cast<const void*>(at), left > 0 ? rest : 0);
+        // a last step that k does not fill: chunks along k past its end would
+        // read the next row
+        const uint32_t u = ALONG_K && (int)first >= left ? kNowhere : v;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) dma16(r, u + off[h][j], lds + (h * 2 + j) * 8192);
     }
 };
 
-template <bool AK, bool BK_, int FM, int FN>
-__device__ __forceinline__ void big_tile(const Panel<AK>& A, const Panel<BK_>& B, unsigned short* sbuf,
-                                         unsigned short* C, int64_t ldc) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
-    constexpr int NA = Panel<AK>::count(FM), NB = Panel<BK_>::count(2 * FN);
-    uint32_t oa[NA], ob[NB];
+// LDS addresses of a wave's operand fragments.
+template <bool ALONG_K>
+struct Frag {
+    // along k: one address for each k sub-step; along i: rows 0 - 63 and
+    // 64 - 127 of a sub-panel (they differ in one bit of the swizzled chunk)
+    uint32_t at[ALONG_K ? 4 : 2];
+    // panel: LDS byte address; first: the wave's first row or column (along i:
+    // below 64 where 64-wide blocks are read, else below 128)
+    __device__ __forceinline__ Frag(uint32_t panel, int first, int lane) {
+        if constexpr (ALONG_K) {
+            const int r = first + (lane & 31);
 #pragma unroll
-    for (int j = 0; j < NA; ++j) oa[j] = A.offset(j, wave, lane);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) ob[j] = B.offset(j, wave, lane);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS void*)sbuf;
-    const int nk = (A.kd + kBK - 1) / kBK;
-
-    auto issue = [&](int kt) __attribute__((always_inline)) {
-        const int k0 = kt * kBK;
-        const i32x4 ra = A.rsrc(k0), rb = B.rsrc(k0);
-        const uint32_t la = lds0 + (kt & 1) * (2 * kStage * 2) + wave * 1024, lb = la + kStage * 2;
-        // a last step that k does not fill: chunks past its end would read the
-        // next row, so they go past the buffer's end too
-        const int left = A.kd - k0;
-#pragma unroll
-        for (int j = 0; j < NA; ++j)
-            dma16(ra, AK && left < kBK && Panel<AK>::chunk_k(j, wave, lane) >= left ? 0xffffff00u : oa[j], la + j * 8192);
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-            dma16(rb, BK_ && left < kBK && Panel<BK_>::chunk_k(j, wave, lane) >= left ? 0xffffff00u : ob[j], lb + j * 8192);
-    };
-
-    f32x16 acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
-
-    if (nk > 0) issue(0);
-    for (int kt = 0; kt < nk; ++kt) {
-        stage_ready();
-        if (kt + 1 < nk) issue(kt + 1);
-        const unsigned short* sa = sbuf + (kt & 1) * 2 * kStage;
-        const unsigned short* sb = sa + kStage;
-#pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk) {
-            bf16x8 av[FM], bv[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) av[i] = Panel<AK>::read(sa, (i * 2 + wm) * 32, kk, lane);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) bv[j] = Panel<BK_>::read(sb, (j * 4 + wn) * 32, kk, lane);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
+            for (int kk = 0; kk < 4; ++kk)
+                at[kk] = panel + r * 128 + (((kk * 2 + (lane >> 5)) ^ ((r >> 1) & 7)) * 16);
+        } else {
+            const int i16 = lane & 15, k = 8 * (lane >> 5) + (i16 >> 2);
+            const int col = first + 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
+            at[0] = panel + k * 256 + (((col >> 3) ^ ((k & 3) * 4)) * 16) + (col & 7) * 2;
+            at[1] = at[0] ^ 128;
         }
     }
+    // from the step of parity p to the other one of the two in LDS
+    __device__ __forceinline__ void flip(int p) {
+#pragma unroll
+        for (uint32_t& x : at) x += p ? -(kPanel * 2) : kPanel * 2;
+    }
+    // MFMA operand of the 32-wide block `off` past `first`, k sub-step kk
+    __device__ __forceinline__ bf16x8 read(int off, int kk) const {
+        if constexpr (ALONG_K) {
+            return *(const LDS_AS bf16x8*)(uintptr_t)(at[kk] + off * 128);
+        } else {
+            const uint32_t b = at[(off >> 6) & 1] + (off >> 7) * (kBK * 256) + kk * 16 * 256;
+            const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(uintptr_t)b);
+            const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(uintptr_t)(b + 4 * 256));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+};
 
-    // result through LDS, then whole 16-byte chunks of rows
-    __syncthreads();
+// The result tile, C[r][c] with r = (2 i + wm) 32 + l32 and
+// c = (4 j + wn) 32 + 8 m + 4 gl + e in acc[i][j][4 m + e] of lane 32 gl + l32.
+// Lanes l and l + 32 exchange halves, so that each stores 16 bytes of a row.
+// All 16 stores are issued whatever the tile's size (those outside are dropped
+// by the buffer's bounds): phase_gate counts them.
+__device__ __forceinline__ void put_result(const f32x16 (&acc)[4][2], unsigned short* C, int64_t ldc, int rows,
+                                           int cols, int wm, int wn, int lane) {
     const int l32 = lane & 31, gl = lane >> 5;
+    const uint32_t row = (uint32_t)(wm * 32 + l32) * (uint32_t)ldc * 2u;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < 4; ++i) {
+        const int64_t at = (int64_t)i * 64 * ldc;
+        const int64_t bytes = i * 64 < rows ? 2 * ((int64_t)(rows - 1) * ldc + cols - at) : 0;
+        const __amdgpu_buffer_rsrc_t rb =
+            __builtin_amdgcn_make_buffer_rsrc(C + at, (short)0, (int)min(bytes, (int64_t)0x7fffff00), 0x00020000);
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const u32x2 v = {pack2(acc[i][j][4 * m], acc[i][j][4 * m + 1]),
-                                 pack2(acc[i][j][4 * m + 2], acc[i][j][4 * m + 3])};
-                *reinterpret_cast<u32x2*>(&sbuf[((i * 2 + wm) * 32 + l32) * kLdc + (j * 4 + wn) * 32 + m * 8 + gl * 4]) = v;
+            for (int t = 0; t < 2; ++t) {
+                const auto& v = acc[i][j];
+                const auto s0 = __builtin_amdgcn_permlane32_swap(pack2(v[8 * t], v[8 * t + 1]), pack2(v[8 * t + 4], v[8 * t + 5]), false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(pack2(v[8 * t + 2], v[8 * t + 3]), pack2(v[8 * t + 6], v[8 * t + 7]), false, false);
+                const u32x4 q = {(unsigned)s0[0], (unsigned)s1[0], (unsigned)s0[1], (unsigned)s1[1]};
+                const int c = (j * 4 + wn) * 32 + t * 16 + gl * 8;
+                __builtin_amdgcn_raw_buffer_store_b128(q, rb, c < cols ? row + c * 2 : kNowhere, 0, 0);
             }
-    __syncthreads();
-    constexpr int CH = FN * 16;   // chunks of a row
+    }
+}
+
+// MODE 0: Y = X W, 1: Y = X W^T, 2: G = X^T D.
+template <int MODE>
+struct Job {
+    static constexpr bool AK = MODE != 2, BKK = MODE == 1;
+    Panel A, B;
+    unsigned short* C;
+    int64_t ldc;
+};
+
+struct GroupTable {
+    int first[kExperts + 2];   // row tiles before each slot (weight gradient: unused)
+    int lo[kExperts + 1];      // first row of each slot
+    int rows[kExperts + 1];
+};
+
+// Tile `id` of the launch (none past the last: an empty job).
+template <int MODE>
+__device__ __forceinline__ void find_job(const GroupedArgs& a, const GroupTable& t, int64_t id, int64_t total,
+                                         Job<MODE>& job) {
+    job.A.p = nullptr;
+    job.B.p = nullptr;
+    job.A.ld = job.B.ld = job.ldc = 0;
+    job.A.side = job.B.side = job.A.kd = job.B.kd = 0;
+    job.C = nullptr;
+    if (id >= total) return;
+    const unsigned short* x = reinterpret_cast<const unsigned short*>(a.x);
+    if constexpr (MODE == 2) {
+        const int ntk = (a.kdim + kBig - 1) / kBig, ntn = (a.ndim + kBig - 1) / kBig;
+        const int e = (int)id / (ntk * ntn), b = (int)id % (ntk * ntn);
+        const int i0 = (b % ntk) * kBig, j0 = (b / ntk) * kBig;
+        const int64_t lo = __builtin_amdgcn_readfirstlane(t.lo[e]);
+        const int kd = __builtin_amdgcn_readfirstlane(t.rows[e]);
+        job.A = {x + lo * a.x_ld + i0, a.x_ld, min(kBig, a.kdim - i0), kd};
+        job.B = {reinterpret_cast<const unsigned short*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(kBig, a.ndim - j0), kd};
+        job.ldc = a.w_ld[e];
+        job.C = reinterpret_cast<unsigned short*>(a.w[e]) + i0 * job.ldc + j0;
+    } else {
+        const int ntn = (a.ndim + kBig - 1) / kBig;
+        // the last slot whose first tile is at or before id
+        int e = 0;
 #pragma unroll
-    for (int it = 0; it < FM * 64 * CH / 512; ++it) {
-        const int id = it * 512 + tid, r = id / CH, c = (id % CH) * 8;
-        if (r < A.side && c < B.side)
-            *reinterpret_cast<u32x4*>(C + r * ldc + c) = *reinterpret_cast<const u32x4*>(&sbuf[r * kLdc + c]);
+        for (int s = 128; s > 0; s >>= 1)
+            if (e + s <= kExperts && (int64_t)__builtin_amdgcn_readfirstlane(t.first[e + s]) * ntn <= id) e += s;
+        const int first = __builtin_amdgcn_readfirstlane(t.first[e]);
+        const int c = __builtin_amdgcn_readfirstlane(t.first[e + 1]) - first;
+        const int off = (int)(id - (int64_t)first * ntn);
+        const int m = (off % c) * kBig, n0 = (off / c) * kBig;
+        const int64_t m0 = __builtin_amdgcn_readfirstlane(t.lo[e]) + m;
+        const int rows = min(kBig, __builtin_amdgcn_readfirstlane(t.rows[e]) - m);
+        job.A = {x + m0 * a.x_ld, a.x_ld, rows, a.kdim};
+        job.B.side = min(kBig, a.ndim - n0);
+        job.ldc = a.y_ld;
+        job.C = reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0;
+        if (e < a.n) {
+            job.B.ld = a.w_ld[e];
+            job.B.kd = a.kdim;
+            job.B.p = reinterpret_cast<const unsigned short*>(a.w[e]) + (MODE == 1 ? n0 * job.B.ld : n0);
+        } else {
+            job.A.kd = 0;   // rows of no expert: zeros
+        }
     }
 }
 
-template <bool AK, bool BK_>
-__device__ __forceinline__ void big_dispatch(const Panel<AK>& A, const Panel<BK_>& B, unsigned short* sbuf,
-                                             unsigned short* C, int64_t ldc) {
-    const int fm = (A.side + 63) / 64;
-    if (B.side > 128) {
-        if (fm == 4) big_tile<AK, BK_, 4, 2>(A, B, sbuf, C, ldc);
-        else if (fm == 3) big_tile<AK, BK_, 3, 2>(A, B, sbuf, C, ldc);
-        else if (fm == 2) big_tile<AK, BK_, 2, 2>(A, B, sbuf, C, ldc);
-        else big_tile<AK, BK_, 1, 2>(A, B, sbuf, C, ldc);
-    } else {
-        if (fm == 4) big_tile<AK, BK_, 4, 1>(A, B, sbuf, C, ldc);
-        else if (fm == 3) big_tile<AK, BK_, 3, 1>(A, B, sbuf, C, ldc);
-        else if (fm == 2) big_tile<AK, BK_, 2, 1>(A, B, sbuf, C, ldc);
-        else big_tile<AK, BK_, 1, 1>(A, B, sbuf, C, ldc);
+// Fills the table from the end rows; returns the launch's row tiles.  A count
+// that the grid was not made for (end rows that decrease) is cut off.
+__device__ __forceinline__ int fill_table(const GroupedArgs& a, GroupTable& t, int most) {
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x, slots = a.n + (a.last ? 1 : 0);
+        int cnt[4], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = lane * 4 + k;
+            int lo = 0, hi = 0;
+            if (i < slots) slot_rows(a, i, lo, hi);
+            cnt[k] = hi > lo ? min((hi - lo - 1) / kBig + 1, most) : 0;
+            sum = min(sum + cnt[k], most);
+            t.lo[i] = lo;
+            t.rows[i] = max(hi - lo, 0);
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o, 64);
+            if (lane >= o) incl = min(incl + v, most);
+        }
+        int at = __shfl_up(incl, 1, 64);
+        if (lane == 0) at = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            t.first[lane * 4 + k] = at;
+            at = min(at + cnt[k], most);
+        }
+        if (lane == 63) t.first[256] = at;
     }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(t.first[256]);
 }
 
-template <bool WT>
-__global__ __launch_bounds__(512) void grouped_mm_big(const GroupedArgs a) {
-    __shared__ __attribute__((aligned(16))) unsigned short sbuf[kBig * kLdc];
-    GroupTile t;
-    if (!find_tile(a, kBig, (a.ndim + kBig - 1) / kBig, t)) return;
-    const int64_t m0 = t.row0 + t.mt * kBig;
-    const int n0 = t.nt * kBig;
-    Panel<true> A{reinterpret_cast<const unsigned short*>(a.x) + m0 * a.x_ld, a.x_ld,
-                  min(kBig, t.rows - t.mt * kBig), a.kdim};
-    Panel<WT> B{nullptr, 0, min(kBig, a.ndim - n0), a.kdim};
-    if (t.e < a.n) {
-        B.ld = a.w_ld[t.e];
-        B.p = reinterpret_cast<const unsigned short*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
-    } else {
-        A.kd = B.kd = 0;   // rows of no expert: zeros
-    }
-    big_dispatch<true, WT>(A, B, sbuf, reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
-}
+template <int MODE>
+__global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const int most) {
+    using J = Job<MODE>;
+    __shared__ __attribute__((aligned(1024))) unsigned short sbuf[4 * kPanel];
+    __shared__ GroupTable table;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
 
-__global__ __launch_bounds__(512) void grouped_wgrad_big(const GroupedArgs a) {
-    __shared__ __attribute__((aligned(16))) unsigned short sbuf[kBig * kLdc];
-    const int ntk = (a.kdim + kBig - 1) / kBig, ntn = (a.ndim + kBig - 1) / kBig;
-    const int total = a.n * ntk * ntn, per = (total + 7) / 8;
-    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
-    const int e = id / (ntk * ntn), b = id % (ntk * ntn);
-    const int i0 = (b % ntk) * kBig, j0 = (b / ntk) * kBig;
-    int lo, hi;
-    slot_rows(a, e, lo, hi);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    const int kd = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
-    const Panel<false> A{reinterpret_cast<const unsigned short*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(kBig, a.kdim - i0), kd};
-    const Panel<false> B{reinterpret_cast<const unsigned short*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(kBig, a.ndim - j0), kd};
-    big_dispatch<false, false>(A, B, sbuf, reinterpret_cast<unsigned short*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
+    // ---- this workgroup's tiles: those of an XCD follow each other (workgroup
+    //      ids go round the eight XCDs), dealt out to its workgroups in turn
+    const int row_tiles = fill_table(a, table, most);
+    int64_t total;
+    if (MODE == 2) total = (int64_t)a.n * ((a.kdim + kBig - 1) / kBig) * ((a.ndim + kBig - 1) / kBig);
+    else total = (int64_t)row_tiles * ((a.ndim + kBig - 1) / kBig);
+    const int64_t per = (total + 7) / 8, stride = gridDim.x >> 3;
+    const int64_t end = min(total, (int64_t)((blockIdx.x & 7) + 1) * per);
+    int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (id >= end) return;
+
+    const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS void*)sbuf;
+    const uint32_t ldsA = lds + wave * 1024, ldsB = ldsA + 4 * kPanel;
+    Frag<J::AK> fa(lds, wm * 32, lane);
+    Frag<J::BKK> fb(lds + 4 * kPanel, wn * 32, lane);
+
+    // ---- loads, ahead of the products: tile `in` ----
+    J in;
+    find_job<MODE>(a, table, id, end, in);
+    J out = in;
+    int64_t cur = id;
+    Feed<J::AK> feed_a;
+    Feed<J::BKK> feed_b;
+    feed_a.start(in.A, wave, lane);
+    feed_b.start(in.B, wave, lane);
+    auto advance = [&]() __attribute__((always_inline)) {
+        feed_a.next();
+        feed_b.next();
+        if (feed_a.left > 0) return;
+        id += stride;
+        find_job<MODE>(a, table, id, end, in);
+        feed_a.start(in.A, wave, lane);
+        feed_b.start(in.B, wave, lane);
+    };
+
+    f32x16 acc[4][2];
+    auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    };
+    bf16x8 av[2][4], bv[2][4];
+    auto read_a = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) av[i][kk] = fa.read((h * 2 + i) * 64, kk);
+    };
+    auto read_b = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) bv[j][kk] = fb.read(j * 128, kk);
+    };
+    auto multiply = [&](int h, int j) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][kk], av[i][kk], acc[2 * h + i][j], 0, 0, 0);
+    };
+
+    // the first step, and the second but for A1
+    feed_a.load(0, ldsA);
+    feed_b.load(0, ldsB);
+    feed_b.load(1, ldsB);
+    feed_a.load(1, ldsA);
+    advance();
+    feed_a.load(0, ldsA + 2 * kPanel);
+    feed_b.load(0, ldsB + 2 * kPanel);
+    feed_b.load(1, ldsB + 2 * kPanel);
+    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+    if (wm == 1) end_multiply();   // one slot behind
+
+    int k = 0;        // step of the tile that is multiplied
+    int stored = 0;   // a result was stored in this step
+    int p = 0;        // parity of the step
+    clear();
+    for (;;) {
+        const bool low = out.A.side > 128, right = out.B.side > 128;
+        read_a(0);
+        read_b(0);
+        read_b(1);
+        feed_a.load(1, ldsA + (p ^ 1) * (2 * kPanel));
+        end_read(stored);
+        __builtin_amdgcn_s_setprio(1);
+        multiply(0, 0);
+        if (right) multiply(0, 1);
+        __builtin_amdgcn_s_setprio(0);
+        end_multiply();
+        read_a(1);
+        advance();
+        feed_a.load(0, ldsA + p * (2 * kPanel));
+        feed_b.load(0, ldsB + p * (2 * kPanel));
+        feed_b.load(1, ldsB + p * (2 * kPanel));
+        fa.flip(p);
+        fb.flip(p);
+        end_read(stored);
+        __builtin_amdgcn_s_setprio(1);
+        if (low) multiply(1, 0);
+        if (low && right) multiply(1, 1);
+        __builtin_amdgcn_s_setprio(0);
+        end_multiply();
+        p ^= 1;
+        stored = 0;
+        if (++k * kBK < out.A.kd) continue;
+        put_result(acc, out.C, out.ldc, out.A.side, out.B.side, wm, wn, lane);
+        cur += stride;
+        if (cur >= end) break;
+        find_job<MODE>(a, table, cur, end, out);
+        clear();
+        k = 0;
+        stored = 1;
+    }
+    if (wm == 0) end_multiply();   // as many barriers as the others
+    // the loads past the last tile still write (zeros) into this workgroup's LDS
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -428,11 +625,23 @@ int64_t grouped_wgrad_grid(const GroupedArgs& a) {
     return cdiv(cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n, 8) * 8;
 }
 
+// Workgroups of the 256 x 256 kernel for at most `tiles` tiles.  One fits a CU.
+// With many tiles each takes its share in turn, so that one tile's loads run
+// while another is multiplied; with few, every tile is a workgroup of its own
+// and goes to the CU that is free first.
+static uint32_t big_grid(int64_t tiles) {
+    static const int cus = [] { const int c = device_cus(); return c > 0 ? c : 256; }();
+    return (uint32_t)(tiles >= 6 * cus ? cus / 8 * 8 : tiles);
+}
+
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
-    const dim3 grid((uint32_t)grouped_mm_grid(a));
+    const int64_t tiles = grouped_mm_grid(a);
+    const dim3 grid((uint32_t)tiles);
     if (a.dtype == 0 && a.vec) {
-        if (trans_w) hipLaunchKernelGGL((grouped_mm_big<true>), grid, dim3(512), 0, s, a);
-        else hipLaunchKernelGGL((grouped_mm_big<false>), grid, dim3(512), 0, s, a);
+        const dim3 big(big_grid(tiles));
+        const int most = a.rows / kBig + a.n + 1;
+        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), big, dim3(512), 0, s, a, most);
+        else hipLaunchKernelGGL((grouped_big<0>), big, dim3(512), 0, s, a, most);
     } else if (a.dtype == 0) {
         if (trans_w) hipLaunchKernelGGL((grouped_mm_kernel<0, true>), grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL((grouped_mm_kernel<0, false>), grid, dim3(256), 0, s, a);
@@ -444,8 +653,9 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)grouped_wgrad_grid(a));
-    if (a.dtype == 0 && a.vec) hipLaunchKernelGGL(grouped_wgrad_big, grid, dim3(512), 0, s, a);
+    const int64_t tiles = grouped_wgrad_grid(a);
+    const dim3 grid((uint32_t)tiles);
+    if (a.dtype == 0 && a.vec) hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, a.rows / kBig + a.n + 1);
     else if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_kernel<0>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((grouped_wgrad_kernel<1>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
