@@ -238,30 +238,22 @@ __device__ __forceinline__ void dma16(i32x4 r, uint32_t off, uint32_t lds) {
                  :: "s"(lds), "v"(off), "s"(r) : "memory");
 }
 // Ends a reading slot: all but this wave's newest loads have landed and its LDS
-// reads are done; then the same of all waves.  A half is loaded one step before
-// this wait for it: four halves (8 loads of the wave) are newer.  In the step
-// after a tile's result, its 16 stores (always issued, see put_result) are too.
-constexpr int kStores = 16;
-__device__ __forceinline__ void end_read(int stores) {
+// reads are done; then the same of all waves.  The half that the next reading
+// slot needs was loaded one step before; four halves (8 loads of the wave) are
+// newer, and near a tile's end so are the stores of its result (8 for each half
+// of the rows, always issued; see put_result): MORE of them when `more` is set.
+template <int MORE>
+__device__ __forceinline__ void end_read(int more) {
     asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lgate%=\n\ts_waitcnt vmcnt(8)\n"
-                 ".Lgate%=:\n\ts_waitcnt vmcnt(24) lgkmcnt(0)\n\ts_barrier" :: "s"(stores) : "memory", "scc");
+                 ".Lgate%=:\n\ts_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" :: "s"(__builtin_amdgcn_readfirstlane(more)), "n"(8 + MORE) : "memory", "scc");
     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0) again, for the compiler's own count
     __builtin_amdgcn_sched_barrier(0);
 }
-static_assert(8 + kStores == 24, "end_read");
 __device__ __forceinline__ void end_multiply() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
-
-// One operand of a tile, 256 rows (or columns) by k.
-struct Panel {
-    const unsigned short* p;   // element (0, 0) of the tile at k = 0
-    int64_t ld;
-    int side;                  // rows (or columns) of the tile inside the operand
-    int kd;                    // length of k (0: no operand, all zeros)
-};
 
 // The loads of one operand, step by step.  An instruction of the workgroup
 // fills 64 rows of 128 bytes (along k) or 32 rows of 256 bytes (along i); a half
@@ -275,18 +267,20 @@ struct Feed {
     uint32_t v, first;  // this lane's byte offset in an instruction; first k element of its chunk
     uint32_t off[2][2]; // byte offset of instruction j of half h
 
-    __device__ __forceinline__ void start(const Panel& q, int wave, int lane) {
-        const uint32_t ld2 = 2u * (uint32_t)q.ld;
-        at = reinterpret_cast<uint64_t>(q.p);
-        left = q.kd;
+    // p: element (0, 0) of the tile at k = 0; side: its rows (or columns) inside
+    // the operand; kd: length of k (0: all zeros)
+    __device__ __forceinline__ void start(uint64_t p, int64_t ld, int side, int kd, int wave, int lane) {
+        const uint32_t ld2 = 2u * (uint32_t)ld;
+        at = p;
+        left = kd;
         if constexpr (ALONG_K) {
             const uint32_t c = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
-            rest = 2 * ((int64_t)(q.side - 1) * q.ld + q.kd);
+            rest = 2 * ((side - 1) * ld + kd);
             move = 2 * kBK;
             v = (uint32_t)(8 * wave + (lane >> 3)) * ld2 + c * 16u;
             first = c * 8;
         } else {
-            rest = 2 * ((int64_t)(q.kd - 1) * q.ld + q.side);
+            rest = 2 * ((kd - 1) * ld + side);
             move = (int64_t)kBK * ld2;
             v = (uint32_t)(4 * wave + (lane >> 4)) * ld2 + (((lane & 15) ^ ((lane >> 4) * 4)) * 16u);
             first = 0;
@@ -297,7 +291,7 @@ struct Feed {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 off[h][j] = ALONG_K ? (h * 128 + j * 64) * ld2
-                                    : h * 128 < q.side ? h * 256 + j * 32 * ld2 : kNowhere;
+                                    : h * 128 < side ? h * 256 + j * 32 * ld2 : kNowhere;
     }
     __device__ __forceinline__ void next() {
         at += move;
@@ -354,96 +348,108 @@ struct Frag {
     }
 };
 
-// The result tile, C[r][c] with r = (2 i + wm) 32 + l32 and
-// c = (4 j + wn) 32 + 8 m + 4 gl + e in acc[i][j][4 m + e] of lane 32 gl + l32.
-// Lanes l and l + 32 exchange halves, so that each stores 16 bytes of a row.
-// All 16 stores are issued whatever the tile's size (those outside are dropped
-// by the buffer's bounds): phase_gate counts them.
-__device__ __forceinline__ void put_result(const f32x16 (&acc)[4][2], unsigned short* C, int64_t ldc, int rows,
-                                           int cols, int wm, int wn, int lane) {
+// Half h of the result tile (rows 128 h ..): C[r][c] with r = (2 i + wm) 32 + l32
+// and c = (4 j + wn) 32 + 8 m + 4 gl + e is acc[i][j][4 m + e] of lane
+// 32 gl + l32.  Each 32 x 32 block goes through the wave's own LDS scratch, so
+// that four neighbouring lanes store 64 bytes of a row: stored from registers
+// in 16-byte pieces, the weight gradient's 0.8 GB of results cost 130 us more
+// than no stores at all (64 experts of 512 x 4096 x 1536).
+// All 8 stores are issued whatever the tile's size (those outside are dropped
+// by the buffer's bounds): end_read counts them.
+constexpr int kScratchLd = 40;                   // elements (80 bytes) a row
+constexpr int kScratch = 32 * kScratchLd;        // elements of a wave
+__device__ __forceinline__ void put_result(const f32x16 (&acc)[4][2], int h, unsigned short* scratch, uint64_t C,
+                                           int ldc, int rows, int cols, int wm, int wn, int lane) {
     const int l32 = lane & 31, gl = lane >> 5;
-    const uint32_t row = (uint32_t)(wm * 32 + l32) * (uint32_t)ldc * 2u;
+    const int r0 = wm * 32 + (lane >> 2), c0 = wn * 32 + (lane & 3) * 8;
+    const uint32_t v0 = (uint32_t)r0 * (uint32_t)ldc * 2u + c0 * 2u, half = (uint32_t)ldc * 32u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 2 * h; i < 2 * h + 2; ++i) {
         const int64_t at = (int64_t)i * 64 * ldc;
         const int64_t bytes = i * 64 < rows ? 2 * ((int64_t)(rows - 1) * ldc + cols - at) : 0;
-        const __amdgpu_buffer_rsrc_t rb =
-            __builtin_amdgcn_make_buffer_rsrc(C + at, (short)0, (int)min(bytes, (int64_t)0x7fffff00), 0x00020000);
+        const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+            reinterpret_cast<void*>(C + 2 * at), (short)0, (int)min(bytes, (int64_t)0x7fffff00), 0x00020000);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
+            const auto& v = acc[i][j];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const auto& v = acc[i][j];
-                const auto s0 = __builtin_amdgcn_permlane32_swap(pack2(v[8 * t], v[8 * t + 1]), pack2(v[8 * t + 4], v[8 * t + 5]), false, false);
-                const auto s1 = __builtin_amdgcn_permlane32_swap(pack2(v[8 * t + 2], v[8 * t + 3]), pack2(v[8 * t + 6], v[8 * t + 7]), false, false);
-                const u32x4 q = {(unsigned)s0[0], (unsigned)s1[0], (unsigned)s0[1], (unsigned)s1[1]};
-                const int c = (j * 4 + wn) * 32 + t * 16 + gl * 8;
-                __builtin_amdgcn_raw_buffer_store_b128(q, rb, c < cols ? row + c * 2 : kNowhere, 0, 0);
+            for (int m = 0; m < 4; ++m) {
+                const u32x2 w = {pack2(v[4 * m], v[4 * m + 1]), pack2(v[4 * m + 2], v[4 * m + 3])};
+                *reinterpret_cast<u32x2*>(&scratch[l32 * kScratchLd + m * 8 + gl * 4]) = w;
             }
+            const uint32_t at_j = j * 128 + c0 < cols ? v0 + j * 256u : kNowhere;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    *reinterpret_cast<const u32x4*>(&scratch[(s * 16 + (lane >> 2)) * kScratchLd + (lane & 3) * 8]), rb,
+                    at_j + s * half, 0, 0);
+        }
     }
 }
 
-// MODE 0: Y = X W, 1: Y = X W^T, 2: G = X^T D.
-template <int MODE>
+// One output tile.
 struct Job {
-    static constexpr bool AK = MODE != 2, BKK = MODE == 1;
-    Panel A, B;
-    unsigned short* C;
-    int64_t ldc;
+    uint64_t a, b, c;    // element (0, 0) of its operands (at k = 0) and result
+    int w_ld;            // row stride of the expert's matrix
+    int rows, cols;      // size of the tile
+    int kd;              // length of k (0: the result is zero)
 };
+constexpr int kJobs = 128;   // tiles of a workgroup
 
 struct GroupTable {
-    int first[kExperts + 2];   // row tiles before each slot (weight gradient: unused)
+    int first[kExperts + 2];   // row tiles before each slot (product)
     int lo[kExperts + 1];      // first row of each slot
     int rows[kExperts + 1];
 };
 
-// Tile `id` of the launch (none past the last: an empty job).
+// MODE 0: Y = X W, 1: Y = X W^T, 2: G = X^T D.
 template <int MODE>
-__device__ __forceinline__ void find_job(const GroupedArgs& a, const GroupTable& t, int64_t id, int64_t total,
-                                         Job<MODE>& job) {
-    job.A.p = nullptr;
-    job.B.p = nullptr;
-    job.A.ld = job.B.ld = job.ldc = 0;
-    job.A.side = job.B.side = job.A.kd = job.B.kd = 0;
-    job.C = nullptr;
-    if (id >= total) return;
+__device__ __forceinline__ Job make_job(const GroupedArgs& a, const GroupTable& t, int64_t id) {
+    Job job;
     const unsigned short* x = reinterpret_cast<const unsigned short*>(a.x);
+    const int ntn = (a.ndim + kBig - 1) / kBig;
     if constexpr (MODE == 2) {
-        const int ntk = (a.kdim + kBig - 1) / kBig, ntn = (a.ndim + kBig - 1) / kBig;
+        const int ntk = (a.kdim + kBig - 1) / kBig;
         const int e = (int)id / (ntk * ntn), b = (int)id % (ntk * ntn);
         const int i0 = (b % ntk) * kBig, j0 = (b / ntk) * kBig;
-        const int64_t lo = __builtin_amdgcn_readfirstlane(t.lo[e]);
-        const int kd = __builtin_amdgcn_readfirstlane(t.rows[e]);
-        job.A = {x + lo * a.x_ld + i0, a.x_ld, min(kBig, a.kdim - i0), kd};
-        job.B = {reinterpret_cast<const unsigned short*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(kBig, a.ndim - j0), kd};
-        job.ldc = a.w_ld[e];
-        job.C = reinterpret_cast<unsigned short*>(a.w[e]) + i0 * job.ldc + j0;
+        job.a = reinterpret_cast<uint64_t>(x + t.lo[e] * a.x_ld + i0);
+        job.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.d) + t.lo[e] * a.d_ld + j0);
+        job.w_ld = (int)a.w_ld[e];
+        job.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.w[e]) + i0 * a.w_ld[e] + j0);
+        job.rows = min(kBig, a.kdim - i0);
+        job.cols = min(kBig, a.ndim - j0);
+        job.kd = t.rows[e];
     } else {
-        const int ntn = (a.ndim + kBig - 1) / kBig;
         // the last slot whose first tile is at or before id
         int e = 0;
 #pragma unroll
         for (int s = 128; s > 0; s >>= 1)
-            if (e + s <= kExperts && (int64_t)__builtin_amdgcn_readfirstlane(t.first[e + s]) * ntn <= id) e += s;
-        const int first = __builtin_amdgcn_readfirstlane(t.first[e]);
-        const int c = __builtin_amdgcn_readfirstlane(t.first[e + 1]) - first;
-        const int off = (int)(id - (int64_t)first * ntn);
+            if (e + s <= kExperts && (int64_t)t.first[e + s] * ntn <= id) e += s;
+        const int c = t.first[e + 1] - t.first[e];
+        const int off = (int)(id - (int64_t)t.first[e] * ntn);
         const int m = (off % c) * kBig, n0 = (off / c) * kBig;
-        const int64_t m0 = __builtin_amdgcn_readfirstlane(t.lo[e]) + m;
-        const int rows = min(kBig, __builtin_amdgcn_readfirstlane(t.rows[e]) - m);
-        job.A = {x + m0 * a.x_ld, a.x_ld, rows, a.kdim};
-        job.B.side = min(kBig, a.ndim - n0);
-        job.ldc = a.y_ld;
-        job.C = reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0;
-        if (e < a.n) {
-            job.B.ld = a.w_ld[e];
-            job.B.kd = a.kdim;
-            job.B.p = reinterpret_cast<const unsigned short*>(a.w[e]) + (MODE == 1 ? n0 * job.B.ld : n0);
-        } else {
-            job.A.kd = 0;   // rows of no expert: zeros
+        const int64_t m0 = t.lo[e] + m;
+        job.a = reinterpret_cast<uint64_t>(x + m0 * a.x_ld);
+        job.b = 0;
+        job.w_ld = 0;
+        job.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0);
+        job.rows = min(kBig, t.rows[e] - m);
+        job.cols = min(kBig, a.ndim - n0);
+        job.kd = 0;
+        if (e < a.n) {   // else rows of no expert
+            job.w_ld = (int)a.w_ld[e];
+            job.kd = a.kdim;
+            job.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.w[e]) +
+                                               (MODE == 1 ? n0 * a.w_ld[e] : n0));
         }
     }
+    return job;
+}
+
+// The job as scalars (every lane reads the same).
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return (uint32_t)uniform((int)(uint32_t)x) | (uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32;
 }
 
 // Fills the table from the end rows; returns the launch's row tiles.  A count
@@ -483,10 +489,12 @@ __device__ __forceinline__ int fill_table(const GroupedArgs& a, GroupTable& t, i
 
 template <int MODE>
 __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const int most) {
-    using J = Job<MODE>;
+    constexpr bool AK = MODE != 2, BKK = MODE == 1;   // operands stored along k
     __shared__ __attribute__((aligned(1024))) unsigned short sbuf[4 * kPanel];
+    __shared__ __attribute__((aligned(16))) unsigned short scratch[8 * kScratch];
+    __shared__ __attribute__((aligned(16))) Job jobs[kJobs];
     __shared__ GroupTable table;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
 
     // ---- this workgroup's tiles: those of an XCD follow each other (workgroup
@@ -497,40 +505,48 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
     else total = (int64_t)row_tiles * ((a.ndim + kBig - 1) / kBig);
     const int64_t per = (total + 7) / 8, stride = gridDim.x >> 3;
     const int64_t end = min(total, (int64_t)((blockIdx.x & 7) + 1) * per);
-    int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (id >= end) return;
+    const int count = (int)min((end - id + stride - 1) / stride, (int64_t)kJobs);
+    for (int m = threadIdx.x; m < count; m += 512) jobs[m] = make_job<MODE>(a, table, id + m * stride);
+    __syncthreads();
 
     const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS void*)sbuf;
     const uint32_t ldsA = lds + wave * 1024, ldsB = ldsA + 4 * kPanel;
-    Frag<J::AK> fa(lds, wm * 32, lane);
-    Frag<J::BKK> fb(lds + 4 * kPanel, wn * 32, lane);
+    Frag<AK> fa(lds, wm * 32, lane);
+    Frag<BKK> fb(lds + 4 * kPanel, wn * 32, lane);
 
     // ---- loads, ahead of the products: tile `in` ----
-    J in;
-    find_job<MODE>(a, table, id, end, in);
-    J out = in;
-    int64_t cur = id;
-    Feed<J::AK> feed_a;
-    Feed<J::BKK> feed_b;
-    feed_a.start(in.A, wave, lane);
-    feed_b.start(in.B, wave, lane);
+    Feed<AK> feed_a;
+    Feed<BKK> feed_b;
+    int in = 0;
+    auto start_feed = [&]() __attribute__((always_inline)) {
+        const Job j = jobs[min(in, count - 1)];
+        const int kd = in < count ? uniform(j.kd) : 0;   // past the last tile: zeros
+        const int64_t w_ld = uniform(j.w_ld);
+        feed_a.start(uniform(j.a), a.x_ld, uniform(j.rows), kd, wave, lane);
+        feed_b.start(uniform(j.b), MODE == 2 ? a.d_ld : w_ld, uniform(j.cols), kd, wave, lane);
+    };
     auto advance = [&]() __attribute__((always_inline)) {
         feed_a.next();
         feed_b.next();
         if (feed_a.left > 0) return;
-        id += stride;
-        find_job<MODE>(a, table, id, end, in);
-        feed_a.start(in.A, wave, lane);
-        feed_b.start(in.B, wave, lane);
+        ++in;
+        start_feed();
     };
 
-    f32x16 acc[4][2];
-    auto clear = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    // ---- products: tile `out` ----
+    int out = 0, rows, cols, kd, ldc;
+    uint64_t C;
+    auto start_tile = [&]() __attribute__((always_inline)) {
+        const Job j = jobs[out];
+        rows = uniform(j.rows);
+        cols = uniform(j.cols);
+        kd = uniform(j.kd);
+        ldc = MODE == 2 ? uniform(j.w_ld) : (int)a.y_ld;
+        C = uniform(j.c);
     };
+    f32x16 acc[4][2] = {};
     bf16x8 av[2][4], bv[2][4];
     auto read_a = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
@@ -542,15 +558,26 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) bv[j][kk] = fb.read(j * 128, kk);
     };
-    auto multiply = [&](int h, int j) __attribute__((always_inline)) {
+    // fresh: the tile's first step, from zero
+    auto multiply = [&](int h, int j, bool fresh) __attribute__((always_inline)) {
+        if (fresh) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+            for (int i = 0; i < 2; ++i)
+                acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][0], av[i][0], f32x16{}, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][0], av[i][0], acc[2 * h + i][j], 0, 0, 0);
+        }
+#pragma unroll
+        for (int kk = 1; kk < 4; ++kk)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][kk], av[i][kk], acc[2 * h + i][j], 0, 0, 0);
     };
 
     // the first step, and the second but for A1
+    start_feed();
     feed_a.load(0, ldsA);
     feed_b.load(0, ldsB);
     feed_b.load(1, ldsB);
@@ -559,48 +586,49 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
     feed_a.load(0, ldsA + 2 * kPanel);
     feed_b.load(0, ldsB + 2 * kPanel);
     feed_b.load(1, ldsB + 2 * kPanel);
+    start_tile();
     asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
     if (wm == 1) end_multiply();   // one slot behind
 
     int k = 0;        // step of the tile that is multiplied
-    int stored = 0;   // a result was stored in this step
+    int after = 0;    // the tile's first step, and there was one before it
     int p = 0;        // parity of the step
-    clear();
     for (;;) {
-        const bool low = out.A.side > 128, right = out.B.side > 128;
+        const bool low = rows > 128, right = cols > 128;
+        const int last = (k + 1) * kBK >= kd;
         read_a(0);
         read_b(0);
         read_b(1);
         feed_a.load(1, ldsA + (p ^ 1) * (2 * kPanel));
-        end_read(stored);
+        end_read<16>(after);
         __builtin_amdgcn_s_setprio(1);
-        multiply(0, 0);
-        if (right) multiply(0, 1);
+        multiply(0, 0, k == 0);
+        if (right) multiply(0, 1, k == 0);
         __builtin_amdgcn_s_setprio(0);
         end_multiply();
         read_a(1);
+        if (last) put_result(acc, 0, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
         advance();
         feed_a.load(0, ldsA + p * (2 * kPanel));
         feed_b.load(0, ldsB + p * (2 * kPanel));
         feed_b.load(1, ldsB + p * (2 * kPanel));
         fa.flip(p);
         fb.flip(p);
-        end_read(stored);
+        end_read<8>(after | last);
         __builtin_amdgcn_s_setprio(1);
-        if (low) multiply(1, 0);
-        if (low && right) multiply(1, 1);
+        if (low) multiply(1, 0, k == 0);
+        if (low && right) multiply(1, 1, k == 0);
         __builtin_amdgcn_s_setprio(0);
         end_multiply();
         p ^= 1;
-        stored = 0;
-        if (++k * kBK < out.A.kd) continue;
-        put_result(acc, out.C, out.ldc, out.A.side, out.B.side, wm, wn, lane);
-        cur += stride;
-        if (cur >= end) break;
-        find_job<MODE>(a, table, cur, end, out);
-        clear();
+        ++k;
+        after = 0;
+        if (!last) continue;
+        put_result(acc, 1, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
+        if (++out == count) break;
+        start_tile();
         k = 0;
-        stored = 1;
+        after = 1;
     }
     if (wm == 0) end_multiply();   // as many barriers as the others
     // the loads past the last tile still write (zeros) into this workgroup's LDS
@@ -631,7 +659,8 @@ int64_t grouped_wgrad_grid(const GroupedArgs& a) {
 // and goes to the CU that is free first.
 static uint32_t big_grid(int64_t tiles) {
     static const int cus = [] { const int c = device_cus(); return c > 0 ? c : 256; }();
-    return (uint32_t)(tiles >= 6 * cus ? cus / 8 * 8 : tiles);
+    if (tiles < 6 * cus) return (uint32_t)tiles;
+    return (uint32_t)std::max<int64_t>(cus / 8 * 8, cdiv(tiles, 8 * (int64_t)kJobs) * 8);
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
