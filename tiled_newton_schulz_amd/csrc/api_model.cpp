@@ -106,7 +106,7 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
     a.y_ld = Y->ld;
     a.ndim = (int32_t)N;
     a.n = std::min(kExperts, n);
-    if (grouped_mm_grid(a) > INT32_MAX) return HIMUON_ERR_LAYOUT;
+    if (grouped_mm_grid(a) > INT32_MAX / 2) return HIMUON_ERR_LAYOUT;
     a.vec = chunked(*X) && chunked(*Y) && K % 8 == 0 && N % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(W[e]);
     return each_launch(a, W, n, [&] {
@@ -137,7 +137,7 @@ himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D
     a.d_ld = D->ld;
     a.ndim = (int32_t)D->cols;
     a.n = std::min(kExperts, n);
-    if (grouped_wgrad_grid(a) > INT32_MAX) return HIMUON_ERR_LAYOUT;
+    if (grouped_wgrad_grid(a) > INT32_MAX / 2) return HIMUON_ERR_LAYOUT;
     a.vec = chunked(*X) && chunked(*D) && a.kdim % 8 == 0 && a.ndim % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(G[e]);
     return each_launch(a, G, n, [&] {

@@ -10,6 +10,7 @@
 // the grid is only bounded there (ragged last tiles included).
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_util.h"
 #include "grouped.h"
@@ -192,19 +193,22 @@ __global__ __launch_bounds__(256) void grouped_wgrad_kernel(const GroupedArgs a)
 // a wave interleave with the other waves' (rows (2 i + wm) 32, columns
 // (4 j + wn) 32), so every wave reads every half.  A step is four slots of a
 // wave, with a barrier after each:
-//     read    A0, B0, B1 into registers; A1 of the next step into LDS
+//     read     A0, B0, B1 into registers
 //     multiply A0 B0, A0 B1 (16 MFMAs)
-//     read    A1 into the registers of A0; A0, B0, B1 two steps on into LDS
+//     read     A1 into the registers of A0
 //     multiply A1 B0, A1 B1
 // Waves 4 - 7 run one slot behind waves 0 - 3, so that of the two waves on a
-// SIMD one always multiplies while the other reads, loads, stores a finished
-// tile or looks up the next one.  (With all waves in step, the reads between the
-// products as in a usual pipeline, the matrix units idled a third of the time
-// around the barriers.)
+// SIMD one always multiplies while the other reads, stores a finished tile or
+// starts the next one.  (With all waves in step, the reads between the products
+// as in a usual pipeline, the matrix units idled a third of the time around the
+// barriers.)  A half is free once both groups have read it; a wave loads its
+// part of the successor in the next reading slot, a step before it has to be
+// there.  (Loading between the products instead, one slot earlier, lost more in
+// the multiplying group than it gained.)
 // The loads run on into the next tile of the workgroup, and the result goes from
 // registers to memory, so neither the pipeline's start nor a tile's end drains it.
 //
-// Ragged tiles: halves of 128 rows or columns outside the tile are not
+// Ragged tiles: blocks of 64 rows or 128 columns outside the tile are not
 // multiplied; their loads end past the buffer and give zeros.
 //
 // An operand is stored in memory either along k (rows i of k) or along its
@@ -222,6 +226,20 @@ constexpr int kPanel = kBig * kBK;         // elements of one operand's step
 constexpr uint32_t kNowhere = 0x80000000u; // byte offset past every buffer
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// A value that every lane holds, as a scalar.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return (uint32_t)uniform((int)(uint32_t)x) | (uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32;
+}
+
+// The same for an operand of the assembly below: the compiler drops uniform()
+// of a value it knows to be uniform, and may still keep it in a vector register.
+__device__ __forceinline__ int scalar(int x) {
+    int r;
+    asm("v_readfirstlane_b32 %0, %1" : "=s"(r) : "v"(x));
+    return r;
+}
 
 // Buffer descriptor of [p, p + bytes): loads past it give zeros, stores are dropped.
 __device__ __forceinline__ i32x4 rsrc_words(const void* p, int64_t bytes) {
@@ -244,11 +262,14 @@ __device__ __forceinline__ void dma16(i32x4 r, uint32_t off, uint32_t lds) {
 // of the rows, always issued; see put_result): MORE of them when `more` is set.
 template <int MORE>
 __device__ __forceinline__ void end_read(int more) {
-    asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lgate%=\n\ts_waitcnt vmcnt(8)\n"
-                 ".Lgate%=:\n\ts_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" :: "s"(__builtin_amdgcn_readfirstlane(more)), "n"(8 + MORE) : "memory", "scc");
+    asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmore%=\n\ts_waitcnt vmcnt(8)\n"
+                 ".Lmore%=:\n\ts_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier"
+                 :: "s"(scalar(more)), "n"(8 + MORE) : "memory", "scc");
     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0) again, for the compiler's own count
     __builtin_amdgcn_sched_barrier(0);
 }
+// Ends a multiplying slot: nothing to wait for but the other waves (waits and
+// tests here, behind the products, cost a tenth of the kernel's time).
 __device__ __forceinline__ void end_multiply() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_barrier" ::: "memory");
@@ -358,7 +379,8 @@ struct Frag {
 // by the buffer's bounds): end_read counts them.
 constexpr int kScratchLd = 40;                   // elements (80 bytes) a row
 constexpr int kScratch = 32 * kScratchLd;        // elements of a wave
-__device__ __forceinline__ void put_result(const f32x16 (&acc)[4][2], int h, unsigned short* scratch, uint64_t C,
+template <int AM, int FN>
+__device__ __forceinline__ void put_result(const f32x16 (&acc)[AM][FN], int h, unsigned short* scratch, uint64_t C,
                                            int ldc, int rows, int cols, int wm, int wn, int lane) {
     const int l32 = lane & 31, gl = lane >> 5;
     const int r0 = wm * 32 + (lane >> 2), c0 = wn * 32 + (lane & 3) * 8;
@@ -371,7 +393,15 @@ __device__ __forceinline__ void put_result(const f32x16 (&acc)[4][2], int h, uns
             reinterpret_cast<void*>(C + 2 * at), (short)0, (int)min(bytes, (int64_t)0x7fffff00), 0x00020000);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const auto& v = acc[i][j];
+            if (i >= AM || j >= FN) {
+                // nothing there: two stores that are dropped (as assembly, so
+                // that neither is removed)
+                const i32x4 none = {0, 0, 0, 0x00020000};
+                asm volatile("buffer_store_dword %0, %0, %1, 0 offen\n\tbuffer_store_dword %0, %0, %1, 0 offen"
+                             :: "v"(kNowhere), "s"(none) : "memory");
+                continue;
+            }
+            const auto& v = acc[i < AM ? i : 0][j < FN ? j : 0];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const u32x2 w = {pack2(v[4 * m], v[4 * m + 1]), pack2(v[4 * m + 2], v[4 * m + 3])};
@@ -394,97 +424,132 @@ struct Job {
     int rows, cols;      // size of the tile
     int kd;              // length of k (0: the result is zero)
 };
-constexpr int kJobs = 128;   // tiles of a workgroup
+constexpr int kJobs = 128;   // tiles of a workgroup planned at a time
 
+// The launch's slots (experts, and the rows of none).
 struct GroupTable {
-    int first[kExperts + 2];   // row tiles before each slot (product)
-    int lo[kExperts + 1];      // first row of each slot
+    int lo[kExperts + 1];      // first row
     int rows[kExperts + 1];
+    int first[kExperts + 2];   // tiles before the slot
+    float cost[kExperts + 2];  // cost of all tiles before the slot
 };
 
-// MODE 0: Y = X W, 1: Y = X W^T, 2: G = X^T D.
+// Tiles of the launch: an expert has a grid of row tiles (product: of its rows;
+// weight gradient: of the K rows of G) by column tiles, counted column by column.
 template <int MODE>
-__device__ __forceinline__ Job make_job(const GroupedArgs& a, const GroupTable& t, int64_t id) {
-    Job job;
-    const unsigned short* x = reinterpret_cast<const unsigned short*>(a.x);
-    const int ntn = (a.ndim + kBig - 1) / kBig;
-    if constexpr (MODE == 2) {
-        const int ntk = (a.kdim + kBig - 1) / kBig;
-        const int e = (int)id / (ntk * ntn), b = (int)id % (ntk * ntn);
-        const int i0 = (b % ntk) * kBig, j0 = (b / ntk) * kBig;
-        job.a = reinterpret_cast<uint64_t>(x + t.lo[e] * a.x_ld + i0);
-        job.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.d) + t.lo[e] * a.d_ld + j0);
-        job.w_ld = (int)a.w_ld[e];
-        job.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.w[e]) + i0 * a.w_ld[e] + j0);
-        job.rows = min(kBig, a.kdim - i0);
-        job.cols = min(kBig, a.ndim - j0);
-        job.kd = t.rows[e];
-    } else {
+struct Grid {
+    const GroupedArgs& a;
+    int ntn;   // column tiles
+    __device__ __forceinline__ explicit Grid(const GroupedArgs& x) : a(x), ntn((x.ndim - 1) / kBig + 1) {}
+    __device__ __forceinline__ int row_tiles(int rows) const {
+        const int h = MODE == 2 ? a.kdim : rows;
+        return h > 0 ? (h - 1) / kBig + 1 : 0;
+    }
+    // Time of a slot's tiles, to share them out: a step of a tile takes about
+    // 1.0 us and 0.12 us for each block of 64 rows, a tile about 4 us (measured
+    // on the experts' products with ragged rows).
+    __device__ __forceinline__ float cost(int rows) const {
+        const int h = MODE == 2 ? a.kdim : rows, steps = ((MODE == 2 ? rows : a.kdim) + kBK - 1) / kBK;
+        return ntn * (row_tiles(rows) * (steps * 1.0f + 4.0f) + (float)((h + 63) / 64) * steps * 0.12f);
+    }
+    __device__ __forceinline__ Job job(const GroupTable& t, int id) const {
         // the last slot whose first tile is at or before id
         int e = 0;
 #pragma unroll
         for (int s = 128; s > 0; s >>= 1)
-            if (e + s <= kExperts && (int64_t)t.first[e + s] * ntn <= id) e += s;
-        const int c = t.first[e + 1] - t.first[e];
-        const int off = (int)(id - (int64_t)t.first[e] * ntn);
-        const int m = (off % c) * kBig, n0 = (off / c) * kBig;
-        const int64_t m0 = t.lo[e] + m;
-        job.a = reinterpret_cast<uint64_t>(x + m0 * a.x_ld);
-        job.b = 0;
-        job.w_ld = 0;
-        job.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0);
-        job.rows = min(kBig, t.rows[e] - m);
-        job.cols = min(kBig, a.ndim - n0);
-        job.kd = 0;
-        if (e < a.n) {   // else rows of no expert
-            job.w_ld = (int)a.w_ld[e];
-            job.kd = a.kdim;
-            job.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.w[e]) +
-                                               (MODE == 1 ? n0 * a.w_ld[e] : n0));
+            if (e + s <= kExperts && t.first[e + s] <= id) e += s;
+        const int R = row_tiles(t.rows[e]), off = id - t.first[e];
+        const int m = off % R * kBig, n0 = off / R * kBig;
+        Job j;
+        const unsigned short* x = reinterpret_cast<const unsigned short*>(a.x);
+        j.cols = min(kBig, a.ndim - n0);
+        if constexpr (MODE == 2) {
+            j.a = reinterpret_cast<uint64_t>(x + t.lo[e] * a.x_ld + m);
+            j.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.d) + t.lo[e] * a.d_ld + n0);
+            j.w_ld = (int)a.w_ld[e];
+            j.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.w[e]) + m * a.w_ld[e] + n0);
+            j.rows = min(kBig, a.kdim - m);
+            j.kd = t.rows[e];
+        } else {
+            const int64_t m0 = (int64_t)t.lo[e] + m;
+            j.a = reinterpret_cast<uint64_t>(x + m0 * a.x_ld);
+            j.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0);
+            j.rows = min(kBig, t.rows[e] - m);
+            j.b = 0;
+            j.w_ld = 0;
+            j.kd = 0;
+            if (e < a.n) {   // else rows of no expert
+                j.w_ld = (int)a.w_ld[e];
+                j.kd = a.kdim;
+                j.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.w[e]) +
+                                                 (MODE == 1 ? n0 * a.w_ld[e] : n0));
+            }
+        }
+        return j;
+    }
+};
+
+// Fills the table (one wave).  `most`: the tiles the launch was made for (end
+// rows that decrease could count more; those are cut off).
+template <int MODE>
+__device__ __forceinline__ void fill_table(const GroupedArgs& a, const Grid<MODE>& g, GroupTable& t, int most) {
+    const int lane = threadIdx.x, slots = a.n + (MODE != 2 && a.last ? 1 : 0);
+    float c[4], csum = 0.f;
+    int n[4], nsum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = lane * 4 + k;
+        int lo = 0, hi = 0;
+        if (i < slots) slot_rows(a, i, lo, hi);
+        const int rows = max(hi - lo, 0);
+        t.lo[i] = lo;
+        t.rows[i] = rows;
+        n[k] = i < slots ? g.row_tiles(rows) * g.ntn : 0;
+        c[k] = i < slots ? g.cost(rows) : 0.f;
+        nsum = min(nsum + n[k], most);
+        csum += c[k];
+    }
+    int nincl = nsum;
+    float cincl = csum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int nv = __shfl_up(nincl, o, 64);
+        const float cv = __shfl_up(cincl, o, 64);
+        if (lane >= o) {
+            nincl = min(nincl + nv, most);
+            cincl += cv;
         }
     }
-    return job;
-}
-
-// The job as scalars (every lane reads the same).
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ uint64_t uniform(uint64_t x) {
-    return (uint32_t)uniform((int)(uint32_t)x) | (uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32;
-}
-
-// Fills the table from the end rows; returns the launch's row tiles.  A count
-// that the grid was not made for (end rows that decrease) is cut off.
-__device__ __forceinline__ int fill_table(const GroupedArgs& a, GroupTable& t, int most) {
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x, slots = a.n + (a.last ? 1 : 0);
-        int cnt[4], sum = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = lane * 4 + k;
-            int lo = 0, hi = 0;
-            if (i < slots) slot_rows(a, i, lo, hi);
-            cnt[k] = hi > lo ? min((hi - lo - 1) / kBig + 1, most) : 0;
-            sum = min(sum + cnt[k], most);
-            t.lo[i] = lo;
-            t.rows[i] = max(hi - lo, 0);
-        }
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(incl, o, 64);
-            if (lane >= o) incl = min(incl + v, most);
-        }
-        int at = __shfl_up(incl, 1, 64);
-        if (lane == 0) at = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            t.first[lane * 4 + k] = at;
-            at = min(at + cnt[k], most);
-        }
-        if (lane == 63) t.first[256] = at;
+    int nat = __shfl_up(nincl, 1, 64);
+    float cat = __shfl_up(cincl, 1, 64);
+    if (lane == 0) {
+        nat = 0;
+        cat = 0.f;
     }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(t.first[256]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        t.first[lane * 4 + k] = nat;
+        t.cost[lane * 4 + k] = cat;
+        nat = min(nat + n[k], most);
+        cat += c[k];
+    }
+    if (lane == 63) {
+        t.first[256] = nat;
+        t.cost[256] = cat;
+    }
+}
+
+// First tile of share x of eight, of about equal cost.
+__device__ __forceinline__ int share(const GroupTable& t, int x) {
+    if (x == 8) return t.first[256];
+    const float at = t.cost[256] * ((float)x / 8.f);
+    int e = 0;
+#pragma unroll
+    for (int s = 128; s > 0; s >>= 1)
+        if (e + s <= kExperts && t.cost[e + s] <= at) e += s;
+    const float c = t.cost[e + 1] - t.cost[e];
+    const int n = t.first[e + 1] - t.first[e];
+    return t.first[e] + (c > 0.f ? max(0, min(n, (int)((at - t.cost[e]) / c * n))) : 0);
 }
 
 template <int MODE>
@@ -497,18 +562,19 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
 
-    // ---- this workgroup's tiles: those of an XCD follow each other (workgroup
-    //      ids go round the eight XCDs), dealt out to its workgroups in turn
-    const int row_tiles = fill_table(a, table, most);
-    int64_t total;
-    if (MODE == 2) total = (int64_t)a.n * ((a.kdim + kBig - 1) / kBig) * ((a.ndim + kBig - 1) / kBig);
-    else total = (int64_t)row_tiles * ((a.ndim + kBig - 1) / kBig);
-    const int64_t per = (total + 7) / 8, stride = gridDim.x >> 3;
-    const int64_t end = min(total, (int64_t)((blockIdx.x & 7) + 1) * per);
-    const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (id >= end) return;
-    const int count = (int)min((end - id + stride - 1) / stride, (int64_t)kJobs);
-    for (int m = threadIdx.x; m < count; m += 512) jobs[m] = make_job<MODE>(a, table, id + m * stride);
+    // ---- this workgroup's tiles.  Each XCD (workgroup ids go round the eight)
+    //      takes a run of tiles, so that what they share sits in one L2, and
+    //      deals them out to its workgroups in turn
+    const Grid<MODE> grid(a);
+    if (wave == 0) fill_table<MODE>(a, grid, table, most);
+    __syncthreads();
+    const int stride = gridDim.x >> 3;
+    const int end = uniform(share(table, (blockIdx.x & 7) + 1));
+    int id = uniform(share(table, blockIdx.x & 7)) + (blockIdx.x >> 3);
+
+  for (; id < end; id += kJobs * stride) {   // kJobs of them at a time (nearly always all)
+    const int count = min((end - id + stride - 1) / stride, kJobs);
+    for (int m = threadIdx.x; m < count; m += 512) jobs[m] = grid.job(table, id + m * stride);
     __syncthreads();
 
     const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS void*)sbuf;
@@ -546,34 +612,74 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
         ldc = MODE == 2 ? uniform(j.w_ld) : (int)a.y_ld;
         C = uniform(j.c);
     };
-    f32x16 acc[4][2] = {};
-    bf16x8 av[2][4], bv[2][4];
-    auto read_a = [&](int h) __attribute__((always_inline)) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) av[i][kk] = fa.read((h * 2 + i) * 64, kk);
+    // loads: A1 of the feeds' step, and A0, B0, B1 of the step after it (q: its
+    // parity)
+    int q = 0;
+    auto load_a1 = [&]() __attribute__((always_inline)) { feed_a.load(1, ldsA + q * (2 * kPanel)); };
+    auto load_rest = [&]() __attribute__((always_inline)) {
+        advance();
+        q ^= 1;
+        feed_a.load(0, ldsA + q * (2 * kPanel));
+        feed_b.load(0, ldsB + q * (2 * kPanel));
+        feed_b.load(1, ldsB + q * (2 * kPanel));
     };
-    auto read_b = [&](int j) __attribute__((always_inline)) {
+    int after = 0;   // the tile's first step comes after another tile's
+    int p = 0;       // parity of the step
+    // the steps of one tile of AM blocks of 64 rows and FN of 128 columns
+    auto run = [&](auto am, auto fn) __attribute__((always_inline)) {
+        constexpr int AM = decltype(am)::value, FN = decltype(fn)::value;
+        f32x16 acc[AM][FN];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) bv[j][kk] = fb.read(j * 128, kk);
-    };
-    // fresh: the tile's first step, from zero
-    auto multiply = [&](int h, int j, bool fresh) __attribute__((always_inline)) {
-        if (fresh) {
+        for (int i = 0; i < AM; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][0], av[i][0], f32x16{}, 0, 0, 0);
-        } else {
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+        bf16x8 av[2][4], bv[2][4];
+        auto read_a = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][0], av[i][0], acc[2 * h + i][j], 0, 0, 0);
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) av[i][kk] = fa.read((h * 2 + i) * 64, kk);
+        };
+        auto read_b = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) bv[j][kk] = fb.read(j * 128, kk);
+        };
+        auto multiply = [&](int h) __attribute__((always_inline)) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (2 * h + i < AM) {
+                            f32x16& c = acc[2 * h + i < AM ? 2 * h + i : 0][j];
+                            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][kk], av[i][kk], c, 0, 0, 0);
+                        }
+            __builtin_amdgcn_s_setprio(0);
+        };
+        for (int k = 0;; ++k) {
+            const int last = (k + 1) * kBK >= kd;
+            read_a(0);
+            read_b(0);
+            if (FN > 1) read_b(1);
+            load_a1();
+            end_read<16>(after);
+            multiply(0);
+            end_multiply();
+            if (AM > 2) read_a(1);
+            if (last) put_result(acc, 0, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
+            load_rest();
+            fa.flip(p);
+            fb.flip(p);
+            end_read<8>(after | last);
+            if (AM > 2) multiply(1);
+            end_multiply();
+            p ^= 1;
+            after = 0;
+            if (last) break;
         }
-#pragma unroll
-        for (int kk = 1; kk < 4; ++kk)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                acc[2 * h + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[j][kk], av[i][kk], acc[2 * h + i][j], 0, 0, 0);
+        put_result(acc, 1, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
     };
 
     // the first step, and the second but for A1
@@ -581,58 +687,38 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
     feed_a.load(0, ldsA);
     feed_b.load(0, ldsB);
     feed_b.load(1, ldsB);
-    feed_a.load(1, ldsA);
-    advance();
-    feed_a.load(0, ldsA + 2 * kPanel);
-    feed_b.load(0, ldsB + 2 * kPanel);
-    feed_b.load(1, ldsB + 2 * kPanel);
+    load_a1();
+    load_rest();
     start_tile();
     asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
     if (wm == 1) end_multiply();   // one slot behind
 
-    int k = 0;        // step of the tile that is multiplied
-    int after = 0;    // the tile's first step, and there was one before it
-    int p = 0;        // parity of the step
     for (;;) {
-        const bool low = rows > 128, right = cols > 128;
-        const int last = (k + 1) * kBK >= kd;
-        read_a(0);
-        read_b(0);
-        read_b(1);
-        feed_a.load(1, ldsA + (p ^ 1) * (2 * kPanel));
-        end_read<16>(after);
-        __builtin_amdgcn_s_setprio(1);
-        multiply(0, 0, k == 0);
-        if (right) multiply(0, 1, k == 0);
-        __builtin_amdgcn_s_setprio(0);
-        end_multiply();
-        read_a(1);
-        if (last) put_result(acc, 0, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
-        advance();
-        feed_a.load(0, ldsA + p * (2 * kPanel));
-        feed_b.load(0, ldsB + p * (2 * kPanel));
-        feed_b.load(1, ldsB + p * (2 * kPanel));
-        fa.flip(p);
-        fb.flip(p);
-        end_read<8>(after | last);
-        __builtin_amdgcn_s_setprio(1);
-        if (low) multiply(1, 0, k == 0);
-        if (low && right) multiply(1, 1, k == 0);
-        __builtin_amdgcn_s_setprio(0);
-        end_multiply();
-        p ^= 1;
-        ++k;
-        after = 0;
-        if (!last) continue;
-        put_result(acc, 1, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
+        const int am = (rows + 63) >> 6;
+        constexpr std::integral_constant<int, 1> c1{};
+        constexpr std::integral_constant<int, 2> c2{};
+        constexpr std::integral_constant<int, 3> c3{};
+        constexpr std::integral_constant<int, 4> c4{};
+        if (cols > 128) {
+            if (am == 4) run(c4, c2);
+            else if (am == 3) run(c3, c2);
+            else if (am == 2) run(c2, c2);
+            else run(c1, c2);
+        } else {
+            if (am == 4) run(c4, c1);
+            else if (am == 3) run(c3, c1);
+            else if (am == 2) run(c2, c1);
+            else run(c1, c1);
+        }
         if (++out == count) break;
         start_tile();
-        k = 0;
         after = 1;
     }
     if (wm == 0) end_multiply();   // as many barriers as the others
     // the loads past the last tile still write (zeros) into this workgroup's LDS
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -653,14 +739,10 @@ int64_t grouped_wgrad_grid(const GroupedArgs& a) {
     return cdiv(cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n, 8) * 8;
 }
 
-// Workgroups of the 256 x 256 kernel for at most `tiles` tiles.  One fits a CU.
-// With many tiles each takes its share in turn, so that one tile's loads run
-// while another is multiplied; with few, every tile is a workgroup of its own
-// and goes to the CU that is free first.
+// Workgroups of the 256 x 256 kernel for at most `tiles` tiles: one fits a CU.
 static uint32_t big_grid(int64_t tiles) {
-    static const int cus = [] { const int c = device_cus(); return c > 0 ? c : 256; }();
-    if (tiles < 6 * cus) return (uint32_t)tiles;
-    return (uint32_t)std::max<int64_t>(cus / 8 * 8, cdiv(tiles, 8 * (int64_t)kJobs) * 8);
+    static const int cus = [] { const int c = device_cus(); return c >= 8 ? std::min(c, 512) : 256; }();
+    return (uint32_t)std::min<int64_t>(tiles, cus / 8 * 8);
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
@@ -668,9 +750,8 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
     const dim3 grid((uint32_t)tiles);
     if (a.dtype == 0 && a.vec) {
         const dim3 big(big_grid(tiles));
-        const int most = a.rows / kBig + a.n + 1;
-        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), big, dim3(512), 0, s, a, most);
-        else hipLaunchKernelGGL((grouped_big<0>), big, dim3(512), 0, s, a, most);
+        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), big, dim3(512), 0, s, a, (int)tiles);
+        else hipLaunchKernelGGL((grouped_big<0>), big, dim3(512), 0, s, a, (int)tiles);
     } else if (a.dtype == 0) {
         if (trans_w) hipLaunchKernelGGL((grouped_mm_kernel<0, true>), grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL((grouped_mm_kernel<0, false>), grid, dim3(256), 0, s, a);
@@ -684,7 +765,7 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
     const int64_t tiles = grouped_wgrad_grid(a);
     const dim3 grid((uint32_t)tiles);
-    if (a.dtype == 0 && a.vec) hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, a.rows / kBig + a.n + 1);
+    if (a.dtype == 0 && a.vec) hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
     else if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_kernel<0>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((grouped_wgrad_kernel<1>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
