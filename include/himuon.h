@@ -413,10 +413,10 @@ typedef enum himuon_index {
  *            pointer and ld); any other overlap is refused.
  * workspace: device scratch of at least himuon_distill_workspace bytes,
  *            16-byte aligned; may be NULL when that is 0.
- * A row whose weight is 0, or that has no entry with p_j > 0, is not read: its
- * loss, lse and gradient are 0 whatever it holds.  In the other rows a logit
+ * A row whose weight is 0, or that has no entry with p_j > 0, counts nothing:
+ * its loss, lse and gradient are 0 whatever it holds.  In the other rows a logit
  * of -inf has q = 0 (an entry there gives the loss +inf); NaN or +inf logits
- * make that row's results NaN.  k up to HIMUON_MAX_ENTRIES.
+ * make that row's results NaN.  k up to HIMUON_MAX_ENTRIES, V up to 2^29.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (dtype, index
  * type, k above the maximum), HIMUON_ERR_LAYOUT, HIMUON_ERR_OVERLAP,
  * HIMUON_ERR_WORKSPACE, HIMUON_ERR_HIP.
@@ -437,7 +437,7 @@ himuon_status_t himuon_distill_workspace(const himuon_matrix_t* Z, himuon_dtype_
  * call on the same inputs.  g is the device array of N fp32 gradients of the
  * unweighted row losses (dL/dloss_i, times the row's weight if one was used);
  * it takes the place of weight above.  Rows with g = 0 or without entries get
- * zeros and are not read.
+ * zeros.
  */
 himuon_status_t himuon_distill_grad(const himuon_matrix_t* Z, const void* idx, himuon_index_t it,
                                     const himuon_matrix_t* T, float temperature, int32_t normalize, const float* lse,
@@ -490,7 +490,7 @@ himuon_status_t himuon_token_logprobs_workspace(const himuon_matrix_t* Z, int32_
  * g_logp, g_entropy : device arrays of N fp32, either may be NULL (zero).
  *            tokens may be NULL when g_logp is.
  * dZ       : N x V in dt, written; may be Z itself.
- * A skipped row, and one whose two gradients are 0, gets zeros and is not read.
+ * A skipped row, and one whose two gradients are 0, gets zeros.
  */
 himuon_status_t himuon_token_logprobs_grad(const himuon_matrix_t* Z, const void* tokens, himuon_index_t it,
                                            float temperature, const float* lse, const float* entropy,

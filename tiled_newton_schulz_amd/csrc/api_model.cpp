@@ -147,6 +147,37 @@ himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D
 }
 
 // ---- losses over logits -----------------------------------------------------------
+constexpr int64_t kMaxCols = 1 << 29;   // the kernels' chunk offsets within a row fit 32 bits
+
+// Workspace of a forward pass over the rows in segments: the segments' sums,
+// then their best keys.  0 where a row is one segment.
+size_t parts_bytes(int64_t rows, const SegPlan& p) {
+    return p.segs > 1 ? (size_t)rows * p.segs * sizeof(SegStats) : 0;
+}
+size_t keys_bytes(int64_t rows, const SegPlan& p, int32_t top) {
+    return p.segs > 1 ? (size_t)rows * p.segs * top * sizeof(uint64_t) : 0;
+}
+// Distillation with a gradient where rows are not kept on chip: the sums, and
+// the lse between the passes.
+size_t distill_bytes(int32_t rows, int32_t cols, int32_t dtype, bool with_grad) {
+    if (rows == 0 || (with_grad && distill_on_chip(rows, cols, dtype))) return 0;
+    return parts_bytes(rows, seg_plan(rows, cols, dtype)) + (with_grad ? (size_t)rows * 2 * sizeof(float) : 0);
+}
+
+himuon_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (need == 0) return HIMUON_OK;
+    if (ws == nullptr || bytes < need) return HIMUON_ERR_WORKSPACE;
+    return aligned(ws, 16) ? HIMUON_OK : HIMUON_ERR_LAYOUT;
+}
+
+// Shape checks of the workspace queries.
+himuon_status_t check_shape(const himuon_matrix_t* Z, himuon_dtype_t dt, const size_t* bytes) {
+    if (Z == nullptr || bytes == nullptr) return HIMUON_ERR_INVALID_ARGUMENT;
+    if (Z->rows < 0 || Z->cols < 1) return HIMUON_ERR_INVALID_ARGUMENT;
+    if (Z->rows > INT32_MAX || Z->cols > kMaxCols) return HIMUON_ERR_LAYOUT;
+    return check_dtype(dt);
+}
+
 himuon_status_t logits_args(const himuon_matrix_t* Z, himuon_index_t it, float temperature, himuon_dtype_t dt,
                             LogitsArgs& a) {
     himuon_status_t st = check_dtype(dt);
@@ -154,6 +185,7 @@ himuon_status_t logits_args(const himuon_matrix_t* Z, himuon_index_t it, float t
     if (it != HIMUON_I32 && it != HIMUON_I64) return HIMUON_ERR_UNSUPPORTED;
     if (Z == nullptr) return HIMUON_ERR_INVALID_ARGUMENT;
     if ((st = check_rows(*Z, elem_size(dt))) != HIMUON_OK) return st;
+    if (Z->cols > kMaxCols) return HIMUON_ERR_LAYOUT;
     if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
         return HIMUON_ERR_INVALID_ARGUMENT;
     a.z = Z->ptr;
@@ -161,6 +193,8 @@ himuon_status_t logits_args(const himuon_matrix_t* Z, himuon_index_t it, float t
     a.rows = (int32_t)Z->rows;
     a.cols = (int32_t)Z->cols;
     a.dtype = dt == HIMUON_FP32 ? 1 : 0;
+    a.plan = seg_plan(a.rows, a.cols, a.dtype);
+    if ((int64_t)a.rows * a.plan.segs > INT32_MAX) return HIMUON_ERR_LAYOUT;
     a.idx64 = it == HIMUON_I64;
     a.inv_temp = 1.f / temperature;
     return HIMUON_OK;
@@ -241,13 +275,22 @@ himuon_status_t distill(const himuon_matrix_t* Z, const void* idx, himuon_index_
     if (dZ != nullptr) arr.add(dZ, es, true);
     if (dZ == nullptr || dZ->ptr != Z->ptr) arr.add(Z, es, false);
     HIMUON_TRY(arr.check());
-    (void)workspace;
-    (void)workspace_bytes;
+    HIMUON_TRY(check_workspace(workspace, workspace_bytes, distill_bytes(a.rows, a.cols, a.dtype, dZ != nullptr)));
     if (a.rows == 0) return HIMUON_OK;
     a.weight = weight;
     a.loss = loss;
     a.lse = lse;
-    const hipError_t e = launch_distill(a, reinterpret_cast<hipStream_t>(stream));
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (dZ != nullptr && distill_on_chip(a.rows, a.cols, a.dtype)) {
+        e = launch_distill_on_chip(a, s);
+    } else {
+        a.part = reinterpret_cast<SegStats*>(workspace);
+        if (dZ != nullptr && a.lse == nullptr)
+            a.lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + parts_bytes(a.rows, a.plan));
+        e = launch_distill(a, s);
+        if (e == hipSuccess && dZ != nullptr) e = launch_distill_grad(a, s);
+    }
     return e == hipSuccess ? HIMUON_OK : hip_fail(e);
 }
 
@@ -294,9 +337,11 @@ himuon_status_t token_logprobs(const himuon_matrix_t* Z, const void* tokens, him
     }
     arr.add(Z, elem_size(dt), false);
     HIMUON_TRY(arr.check());
-    (void)workspace;
-    (void)workspace_bytes;
+    HIMUON_TRY(check_workspace(workspace, workspace_bytes,
+                               parts_bytes(a.rows, a.plan) + keys_bytes(a.rows, a.plan, top)));
     if (a.rows == 0) return HIMUON_OK;
+    a.part = reinterpret_cast<SegStats*>(workspace);
+    a.keys = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(workspace) + parts_bytes(a.rows, a.plan));
     a.tokens = tokens;
     a.top = top;
     a.logp = logp;
@@ -364,12 +409,8 @@ himuon_status_t himuon_distill(const himuon_matrix_t* Z, const void* idx, himuon
 
 himuon_status_t himuon_distill_workspace(const himuon_matrix_t* Z, himuon_dtype_t dt, int32_t with_grad,
                                          size_t* bytes) {
-    (void)with_grad;
-    if (Z == nullptr || bytes == nullptr) return HIMUON_ERR_INVALID_ARGUMENT;
-    if (Z->rows < 0 || Z->cols < 1) return HIMUON_ERR_INVALID_ARGUMENT;
-    if (Z->rows > INT32_MAX || Z->cols > INT32_MAX) return HIMUON_ERR_LAYOUT;
-    HIMUON_TRY(check_dtype(dt));
-    *bytes = 0;
+    HIMUON_TRY(check_shape(Z, dt, bytes));
+    *bytes = distill_bytes((int32_t)Z->rows, (int32_t)Z->cols, dt == HIMUON_FP32 ? 1 : 0, with_grad != 0);
     return HIMUON_OK;
 }
 
@@ -391,12 +432,11 @@ himuon_status_t himuon_token_logprobs(const himuon_matrix_t* Z, const void* toke
 
 himuon_status_t himuon_token_logprobs_workspace(const himuon_matrix_t* Z, int32_t top, himuon_dtype_t dt,
                                                 size_t* bytes) {
-    if (Z == nullptr || bytes == nullptr) return HIMUON_ERR_INVALID_ARGUMENT;
-    if (Z->rows < 0 || Z->cols < 1 || top < 0 || top > Z->cols) return HIMUON_ERR_INVALID_ARGUMENT;
+    HIMUON_TRY(check_shape(Z, dt, bytes));
+    if (top < 0 || top > Z->cols) return HIMUON_ERR_INVALID_ARGUMENT;
     if (top > kMaxTop) return HIMUON_ERR_UNSUPPORTED;
-    if (Z->rows > INT32_MAX || Z->cols > INT32_MAX) return HIMUON_ERR_LAYOUT;
-    HIMUON_TRY(check_dtype(dt));
-    *bytes = 0;
+    const SegPlan p = seg_plan((int32_t)Z->rows, (int32_t)Z->cols, dt == HIMUON_FP32 ? 1 : 0);
+    *bytes = parts_bytes(Z->rows, p) + keys_bytes(Z->rows, p, top);
     return HIMUON_OK;
 }
 

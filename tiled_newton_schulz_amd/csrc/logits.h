@@ -11,6 +11,19 @@ namespace himuon {
 constexpr int kMaxEntries = 1024;   // teacher entries of a row (matches HIMUON_MAX_ENTRIES)
 constexpr int kMaxTop = 64;         // alternatives of a row (matches HIMUON_MAX_TOP)
 
+// How the rows are cut for the passes that read them in segments: one workgroup
+// of 256 threads reads `chunks` 16-byte chunks, at most 256 * u.
+struct SegPlan {
+    int32_t segs;     // segments of a row
+    int32_t chunks;   // chunks of a segment
+    int32_t u;        // chunks of a thread: 1, 2, 4 or 8
+};
+
+// Result of a segment in the workspace (m the largest logit, the sums relative to it).
+struct SegStats {
+    float m, s, e, pad;
+};
+
 struct LogitsArgs {
     const void* z;            // N x V logits
     void* dz;                 // gradient, or null
@@ -26,7 +39,7 @@ struct LogitsArgs {
     int32_t k, normalize;
     const float* weight;      // forward: null = 1; gradient: dL/dloss
     float* loss;
-    float* lse;               // N x 2 (value, rest); written by a forward pass, read by a gradient (may be null in a forward pass)
+    float* lse;               // N x 2 (value, rest); written by a forward pass, read by a gradient (null: not wanted)
     // token log probabilities
     const void* tokens;
     int32_t top;
@@ -36,9 +49,19 @@ struct LogitsArgs {
     float* top_logp;
     const float* g_logp;
     const float* g_entropy;
+    // segments
+    SegPlan plan;
+    SegStats* part;           // workspace: rows x segs (segs > 1)
+    uint64_t* keys;           // workspace: rows x segs x top (segs > 1)
 };
 
-hipError_t launch_distill(const LogitsArgs& a, hipStream_t s);
+SegPlan seg_plan(int32_t rows, int32_t cols, int32_t dtype);
+// True if himuon_distill with a gradient keeps every row on chip (one launch,
+// one pass over the logits).
+bool distill_on_chip(int32_t rows, int32_t cols, int32_t dtype);
+
+hipError_t launch_distill(const LogitsArgs& a, hipStream_t s);         // loss (and lse)
+hipError_t launch_distill_on_chip(const LogitsArgs& a, hipStream_t s); // loss, lse and gradient
 hipError_t launch_distill_grad(const LogitsArgs& a, hipStream_t s);
 hipError_t launch_logprobs(const LogitsArgs& a, hipStream_t s);
 hipError_t launch_logprobs_grad(const LogitsArgs& a, hipStream_t s);

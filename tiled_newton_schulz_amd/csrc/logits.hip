@@ -1,9 +1,24 @@
 // Losses over rows of logits on gfx950: distillation from a teacher's top
 // logits and log probabilities of given tokens (include/himuon.h has the
-// formulas).  With s = z / temperature and m = max s, a row needs
-//     S = sum exp(s - m),  lse = m + log S,  E = sum exp(s - m) (s - m),
-//     entropy = log S - E / S,
-// all in fp32.  One workgroup per row: a pass for m, one for the sums.
+// formulas).  With s = z / temperature and m = max z, a row needs
+//     S = sum exp(s - s_m),  E = sum exp(s - s_m) (z - m),
+//     lse = s_m + log S,     entropy = log S - E / (S temperature),
+// all in fp32.  The differences are taken before they are scaled, so a row
+// masked by the type's lowest value loses nothing.
+//
+// The work is a stream over the logits (HBM bound, a read for a forward pass, a
+// read and a write for a gradient), so rows move in 16-byte chunks and stay
+// packed in registers between the maximum and the sums:
+// - forward passes cut a row into segments of up to 256 x 8 chunks, one
+//   workgroup each (few rows: smaller segments, so that the chip is filled), and
+//   a second launch joins them; a row of one segment ends in the first;
+// - the distillation loss with its gradient keeps the whole row in the
+//   registers of one workgroup: one read and one write in all;
+// - gradients from a known lse are element-wise, in segments.
+// Rows may start at any alignment: a row's chunks are those of the 16-byte grid,
+// and the elements of its first and last chunk are moved one by one.
+
+#include <algorithm>
 
 #include "device_util.h"
 #include "logits.h"
@@ -13,310 +28,945 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
 
-__device__ __forceinline__ float load_z(const LogitsArgs& a, int64_t row, int64_t col) {
-    const int64_t o = row * a.z_ld + col;
-    return a.dtype == 0 ? bf2f(reinterpret_cast<const unsigned short*>(a.z)[o])
-                        : reinterpret_cast<const float*>(a.z)[o];
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float ln_hw(float x) { return __builtin_amdgcn_logf(x) * kLn2; }
+
+// ---- rows in 16-byte chunks ------------------------------------------------
+template <int DT> constexpr int kEpc = DT == 0 ? 8 : 4;   // elements of a chunk
+// A chunk past every row: with at most 2^29 columns, neither its first column
+// nor the one after its last overflows an int.
+constexpr int kNoChunk = (1 << 27) + 8;
+static_assert(int64_t(kNoChunk) * 4 > (1 << 29) + 4 && int64_t(kNoChunk + 1) * 8 < INT32_MAX, "kNoChunk");
+
+// Element e of a chunk.
+template <int DT>
+__device__ __forceinline__ float elem(const u32x4& c, int e) {
+    if constexpr (DT == 0) return (e & 1) ? hi_f(c[e >> 1]) : lo_f(c[e >> 1]);
+    else return __uint_as_float(c[e]);
 }
-__device__ __forceinline__ void store_dz(const LogitsArgs& a, int64_t row, int64_t col, float v) {
-    const int64_t o = row * a.dz_ld + col;
-    if (a.dtype == 0) reinterpret_cast<unsigned short*>(a.dz)[o] = f2bf(v);
-    else reinterpret_cast<float*>(a.dz)[o] = v;
+template <int DT>
+__device__ __forceinline__ u32x4 pack(const float (&v)[kEpc<DT>]) {
+    u32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = DT == 0 ? pack2(v[(2 * i) % kEpc<DT>], v[(2 * i + 1) % kEpc<DT>]) : __float_as_uint(v[i]);
+    return c;
 }
+
+// FLUSH: the caller's rows all start and end on the grid.
+template <int DT, bool FLUSH>
+struct Row {
+    static constexpr int EPC = kEpc<DT>, ES = 16 / EPC;
+    char* base;    // 16-byte aligned, at or before the row's first element
+    int mis;       // elements from there to it
+    int cols;
+    __device__ __forceinline__ Row(const void* p, int64_t ld, int64_t row, int n) : cols(n) {
+        const uint64_t at = reinterpret_cast<uint64_t>(p) + (uint64_t)(row * ld) * ES;
+        mis = FLUSH ? 0 : (int)(at & 15) / ES;
+        base = reinterpret_cast<char*>(at & ~uint64_t(15));
+    }
+    __device__ __forceinline__ int chunks() const { return (mis + cols + EPC - 1) / EPC; }
+    __device__ __forceinline__ int first(int c) const { return c * EPC - mis; }   // column of element 0
+    __device__ __forceinline__ bool whole(int c) const {
+        return FLUSH ? c * EPC < cols : first(c) >= 0 && first(c) + EPC <= cols;
+    }
+    // byte offsets fit 32 bits (the host allows 2^29 columns)
+    __device__ __forceinline__ char* at(int c) const { return base + (uint32_t)c * 16u; }
+    // Chunk c; what lies outside the row is -inf.  (The element loops of this
+    // and of store() are kept rolled: they run for a row's two ends only.)
+    __device__ __forceinline__ u32x4 load(int c) const {
+        if (whole(c)) return *reinterpret_cast<const u32x4*>(at(c));
+        constexpr uint64_t kFill = DT == 0 ? 0xff80ff80ff80ff80ull : 0xff800000ff800000ull;
+        uint64_t w[2] = {kFill, kFill};
+        const int v0 = first(c);
+        if (!FLUSH && v0 < cols) {
+#pragma unroll 1
+            for (int e = max(0, -v0); e < min(EPC, cols - v0); ++e) {
+                const char* p = base + ((int64_t)c * EPC + e) * ES;
+                const uint64_t x = DT == 0 ? *reinterpret_cast<const unsigned short*>(p)
+                                           : *reinterpret_cast<const unsigned*>(p);
+                const int at = 8 * ES * (e % (EPC / 2));
+                const uint64_t keep = ~((DT == 0 ? 0xffffull : 0xffffffffull) << at);
+                if (e < EPC / 2) w[0] = (w[0] & keep) | x << at;
+                else w[1] = (w[1] & keep) | x << at;
+            }
+        }
+        return u32x4{(unsigned)w[0], (unsigned)(w[0] >> 32), (unsigned)w[1], (unsigned)(w[1] >> 32)};
+    }
+    __device__ __forceinline__ void store_elem(int col, float v) const {
+        char* p = base + ((int64_t)mis + col) * ES;
+        if constexpr (DT == 0) *reinterpret_cast<unsigned short*>(p) = f2bf(v);
+        else *reinterpret_cast<float*>(p) = v;
+    }
+    __device__ __forceinline__ float load_elem(int col) const {
+        const char* p = base + ((int64_t)mis + col) * ES;
+        if constexpr (DT == 0) return bf2f(*reinterpret_cast<const unsigned short*>(p));
+        else return *reinterpret_cast<const float*>(p);
+    }
+    // Elements of chunk c of a row that starts `from` elements into its chunk
+    // grid (the row the values were read from; the same grid when equal).
+    __device__ __forceinline__ void store(int c, const u32x4& v, int from) const {
+        const int v0 = c * EPC - from;
+        if (mis == from && whole(c)) {
+            *reinterpret_cast<u32x4*>(at(c)) = v;
+            return;
+        }
+        if (FLUSH) return;
+        const uint64_t w0 = v[0] | (uint64_t)v[1] << 32, w1 = v[2] | (uint64_t)v[3] << 32;
+#pragma unroll 1
+        for (int e = max(0, -v0); e < min(EPC, cols - v0); ++e) {
+            const uint64_t x = (e < EPC / 2 ? w0 : w1) >> (8 * ES * (e % (EPC / 2)));
+            char* p = base + ((int64_t)mis + v0 + e) * ES;
+            if constexpr (DT == 0) *reinterpret_cast<unsigned short*>(p) = (unsigned short)x;
+            else *reinterpret_cast<unsigned*>(p) = (unsigned)x;
+        }
+    }
+};
+
+// Makes chunks opaque to the optimiser, which would otherwise keep them unpacked
+// in registers from one pass over them to the next.
+template <int U>
+__device__ __forceinline__ void stay_packed(u32x4 (&r)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) asm volatile("" : "+v"(r[u]));
+}
+
 // Id i of an array, -1 if it lies outside [0, V).
 __device__ __forceinline__ int load_id(const void* p, int idx64, int64_t i, int cols) {
     const int64_t v = idx64 ? reinterpret_cast<const int64_t*>(p)[i] : reinterpret_cast<const int32_t*>(p)[i];
     return v >= 0 && v < cols ? (int)v : -1;
 }
 
-
+// ---- reductions ----------------------------------------------------------------
+// Over a wave, in a fixed order (lanes without a source take `none`).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float none, float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
 template <typename F>
-__device__ __forceinline__ float block_reduce(float v, float* red, F f) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = f(v, __shfl_xor(v, o, 64));
-    __syncthreads();   // red may still be read from the last use
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float r = red[0];
-    for (int i = 1; i < (int)(blockDim.x >> 6); ++i) r = f(r, red[i]);
+__device__ __forceinline__ float wave_reduce(float v, float none, F f) {
+    v = f(v, dpp<0x111, 0xf>(none, v));   // row_shr 1, 2, 4, 8
+    v = f(v, dpp<0x112, 0xf>(none, v));
+    v = f(v, dpp<0x114, 0xf>(none, v));
+    v = f(v, dpp<0x118, 0xf>(none, v));
+    v = f(v, dpp<0x142, 0xa>(none, v));   // row_bcast 15, 31
+    v = f(v, dpp<0x143, 0xc>(none, v));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wsum(float v) {
+    return wave_reduce(v, 0.f, [](float x, float y) { return x + y; });
+}
+__device__ __forceinline__ float wmax(float v) {
+    return wave_reduce(v, kNegInf, [](float x, float y) { return fmaxf(x, y); });
+}
+
+// ---- statistics of a set of logits --------------------------------------------
+struct Stats {
+    float m, s, e;   // largest logit (NaN passed over), S and E relative to it
+};
+constexpr Stats kEmpty = {kNegInf, 0.f, 0.f};
+// c: log2(e) / temperature.  A NaN reaches s and with it every result of the
+// row, and so does +inf (inf - inf); sets of -inf only have s = e = 0.
+__device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    if (m == kNegInf) return {m, a.s + b.s, 0.f};
+    const float da = a.m - m, db = b.m - m;
+    const float ea = exp2_hw(da * c), eb = exp2_hw(db * c);
+    Stats r;
+    r.m = m;
+    r.s = a.s * ea + b.s * eb;
+    r.e = ea * (a.e + fmaxf(da, -1e30f) * a.s) + eb * (b.e + fmaxf(db, -1e30f) * b.s);
     return r;
-}
-__device__ __forceinline__ float block_sum(float v, float* red) {
-    return block_reduce(v, red, [](float x, float y) { return x + y; });
-}
-__device__ __forceinline__ float block_max(float v, float* red) {
-    return block_reduce(v, red, [](float x, float y) { return fmaxf(x, y); });
 }
 
 // log sum exp of a row as hi + lo: hi is its fp32 value and lo what that
-// rounding lost, which counts where |m| is large (a row masked by the lowest
+// rounding lost, which counts where it is large (a row masked by the lowest
 // value would lose log S altogether).
 struct Lse {
     float hi, lo;
 };
-__device__ __forceinline__ Lse make_lse(float m, float S) {
-    if (S == 0.f) return {kNegInf, 0.f};   // -inf only
-    const float l = __logf(S), hi = m + l;
-    // |m| >= |l| or not: the exact rest of the sum either way
+__device__ __forceinline__ Lse make_lse(const Stats& st, float inv_temp) {
+    if (st.s == 0.f) return {kNegInf, 0.f};   // -inf only
+    const float m = st.m * inv_temp, l = ln_hw(st.s), hi = m + l;
     const float lo = fabsf(m) >= fabsf(l) ? (m - hi) + l : (l - hi) + m;
     return {hi, lo};
 }
-__device__ __forceinline__ float log_q_of(float s, Lse l) {
+__device__ __forceinline__ float entropy_of(const Stats& st, float inv_temp) {
+    return st.s == 0.f ? 0.f : ln_hw(st.s) - inv_temp * (st.e / st.s);
+}
+// log q of a logit.
+__device__ __forceinline__ float log_q(float z, float inv_temp, Lse l) {
+    const float s = z * inv_temp;
     if (s == kNegInf && l.hi == l.hi) return kNegInf;
     return (s - l.hi) - l.lo;
 }
-
-struct RowStats {
-    Lse lse;
-    float entropy;
+// q = exp2(fma(fma(z, inv_temp, -hi), log2 e, -lo log2 e)); a row of -inf only
+// takes hi = 0 and has q = 0.
+struct Softmax {
+    float inv_temp, neg_hi, neg_lo2;
+    __device__ __forceinline__ Softmax(float it, Lse l)
+        : inv_temp(it), neg_hi(l.hi == kNegInf ? 0.f : -l.hi), neg_lo2(-l.lo * kLog2e) {}
+    __device__ __forceinline__ float operator()(float z) const {
+        return exp2_hw(__builtin_fmaf(__builtin_fmaf(z, inv_temp, neg_hi), kLog2e, neg_lo2));
+    }
 };
 
 __device__ __forceinline__ void put_lse(const LogitsArgs& a, int64_t row, Lse l) {
+    if (a.lse == nullptr) return;
     a.lse[2 * row] = l.hi;
     a.lse[2 * row + 1] = l.lo;
 }
-__device__ __forceinline__ Lse get_lse(const LogitsArgs& a, int64_t row) { return {a.lse[2 * row], a.lse[2 * row + 1]}; }
+__device__ __forceinline__ Lse get_lse(const LogitsArgs& a, int64_t row) {
+    return {a.lse[2 * row], a.lse[2 * row + 1]};
+}
 
-// lse and entropy of a row.  NaN: fmaxf passes over it, the sum takes it in.
-// A maximum of +inf gives inf - inf = NaN in the sum, one of -inf leaves
-// nothing (lse -inf, entropy 0).
-__device__ __forceinline__ RowStats row_stats(const LogitsArgs& a, int64_t row, float* red) {
+// Statistics of the chunks a wave holds.
+template <int DT, int U>
+__device__ __forceinline__ Stats wave_stats(u32x4 (&r)[U], float c, bool want_e) {
     float m = kNegInf;
-    for (int v = threadIdx.x; v < a.cols; v += kThreads) m = fmaxf(m, load_z(a, row, v) * a.inv_temp);
-    m = block_max(m, red);
-    float s = 0.f, e = 0.f;
-    for (int v = threadIdx.x; v < a.cols; v += kThreads) {
-        const float z = load_z(a, row, v) * a.inv_temp;
-        if (z == kNegInf) continue;
-        const float d = z - m, x = __expf(d);
-        s += x;
-        e += x > 0.f ? x * d : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < kEpc<DT>; ++e) m = fmaxf(m, elem<DT>(r[u], e));
+    m = wmax(m);
+    stay_packed(r);
+    const float ref = m == kNegInf ? 0.f : m;
+    float s = 0.f, t = 0.f;
+    if (want_e) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < kEpc<DT>; ++e) {
+                const float d = elem<DT>(r[u], e) - ref, x = exp2_hw(d * c);
+                s += x;
+                t = __builtin_fmaf(x, fmaxf(d, -1e30f), t);
+            }
+        t = wsum(t);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < kEpc<DT>; ++e) s += exp2_hw((elem<DT>(r[u], e) - ref) * c);
     }
-    s = block_sum(s, red);
-    e = block_sum(e, red);
-    return {make_lse(m, s), s == 0.f ? 0.f : __logf(s) - e / s};
+    return {m, wsum(s), t};
 }
 
-// ---- distillation ------------------------------------------------------------
-
-// The teacher's entries of a row: ids (-1: absent) and probabilities in LDS.
-struct Teacher {
-    int* id;
-    float* p;
-    float P;       // their sum
-    float plogp;   // sum p log p
-    bool live;     // some entry has p > 0 (or is NaN)
+// ---- the teacher's entries ---------------------------------------------------------
+// Sums over the entries of a row, with u_j = t_j / temperature (normalize) or
+// t_j, M the largest u (normalize) or 0, e_j = exp(u_j - M), and b_j the log
+// probability of the id under the student up to a constant B:
+//     S = sum e,  E = sum e (u - M),  G = sum e b.
+// Then P = 1 or S, p_j = e_j / S or e_j, and
+//     loss = sum p log p - sum p log q = (E / S - log S - G / S) - P B   (or E - G - P B).
+struct Entry {
+    int id;      // -1: absent
+    float u;
+    float z;     // the student's logit at the id
 };
-
-__device__ __forceinline__ Teacher load_teacher(const LogitsArgs& a, int64_t row, int* id, float* p, float* red) {
-    const float it = a.normalize ? a.inv_temp : 1.f;
-    float m = kNegInf, some = 0.f;
-    for (int j = threadIdx.x; j < a.k; j += kThreads) {
-        id[j] = load_id(a.idx, a.idx64, row * a.k + j, a.cols);
-        const float t = id[j] >= 0 ? a.t[row * a.t_ld + j] * it : kNegInf;
-        p[j] = t;
-        m = fmaxf(m, t);
-        if (!(t == kNegInf)) some = 1.f;
-    }
-    Teacher r{id, p, 0.f, 0.f, block_max(some, red) > 0.f};
-    if (!r.live) return r;
-    m = a.normalize ? block_max(m, red) : 0.f;
-    float S = 0.f;
-    for (int j = threadIdx.x; j < a.k; j += kThreads) S += p[j] == kNegInf ? 0.f : __expf(p[j] - m);
-    S = block_sum(S, red);
-    const float l = a.normalize ? m + __logf(S) : 0.f;
-    float sum = 0.f, plogp = 0.f;
-    for (int j = threadIdx.x; j < a.k; j += kThreads) {
-        const float lp = p[j] - l;
-        const float q = p[j] == kNegInf ? 0.f : __expf(lp);
-        sum += q;
-        plogp += q == 0.f ? 0.f : q * lp;
-        p[j] = q;
-    }
-    r.P = block_sum(sum, red);
-    r.plogp = block_sum(plogp, red);   // its barriers also publish id and p
-    return r;
+template <int DT, bool FL>
+__device__ __forceinline__ Entry load_entry(const LogitsArgs& a, const Row<DT, FL>& z, int64_t row, int j) {
+    Entry x = {-1, kNegInf, 0.f};
+    if (j >= a.k) return x;
+    x.id = load_id(a.idx, a.idx64, row * a.k + j, a.cols);
+    if (x.id < 0) return x;
+    const float t = a.t[row * a.t_ld + j];
+    x.u = a.normalize ? t * a.inv_temp : t;
+    x.z = z.load_elem(x.id);
+    return x;
 }
 
-__device__ __forceinline__ void zero_row(const LogitsArgs& a, int64_t row) {
-    for (int v = threadIdx.x; v < a.cols; v += kThreads) store_dz(a, row, v, 0.f);
+struct TeacherSums {
+    float P, scale, loss;   // p_j = e_j scale; loss without P B
+};
+__device__ __forceinline__ TeacherSums teacher_sums(const LogitsArgs& a, float S, float E, float G) {
+    if (a.normalize) {
+        const float r = 1.f / S;
+        return {1.f, r, E * r - ln_hw(S) - G * r};
+    }
+    return {S, 1.f, E - G};
 }
 
-// Teacher probability of the row's entries that hold the same id as entry j
-// (usually entry j alone), in the entries' order.
-__device__ __forceinline__ float mass_at(const Teacher& t, int k, int j) {
+// Teacher probability of the row's entries that hold entry j's id (usually j
+// alone), in the entries' order.
+__device__ __forceinline__ float mass_at(const int* id, const float* p, int k, int mine) {
     float sum = 0.f;
-    for (int i = 0; i < k; ++i) sum += t.id[i] == t.id[j] ? t.p[i] : 0.f;
+    for (int i = 0; i < k; ++i) sum += id[i] == mine ? p[i] : 0.f;
     return sum;
 }
 
-// dz = c (P q - p), q from lse.  The ids of entries are written after the
-// others, from logits taken before any gradient is stored (dz may be z); equal
-// ids write the same value.
-__device__ __forceinline__ void distill_grad_row(const LogitsArgs& a, int64_t row, const Teacher& t, Lse lse, float w) {
-    const float c = w * a.inv_temp;
-    float fix[kMaxEntries / kThreads];
-    auto q_of = [&](int64_t v) { return __expf(log_q_of(load_z(a, row, v) * a.inv_temp, lse)); };
+// Joins the waves' values of several reductions of a workgroup of NT threads in
+// one go (v[i] holds the wave's; afterwards all threads hold the workgroup's).
+template <int NT, int N, typename F>
+__device__ __forceinline__ void block_join(float (&v)[N], float (*red)[N], float none, F f) {
+    __syncthreads();   // red may still be read from the last use
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int u = 0; u < kMaxEntries / kThreads; ++u) {
-        const int j = u * kThreads + threadIdx.x;
-        fix[u] = j < a.k && t.id[j] >= 0 ? c * (t.P * q_of(t.id[j]) - mass_at(t, a.k, j)) : 0.f;
-    }
+        for (int i = 0; i < N; ++i) red[threadIdx.x >> 6][i] = v[i];
     __syncthreads();
-    for (int v = threadIdx.x; v < a.cols; v += kThreads) store_dz(a, row, v, c * (t.P * q_of(v)));
-    __syncthreads();
+    const int w = threadIdx.x & 63;
 #pragma unroll
-    for (int u = 0; u < kMaxEntries / kThreads; ++u) {
-        const int j = u * kThreads + threadIdx.x;
-        if (j < a.k && t.id[j] >= 0) store_dz(a, row, t.id[j], fix[u]);
-    }
+    for (int i = 0; i < N; ++i) v[i] = wave_reduce(w < NT / 64 ? red[w][i] : none, none, f);
 }
+struct Max {
+    __device__ __forceinline__ float operator()(float x, float y) const { return fmaxf(x, y); }
+};
+struct Sum {
+    __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
+};
 
-__global__ __launch_bounds__(kThreads) void distill_kernel(const LogitsArgs a) {
-    __shared__ float red[kThreads / 64];
-    __shared__ int id[kMaxEntries];
-    __shared__ float p[kMaxEntries];
-    const int64_t row = blockIdx.x;
-    const float w = a.weight ? a.weight[row] : 1.f;
-    Teacher t{};
-    if (w != 0.f) t = load_teacher(a, row, id, p, red);
-    if (!t.live) {
+// Loss of a row whose lse is known (a workgroup of 256 threads).
+template <int DT, bool FL>
+__device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, Lse l) {
+    __shared__ float red1[4][2], red2[4][3];
+    const Row<DT, FL> z(a.z, a.z_ld, row, a.cols);
+    Entry x[kMaxEntries / kThreads];
+    float mx[2] = {kNegInf, 0.f};
+#pragma unroll
+    for (int i = 0; i < kMaxEntries / kThreads; ++i) {
+        x[i] = load_entry<DT, FL>(a, z, row, i * kThreads + threadIdx.x);
+        mx[0] = fmaxf(mx[0], x[i].u);
+        if (!(x[i].u == kNegInf)) mx[1] = 1.f;
+    }
+    mx[0] = wmax(mx[0]);
+    mx[1] = wmax(mx[1]);
+    block_join<kThreads>(mx, red1, kNegInf, Max());
+    if (mx[1] == 0.f) {   // no entry counts
         if (threadIdx.x == 0) {
             a.loss[row] = 0.f;
-            if (a.lse) put_lse(a, row, {0.f, 0.f});
+            put_lse(a, row, {0.f, 0.f});
         }
-        if (a.dz) zero_row(a, row);
         return;
     }
-    const RowStats r = row_stats(a, row, red);
-    float cross = 0.f;
-    for (int j = threadIdx.x; j < a.k; j += kThreads) {
-        if (t.p[j] == 0.f) continue;
-        cross += t.p[j] * log_q_of(load_z(a, row, t.id[j]) * a.inv_temp, r.lse);
+    const float M = a.normalize ? mx[0] : 0.f;
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kMaxEntries / kThreads; ++i) {
+        if (x[i].u == kNegInf) continue;
+        const float e = exp2_hw((x[i].u - M) * kLog2e);
+        if (e == 0.f) continue;   // adds nothing, whatever the student has there
+        sum[0] += e;
+        sum[1] += e * (x[i].u - M);
+        sum[2] += e * log_q(x[i].z, a.inv_temp, l);
     }
-    cross = block_sum(cross, red);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) sum[i] = wsum(sum[i]);
+    block_join<kThreads>(sum, red2, 0.f, Sum());
     if (threadIdx.x == 0) {
-        a.loss[row] = w * (t.plogp - cross);
-        if (a.lse) put_lse(a, row, r.lse);
+        a.loss[row] = (a.weight ? a.weight[row] : 1.f) * teacher_sums(a, sum[0], sum[1], sum[2]).loss;
+        put_lse(a, row, l);
     }
-    if (a.dz) distill_grad_row(a, row, t, r.lse, w);
 }
 
-__global__ __launch_bounds__(kThreads) void distill_grad_kernel(const LogitsArgs a) {
-    __shared__ float red[kThreads / 64];
-    __shared__ int id[kMaxEntries];
-    __shared__ float p[kMaxEntries];
-    const int64_t row = blockIdx.x;
-    const float w = a.weight[row];
-    Teacher t{};
-    if (w != 0.f) t = load_teacher(a, row, id, p, red);
-    if (t.live) distill_grad_row(a, row, t, get_lse(a, row), w);
-    else zero_row(a, row);
-}
-
-// ---- log probabilities of given tokens -----------------------------------------
-
-// Order of the alternatives: larger logit first (NaN as -inf), equal ones by
-// the lower id.  0 is below every key of an element.
+// ---- alternatives -----------------------------------------------------------------
+// Order: larger logit first (NaN as -inf), equal ones by the lower id.  0 is
+// below every key of an element.
 __device__ __forceinline__ uint64_t rank_key(float z, int id) {
     z = z != z ? kNegInf : z + 0.f;   // -0 as +0
     const uint32_t u = __float_as_uint(z);
     const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
     return ((uint64_t)o << 32) | (uint32_t)~id;
 }
-
-__device__ __forceinline__ uint64_t block_max_key(uint64_t v, uint64_t* red) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        const uint64_t w = __shfl_xor((unsigned long long)v, o, 64);
-        v = v > w ? v : w;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    uint64_t r = red[0];
-    for (int i = 1; i < kThreads / 64; ++i) r = r > red[i] ? r : red[i];
-    return r;
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t o = (uint32_t)(key >> 32);
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
+__device__ __forceinline__ int key_id(uint64_t key) { return (int)~(uint32_t)key; }
 
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogitsArgs a) {
-    __shared__ float red[kThreads / 64];
-    __shared__ uint64_t redk[kThreads / 64];
-    const int64_t row = blockIdx.x;
-    const int tok = a.tokens ? load_id(a.tokens, a.idx64, row, a.cols) : 0;
-    if (tok < 0) {
-        if (threadIdx.x == 0) {
-            if (a.logp) a.logp[row] = 0.f;
-            if (a.entropy) a.entropy[row] = 0.f;
-            if (a.lse) put_lse(a, row, {0.f, 0.f});
-        }
-        for (int j = threadIdx.x; j < a.top; j += kThreads) {
-            a.top_idx[row * a.top + j] = -1;
-            a.top_logp[row * a.top + j] = kNegInf;
-        }
-        return;
+constexpr int kCand = 1024;
+struct TopShared {
+    uint64_t cand[kCand];
+    uint64_t best[4];
+    float low[4];
+    int count;
+};
+
+// The `top` largest of the elements a workgroup of 256 threads holds, in order:
+// emit(rank, key).  each(f) calls f(value, id) on a thread's elements (id < 0:
+// none); mine: the thread's largest value.
+//
+// A bound first: every wave takes the ceil(top / 4)-th largest of its lanes'
+// maxima, and at least `top` elements reach the smallest of the four.  The few
+// elements that do are ranked against each other.  Where too many do (long runs
+// of equal logits, rows masked but for a few ids) each rank is searched for.
+template <typename Each, typename Emit>
+__device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, Each each, Emit emit) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float v = mine, low = kNegInf;
+    for (int i = 0; i < (top + 3) / 4; ++i) {
+        low = wmax(v);
+        const unsigned long long at = __ballot(v == low);
+        if (at != 0 && lane == __builtin_ctzll(at)) v = __builtin_nanf("");   // passed over from here on
+        if (at == 0) low = kNegInf;
     }
-    const RowStats r = row_stats(a, row, red);
-    auto log_q = [&](int v) { return log_q_of(load_z(a, row, v) * a.inv_temp, r.lse); };
-    if (threadIdx.x == 0) {
-        if (a.logp) a.logp[row] = log_q(tok);
-        if (a.entropy) a.entropy[row] = r.entropy;
-        if (a.lse) put_lse(a, row, r.lse);
+    __syncthreads();   // sh may still be read from the last use
+    if (lane == 0) sh.low[wave] = low;
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    low = fminf(fminf(sh.low[0], sh.low[1]), fminf(sh.low[2], sh.low[3]));
+    if (mine >= low)   // a NaN beside smaller values ranks with -inf, below them
+        each([&](float z, int id) {
+            if (id >= 0 && (z >= low || (z != z && low == kNegInf))) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kCand) sh.cand[at] = rank_key(z, id);
+            }
+        });
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kCand) {
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint64_t key = sh.cand[i];
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += sh.cand[j] > key ? 1 : 0;
+            if (rank < top) emit(rank, key);
+        }
+        for (int i = n + threadIdx.x; i < top; i += kThreads) emit(i, 0);
+        return;
     }
     uint64_t below = ~0ull;
-    for (int j = 0; j < a.top; ++j) {   // the largest key below the last one taken
+    for (int j = 0; j < top; ++j) {   // the largest key below the last one taken
         uint64_t best = 0;
-        for (int v = threadIdx.x; v < a.cols; v += kThreads) {
-            const uint64_t key = rank_key(load_z(a, row, v), v);
+        each([&](float z, int id) {
+            const uint64_t key = id >= 0 ? rank_key(z, id) : 0;
             if (key < below && key > best) best = key;
+        });
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const uint64_t w = __shfl_xor((unsigned long long)best, o, 64);
+            best = best > w ? best : w;
         }
-        below = block_max_key(best, redk);
-        if (threadIdx.x == 0) {
-            const int v = (int)~(uint32_t)below;
-            a.top_idx[row * a.top + j] = v;
-            a.top_logp[row * a.top + j] = log_q(v);
+        __syncthreads();
+        if (lane == 0) sh.best[wave] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) best = best > sh.best[i] ? best : sh.best[i];
+        if (threadIdx.x == 0) emit(j, best);
+        below = best;
+    }
+}
+
+// Results of a row of log probabilities.
+template <int DT, bool FL>
+__device__ __forceinline__ void put_logprobs(const LogitsArgs& a, int64_t row, int tok, const Stats& st, Lse l) {
+    if (a.logp) a.logp[row] = log_q(Row<DT, FL>(a.z, a.z_ld, row, a.cols).load_elem(tok), a.inv_temp, l);
+    if (a.entropy) a.entropy[row] = st.s == st.s ? entropy_of(st, a.inv_temp) : st.s;
+    put_lse(a, row, l);
+}
+__device__ __forceinline__ void skip_logprobs(const LogitsArgs& a, int64_t row) {
+    if (threadIdx.x == 0) {
+        if (a.logp) a.logp[row] = 0.f;
+        if (a.entropy) a.entropy[row] = 0.f;
+        put_lse(a, row, {0.f, 0.f});
+    }
+    for (int j = threadIdx.x; j < a.top; j += kThreads) {
+        a.top_idx[row * a.top + j] = -1;
+        a.top_logp[row * a.top + j] = kNegInf;
+    }
+}
+__device__ __forceinline__ void put_alternative(const LogitsArgs& a, int64_t row, Lse l, int rank, uint64_t key) {
+    a.top_idx[row * a.top + rank] = key_id(key);
+    a.top_logp[row * a.top + rank] = log_q(key_value(key), a.inv_temp, l);
+}
+
+// ---- forward passes --------------------------------------------------------------
+// One workgroup per segment.  KIND 0: distillation, 1: log probabilities, 2:
+// the same with alternatives.
+template <int DT, int U, int KIND, bool FL>
+__global__ __launch_bounds__(kThreads) void forward_kernel(const LogitsArgs a) {
+    __shared__ Stats part[4];
+    const int64_t row = blockIdx.x / a.plan.segs;
+    const int seg = blockIdx.x % a.plan.segs;
+    const bool alone = a.plan.segs == 1;
+    int tok = 0;
+    if constexpr (KIND == 0) {
+        if (a.weight && a.weight[row] == 0.f) {
+            if (alone && threadIdx.x == 0) {
+                a.loss[row] = 0.f;
+                put_lse(a, row, {0.f, 0.f});
+            }
+            return;
+        }
+    } else {
+        if (a.tokens) tok = load_id(a.tokens, a.idx64, row, a.cols);
+        if (tok < 0) {
+            if (alone) skip_logprobs(a, row);
+            return;
+        }
+    }
+    const Row<DT, FL> z(a.z, a.z_ld, row, a.cols);
+    const int c0 = seg * a.plan.chunks, cn = min(a.plan.chunks, z.chunks() - c0);
+    u32x4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + threadIdx.x;
+        r[u] = z.load(i < cn ? c0 + i : kNoChunk);
+    }
+    const float c = a.inv_temp * kLog2e;
+    Stats st = wave_stats<DT, U>(r, c, KIND != 0 && a.entropy != nullptr);
+    stay_packed(r);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = st;
+    __syncthreads();
+    st = join(join(part[0], part[1], c), join(part[2], part[3], c), c);
+    if (!alone && threadIdx.x == 0) a.part[row * a.plan.segs + seg] = {st.m, st.s, st.e, 0.f};
+    const Lse l = make_lse(st, a.inv_temp);
+    if constexpr (KIND == 0) {
+        if (alone) distill_loss<DT, FL>(a, row, l);
+    } else {
+        if (alone && threadIdx.x == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
+        if constexpr (KIND == 2) {
+            __shared__ TopShared sh;
+            float mine = kNegInf;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < kEpc<DT>; ++e) mine = fmaxf(mine, elem<DT>(r[u], e));
+            stay_packed(r);
+            select_top(
+                sh, a.top, mine,
+                [&](auto f) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int i = u * kThreads + threadIdx.x;
+                        const int v0 = i < cn ? z.first(c0 + i) : a.cols;
+#pragma unroll
+                        for (int e = 0; e < kEpc<DT>; ++e)
+                            f(elem<DT>(r[u], e), v0 + e < a.cols ? v0 + e : -1);
+                    }
+                },
+                [&](int rank, uint64_t key) {
+                    if (alone) put_alternative(a, row, l, rank, key);
+                    else a.keys[(row * a.plan.segs + seg) * a.top + rank] = key;
+                });
         }
     }
 }
 
-__global__ __launch_bounds__(kThreads) void logprobs_grad_kernel(const LogitsArgs a) {
+// Joins the segments of a row (one workgroup).
+constexpr int kMergeKeys = 8;   // keys a thread holds
+template <int DT, int KIND, bool FL>
+__global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
+    __shared__ Stats all;
     const int64_t row = blockIdx.x;
-    const int tok = a.tokens ? load_id(a.tokens, a.idx64, row, a.cols) : -1;
-    float gl = a.g_logp ? a.g_logp[row] * a.inv_temp : 0.f;
-    float gh = a.g_entropy ? a.g_entropy[row] * a.inv_temp : 0.f;
-    if (a.tokens && tok < 0) gl = gh = 0.f;
-    if (gl == 0.f && gh == 0.f) {
-        zero_row(a, row);
+    int tok = 0;
+    if constexpr (KIND == 0) {
+        if (a.weight && a.weight[row] == 0.f) {
+            if (threadIdx.x == 0) {
+                a.loss[row] = 0.f;
+                put_lse(a, row, {0.f, 0.f});
+            }
+            return;
+        }
+    } else {
+        if (a.tokens) tok = load_id(a.tokens, a.idx64, row, a.cols);
+        if (tok < 0) {
+            skip_logprobs(a, row);
+            return;
+        }
+    }
+    const float c = a.inv_temp * kLog2e;
+    if (threadIdx.x < 64) {
+        Stats st = kEmpty;
+        for (int i = threadIdx.x; i < a.plan.segs; i += 64) {
+            const SegStats p = a.part[row * a.plan.segs + i];
+            st = join(st, Stats{p.m, p.s, p.e}, c);
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            // the same order in every lane, so that all have the same result
+            const Stats b = {__shfl_xor(st.m, o, 64), __shfl_xor(st.s, o, 64), __shfl_xor(st.e, o, 64)};
+            st = (threadIdx.x & o) ? join(b, st, c) : join(st, b, c);
+        }
+        if (threadIdx.x == 0) all = st;
+    }
+    __syncthreads();
+    const Stats st = all;
+    const Lse l = make_lse(st, a.inv_temp);
+    if constexpr (KIND == 0) {
+        distill_loss<DT, FL>(a, row, l);
+    } else {
+        if (threadIdx.x == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
+        if constexpr (KIND == 2) {
+            __shared__ TopShared sh;
+            __shared__ uint64_t carry[kMaxTop];
+            // batches of keys, the best so far among the next
+            const int64_t n = (int64_t)a.plan.segs * a.top;
+            const uint64_t* keys = a.keys + row * n;
+            const int batch = kThreads * kMergeKeys - a.top;
+            for (int64_t b = 0; b < n; b += batch) {
+                uint64_t key[kMergeKeys];
+                float mine = kNegInf;
+#pragma unroll
+                for (int u = 0; u < kMergeKeys; ++u) {
+                    const int i = u * kThreads + threadIdx.x;   // the first `top` are the best so far
+                    key[u] = i < a.top ? (b > 0 ? carry[i] : 0)
+                                       : (i - a.top < batch && b + i - a.top < n ? keys[b + i - a.top] : 0);
+                    if (key[u] != 0) mine = fmaxf(mine, key_value(key[u]));
+                }
+                const bool last = b + batch >= n;
+                __syncthreads();
+                select_top(
+                    sh, a.top, mine,
+                    [&](auto f) {
+#pragma unroll
+                        for (int u = 0; u < kMergeKeys; ++u)
+                            f(key_value(key[u]), key[u] != 0 ? key_id(key[u]) : -1);
+                    },
+                    [&](int rank, uint64_t k) {
+                        if (last) put_alternative(a, row, l, rank, k);
+                        else carry[rank] = k;
+                    });
+                __syncthreads();
+            }
+        }
+    }
+}
+
+// ---- gradients from a known lse ------------------------------------------------------
+// One workgroup per segment.  KIND 0: distillation, 1: log probabilities.
+// In place each chunk is read before its own element is written, and the
+// entries' logits before any.
+template <int DT, int KIND, bool FL>
+__global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
+    constexpr int U = 4, EPC = kEpc<DT>;
+    const int64_t row = blockIdx.x / a.plan.segs;
+    const int seg = blockIdx.x % a.plan.segs;
+    const Row<DT, FL> z(a.z, a.z_ld, row, a.cols), dz(a.dz, a.dz_ld, row, a.cols);
+    const int c0 = seg * a.plan.chunks, c1 = min(z.chunks(), c0 + a.plan.chunks);
+    const int v_lo = max(0, z.first(c0)), v_hi = min(a.cols, z.first(c1));   // this segment's columns
+
+    // ---- what the row's gradient is made of ----
+    int tok = -1;
+    float gl = 0.f, gh = 0.f, scale = 0.f;
+    constexpr int KE = KIND == 0 ? kMaxEntries / kThreads : 1;
+    int fix_id[KE];
+    float fix[KE];
+    bool live = true;
+    Lse l = {0.f, 0.f};
+    if constexpr (KIND == 1) {
+        if (a.tokens) tok = load_id(a.tokens, a.idx64, row, a.cols);
+        gl = a.g_logp ? a.g_logp[row] * a.inv_temp : 0.f;
+        gh = a.g_entropy ? a.g_entropy[row] * a.inv_temp : 0.f;
+        if (a.tokens && tok < 0) gl = gh = 0.f;
+        live = !(gl == 0.f && gh == 0.f);
+        if (live) l = get_lse(a, row);
+    } else {
+        __shared__ float red1[4][2], red2[4][1];
+        __shared__ int ids[kMaxEntries];
+        __shared__ float ps[kMaxEntries];
+        const float w = a.weight[row];
+        live = w != 0.f;
+        if (live) {
+            Entry x[KE];
+            float mx[2] = {kNegInf, 0.f};
+#pragma unroll
+            for (int i = 0; i < KE; ++i) {
+                x[i] = load_entry<DT, FL>(a, z, row, i * kThreads + threadIdx.x);
+                mx[0] = fmaxf(mx[0], x[i].u);
+                if (!(x[i].u == kNegInf)) mx[1] = 1.f;
+            }
+            mx[0] = wmax(mx[0]);
+            mx[1] = wmax(mx[1]);
+            block_join<kThreads>(mx, red1, kNegInf, Max());
+            live = mx[1] != 0.f;
+            if (live) {
+                l = get_lse(a, row);
+                const float M = a.normalize ? mx[0] : 0.f;
+                float sum[1] = {0.f};
+#pragma unroll
+                for (int i = 0; i < KE; ++i) {
+                    const int j = i * kThreads + threadIdx.x;
+                    const float e = x[i].u == kNegInf ? 0.f : exp2_hw((x[i].u - M) * kLog2e);
+                    sum[0] += e;
+                    if (j < a.k) {
+                        ids[j] = x[i].id;
+                        ps[j] = e;
+                    }
+                }
+                sum[0] = wsum(sum[0]);
+                block_join<kThreads>(sum, red2, 0.f, Sum());   // publishes ids, ps
+                const float P = a.normalize ? 1.f : sum[0], r = a.normalize ? 1.f / sum[0] : 1.f;
+                const float cw = w * a.inv_temp;
+                scale = cw * P;
+                const Softmax q(a.inv_temp, l);
+#pragma unroll
+                for (int i = 0; i < KE; ++i) {
+                    fix_id[i] = x[i].id >= v_lo && x[i].id < v_hi ? x[i].id : -1;
+                    fix[i] = 0.f;
+                    if (fix_id[i] >= 0)
+                        fix[i] = cw * (P * q(z.load_elem(x[i].id)) - r * mass_at(ids, ps, a.k, x[i].id));
+                }
+            }
+        }
+        __syncthreads();   // in place: every entry's logit is read before a gradient is stored in the segment
+    }
+    if (!live) {
+        for (int ch = c0 + threadIdx.x; ch < c1; ch += kThreads) dz.store(ch, u32x4{0u, 0u, 0u, 0u}, z.mis);
         return;
     }
-    const Lse lse = get_lse(a, row);
-    const float H = gh != 0.f ? a.entropy[row] : 0.f;
-    for (int v = threadIdx.x; v < a.cols; v += kThreads) {
-        const float lq = log_q_of(load_z(a, row, v) * a.inv_temp, lse), q = __expf(lq);
-        float g = v == tok ? gl * (1.f - q) : -gl * q;
-        if (gh != 0.f && q != 0.f) g -= gh * (q * (lq + H));
-        store_dz(a, row, v, g);
+
+    const Softmax q(a.inv_temp, l);
+    // log probabilities: dz = -q (gl + gh (s - lse + H)), and gl more at the token
+    const float H = KIND == 1 && gh != 0.f ? a.entropy[row] : 0.f;
+    const float slope = a.inv_temp * gh, at0 = gl + (gh != 0.f ? gh * ((H - l.hi) - l.lo) : 0.f);
+    for (int b = c0; b < c1; b += kThreads * U) {
+        u32x4 r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int ch = b + u * kThreads + threadIdx.x;
+            r[u] = z.load(ch < c1 ? ch : kNoChunk);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int ch = b + u * kThreads + threadIdx.x;
+            if (ch >= c1) continue;
+            float g[EPC];
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) {
+                const float x = elem<DT>(r[u], e), p = q(x);
+                if constexpr (KIND == 0) {
+                    g[e] = scale * p;
+                } else if (gh == 0.f) {
+                    g[e] = -gl * p;
+                } else {
+                    const float t = __builtin_fmaf(x, slope, at0);
+                    g[e] = p == 0.f ? 0.f : -p * t;
+                }
+            }
+            if constexpr (KIND == 1) {
+                const int d = tok - z.first(ch);
+                if (d >= 0 && d < EPC && tok >= 0)
+#pragma unroll
+                    for (int e = 0; e < EPC; ++e)
+                        if (e == d) g[e] += gl;
+            }
+            dz.store(ch, pack<DT>(g), z.mis);
+        }
     }
+    if constexpr (KIND == 0) {
+        __syncthreads();   // after the stores of the whole segment
+#pragma unroll
+        for (int i = 0; i < KE; ++i)
+            if (fix_id[i] >= 0) dz.store_elem(fix_id[i], fix[i]);
+    }
+}
+
+// ---- distillation, loss and gradient, the row on chip ---------------------------------
+// One workgroup of NT threads a row, U chunks a thread, rows in turn.  A thread
+// holds its chunks packed in registers; as each is turned into its gradient and
+// stored, the next row's chunk is loaded in its place, so that one row's stores
+// and the next one's loads overlap the products between them.
+template <int DT, int NT, int U, bool FL>
+__global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
+    constexpr int EPC = kEpc<DT>, KE = kMaxEntries / NT;
+    __shared__ float red1[NT / 64][3], red2[NT / 64][4];
+    __shared__ int ids[kMaxEntries];
+    __shared__ float ps[kMaxEntries];
+    const float c = a.inv_temp * kLog2e;
+    auto weight_of = [&](int64_t row) { return row < a.rows ? (a.weight ? a.weight[row] : 1.f) : 0.f; };
+
+    int64_t row = blockIdx.x;
+    float w = weight_of(row);
+    u32x4 r[U];
+    {
+        // a row that counts nothing is not read: no columns
+        const Row<DT, FL> z(a.z, a.z_ld, row, w != 0.f ? a.cols : 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = z.load(u * NT + threadIdx.x);
+    }
+    for (; row < a.rows; row += gridDim.x) {
+        const Row<DT, FL> z(a.z, a.z_ld, row, a.cols), dz(a.dz, a.dz_ld, row, a.cols);
+        const int64_t next = row + gridDim.x;
+        const float w_next = weight_of(next);
+        const Row<DT, FL> zn(a.z, a.z_ld, next < a.rows ? next : row, w_next != 0.f ? a.cols : 0);
+
+        // ---- largest logit, the teacher's entries ----
+        Entry x[KE];
+#pragma unroll
+        for (int i = 0; i < KE; ++i) x[i] = {-1, kNegInf, 0.f};
+        float mx[3] = {kNegInf, 0.f, kNegInf};   // teacher's largest u, any entry, largest logit
+        if (w != 0.f) {
+#pragma unroll
+            for (int i = 0; i < KE; ++i) {
+                x[i] = load_entry<DT, FL>(a, z, row, i * NT + threadIdx.x);
+                mx[0] = fmaxf(mx[0], x[i].u);
+                if (!(x[i].u == kNegInf)) mx[1] = 1.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < EPC; ++e) mx[2] = fmaxf(mx[2], elem<DT>(r[u], e));
+#pragma unroll
+            for (int i = 0; i < 3; ++i) mx[i] = wmax(mx[i]);
+            block_join<NT>(mx, red1, kNegInf, Max());
+        }
+        const bool live = mx[1] != 0.f;
+        stay_packed(r);
+
+        // ---- sums ----
+        const float ref = mx[2] == kNegInf ? 0.f : mx[2], M = a.normalize ? mx[0] : 0.f;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};   // S of the row; S, E, G of the teacher
+        Lse l = {0.f, 0.f};
+        float scale = 0.f, loss = 0.f, fix[KE];
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < KE; ++i) {
+                const float e = x[i].u == kNegInf ? 0.f : exp2_hw((x[i].u - M) * kLog2e);
+                const int j = i * NT + threadIdx.x;
+                if (j < a.k) {
+                    ids[j] = x[i].id;
+                    ps[j] = e;
+                }
+                if (e == 0.f) continue;
+                sum[1] += e;
+                sum[2] += e * (x[i].u - M);
+                sum[3] += e * ((x[i].z - ref) * a.inv_temp);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < EPC; ++e) sum[0] += exp2_hw((elem<DT>(r[u], e) - ref) * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = wsum(sum[i]);
+            block_join<NT>(sum, red2, 0.f, Sum());   // publishes ids and ps
+            l = make_lse(Stats{mx[2], sum[0], 0.f}, a.inv_temp);
+            const TeacherSums t = teacher_sums(a, sum[1], sum[2], sum[3]);
+            // b is relative to the row's largest logit: B = -log S
+            loss = w * (t.loss + (sum[0] == 0.f ? 0.f : t.P * ln_hw(sum[0])));
+            const float cw = w * a.inv_temp;
+            scale = cw * t.P;
+            const Softmax q(a.inv_temp, l);
+#pragma unroll
+            for (int i = 0; i < KE; ++i)
+                fix[i] = x[i].id >= 0 ? cw * (t.P * q(x[i].z) - t.scale * mass_at(ids, ps, a.k, x[i].id)) : 0.f;
+        }
+        if (threadIdx.x == 0) {
+            a.loss[row] = loss;
+            put_lse(a, row, l);
+        }
+        stay_packed(r);
+
+        // ---- the gradient, and the next row's loads ----
+        const Softmax q(a.inv_temp, l);
+        const unsigned mask = live ? ~0u : 0u;   // a row that counts nothing gets zeros whatever it holds
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float g[EPC];
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) g[e] = scale * q(elem<DT>(r[u], e));
+            dz.store(u * NT + threadIdx.x, pack<DT>(g) & mask, z.mis);
+            r[u] = zn.load(u * NT + threadIdx.x);
+            __builtin_amdgcn_sched_barrier(0);   // else all chunks of both rows are held at once
+        }
+        __syncthreads();   // the row's stores before those of its entries; ids and ps are free
+        if (live)
+#pragma unroll
+            for (int i = 0; i < KE; ++i)
+                if (x[i].id >= 0) dz.store_elem(x[i].id, fix[i]);
+        w = w_next;
+    }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// chunks a row takes at the worst alignment
+int64_t row_chunks(int32_t cols, int32_t dtype) { return cdiv(cols, dtype == 0 ? 8 : 4) + 1; }
+// ... and of these rows: one less where every row starts a chunk
+int64_t row_chunks(const LogitsArgs& a) {
+    const int epc = a.dtype == 0 ? 8 : 4;
+    const bool flush = (reinterpret_cast<uintptr_t>(a.z) & 15) == 0 && (a.z_ld % epc == 0 || a.rows == 1);
+    return cdiv(a.cols, epc) + (flush ? 0 : 1);
+}
+
+// every row of both starts and ends on the 16-byte grid
+bool flush(const LogitsArgs& a) {
+    const int epc = a.dtype == 0 ? 8 : 4;
+    auto on = [&](const void* p, int64_t ld) {
+        return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld % epc == 0 || a.rows == 1);
+    };
+    return a.cols % epc == 0 && on(a.z, a.z_ld) && (a.dz == nullptr || on(a.dz, a.dz_ld));
+}
+
+template <int DT, int KIND, bool FL>
+hipError_t forward_fl(const LogitsArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)((int64_t)a.rows * a.plan.segs)), block(kThreads);
+    switch (a.plan.u) {
+        case 1: hipLaunchKernelGGL((forward_kernel<DT, 1, KIND, FL>), grid, block, 0, s, a); break;
+        case 2: hipLaunchKernelGGL((forward_kernel<DT, 2, KIND, FL>), grid, block, 0, s, a); break;
+        case 4: hipLaunchKernelGGL((forward_kernel<DT, 4, KIND, FL>), grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL((forward_kernel<DT, 8, KIND, FL>), grid, block, 0, s, a); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.plan.segs == 1) return e;
+    hipLaunchKernelGGL((merge_kernel<DT, KIND, FL>), dim3(a.rows), block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t forward(const LogitsArgs& a, hipStream_t s) {
+    if (flush(a)) return a.dtype == 0 ? forward_fl<0, KIND, true>(a, s) : forward_fl<1, KIND, true>(a, s);
+    return a.dtype == 0 ? forward_fl<0, KIND, false>(a, s) : forward_fl<1, KIND, false>(a, s);
+}
+
+template <int KIND, bool FL>
+hipError_t grad_fl(const LogitsArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)((int64_t)a.rows * a.plan.segs));
+    if (a.dtype == 0) hipLaunchKernelGGL((grad_kernel<0, KIND, FL>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((grad_kernel<1, KIND, FL>), grid, dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+template <int KIND>
+hipError_t grad(LogitsArgs a, hipStream_t s) {
+    a.plan = seg_plan(a.rows, a.cols, a.dtype);
+    return flush(a) ? grad_fl<KIND, true>(a, s) : grad_fl<KIND, false>(a, s);
+}
+
+template <int DT, int NT, int U, bool FL>
+hipError_t row_launch(const LogitsArgs& a, hipStream_t s) {
+    static const int cus = [] { const int c = device_cus(); return c > 0 ? c : 256; }();
+    const int64_t most = (int64_t)cus * (1024 / NT);
+    hipLaunchKernelGGL((distill_row_kernel<DT, NT, U, FL>), dim3((uint32_t)std::min<int64_t>(a.rows, most)), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int DT, bool FL>
+hipError_t row_fl(const LogitsArgs& a, hipStream_t s) {
+    const int64_t n = row_chunks(a);
+    if (n <= 256 * 2) return row_launch<DT, 256, 2, FL>(a, s);
+    if (n <= 256 * 8) return row_launch<DT, 256, 8, FL>(a, s);
+    if (n <= 512 * 8) return row_launch<DT, 512, 8, FL>(a, s);
+    if (n <= 1024 * 8) return row_launch<DT, 1024, 8, FL>(a, s);
+    if (n <= 1024 * 16) return row_launch<DT, 1024, 16, FL>(a, s);
+    return row_launch<DT, 1024, 20, FL>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_distill(const LogitsArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(distill_kernel, dim3(a.rows), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+SegPlan seg_plan(int32_t rows, int32_t cols, int32_t dtype) {
+    const int64_t n = row_chunks(cols, dtype);
+    // a thousand workgroups fill the chip; the smaller the segments, the more
+    // there is to join
+    int u = 8;
+    while (u > 1 && rows * cdiv(n, kThreads * (int64_t)u) < 1024) u /= 2;
+    SegPlan p;
+    p.u = u;
+    p.segs = (int32_t)cdiv(n, kThreads * u);
+    p.chunks = (int32_t)cdiv(n, p.segs);
+    return p;
 }
-hipError_t launch_distill_grad(const LogitsArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(distill_grad_kernel, dim3(a.rows), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+
+bool distill_on_chip(int32_t rows, int32_t cols, int32_t dtype) { return row_chunks(cols, dtype) <= 1024 * 20; }
+
+hipError_t launch_distill(const LogitsArgs& a, hipStream_t s) { return forward<0>(a, s); }
+hipError_t launch_distill_on_chip(const LogitsArgs& a, hipStream_t s) {
+    if (flush(a)) return a.dtype == 0 ? row_fl<0, true>(a, s) : row_fl<1, true>(a, s);
+    return a.dtype == 0 ? row_fl<0, false>(a, s) : row_fl<1, false>(a, s);
 }
+hipError_t launch_distill_grad(const LogitsArgs& a, hipStream_t s) { return grad<0>(a, s); }
 hipError_t launch_logprobs(const LogitsArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(logprobs_kernel, dim3(a.rows), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+    return a.top > 0 ? forward<2>(a, s) : forward<1>(a, s);
 }
-hipError_t launch_logprobs_grad(const LogitsArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(logprobs_grad_kernel, dim3(a.rows), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
-}
+hipError_t launch_logprobs_grad(const LogitsArgs& a, hipStream_t s) { return grad<1>(a, s); }
 
 }  // namespace himuon
