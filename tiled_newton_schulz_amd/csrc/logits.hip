@@ -223,16 +223,23 @@ __device__ __forceinline__ Lse get_lse(const LogitsArgs& a, int64_t row) {
     return {a.lse[2 * row], a.lse[2 * row + 1]};
 }
 
-// Statistics of the chunks a wave holds.
+// Largest element of each chunk, and of all.
 template <int DT, int U>
-__device__ __forceinline__ Stats wave_stats(u32x4 (&r)[U], float c, bool want_e) {
+__device__ __forceinline__ float chunk_max(u32x4 (&r)[U], float (&cm)[U]) {
     float m = kNegInf;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+        cm[u] = kNegInf;
 #pragma unroll
-        for (int e = 0; e < kEpc<DT>; ++e) m = fmaxf(m, elem<DT>(r[u], e));
-    m = wmax(m);
+        for (int e = 0; e < kEpc<DT>; ++e) cm[u] = fmaxf(cm[u], elem<DT>(r[u], e));
+        m = fmaxf(m, cm[u]);
+    }
     stay_packed(r);
+    return m;
+}
+// Statistics of the chunks a wave holds, m their largest element.
+template <int DT, int U>
+__device__ __forceinline__ Stats wave_stats(u32x4 (&r)[U], float m, float c, bool want_e) {
     const float ref = m == kNegInf ? 0.f : m;
     float s = 0.f, t = 0.f;
     if (want_e) {
@@ -251,6 +258,7 @@ __device__ __forceinline__ Stats wave_stats(u32x4 (&r)[U], float c, bool want_e)
 #pragma unroll
             for (int e = 0; e < kEpc<DT>; ++e) s += exp2_hw((elem<DT>(r[u], e) - ref) * c);
     }
+    stay_packed(r);
     return {m, wsum(s), t};
 }
 
@@ -375,24 +383,26 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 }
 __device__ __forceinline__ int key_id(uint64_t key) { return (int)~(uint32_t)key; }
 
-constexpr int kCand = 1024;
+constexpr int kCand = 1024, kChunkCand = 512;
 struct TopShared {
     uint64_t cand[kCand];
     uint64_t best[4];
+    int chunk[kChunkCand];
     float low[4];
-    int count;
+    int count, chunks;
 };
 
-// The `top` largest of the elements a workgroup of 256 threads holds, in order:
-// emit(rank, key).  each(f) calls f(value, id) on a thread's elements (id < 0:
-// none); mine: the thread's largest value.
+// The `top` largest of a workgroup's elements, in order: emit(rank, key).  mine:
+// the largest of this thread's share of them; collect(low, add) calls
+// add(value, id) on at least those that are not below low, or returns false
+// (all threads alike) if they are too many; all(f) calls f(value, id) on each.
 //
 // A bound first: every wave takes the ceil(top / 4)-th largest of its lanes'
 // maxima, and at least `top` elements reach the smallest of the four.  The few
 // elements that do are ranked against each other.  Where too many do (long runs
 // of equal logits, rows masked but for a few ids) each rank is searched for.
-template <typename Each, typename Emit>
-__device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, Each each, Emit emit) {
+template <typename Collect, typename All, typename Emit>
+__device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, Collect collect, All all, Emit emit) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float v = mine, low = kNegInf;
     for (int i = 0; i < (top + 3) / 4; ++i) {
@@ -403,19 +413,18 @@ __device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, E
     }
     __syncthreads();   // sh may still be read from the last use
     if (lane == 0) sh.low[wave] = low;
-    if (threadIdx.x == 0) sh.count = 0;
+    if (threadIdx.x == 0) sh.count = sh.chunks = 0;
     __syncthreads();
     low = fminf(fminf(sh.low[0], sh.low[1]), fminf(sh.low[2], sh.low[3]));
-    if (mine >= low)   // a NaN beside smaller values ranks with -inf, below them
-        each([&](float z, int id) {
-            if (id >= 0 && (z >= low || (z != z && low == kNegInf))) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kCand) sh.cand[at] = rank_key(z, id);
-            }
-        });
+    // (a NaN is not below low: it is ranked with -inf, behind the `top` at hand)
+    const bool few = collect(low, [&](float z, int id) {
+        if (z < low) return;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kCand) sh.cand[at] = rank_key(z, id);
+    });
     __syncthreads();
     const int n = sh.count;
-    if (n <= kCand) {
+    if (few && n <= kCand) {
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const uint64_t key = sh.cand[i];
             int rank = 0;
@@ -428,8 +437,8 @@ __device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, E
     uint64_t below = ~0ull;
     for (int j = 0; j < top; ++j) {   // the largest key below the last one taken
         uint64_t best = 0;
-        each([&](float z, int id) {
-            const uint64_t key = id >= 0 ? rank_key(z, id) : 0;
+        all([&](float z, int id) {
+            const uint64_t key = rank_key(z, id);
             if (key < below && key > best) best = key;
         });
 #pragma unroll
@@ -504,8 +513,9 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const LogitsArgs a) {
         r[u] = z.load(i < cn ? c0 + i : kNoChunk);
     }
     const float c = a.inv_temp * kLog2e;
-    Stats st = wave_stats<DT, U>(r, c, KIND != 0 && a.entropy != nullptr);
-    stay_packed(r);
+    float cm[U];
+    const float mine = chunk_max<DT, U>(r, cm);
+    Stats st = wave_stats<DT, U>(r, wmax(mine), c, KIND != 0 && a.entropy != nullptr);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = st;
     __syncthreads();
     st = join(join(part[0], part[1], c), join(part[2], part[3], c), c);
@@ -517,23 +527,33 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const LogitsArgs a) {
         if (alone && threadIdx.x == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
         if constexpr (KIND == 2) {
             __shared__ TopShared sh;
-            float mine = kNegInf;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < kEpc<DT>; ++e) mine = fmaxf(mine, elem<DT>(r[u], e));
-            stay_packed(r);
+            // the few chunks that reach the bound are read again, an element a
+            // thread (looking through the registers' chunks took 190 registers)
+            auto chunk_elem = [&](int i, int e, auto f) {
+                const int v = z.first(c0 + i) + e;
+                if (v >= 0 && v < a.cols) f(z.load_elem(v), v);
+            };
             select_top(
                 sh, a.top, mine,
-                [&](auto f) {
+                [&](float low, auto add) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int i = u * kThreads + threadIdx.x;
-                        const int v0 = i < cn ? z.first(c0 + i) : a.cols;
-#pragma unroll
-                        for (int e = 0; e < kEpc<DT>; ++e)
-                            f(elem<DT>(r[u], e), v0 + e < a.cols ? v0 + e : -1);
+                        if (i < cn && cm[u] >= low) {
+                            const int at = atomicAdd(&sh.chunks, 1);
+                            if (at < kChunkCand) sh.chunk[at] = i;
+                        }
                     }
+                    __syncthreads();
+                    const int n = sh.chunks;
+                    if (n > kChunkCand) return false;
+                    for (int j = threadIdx.x; j < n * kEpc<DT>; j += kThreads)
+                        chunk_elem(sh.chunk[j / kEpc<DT>], j % kEpc<DT>, add);
+                    return true;
+                },
+                [&](auto f) {
+                    for (int j = threadIdx.x; j < cn * kEpc<DT>; j += kThreads)
+                        chunk_elem(j / kEpc<DT>, j % kEpc<DT>, f);
                 },
                 [&](int rank, uint64_t key) {
                     if (alone) put_alternative(a, row, l, rank, key);
@@ -608,10 +628,17 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
                 __syncthreads();
                 select_top(
                     sh, a.top, mine,
+                    [&](float low, auto add) {
+                        if (mine >= low)
+#pragma unroll
+                            for (int u = 0; u < kMergeKeys; ++u)
+                                if (key[u] != 0) add(key_value(key[u]), key_id(key[u]));
+                        return true;
+                    },
                     [&](auto f) {
 #pragma unroll
                         for (int u = 0; u < kMergeKeys; ++u)
-                            f(key_value(key[u]), key[u] != 0 ? key_id(key[u]) : -1);
+                            if (key[u] != 0) f(key_value(key[u]), key_id(key[u]));
                     },
                     [&](int rank, uint64_t k) {
                         if (last) put_alternative(a, row, l, rank, k);
