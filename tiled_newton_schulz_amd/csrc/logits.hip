@@ -325,24 +325,28 @@ struct Sum {
     __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
 };
 
-// Loss of a row whose lse is known (a workgroup of 256 threads).
-template <int DT, bool FL>
+// Loss of a row whose lse is known.  NT 256: a workgroup; 64: a wave (k <= 64).
+template <int DT, bool FL, int NT>
 __device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, Lse l) {
-    __shared__ float red1[4][2], red2[4][3];
+    constexpr int KE = NT == 64 ? 1 : kMaxEntries / NT;
+    const int tid = threadIdx.x % NT;
     const Row<DT, FL> z(a.z, a.z_ld, row, a.cols);
-    Entry x[kMaxEntries / kThreads];
+    Entry x[KE];
     float mx[2] = {kNegInf, 0.f};
 #pragma unroll
-    for (int i = 0; i < kMaxEntries / kThreads; ++i) {
-        x[i] = load_entry<DT, FL>(a, z, row, i * kThreads + threadIdx.x);
+    for (int i = 0; i < KE; ++i) {
+        x[i] = load_entry<DT, FL>(a, z, row, i * NT + tid);
         mx[0] = fmaxf(mx[0], x[i].u);
         if (!(x[i].u == kNegInf)) mx[1] = 1.f;
     }
     mx[0] = wmax(mx[0]);
     mx[1] = wmax(mx[1]);
-    block_join<kThreads>(mx, red1, kNegInf, Max());
+    if constexpr (NT != 64) {
+        __shared__ float red[NT / 64][2];
+        block_join<NT>(mx, red, kNegInf, Max());
+    }
     if (mx[1] == 0.f) {   // no entry counts
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             a.loss[row] = 0.f;
             put_lse(a, row, {0.f, 0.f});
         }
@@ -351,7 +355,7 @@ __device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, L
     const float M = a.normalize ? mx[0] : 0.f;
     float sum[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kMaxEntries / kThreads; ++i) {
+    for (int i = 0; i < KE; ++i) {
         if (x[i].u == kNegInf) continue;
         const float e = exp2_hw((x[i].u - M) * kLog2e);
         if (e == 0.f) continue;   // adds nothing, whatever the student has there
@@ -361,8 +365,11 @@ __device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, L
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) sum[i] = wsum(sum[i]);
-    block_join<kThreads>(sum, red2, 0.f, Sum());
-    if (threadIdx.x == 0) {
+    if constexpr (NT != 64) {
+        __shared__ float red[NT / 64][3];
+        block_join<NT>(sum, red, 0.f, Sum());
+    }
+    if (tid == 0) {
         a.loss[row] = (a.weight ? a.weight[row] : 1.f) * teacher_sums(a, sum[0], sum[1], sum[2]).loss;
         put_lse(a, row, l);
     }
@@ -389,56 +396,28 @@ struct TopShared {
     uint64_t best[4];
     int chunk[kChunkCand];
     float low[4];
+    int ties[4];
     int count, chunks;
 };
 
-// The `top` largest of a workgroup's elements, in order: emit(rank, key).  mine:
-// the largest of this thread's share of them; collect(low, add) calls
-// add(value, id) on at least those that are not below low, or returns false
-// (all threads alike) if they are too many; all(f) calls f(value, id) on each.
-//
-// A bound first: every wave takes the ceil(top / 4)-th largest of its lanes'
-// maxima, and at least `top` elements reach the smallest of the four.  The few
-// elements that do are ranked against each other.  Where too many do (long runs
-// of equal logits, rows masked but for a few ids) each rank is searched for.
-template <typename Collect, typename All, typename Emit>
-__device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, Collect collect, All all, Emit emit) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float v = mine, low = kNegInf;
-    for (int i = 0; i < (top + 3) / 4; ++i) {
-        low = wmax(v);
-        const unsigned long long at = __ballot(v == low);
-        if (at != 0 && lane == __builtin_ctzll(at)) v = __builtin_nanf("");   // passed over from here on
-        if (at == 0) low = kNegInf;
+// Ranks the n candidates among each other; emit(rank, key) for the first `top`.
+template <typename Emit>
+__device__ __forceinline__ void rank_candidates(const TopShared& sh, int n, int top, Emit emit) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t key = sh.cand[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sh.cand[j] > key ? 1 : 0;
+        if (rank < top) emit(rank, key);
     }
-    __syncthreads();   // sh may still be read from the last use
-    if (lane == 0) sh.low[wave] = low;
-    if (threadIdx.x == 0) sh.count = sh.chunks = 0;
-    __syncthreads();
-    low = fminf(fminf(sh.low[0], sh.low[1]), fminf(sh.low[2], sh.low[3]));
-    // (a NaN is not below low: it is ranked with -inf, behind the `top` at hand)
-    const bool few = collect(low, [&](float z, int id) {
-        if (z < low) return;
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kCand) sh.cand[at] = rank_key(z, id);
-    });
-    __syncthreads();
-    const int n = sh.count;
-    if (few && n <= kCand) {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const uint64_t key = sh.cand[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += sh.cand[j] > key ? 1 : 0;
-            if (rank < top) emit(rank, key);
-        }
-        for (int i = n + threadIdx.x; i < top; i += kThreads) emit(i, 0);
-        return;
-    }
+}
+// Searches each rank in turn: the largest key below the last one.  all(f) calls
+// f(key) on every element of this thread.
+template <typename All, typename Emit>
+__device__ __forceinline__ void search_ranks(TopShared& sh, int top, All all, Emit emit) {
     uint64_t below = ~0ull;
-    for (int j = 0; j < top; ++j) {   // the largest key below the last one taken
+    for (int j = 0; j < top; ++j) {
         uint64_t best = 0;
-        all([&](float z, int id) {
-            const uint64_t key = rank_key(z, id);
+        all([&](uint64_t key) {
             if (key < below && key > best) best = key;
         });
 #pragma unroll
@@ -447,12 +426,160 @@ __device__ __forceinline__ void select_top(TopShared& sh, int top, float mine, C
             best = best > w ? best : w;
         }
         __syncthreads();
-        if (lane == 0) sh.best[wave] = best;
+        if ((threadIdx.x & 63) == 0) sh.best[threadIdx.x >> 6] = best;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) best = best > sh.best[i] ? best : sh.best[i];
         if (threadIdx.x == 0) emit(j, best);
         below = best;
+    }
+}
+
+// The `top` largest elements of a segment (cn chunks from c0 on, chunk
+// u * 256 + thread in this thread, cm its largest element): emit(rank, key).
+//
+// A bound first: every full wave takes the m-th largest of its lanes' maxima,
+// m = ceil(top / full waves), and at least `top` elements reach the smallest of
+// these.  The elements above it are few: the chunks that hold any are read
+// again, an element a thread (looking through the registers' chunks took 190
+// registers), and ranked against each other.  If they are fewer than `top`, the
+// rest equals the bound and follows in the order of the ids, which is the order
+// of the chunks (constant rows, rows masked but for a few ids).  Where too many
+// lie above the bound, each rank is searched for.
+template <int DT, bool FL, int U, typename Emit>
+__device__ __forceinline__ void segment_top(TopShared& sh, int top, const Row<DT, FL>& z, int c0, int cn,
+                                            const float (&cm)[U], float mine, Emit emit) {
+    constexpr int EPC = kEpc<DT>;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int full = min(cn, kThreads) / 64;   // waves whose lanes all hold a chunk
+    float low = kNegInf;
+    if (wave < full) {
+        float v = mine;
+        for (int i = 0; i < (top + full - 1) / full; ++i) {
+            low = wmax(v);
+            const unsigned long long at = __ballot(v == low);
+            if (at != 0 && lane == __builtin_ctzll(at)) v = __builtin_nanf("");   // passed over from here on
+            if (at == 0) low = kNegInf;
+        }
+    }
+    __syncthreads();   // sh may still be read from the last use
+    if (lane == 0) sh.low[wave] = low;
+    if (threadIdx.x == 0) sh.count = sh.chunks = 0;
+    __syncthreads();
+    low = full > 0 ? sh.low[0] : kNegInf;
+    for (int w = 1; w < full; ++w) low = fminf(low, sh.low[w]);
+
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + threadIdx.x;
+        if (i < cn && cm[u] > low) {
+            const int at = atomicAdd(&sh.chunks, 1);
+            if (at < kChunkCand) sh.chunk[at] = i;
+        }
+    }
+    __syncthreads();
+    const int chunks = sh.chunks;
+    auto element = [&](int i, int e, auto f) {
+        const int v = z.first(c0 + i) + e;
+        if (v >= 0 && v < z.cols) f(z.load_elem(v), v);
+    };
+    if (chunks <= kChunkCand)
+        for (int j = threadIdx.x; j < chunks * EPC; j += kThreads)
+            element(sh.chunk[j / EPC], j % EPC, [&](float x, int v) {
+                if (!(x > low)) return;
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kCand) sh.cand[at] = rank_key(x, v);
+            });
+    __syncthreads();
+    const int n = sh.count;
+    if (chunks > kChunkCand || n > kCand) {
+        search_ranks(
+            sh, top,
+            [&](auto f) {
+                for (int j = threadIdx.x; j < cn * EPC; j += kThreads)
+                    element(j / EPC, j % EPC, [&](float x, int v) { f(rank_key(x, v)); });
+            },
+            emit);
+        return;
+    }
+    rank_candidates(sh, n, top, emit);
+    // NaN ranks with -inf
+    auto tie = [&](float x) { return x == low || (x != x && low == kNegInf); };
+    int at = n;   // ranks given so far
+    for (int b = 0; at < top && b < cn; b += kThreads) {
+        const int i = b + threadIdx.x;
+        int mine_ties = 0;
+        if (i < cn)
+            for (int e = 0; e < EPC; ++e) element(i, e, [&](float x, int) { mine_ties += tie(x) ? 1 : 0; });
+        int upto = mine_ties;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += v;
+        }
+        __syncthreads();
+        if (lane == 63) sh.ties[wave] = upto;
+        __syncthreads();
+        int rank = at + upto - mine_ties, all = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            rank += w < wave ? sh.ties[w] : 0;
+            all += sh.ties[w];
+        }
+        if (mine_ties > 0 && rank < top)
+            for (int e = 0; e < EPC; ++e)
+                element(i, e, [&](float x, int v) {
+                    if (tie(x) && rank < top) emit(rank++, rank_key(x, v));
+                });
+        at += all;
+    }
+    for (int j = at + threadIdx.x; j < top; j += kThreads) emit(j, 0);   // fewer elements than that
+}
+
+// The `top` largest of the keys a workgroup holds (0: none), all different.
+template <int U, typename Emit>
+__device__ __forceinline__ void keys_top(TopShared& sh, int top, const uint64_t (&key)[U], Emit emit) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t v = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v = v > key[u] ? v : key[u];
+    const uint64_t mine = v;
+    uint64_t low = 0;
+    for (int i = 0; i < (top + 3) / 4; ++i) {
+        low = v;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const uint64_t w = __shfl_xor((unsigned long long)low, o, 64);
+            low = low > w ? low : w;
+        }
+        if (v == low) v = 0;
+    }
+    __syncthreads();   // sh may still be read from the last use
+    if (lane == 0) sh.best[wave] = low;
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) low = low < sh.best[w] ? low : sh.best[w];
+    if (mine >= low)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (key[u] >= low && key[u] != 0) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kCand) sh.cand[at] = key[u];
+            }
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kCand) {
+        rank_candidates(sh, n, top, emit);
+        for (int j = n + threadIdx.x; j < top; j += kThreads) emit(j, 0);
+    } else {
+        search_ranks(
+            sh, top,
+            [&](auto f) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) f(key[u]);
+            },
+            emit);
     }
 }
 
@@ -463,13 +590,15 @@ __device__ __forceinline__ void put_logprobs(const LogitsArgs& a, int64_t row, i
     if (a.entropy) a.entropy[row] = st.s == st.s ? entropy_of(st, a.inv_temp) : st.s;
     put_lse(a, row, l);
 }
+template <int NT>
 __device__ __forceinline__ void skip_logprobs(const LogitsArgs& a, int64_t row) {
-    if (threadIdx.x == 0) {
+    const int tid = threadIdx.x % NT;
+    if (tid == 0) {
         if (a.logp) a.logp[row] = 0.f;
         if (a.entropy) a.entropy[row] = 0.f;
         put_lse(a, row, {0.f, 0.f});
     }
-    for (int j = threadIdx.x; j < a.top; j += kThreads) {
+    for (int j = tid; j < a.top; j += NT) {
         a.top_idx[row * a.top + j] = -1;
         a.top_logp[row * a.top + j] = kNegInf;
     }
@@ -500,7 +629,7 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const LogitsArgs a) {
     } else {
         if (a.tokens) tok = load_id(a.tokens, a.idx64, row, a.cols);
         if (tok < 0) {
-            if (alone) skip_logprobs(a, row);
+            if (alone) skip_logprobs<kThreads>(a, row);
             return;
         }
     }
@@ -522,57 +651,32 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const LogitsArgs a) {
     if (!alone && threadIdx.x == 0) a.part[row * a.plan.segs + seg] = {st.m, st.s, st.e, 0.f};
     const Lse l = make_lse(st, a.inv_temp);
     if constexpr (KIND == 0) {
-        if (alone) distill_loss<DT, FL>(a, row, l);
+        if (alone) distill_loss<DT, FL, kThreads>(a, row, l);
     } else {
         if (alone && threadIdx.x == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
         if constexpr (KIND == 2) {
             __shared__ TopShared sh;
-            // the few chunks that reach the bound are read again, an element a
-            // thread (looking through the registers' chunks took 190 registers)
-            auto chunk_elem = [&](int i, int e, auto f) {
-                const int v = z.first(c0 + i) + e;
-                if (v >= 0 && v < a.cols) f(z.load_elem(v), v);
-            };
-            select_top(
-                sh, a.top, mine,
-                [&](float low, auto add) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int i = u * kThreads + threadIdx.x;
-                        if (i < cn && cm[u] >= low) {
-                            const int at = atomicAdd(&sh.chunks, 1);
-                            if (at < kChunkCand) sh.chunk[at] = i;
-                        }
-                    }
-                    __syncthreads();
-                    const int n = sh.chunks;
-                    if (n > kChunkCand) return false;
-                    for (int j = threadIdx.x; j < n * kEpc<DT>; j += kThreads)
-                        chunk_elem(sh.chunk[j / kEpc<DT>], j % kEpc<DT>, add);
-                    return true;
-                },
-                [&](auto f) {
-                    for (int j = threadIdx.x; j < cn * kEpc<DT>; j += kThreads)
-                        chunk_elem(j / kEpc<DT>, j % kEpc<DT>, f);
-                },
-                [&](int rank, uint64_t key) {
-                    if (alone) put_alternative(a, row, l, rank, key);
-                    else a.keys[(row * a.plan.segs + seg) * a.top + rank] = key;
-                });
+            segment_top<DT, FL, U>(sh, a.top, z, c0, cn, cm, mine, [&](int rank, uint64_t key) {
+                if (alone) put_alternative(a, row, l, rank, key);
+                else a.keys[(row * a.plan.segs + seg) * a.top + rank] = key;
+            });
         }
     }
 }
 
-// Joins the segments of a row (one workgroup).
+// Joins the segments of a row: one workgroup, or (WAVE) one wave where a wave
+// holds all keys or entries.
 constexpr int kMergeKeys = 8;   // keys a thread holds
-template <int DT, int KIND, bool FL>
+template <int DT, int KIND, bool FL, bool WAVE>
 __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
-    __shared__ Stats all;
-    const int64_t row = blockIdx.x;
+    constexpr int NT = WAVE ? 64 : kThreads;
+    const int lane = threadIdx.x & 63;
+    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (row >= a.rows) return;
     int tok = 0;
     if constexpr (KIND == 0) {
         if (a.weight && a.weight[row] == 0.f) {
-            if (threadIdx.x == 0) {
+            if (threadIdx.x % NT == 0) {
                 a.loss[row] = 0.f;
                 put_lse(a, row, {0.f, 0.f});
             }
@@ -581,70 +685,60 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
     } else {
         if (a.tokens) tok = load_id(a.tokens, a.idx64, row, a.cols);
         if (tok < 0) {
-            skip_logprobs(a, row);
+            skip_logprobs<NT>(a, row);
             return;
         }
     }
     const float c = a.inv_temp * kLog2e;
-    if (threadIdx.x < 64) {
-        Stats st = kEmpty;
-        for (int i = threadIdx.x; i < a.plan.segs; i += 64) {
-            const SegStats p = a.part[row * a.plan.segs + i];
-            st = join(st, Stats{p.m, p.s, p.e}, c);
-        }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-            // the same order in every lane, so that all have the same result
-            const Stats b = {__shfl_xor(st.m, o, 64), __shfl_xor(st.s, o, 64), __shfl_xor(st.e, o, 64)};
-            st = (threadIdx.x & o) ? join(b, st, c) : join(st, b, c);
-        }
-        if (threadIdx.x == 0) all = st;
+    // every wave joins them all, in the same order
+    Stats st = kEmpty;
+    for (int i = lane; i < a.plan.segs; i += 64) {
+        const SegStats p = a.part[row * a.plan.segs + i];
+        st = join(st, Stats{p.m, p.s, p.e}, c);
     }
-    __syncthreads();
-    const Stats st = all;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        const Stats b = {__shfl_xor(st.m, o, 64), __shfl_xor(st.s, o, 64), __shfl_xor(st.e, o, 64)};
+        st = (lane & o) ? join(b, st, c) : join(st, b, c);
+    }
     const Lse l = make_lse(st, a.inv_temp);
     if constexpr (KIND == 0) {
-        distill_loss<DT, FL>(a, row, l);
+        distill_loss<DT, FL, NT>(a, row, l);
     } else {
-        if (threadIdx.x == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
+        if (threadIdx.x % NT == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
         if constexpr (KIND == 2) {
-            __shared__ TopShared sh;
-            __shared__ uint64_t carry[kMaxTop];
-            // batches of keys, the best so far among the next
             const int64_t n = (int64_t)a.plan.segs * a.top;
             const uint64_t* keys = a.keys + row * n;
-            const int batch = kThreads * kMergeKeys - a.top;
-            for (int64_t b = 0; b < n; b += batch) {
-                uint64_t key[kMergeKeys];
-                float mine = kNegInf;
-#pragma unroll
-                for (int u = 0; u < kMergeKeys; ++u) {
-                    const int i = u * kThreads + threadIdx.x;   // the first `top` are the best so far
-                    key[u] = i < a.top ? (b > 0 ? carry[i] : 0)
-                                       : (i - a.top < batch && b + i - a.top < n ? keys[b + i - a.top] : 0);
-                    if (key[u] != 0) mine = fmaxf(mine, key_value(key[u]));
+            if constexpr (WAVE) {   // a key a lane
+                const uint64_t key = lane < n ? keys[lane] : 0;
+                int rank = 0;
+                for (int j = 0; j < (int)n; ++j) {
+                    const uint64_t o = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, j) |
+                                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), j) << 32;
+                    rank += o > key ? 1 : 0;
                 }
-                const bool last = b + batch >= n;
-                __syncthreads();
-                select_top(
-                    sh, a.top, mine,
-                    [&](float low, auto add) {
-                        if (mine >= low)
+                if (key != 0 && rank < a.top) put_alternative(a, row, l, rank, key);
+            } else {
+                __shared__ TopShared sh;
+                __shared__ uint64_t carry[kMaxTop];
+                // batches of keys, the best so far among the next
+                const int batch = kThreads * kMergeKeys - a.top;
+                for (int64_t b = 0; b < n; b += batch) {
+                    uint64_t key[kMergeKeys];
 #pragma unroll
-                            for (int u = 0; u < kMergeKeys; ++u)
-                                if (key[u] != 0) add(key_value(key[u]), key_id(key[u]));
-                        return true;
-                    },
-                    [&](auto f) {
-#pragma unroll
-                        for (int u = 0; u < kMergeKeys; ++u)
-                            if (key[u] != 0) f(key_value(key[u]), key_id(key[u]));
-                    },
-                    [&](int rank, uint64_t k) {
+                    for (int u = 0; u < kMergeKeys; ++u) {
+                        const int i = u * kThreads + threadIdx.x;   // the first `top` are the best so far
+                        key[u] = i < a.top ? (b > 0 ? carry[i] : 0)
+                                           : (i - a.top < batch && b + i - a.top < n ? keys[b + i - a.top] : 0);
+                    }
+                    const bool last = b + batch >= n;
+                    __syncthreads();
+                    keys_top(sh, a.top, key, [&](int rank, uint64_t k) {
                         if (last) put_alternative(a, row, l, rank, k);
                         else carry[rank] = k;
                     });
-                __syncthreads();
+                    __syncthreads();
+                }
             }
         }
     }
@@ -926,7 +1020,9 @@ hipError_t forward_fl(const LogitsArgs& a, hipStream_t s) {
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.plan.segs == 1) return e;
-    hipLaunchKernelGGL((merge_kernel<DT, KIND, FL>), dim3(a.rows), block, 0, s, a);
+    const bool wave = KIND == 0 ? a.k <= 64 : KIND == 1 || (int64_t)a.plan.segs * a.top <= 64;
+    if (wave) hipLaunchKernelGGL((merge_kernel<DT, KIND, FL, true>), dim3((uint32_t)cdiv(a.rows, 4)), block, 0, s, a);
+    else hipLaunchKernelGGL((merge_kernel<DT, KIND, FL, false>), dim3(a.rows), block, 0, s, a);
     return hipGetLastError();
 }
 
