@@ -86,102 +86,231 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
     return true;
 }
 
+// ---------------------------------------------------------------------------
+// Any operand (fp32; bf16 rows and widths that are not whole 16-byte chunks):
+// 128 x 128 tiles, four waves of 64 x 64 each, k in steps of 64 (bf16) or 32
+// (fp32).  The next step's chunks are loaded into registers while the present
+// one is multiplied from LDS, then stored in the other LDS buffer.  Loads and
+// stores are 16 bytes wide at any alignment of the element; chunks at the
+// operand's ends are moved element by element.  An operand stays in LDS in its
+// own order, as below for the larger tiles; fp32 products take four k at a time
+// (lane group g holds k = 4 g .. 4 g + 3 of eight, for both operands alike).
+// ---------------------------------------------------------------------------
 template <int DT> struct Io;
 template <> struct Io<0> {
     using T = unsigned short;
-    static constexpr int BK = 32;
+    static constexpr int EPC = 8, BK = 64, KLD = 64, ILD = 128;   // LDS row strides along k and along i
     __device__ static T cv(float f) { return f2bf(f); }
 };
 template <> struct Io<1> {
     using T = float;
-    static constexpr int BK = 16;
+    static constexpr int EPC = 4, BK = 32, KLD = 36, ILD = 132;
     __device__ static T cv(float f) { return f; }
 };
+struct __attribute__((packed, aligned(2))) Loose16 { u32x4 v; };   // 16 bytes at an element's alignment
+struct __attribute__((packed, aligned(2))) Loose8 { u32x2 v; };
 
-// C (64 x 64) += A (64 x k) B (k x 64) of one workgroup of four waves, each
-// 32 x 32.  Element (i, k) of A sits at A[i * ai + k * ak], (k, j) of B at
-// B[k * bk + j * bj]; elements past mi, kd or nj are zero.  Both panels are
-// kept in LDS along k.
-template <int DT>
-__device__ __forceinline__ void tile64(const typename Io<DT>::T* A, int64_t ai, int64_t ak,
-                                       const typename Io<DT>::T* B, int64_t bk, int64_t bj, int mi, int kd, int nj,
-                                       f32x16& acc) {
+// One operand of a tile: `side` rows (or columns) of the tile by kd.
+template <int DT, bool ALONG_K>
+struct Staged {
     using T = typename Io<DT>::T;
-    constexpr int BK = Io<DT>::BK;
-    constexpr int LD = BK + (DT == 0 ? 8 : 1);
-    __shared__ __attribute__((aligned(16))) T sA[64 * LD], sB[64 * LD];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int l32 = lane & 31, gl = lane >> 5, wm = wave >> 1, wn = wave & 1;
-    for (int k0 = 0; k0 < kd; k0 += BK) {
-        __syncthreads();
-        for (int p = tid; p < 64 * BK; p += 256) {
-            // consecutive threads along the operand's unit stride
-            const int i = ak == 1 ? p / BK : p % 64, k = ak == 1 ? p % BK : p / 64;
-            sA[i * LD + k] = (i < mi && k0 + k < kd) ? A[i * ai + (k0 + k) * ak] : T(0);
-            const int j = bk == 1 ? p / BK : p % 64, kb = bk == 1 ? p % BK : p / 64;
-            sB[j * LD + kb] = (j < nj && k0 + kb < kd) ? B[(k0 + kb) * bk + j * bj] : T(0);
-        }
-        __syncthreads();
-        if constexpr (DT == 0) {
+    static constexpr int EPC = Io<DT>::EPC, BK = Io<DT>::BK;
+    static constexpr int CPR = (ALONG_K ? BK : 128) / EPC;   // chunks of an LDS row
+    static constexpr int ROWS = 256 / CPR;                   // LDS rows 256 threads fill at a time
+    static constexpr int LD = ALONG_K ? Io<DT>::KLD : Io<DT>::ILD;
+    static constexpr int SIZE = (ALONG_K ? 128 : BK) * LD;   // elements of a buffer
+    static_assert(1024 % 256 == 0 && ROWS * 4 == (ALONG_K ? 128 : BK), "four chunks a thread");
+    const T* p;
+    int64_t ld;
+    int side, kd;
+
+    // chunk j of this thread at k0: row and first column of the stored matrix
+    // (a row of k elements, or a k row)
+    __device__ __forceinline__ void load(int k0, u32x4 (&r)[4]) const {
+        const int row0 = threadIdx.x / CPR, c = (threadIdx.x % CPR) * EPC;
+        const int rows = ALONG_K ? side : kd - k0, cols = ALONG_K ? kd - k0 : side;
+        const T* q = p + (ALONG_K ? (int64_t)k0 : k0 * ld) + c;
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-                const u32x4 av = *reinterpret_cast<const u32x4*>(&sA[(wm * 32 + l32) * LD + kk * 16 + gl * 8]);
-                const u32x4 bv = *reinterpret_cast<const u32x4*>(&sB[(wn * 32 + l32) * LD + kk * 16 + gl * 8]);
-                acc = mfma32w(av, bv, acc);
+        for (int j = 0; j < 4; ++j) {
+            const int row = row0 + j * ROWS;
+            const T* at = q + row * ld;
+            if (row < rows && c + EPC <= cols) {
+                r[j] = reinterpret_cast<const Loose16*>(at)->v;
+                continue;
             }
-        } else {
-#pragma unroll
-            for (int kk = 0; kk < BK / 2; ++kk)
-                acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sA[(wm * 32 + l32) * LD + kk * 2 + gl],
-                                                           sB[(wn * 32 + l32) * LD + kk * 2 + gl], acc, 0, 0, 0);
+            uint64_t w[2] = {0, 0};
+            if (row < rows)
+#pragma unroll 1
+                for (int e = 0; e < cols - c; ++e) {
+                    const uint64_t x = DT == 0 ? (uint64_t)reinterpret_cast<const unsigned short*>(at)[e]
+                                               : (uint64_t)reinterpret_cast<const unsigned*>(at)[e];
+                    const uint64_t y = x << (sizeof(T) * 8 * (e % (EPC / 2)));
+                    if (e < EPC / 2) w[0] |= y;
+                    else w[1] |= y;
+                }
+            r[j] = u32x4{(unsigned)w[0], (unsigned)(w[0] >> 32), (unsigned)w[1], (unsigned)(w[1] >> 32)};
         }
+    }
+    __device__ __forceinline__ static void put(T* s, const u32x4 (&r)[4]) {
+        const int row0 = threadIdx.x / CPR, ch = threadIdx.x % CPR;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = row0 + j * ROWS;
+            int place = ch;
+            if (DT == 0) place ^= ALONG_K ? (row >> 1) & 7 : 4 * (row & 3);
+            *reinterpret_cast<u32x4*>(&s[row * LD + place * EPC]) = r[j];
+        }
+    }
+    // operand of the 32-wide block `first`: bf16 16 k from kk * 16, fp32 8 k from kk * 8
+    __device__ __forceinline__ static u32x4 frag(const T* s, int first, int kk) {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+        if constexpr (DT == 0 && ALONG_K) {
+            const int r = first + l32;
+            return *reinterpret_cast<const u32x4*>(&s[r * LD + (((kk * 2 + gl) ^ ((r >> 1) & 7)) * 8)]);
+        } else if constexpr (DT == 0) {
+            const int i16 = lane & 15, k = kk * 16 + 8 * gl + (i16 >> 2);
+            const int col = first + 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
+            const T* q = &s[k * LD + (((col >> 3) ^ (4 * (k & 3))) * 8) + (col & 7)];
+            const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q));
+            const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q + 4 * LD));
+            return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else if constexpr (ALONG_K) {
+            return *reinterpret_cast<const u32x4*>(&s[(first + l32) * LD + kk * 8 + gl * 4]);
+        } else {
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(s[(kk * 8 + gl * 4 + e) * LD + first + l32]);
+            return v;
+        }
+    }
+};
+
+// C = A B of one tile (operands exchanged in the MFMA, so that a lane holds
+// runs of four columns of one row).
+template <int DT, bool AK, bool BKK>
+__device__ __forceinline__ void staged_tile(const Staged<DT, AK>& A, const Staged<DT, BKK>& B, typename Io<DT>::T* C,
+                                            int64_t ldc) {
+    using T = typename Io<DT>::T;
+    constexpr int BK = Io<DT>::BK, SUB = DT == 0 ? 16 : 8;
+    __shared__ __attribute__((aligned(16))) T sa[2][Staged<DT, AK>::SIZE], sb[2][Staged<DT, BKK>::SIZE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l32 = lane & 31, gl = lane >> 5, wm = wave >> 1, wn = wave & 1;
+    const bool work = wm * 64 < A.side && wn * 64 < B.side;
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    if (A.kd > 0) {
+        u32x4 ra[4], rb[4];
+        A.load(0, ra);
+        B.load(0, rb);
+        Staged<DT, AK>::put(sa[0], ra);
+        Staged<DT, BKK>::put(sb[0], rb);
+        __syncthreads();
+        for (int k0 = 0, cur = 0; k0 < A.kd; k0 += BK, cur ^= 1) {
+            const bool more = k0 + BK < A.kd;
+            if (more) {
+                A.load(k0 + BK, ra);
+                B.load(k0 + BK, rb);
+            }
+            if (work) {
+#pragma unroll
+                for (int kk = 0; kk < BK / SUB; ++kk) {
+                    u32x4 av[2], bv[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) av[i] = Staged<DT, AK>::frag(sa[cur], wm * 64 + i * 32, kk);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) bv[j] = Staged<DT, BKK>::frag(sb[cur], wn * 64 + j * 32, kk);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if constexpr (DT == 0) {
+                                acc[i][j] = mfma32w(bv[j], av[i], acc[i][j]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                        __uint_as_float(bv[j][e]), __uint_as_float(av[i][e]), acc[i][j], 0, 0, 0);
+                            }
+                        }
+                }
+            }
+            if (more) {
+                Staged<DT, AK>::put(sa[cur ^ 1], ra);
+                Staged<DT, BKK>::put(sb[cur ^ 1], rb);
+            }
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = wm * 64 + i * 32 + l32;
+        if (row >= A.side) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int col = wn * 64 + j * 32 + m * 8 + gl * 4;
+                T* at = C + row * ldc + col;
+                if (col + 4 <= B.side) {
+                    if constexpr (DT == 0) {
+                        const Loose8 v = {u32x2{pack2(acc[i][j][4 * m], acc[i][j][4 * m + 1]),
+                                                pack2(acc[i][j][4 * m + 2], acc[i][j][4 * m + 3])}};
+                        *reinterpret_cast<Loose8*>(at) = v;
+                    } else {
+                        Loose16 v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v.v[e] = __float_as_uint(acc[i][j][4 * m + e]);
+                        *reinterpret_cast<Loose16*>(at) = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < B.side) at[e] = Io<DT>::cv(acc[i][j][4 * m + e]);
+                }
+            }
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void store64(typename Io<DT>::T* C, int64_t ld, int mi, int nj, const f32x16& acc) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int l32 = lane & 31, gl = lane >> 5, wm = wave >> 1, wn = wave & 1;
-    const int j = wn * 32 + l32;
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-        const int i = wm * 32 + (q >> 2) * 8 + gl * 4 + (q & 3);
-        if (i < mi && j < nj) C[(int64_t)i * ld + j] = Io<DT>::cv(acc[q]);
-    }
-}
+constexpr int kStagedEdge = 128;
 
 template <int DT, bool WT>
-__global__ __launch_bounds__(256) void grouped_mm_kernel(const GroupedArgs a) {
+__global__ __launch_bounds__(256) void grouped_mm_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
     GroupTile t;
-    if (!find_tile(a, 64, (a.ndim + 63) / 64, t)) return;
-    const int m0 = t.row0 + t.mt * 64, n0 = t.nt * 64;
-    const int mi = min(64, t.row0 + t.rows - m0), nj = min(64, a.ndim - n0);
-    f32x16 acc{};
+    if (!find_tile(a, kStagedEdge, (a.ndim + kStagedEdge - 1) / kStagedEdge, t)) return;
+    const int64_t m0 = (int64_t)t.row0 + t.mt * kStagedEdge;
+    const int n0 = t.nt * kStagedEdge;
+    Staged<DT, true> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
+                       min(kStagedEdge, t.rows - t.mt * kStagedEdge), a.kdim};
+    Staged<DT, WT> B{nullptr, 0, min(kStagedEdge, a.ndim - n0), a.kdim};
     if (t.e < a.n) {
-        const T* W = reinterpret_cast<const T*>(a.w[t.e]);
-        const int64_t ld = a.w_ld[t.e];
-        tile64<DT>(reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld, 1, WT ? W + n0 * ld : W + n0, WT ? 1 : ld,
-                   WT ? ld : 1, mi, a.kdim, nj, acc);
+        B.ld = a.w_ld[t.e];
+        B.p = reinterpret_cast<const T*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
+    } else {
+        A.kd = B.kd = 0;   // rows of no expert: zeros
     }
-    store64<DT>(reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, mi, nj, acc);
+    staged_tile<DT, true, WT>(A, B, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
 }
 
 template <int DT>
-__global__ __launch_bounds__(256) void grouped_wgrad_kernel(const GroupedArgs a) {
+__global__ __launch_bounds__(256) void grouped_wgrad_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
-    const int ntk = (a.kdim + 63) / 64, ntn = (a.ndim + 63) / 64;
-    if ((int)blockIdx.x >= a.n * ntk * ntn) return;
-    const int e = blockIdx.x / (ntk * ntn), b = blockIdx.x % (ntk * ntn);
-    const int i0 = (b % ntk) * 64, j0 = (b / ntk) * 64;
+    const int ntk = (a.kdim + kStagedEdge - 1) / kStagedEdge, ntn = (a.ndim + kStagedEdge - 1) / kStagedEdge;
+    const int total = a.n * ntk * ntn, per = (total + 7) / 8;
+    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+    const int e = id / (ntk * ntn), b = id % (ntk * ntn);
+    const int i0 = (b % ntk) * kStagedEdge, j0 = (b / ntk) * kStagedEdge;
     int lo, hi;
     slot_rows(a, e, lo, hi);
-    const int mi = min(64, a.kdim - i0), nj = min(64, a.ndim - j0);
-    f32x16 acc{};
-    if (hi > lo)
-        tile64<DT>(reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, 1, a.x_ld,
-                   reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, 1, mi, hi - lo, nj, acc);
-    store64<DT>(reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], mi, nj, acc);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    const int kd = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
+    const Staged<DT, false> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(kStagedEdge, a.kdim - i0), kd};
+    const Staged<DT, false> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(kStagedEdge, a.ndim - j0), kd};
+    staged_tile<DT, false, false>(A, B, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
 }
 
 // ---------------------------------------------------------------------------
@@ -723,7 +852,7 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int tile_edge(const GroupedArgs& a) { return a.dtype == 0 && a.vec ? kBig : 64; }
+int tile_edge(const GroupedArgs& a) { return a.dtype == 0 && a.vec ? kBig : kStagedEdge; }
 
 }  // namespace
 
@@ -753,11 +882,11 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
         if (trans_w) hipLaunchKernelGGL((grouped_big<1>), big, dim3(512), 0, s, a, (int)tiles);
         else hipLaunchKernelGGL((grouped_big<0>), big, dim3(512), 0, s, a, (int)tiles);
     } else if (a.dtype == 0) {
-        if (trans_w) hipLaunchKernelGGL((grouped_mm_kernel<0, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((grouped_mm_kernel<0, false>), grid, dim3(256), 0, s, a);
+        if (trans_w) hipLaunchKernelGGL((grouped_mm_staged<0, true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((grouped_mm_staged<0, false>), grid, dim3(256), 0, s, a);
     } else {
-        if (trans_w) hipLaunchKernelGGL((grouped_mm_kernel<1, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((grouped_mm_kernel<1, false>), grid, dim3(256), 0, s, a);
+        if (trans_w) hipLaunchKernelGGL((grouped_mm_staged<1, true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((grouped_mm_staged<1, false>), grid, dim3(256), 0, s, a);
     }
     return hipGetLastError();
 }
@@ -766,8 +895,8 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
     const int64_t tiles = grouped_wgrad_grid(a);
     const dim3 grid((uint32_t)tiles);
     if (a.dtype == 0 && a.vec) hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
-    else if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_kernel<0>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grouped_wgrad_kernel<1>), grid, dim3(256), 0, s, a);
+    else if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_staged<0>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grouped_wgrad_staged<1>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
