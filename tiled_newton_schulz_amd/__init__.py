@@ -467,19 +467,37 @@ def _rows(t) -> himuon_matrix_t:
     return himuon_matrix_t(t.data_ptr() if H else None, H, W, s0 if H > 1 else max(W, 1))
 
 
-@contextlib.contextmanager
-def _placed(device, stream):
+class _placed:
     """The device and stream of a call, set for the tensors allocated in it, so
-    that their memory belongs to the stream that uses it; yields the handle."""
-    import torch
-    with torch.cuda.device(device):
+    that their memory belongs to the stream that uses it; yields the stream's
+    handle.  Where both are the current ones nothing is set (setting them costs
+    more host time than the rest of a small call)."""
+    __slots__ = ("device", "stream", "set")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.set = device, stream, None
+
+    def __enter__(self):
+        import torch
+        index = self.device.index
+        if self.stream is None and index == torch.cuda.current_device():
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream()'s time
+            return ctypes.c_void_p(raw(index) if raw else torch.cuda.current_stream(index).cuda_stream)
+        self.set = contextlib.ExitStack()
+        self.set.enter_context(torch.cuda.device(self.device))
+        stream = self.stream
         if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            stream = torch.cuda.current_stream()
         else:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            self.set.enter_context(torch.cuda.stream(stream))
+        return ctypes.c_void_p(stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.set is not None:
+            self.set.close()
+        return False
 
 
 def _ends(ends, n, device):

@@ -88,8 +88,8 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
 
 // ---------------------------------------------------------------------------
 // Any operand (fp32; bf16 rows and widths that are not whole 16-byte chunks):
-// 128 x 128 tiles, four waves of 64 x 64 each, k in steps of 64 (bf16) or 32
-// (fp32).  The next step's chunks are loaded into registers while the present
+// tiles of 128 x 128 (four waves of 64 x 64 each) or, where those would leave
+// CUs idle, 64 x 64, k in steps of 64 (bf16) or 32 (fp32).  The next step's chunks are loaded into registers while the present
 // one is multiplied from LDS, then stored in the other LDS buffer.  Loads and
 // stores are 16 bytes wide at any alignment of the element; chunks at the
 // operand's ends are moved element by element.  An operand stays in LDS in its
@@ -99,39 +99,43 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
 template <int DT> struct Io;
 template <> struct Io<0> {
     using T = unsigned short;
-    static constexpr int EPC = 8, BK = 64, KLD = 64, ILD = 128;   // LDS row strides along k and along i
+    static constexpr int EPC = 8, BK = 64, KLD = 64, IPAD = 0;   // LDS row stride along k, padding along i
     __device__ static T cv(float f) { return f2bf(f); }
 };
 template <> struct Io<1> {
     using T = float;
-    static constexpr int EPC = 4, BK = 32, KLD = 36, ILD = 132;
+    static constexpr int EPC = 4, BK = 32, KLD = 36, IPAD = 4;
     __device__ static T cv(float f) { return f; }
 };
 struct __attribute__((packed, aligned(2))) Loose16 { u32x4 v; };   // 16 bytes at an element's alignment
 struct __attribute__((packed, aligned(2))) Loose8 { u32x2 v; };
 
 // One operand of a tile: `side` rows (or columns) of the tile by kd.
-template <int DT, bool ALONG_K>
+template <int DT, bool ALONG_K, int EDGE>
 struct Staged {
     using T = typename Io<DT>::T;
     static constexpr int EPC = Io<DT>::EPC, BK = Io<DT>::BK;
-    static constexpr int CPR = (ALONG_K ? BK : 128) / EPC;   // chunks of an LDS row
-    static constexpr int ROWS = 256 / CPR;                   // LDS rows 256 threads fill at a time
-    static constexpr int LD = ALONG_K ? Io<DT>::KLD : Io<DT>::ILD;
-    static constexpr int SIZE = (ALONG_K ? 128 : BK) * LD;   // elements of a buffer
-    static_assert(1024 % 256 == 0 && ROWS * 4 == (ALONG_K ? 128 : BK), "four chunks a thread");
+    static constexpr int CPR = (ALONG_K ? BK : EDGE) / EPC;   // chunks of an LDS row
+    static constexpr int ROWS = 256 / CPR;                    // LDS rows 256 threads fill at a time
+    static constexpr int NCH = EDGE * BK / EPC / 256;         // chunks of a thread
+    static constexpr int LD = ALONG_K ? Io<DT>::KLD : EDGE + Io<DT>::IPAD;
+    static constexpr int SIZE = (ALONG_K ? EDGE : BK) * LD;   // elements of a buffer
+    static_assert(ROWS * NCH == (ALONG_K ? EDGE : BK), "the chunks cover the panel");
     const T* p;
     int64_t ld;
     int side, kd;
 
+    // bf16 along i: place of chunk c of k row k is c ^ swap(k), so that the four
+    // rows and 32 columns that are read together lie on different banks
+    __device__ __forceinline__ static int swap(int k) { return EDGE == 128 ? 4 * (k & 3) : 2 * (k & 2); }
     // chunk j of this thread at k0: row and first column of the stored matrix
     // (a row of k elements, or a k row)
-    __device__ __forceinline__ void load(int k0, u32x4 (&r)[4]) const {
+    __device__ __forceinline__ void load(int k0, u32x4 (&r)[NCH]) const {
         const int row0 = threadIdx.x / CPR, c = (threadIdx.x % CPR) * EPC;
         const int rows = ALONG_K ? side : kd - k0, cols = ALONG_K ? kd - k0 : side;
         const T* q = p + (ALONG_K ? (int64_t)k0 : k0 * ld) + c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < NCH; ++j) {
             const int row = row0 + j * ROWS;
             const T* at = q + row * ld;
             if (row < rows && c + EPC <= cols) {
@@ -151,13 +155,13 @@ struct Staged {
             r[j] = u32x4{(unsigned)w[0], (unsigned)(w[0] >> 32), (unsigned)w[1], (unsigned)(w[1] >> 32)};
         }
     }
-    __device__ __forceinline__ static void put(T* s, const u32x4 (&r)[4]) {
+    __device__ __forceinline__ static void put(T* s, const u32x4 (&r)[NCH]) {
         const int row0 = threadIdx.x / CPR, ch = threadIdx.x % CPR;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < NCH; ++j) {
             const int row = row0 + j * ROWS;
             int place = ch;
-            if (DT == 0) place ^= ALONG_K ? (row >> 1) & 7 : 4 * (row & 3);
+            if (DT == 0) place ^= ALONG_K ? (row >> 1) & 7 : swap(row);
             *reinterpret_cast<u32x4*>(&s[row * LD + place * EPC]) = r[j];
         }
     }
@@ -170,7 +174,7 @@ struct Staged {
         } else if constexpr (DT == 0) {
             const int i16 = lane & 15, k = kk * 16 + 8 * gl + (i16 >> 2);
             const int col = first + 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
-            const T* q = &s[k * LD + (((col >> 3) ^ (4 * (k & 3))) * 8) + (col & 7)];
+            const T* q = &s[k * LD + (((col >> 3) ^ swap(k)) * 8) + (col & 7)];
             const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q));
             const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q + 4 * LD));
             return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -187,26 +191,27 @@ struct Staged {
 
 // C = A B of one tile (operands exchanged in the MFMA, so that a lane holds
 // runs of four columns of one row).
-template <int DT, bool AK, bool BKK>
-__device__ __forceinline__ void staged_tile(const Staged<DT, AK>& A, const Staged<DT, BKK>& B, typename Io<DT>::T* C,
-                                            int64_t ldc) {
+template <int DT, bool AK, bool BKK, int EDGE>
+__device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE>& B,
+                                            typename Io<DT>::T* C, int64_t ldc) {
     using T = typename Io<DT>::T;
+    constexpr int WE = EDGE / 2, F = WE / 32;   // edge of a wave's part, in 32-wide blocks
     constexpr int BK = Io<DT>::BK, SUB = DT == 0 ? 16 : 8;
-    __shared__ __attribute__((aligned(16))) T sa[2][Staged<DT, AK>::SIZE], sb[2][Staged<DT, BKK>::SIZE];
+    __shared__ __attribute__((aligned(16))) T sa[2][Staged<DT, AK, EDGE>::SIZE], sb[2][Staged<DT, BKK, EDGE>::SIZE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, gl = lane >> 5, wm = wave >> 1, wn = wave & 1;
-    const bool work = wm * 64 < A.side && wn * 64 < B.side;
-    f32x16 acc[2][2];
+    const bool work = wm * WE < A.side && wn * WE < B.side;
+    f32x16 acc[F][F];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+        for (int j = 0; j < F; ++j) acc[i][j] = f32x16{};
     if (A.kd > 0) {
-        u32x4 ra[4], rb[4];
+        u32x4 ra[Staged<DT, AK, EDGE>::NCH], rb[Staged<DT, BKK, EDGE>::NCH];
         A.load(0, ra);
         B.load(0, rb);
-        Staged<DT, AK>::put(sa[0], ra);
-        Staged<DT, BKK>::put(sb[0], rb);
+        Staged<DT, AK, EDGE>::put(sa[0], ra);
+        Staged<DT, BKK, EDGE>::put(sb[0], rb);
         __syncthreads();
         for (int k0 = 0, cur = 0; k0 < A.kd; k0 += BK, cur ^= 1) {
             const bool more = k0 + BK < A.kd;
@@ -217,15 +222,15 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK>& A, const Stage
             if (work) {
 #pragma unroll
                 for (int kk = 0; kk < BK / SUB; ++kk) {
-                    u32x4 av[2], bv[2];
+                    u32x4 av[F], bv[F];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) av[i] = Staged<DT, AK>::frag(sa[cur], wm * 64 + i * 32, kk);
+                    for (int i = 0; i < F; ++i) av[i] = Staged<DT, AK, EDGE>::frag(sa[cur], wm * WE + i * 32, kk);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) bv[j] = Staged<DT, BKK>::frag(sb[cur], wn * 64 + j * 32, kk);
+                    for (int j = 0; j < F; ++j) bv[j] = Staged<DT, BKK, EDGE>::frag(sb[cur], wn * WE + j * 32, kk);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < F; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < F; ++j) {
                             if constexpr (DT == 0) {
                                 acc[i][j] = mfma32w(bv[j], av[i], acc[i][j]);
                             } else {
@@ -238,21 +243,21 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK>& A, const Stage
                 }
             }
             if (more) {
-                Staged<DT, AK>::put(sa[cur ^ 1], ra);
-                Staged<DT, BKK>::put(sb[cur ^ 1], rb);
+                Staged<DT, AK, EDGE>::put(sa[cur ^ 1], ra);
+                Staged<DT, BKK, EDGE>::put(sb[cur ^ 1], rb);
             }
             __syncthreads();
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = wm * 64 + i * 32 + l32;
+    for (int i = 0; i < F; ++i) {
+        const int row = wm * WE + i * 32 + l32;
         if (row >= A.side) continue;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < F; ++j)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const int col = wn * 64 + j * 32 + m * 8 + gl * 4;
+                const int col = wn * WE + j * 32 + m * 8 + gl * 4;
                 T* at = C + row * ldc + col;
                 if (col + 4 <= B.side) {
                     if constexpr (DT == 0) {
@@ -274,43 +279,41 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK>& A, const Stage
     }
 }
 
-constexpr int kStagedEdge = 128;
-
-template <int DT, bool WT>
+template <int DT, bool WT, int EDGE>
 __global__ __launch_bounds__(256) void grouped_mm_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
     GroupTile t;
-    if (!find_tile(a, kStagedEdge, (a.ndim + kStagedEdge - 1) / kStagedEdge, t)) return;
-    const int64_t m0 = (int64_t)t.row0 + t.mt * kStagedEdge;
-    const int n0 = t.nt * kStagedEdge;
-    Staged<DT, true> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
-                       min(kStagedEdge, t.rows - t.mt * kStagedEdge), a.kdim};
-    Staged<DT, WT> B{nullptr, 0, min(kStagedEdge, a.ndim - n0), a.kdim};
+    if (!find_tile(a, EDGE, (a.ndim + EDGE - 1) / EDGE, t)) return;
+    const int64_t m0 = (int64_t)t.row0 + t.mt * EDGE;
+    const int n0 = t.nt * EDGE;
+    Staged<DT, true, EDGE> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
+                       min(EDGE, t.rows - t.mt * EDGE), a.kdim};
+    Staged<DT, WT, EDGE> B{nullptr, 0, min(EDGE, a.ndim - n0), a.kdim};
     if (t.e < a.n) {
         B.ld = a.w_ld[t.e];
         B.p = reinterpret_cast<const T*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
     } else {
         A.kd = B.kd = 0;   // rows of no expert: zeros
     }
-    staged_tile<DT, true, WT>(A, B, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
+    staged_tile<DT, true, WT, EDGE>(A, B, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
 }
 
-template <int DT>
+template <int DT, int EDGE>
 __global__ __launch_bounds__(256) void grouped_wgrad_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
-    const int ntk = (a.kdim + kStagedEdge - 1) / kStagedEdge, ntn = (a.ndim + kStagedEdge - 1) / kStagedEdge;
+    const int ntk = (a.kdim + EDGE - 1) / EDGE, ntn = (a.ndim + EDGE - 1) / EDGE;
     const int total = a.n * ntk * ntn, per = (total + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
     const int e = id / (ntk * ntn), b = id % (ntk * ntn);
-    const int i0 = (b % ntk) * kStagedEdge, j0 = (b / ntk) * kStagedEdge;
+    const int i0 = (b % ntk) * EDGE, j0 = (b / ntk) * EDGE;
     int lo, hi;
     slot_rows(a, e, lo, hi);
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int kd = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
-    const Staged<DT, false> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(kStagedEdge, a.kdim - i0), kd};
-    const Staged<DT, false> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(kStagedEdge, a.ndim - j0), kd};
-    staged_tile<DT, false, false>(A, B, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
+    const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(EDGE, a.kdim - i0), kd};
+    const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(EDGE, a.ndim - j0), kd};
+    staged_tile<DT, false, false, EDGE>(A, B, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
 }
 
 // ---------------------------------------------------------------------------
@@ -852,51 +855,76 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int tile_edge(const GroupedArgs& a) { return a.dtype == 0 && a.vec ? kBig : kStagedEdge; }
+int device_cus_or_256() {
+    static const int cus = [] { const int c = device_cus(); return c >= 8 ? std::min(c, 512) : 256; }();
+    return cus;
+}
+
+int64_t mm_tiles(const GroupedArgs& a, int edge) {
+    // every slot ends in at most one partial row tile
+    return (a.rows / edge + a.n + 1) * cdiv(a.ndim, edge);
+}
+int64_t wgrad_tiles(const GroupedArgs& a, int edge) { return cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n; }
+
+// Tile edge: 256 where the fast kernel runs.  Else 128, or 64 where tiles of 128
+// do not fill the chip.  (Rows that no expert has are counted as if it had
+// some: the host does not know.)
+int mm_edge(const GroupedArgs& a) {
+    if (a.dtype == 0 && a.vec) return kBig;
+    return mm_tiles(a, 128) < device_cus_or_256() ? 64 : 128;
+}
+int wgrad_edge(const GroupedArgs& a) {
+    if (a.dtype == 0 && a.vec) return kBig;
+    return wgrad_tiles(a, 128) < device_cus_or_256() ? 64 : 128;
+}
 
 }  // namespace
 
-int64_t grouped_mm_grid(const GroupedArgs& a) {
-    // every slot ends in at most one partial row tile
-    const int edge = tile_edge(a);
-    const int64_t row_tiles = a.rows / edge + a.n + 1;
-    return cdiv(row_tiles * cdiv(a.ndim, edge), 8) * 8;
-}
-
-int64_t grouped_wgrad_grid(const GroupedArgs& a) {
-    const int edge = tile_edge(a);
-    return cdiv(cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n, 8) * 8;
-}
+int64_t grouped_mm_grid(const GroupedArgs& a) { return cdiv(mm_tiles(a, mm_edge(a)), 8) * 8; }
+int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, wgrad_edge(a)), 8) * 8; }
 
 // Workgroups of the 256 x 256 kernel for at most `tiles` tiles: one fits a CU.
-static uint32_t big_grid(int64_t tiles) {
-    static const int cus = [] { const int c = device_cus(); return c >= 8 ? std::min(c, 512) : 256; }();
-    return (uint32_t)std::min<int64_t>(tiles, cus / 8 * 8);
+static uint32_t big_grid(int64_t tiles) { return (uint32_t)std::min<int64_t>(tiles, device_cus_or_256() / 8 * 8); }
+
+template <int DT, bool WT>
+static void mm_staged(const GroupedArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)grouped_mm_grid(a));
+    if (mm_edge(a) == 64) hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 64>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 128>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
-    const int64_t tiles = grouped_mm_grid(a);
-    const dim3 grid((uint32_t)tiles);
     if (a.dtype == 0 && a.vec) {
-        const dim3 big(big_grid(tiles));
-        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), big, dim3(512), 0, s, a, (int)tiles);
-        else hipLaunchKernelGGL((grouped_big<0>), big, dim3(512), 0, s, a, (int)tiles);
+        const int64_t tiles = grouped_mm_grid(a);
+        const dim3 grid(big_grid(tiles));
+        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), grid, dim3(512), 0, s, a, (int)tiles);
+        else hipLaunchKernelGGL((grouped_big<0>), grid, dim3(512), 0, s, a, (int)tiles);
     } else if (a.dtype == 0) {
-        if (trans_w) hipLaunchKernelGGL((grouped_mm_staged<0, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((grouped_mm_staged<0, false>), grid, dim3(256), 0, s, a);
+        if (trans_w) mm_staged<0, true>(a, s);
+        else mm_staged<0, false>(a, s);
     } else {
-        if (trans_w) hipLaunchKernelGGL((grouped_mm_staged<1, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((grouped_mm_staged<1, false>), grid, dim3(256), 0, s, a);
+        if (trans_w) mm_staged<1, true>(a, s);
+        else mm_staged<1, false>(a, s);
     }
     return hipGetLastError();
 }
 
+template <int DT>
+static void wgrad_staged(const GroupedArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)grouped_wgrad_grid(a));
+    if (wgrad_edge(a) == 64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grouped_wgrad_staged<DT, 128>), grid, dim3(256), 0, s, a);
+}
+
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-    const int64_t tiles = grouped_wgrad_grid(a);
-    const dim3 grid((uint32_t)tiles);
-    if (a.dtype == 0 && a.vec) hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
-    else if (a.dtype == 0) hipLaunchKernelGGL((grouped_wgrad_staged<0>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grouped_wgrad_staged<1>), grid, dim3(256), 0, s, a);
+    if (a.dtype == 0 && a.vec) {
+        const int64_t tiles = grouped_wgrad_grid(a);
+        hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
+    } else if (a.dtype == 0) {
+        wgrad_staged<0>(a, s);
+    } else {
+        wgrad_staged<1>(a, s);
+    }
     return hipGetLastError();
 }
 
