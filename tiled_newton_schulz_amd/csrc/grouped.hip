@@ -853,7 +853,126 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows an expert (tokens being decoded; bf16, 16-byte chunks): a stream of
+// the weights, HBM bound.  Tiles of 16 rows by 64 columns; the four waves of a
+// workgroup take a quarter of k each, with no barrier until their sums are
+// joined.  A wave keeps a ring of kRing stages of 32 k in LDS (16 rows of X and 64
+// columns of W, 5 KB), loaded straight from global memory: two workgroups hold
+// 120 KB a CU in flight, which covers the memory's latency.  In a larger tile
+// the same weights would wait for a pipeline's start and end at every tile.
+//   along k: rows of four 16-byte chunks, chunk c of row r at c ^ ((r / 4) & 3)
+//   along i: 32 k rows of eight chunks, chunk c of row k at c ^ (2 (k & 2))
+// ---------------------------------------------------------------------------
+constexpr int kThinRows = 16, kThinCols = 64, kRing = 4, kThinK = 32;
+constexpr int kThinStage = (kThinRows + kThinCols) * kThinK;   // elements
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <bool WT>
+__global__ __launch_bounds__(256) void grouped_mm_thin(const GroupedArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned short ring[4 * kRing * kThinStage];
+    constexpr int kSumLd = kThinCols + 4;
+    static_assert(4 * kThinRows * kSumLd * 4 <= (int)sizeof(ring), "the sums are joined in the ring's memory");
+    GroupTile t;
+    if (!find_tile(a, kThinRows, (a.ndim + kThinCols - 1) / kThinCols, t)) return;
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+    const int64_t m0 = (int64_t)t.row0 + t.mt * kThinRows;
+    const int n0 = t.nt * kThinCols;
+    const int rows = min(kThinRows, t.rows - t.mt * kThinRows), cols = min(kThinCols, a.ndim - n0);
+    // this wave's k
+    const int kw = (a.kdim + 4 * kThinK - 1) / (4 * kThinK) * kThinK;
+    const int kb = min(a.kdim, wave * kw);
+    int left = t.e < a.n ? min(kw, a.kdim - kb) : 0;   // none: rows of no expert
+    const int64_t ldw = t.e < a.n ? a.w_ld[t.e] : 0;
+
+    // ---- loads ----
+    const uint32_t ldx2 = 2u * (uint32_t)a.x_ld, ldw2 = 2u * (uint32_t)ldw;
+    const int r4 = lane >> 2, c4 = (lane & 3) ^ ((r4 >> 2) & 3);   // along k
+    const int k8 = lane >> 3, c8 = (lane & 7) ^ (2 * (k8 & 2));    // along i
+    uint64_t px = reinterpret_cast<uint64_t>(a.x) + 2 * (m0 * a.x_ld + kb), pw = 0;
+    int64_t rest_x = 2 * ((int64_t)(rows - 1) * a.x_ld + left), rest_w = 0;
+    if (t.e < a.n) {
+        pw = reinterpret_cast<uint64_t>(a.w[t.e]) + 2 * (WT ? n0 * ldw + kb : kb * ldw + n0);
+        rest_w = WT ? 2 * ((int64_t)(cols - 1) * ldw + left) : 2 * ((int64_t)(left - 1) * ldw + cols);
+    }
+    const uint32_t vx = r4 * ldx2 + c4 * 16u;
+    const uint32_t vw = WT ? r4 * ldw2 + c4 * 16u : c8 * 8 < cols ? k8 * ldw2 + c8 * 16u : kNowhere;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS void*)ring + wave * (kRing * kThinStage * 2);
+    auto load = [&](int slot) __attribute__((always_inline)) {
+        const uint32_t lds = lds0 + slot * (kThinStage * 2);
+        const i32x4 rx = rsrc_words(reinterpret_cast<const void*>(px), left > 0 ? rest_x : 0);
+        const i32x4 rw = rsrc_words(reinterpret_cast<const void*>(pw), left > 0 ? rest_w : 0);
+        const bool past = c4 * 8 >= left;   // chunks along k past the wave's end
+        dma16(rx, past ? kNowhere : vx, lds);
+        const uint32_t v = WT && past ? kNowhere : vw;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dma16(rw, v == kNowhere ? v : v + j * (WT ? 16 : 8) * ldw2, lds + (kThinRows * kThinK * 2) + j * 1024);
+        px += 2 * kThinK;
+        rest_x -= 2 * kThinK;
+        const int64_t move = WT ? 2 * kThinK : (int64_t)kThinK * ldw2;
+        pw += move;
+        rest_w -= move;
+        left -= kThinK;
+    };
+
+    // ---- products: columns as the MFMA's rows ----
+    f32x4 acc[4] = {};
+    const int steps = (left + kThinK - 1) / kThinK;
+    const int i16 = lane & 15, g = lane >> 4;
+    const int at_x = i16 * kThinK + ((g ^ ((i16 >> 2) & 3)) * 8);
+    const int kr = 8 * g + (i16 >> 2), sw = 2 * (kr & 2);
+#pragma unroll
+    for (int s = 0; s < kRing; ++s) load(s);
+    for (int s = 0, slot = 0; s < steps; ++s, slot = (slot + 1) % kRing) {
+        // all but the newest three stages have landed
+        asm volatile("s_waitcnt vmcnt(15)" ::: "memory");
+        const unsigned short* st = ring + (wave * kRing + slot) * kThinStage;
+        const unsigned short* sw_ = st + kThinRows * kThinK;
+        const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&st[at_x]);
+        bf16x8 wv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (WT) {
+                wv[j] = *reinterpret_cast<const bf16x8*>(&sw_[j * 16 * kThinK + at_x]);
+            } else {
+                const unsigned short* q = &sw_[kr * kThinCols + (((j * 2 + ((i16 & 3) >> 1)) ^ sw) * 8) + 4 * (i16 & 1)];
+                const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q));
+                const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LDS_AS bf16x4*)(q + 4 * kThinCols));
+                wv[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+        }
+        // in registers: the stage can be filled again
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // (the same, for the compiler's own count)
+        load(slot);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], xv, acc[j], 0, 0, 0);
+    }
+    static_assert(kRing == 4, "the wait above counts five loads for each of three stages");
+
+    // ---- the four waves' sums, in order ----
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(&sums[(wave * kThinRows + i16) * kSumLd + j * 16 + g * 4]) = acc[j];
+    __syncthreads();
+    const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) * 4;
+    f32x4 v = *reinterpret_cast<const f32x4*>(&sums[r * kSumLd + c]);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[(w * kThinRows + r) * kSumLd + c]);
+    if (r < rows && c < cols) {
+        const u32x2 o = {pack2(v[0], v[1]), pack2(v[2], v[3])};
+        *reinterpret_cast<u32x2*>(reinterpret_cast<unsigned short*>(a.y) + (m0 + r) * a.y_ld + n0 + c) = o;
+    }
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Mean rows an expert up to which the thin kernel is taken.
+constexpr int kThinMean = 16;
 
 int device_cus_or_256() {
     static const int cus = [] { const int c = device_cus(); return c >= 8 ? std::min(c, 512) : 256; }();
@@ -869,6 +988,7 @@ int64_t wgrad_tiles(const GroupedArgs& a, int edge) { return cdiv(a.kdim, edge) 
 // Tile edge: 256 where the fast kernel runs.  Else 128, or 64 where tiles of 128
 // do not fill the chip.  (Rows that no expert has are counted as if it had
 // some: the host does not know.)
+bool mm_thin(const GroupedArgs& a) { return a.dtype == 0 && a.vec && a.rows <= kThinMean * (int64_t)a.n; }
 int mm_edge(const GroupedArgs& a) {
     if (a.dtype == 0 && a.vec) return kBig;
     return mm_tiles(a, 128) < device_cus_or_256() ? 64 : 128;
@@ -880,7 +1000,10 @@ int wgrad_edge(const GroupedArgs& a) {
 
 }  // namespace
 
-int64_t grouped_mm_grid(const GroupedArgs& a) { return cdiv(mm_tiles(a, mm_edge(a)), 8) * 8; }
+int64_t grouped_mm_grid(const GroupedArgs& a) {
+    if (mm_thin(a)) return cdiv((a.rows / kThinRows + a.n + 1) * cdiv(a.ndim, kThinCols), 8) * 8;
+    return cdiv(mm_tiles(a, mm_edge(a)), 8) * 8;
+}
 int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, wgrad_edge(a)), 8) * 8; }
 
 // Workgroups of the 256 x 256 kernel for at most `tiles` tiles: one fits a CU.
@@ -894,7 +1017,11 @@ static void mm_staged(const GroupedArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
-    if (a.dtype == 0 && a.vec) {
+    if (mm_thin(a)) {
+        const dim3 grid((uint32_t)grouped_mm_grid(a));
+        if (trans_w) hipLaunchKernelGGL((grouped_mm_thin<true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((grouped_mm_thin<false>), grid, dim3(256), 0, s, a);
+    } else if (a.dtype == 0 && a.vec) {
         const int64_t tiles = grouped_mm_grid(a);
         const dim3 grid(big_grid(tiles));
         if (trans_w) hipLaunchKernelGGL((grouped_big<1>), grid, dim3(512), 0, s, a, (int)tiles);
