@@ -253,3 +253,67 @@ def test_large_products(cuda):
                 close(g[e][i:i + 1], *product(x[r:r + c, i:i + 1].t(), d[r:r + c], "bf16"))
         r += c
     assert torch.all(g[1] == 0)
+
+
+def ragged(n, most, seed, none=0.1):
+    g = torch.Generator().manual_seed(seed)
+    c = torch.randint(1, most + 1, (n,), generator=g)
+    c[torch.rand(n, generator=g) < none] = 0
+    return c.tolist()
+
+
+# (experts, most rows of one, K, N): many 256-wide tiles, K and N that end
+# inside a step of 64 or a tile of 256, row tiles of one to four blocks of 64
+TILED = [(64, 300, 200, 1416), (40, 700, 72, 2048), (64, 90, 520, 1408), (300, 60, 64, 264), (33, 260, 128, 1800)]
+
+
+@pytest.mark.parametrize("stored", ["kn", "nk"])
+@pytest.mark.parametrize("n,most,K,N", TILED)
+def test_many_tiles(cuda, n, most, K, N, stored):
+    """Enough tiles for the largest tile kernel, several to a workgroup."""
+    counts = ragged(n, most, n)
+    M = sum(counts)
+    print(f"many tiles {n} x {most} x {K} x {N} {stored}, {M} rows", flush=True)
+    x = randn((M + 11, K), "bf16", 40)
+    w = randn((n, K, N), "bf16", 41) if stored == "kn" else randn((n, N, K), "bf16", 41).transpose(1, 2)
+    # NaN beside the operands: in rows of no expert, in the weights of experts without rows
+    x[M:] = float("nan")
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = float("nan")
+    check_mm(x, w, counts, "bf16")
+
+
+@pytest.mark.parametrize("n,most,K,N", [(64, 300, 200, 520), (20, 700, 1032, 776), (300, 40, 264, 72), (64, 130, 264, 640)])
+def test_many_gradient_tiles(cuda, n, most, K, N):
+    counts = ragged(n, most, n + 1)
+    M = sum(counts)
+    print(f"many gradient tiles {n} x {most} x {K} x {N}, {M} rows", flush=True)
+    x, d = randn((M + 11, K), "bf16", 42), randn((M + 11, N), "bf16", 43)
+    x[M:] = float("nan")
+    d[M:] = float("nan")
+    check_wgrad(x, d, counts, "bf16")
+
+
+def test_many_tiles_strided_and_repeated(cuda):
+    """Column blocks of wider tensors at 16-byte offsets whose other columns hold
+    NaN, results into the middle of a wider tensor, the same bits again, and one
+    expert that holds nearly all rows."""
+    n, K, N = 48, 136, 1288
+    counts = ragged(n, 200, 7)
+    counts[5] = 9000
+    M = sum(counts)
+    big = torch.full((M, K + 24), float("nan"), dtype=torch.bfloat16, device=cuda)
+    x = big[:, 8:8 + K]
+    x.copy_(randn((M, K), "bf16", 44))
+    wide = torch.full((n, K, N + 16), float("nan"), dtype=torch.bfloat16, device=cuda)
+    w = wide[:, :, 8:8 + N]
+    w.copy_(randn((n, K, N), "bf16", 45))
+    store = torch.full((M, N + 16), 7.0, dtype=torch.bfloat16, device=cuda)
+    y = check_mm(x, w, counts, "bf16", out=store[:, 8:8 + N])
+    assert torch.all(store[:, :8] == 7.0) and torch.all(store[:, 8 + N:] == 7.0)
+    ends = ends_of(counts)
+    assert torch.equal(y, H.himuon_grouped_mm(x, w, ends))
+    d = randn((M, N), "bf16", 46)
+    g = check_wgrad(x, d, counts, "bf16")
+    assert torch.equal(g, H.himuon_grouped_wgrad(x, d, ends))

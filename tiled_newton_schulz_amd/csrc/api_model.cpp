@@ -69,6 +69,15 @@ himuon_status_t grouped_args(const himuon_matrix_t* X, const himuon_matrix_t* W,
     return HIMUON_OK;
 }
 
+// True if every launch of the call has a grid that fits (the full ones and the last).
+bool grids_fit(GroupedArgs a, int32_t n, int64_t (*grid)(const GroupedArgs&)) {
+    for (const int32_t part : {std::min(kExperts, n), (n - 1) % kExperts + 1}) {
+        a.n = part;
+        if (grid(a) > INT32_MAX / 2) return false;
+    }
+    return true;
+}
+
 // Runs f over the launches of the call.
 template <typename F>
 himuon_status_t each_launch(GroupedArgs& a, const himuon_matrix_t* W, int32_t n, F f) {
@@ -105,10 +114,9 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
     a.y = Y->ptr;
     a.y_ld = Y->ld;
     a.ndim = (int32_t)N;
-    a.n = std::min(kExperts, n);
-    if (grouped_mm_grid(a) > INT32_MAX / 2) return HIMUON_ERR_LAYOUT;
     a.vec = chunked(*X) && chunked(*Y) && K % 8 == 0 && N % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(W[e]);
+    if (!grids_fit(a, n, grouped_mm_grid)) return HIMUON_ERR_LAYOUT;
     return each_launch(a, W, n, [&] {
         const hipError_t e = launch_grouped_mm(a, trans_w != 0, reinterpret_cast<hipStream_t>(stream));
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);
@@ -136,10 +144,9 @@ himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D
     a.d = D->ptr;
     a.d_ld = D->ld;
     a.ndim = (int32_t)D->cols;
-    a.n = std::min(kExperts, n);
-    if (grouped_wgrad_grid(a) > INT32_MAX / 2) return HIMUON_ERR_LAYOUT;
     a.vec = chunked(*X) && chunked(*D) && a.kdim % 8 == 0 && a.ndim % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(G[e]);
+    if (!grids_fit(a, n, grouped_wgrad_grid)) return HIMUON_ERR_LAYOUT;
     return each_launch(a, G, n, [&] {
         const hipError_t e = launch_grouped_wgrad(a, reinterpret_cast<hipStream_t>(stream));
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);

@@ -27,7 +27,7 @@ struct GroupedArgs {
     int64_t w_ld[kExperts];
 };
 
-// Largest grid the launchers would use (checked against INT32_MAX before any launch).
+// Most tiles of a launch (checked before any launch).
 int64_t grouped_mm_grid(const GroupedArgs& a);
 int64_t grouped_wgrad_grid(const GroupedArgs& a);
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s);

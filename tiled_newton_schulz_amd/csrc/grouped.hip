@@ -971,9 +971,6 @@ __global__ __launch_bounds__(256) void grouped_mm_thin(const GroupedArgs a) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Mean rows an expert up to which the thin kernel is taken.
-constexpr int kThinMean = 16;
-
 int device_cus_or_256() {
     static const int cus = [] { const int c = device_cus(); return c >= 8 ? std::min(c, 512) : 256; }();
     return cus;
@@ -985,73 +982,92 @@ int64_t mm_tiles(const GroupedArgs& a, int edge) {
 }
 int64_t wgrad_tiles(const GroupedArgs& a, int edge) { return cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n; }
 
-// Tile edge: 256 where the fast kernel runs.  Else 128, or 64 where tiles of 128
-// do not fill the chip.  (Rows that no expert has are counted as if it had
-// some: the host does not know.)
-bool mm_thin(const GroupedArgs& a) { return a.dtype == 0 && a.vec && a.rows <= kThinMean * (int64_t)a.n; }
-int mm_edge(const GroupedArgs& a) {
-    if (a.dtype == 0 && a.vec) return kBig;
-    return mm_tiles(a, 128) < device_cus_or_256() ? 64 : 128;
+// Tiles to expect: the host knows the rows and the experts, not which expert has
+// how many; half a partial row tile each.
+double mm_expect(const GroupedArgs& a, int edge) {
+    return ((double)a.rows / edge + 0.5 * a.n) * (double)cdiv(a.ndim, edge);
 }
-int wgrad_edge(const GroupedArgs& a) {
-    if (a.dtype == 0 && a.vec) return kBig;
-    return wgrad_tiles(a, 128) < device_cus_or_256() ? 64 : 128;
+
+// Which kernel.  Measured in us, experts x rows x K x N (K x N stored, bf16):
+//                           thin   256-tiles   staged 128   staged 64
+//   64 x  16 x 4096 x 1408   134         148
+//   64 x  17 x 4096 x 1408   160         147
+//    1 x 512 x 1024 x 1024   8.7          25           11          11
+//    8 x 128 x 2048 x 2048    46          39           36          27
+//    8 x 512 x 4096 x 1024   140          78           65          65
+//    2 x 2048 x 512 x 2048    78          21           21          25
+// so: thin up to 16 rows an expert (32 where 256-tiles are too few), 256-tiles
+// from three quarters of a tile a CU, else staged with tiles of 128 from one a
+// CU.  Weight gradients alike: 1 x 1024 x 1024 x 1024 (16 tiles of 256) 30
+// against 7 us staged, 1 x 256 x 4096 x 4096 (256 tiles) 19 against 27 us.
+enum class Kernel { Thin, Big, Staged128, Staged64 };
+bool enough_big(double tiles) { return tiles >= 0.75 * device_cus_or_256(); }
+Kernel mm_kernel(const GroupedArgs& a) {
+    if (a.dtype == 0 && a.vec) {
+        const bool big = enough_big(mm_expect(a, kBig));
+        if (a.rows <= (big ? 16 : 32) * (int64_t)a.n) return Kernel::Thin;
+        if (big) return Kernel::Big;
+    }
+    return mm_expect(a, 128) < device_cus_or_256() ? Kernel::Staged64 : Kernel::Staged128;
 }
+Kernel wgrad_kernel(const GroupedArgs& a) {
+    if (a.dtype == 0 && a.vec && enough_big((double)wgrad_tiles(a, kBig))) return Kernel::Big;
+    return wgrad_tiles(a, 128) < device_cus_or_256() ? Kernel::Staged64 : Kernel::Staged128;
+}
+int edge_of(Kernel k) { return k == Kernel::Big ? kBig : k == Kernel::Staged128 ? 128 : 64; }
 
 }  // namespace
 
 int64_t grouped_mm_grid(const GroupedArgs& a) {
-    if (mm_thin(a)) return cdiv((a.rows / kThinRows + a.n + 1) * cdiv(a.ndim, kThinCols), 8) * 8;
-    return cdiv(mm_tiles(a, mm_edge(a)), 8) * 8;
+    const Kernel k = mm_kernel(a);
+    if (k == Kernel::Thin) return cdiv((a.rows / kThinRows + a.n + 1) * cdiv(a.ndim, kThinCols), 8) * 8;
+    return cdiv(mm_tiles(a, edge_of(k)), 8) * 8;
 }
-int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, wgrad_edge(a)), 8) * 8; }
+int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, edge_of(wgrad_kernel(a))), 8) * 8; }
 
 // Workgroups of the 256 x 256 kernel for at most `tiles` tiles: one fits a CU.
 static uint32_t big_grid(int64_t tiles) { return (uint32_t)std::min<int64_t>(tiles, device_cus_or_256() / 8 * 8); }
 
 template <int DT, bool WT>
-static void mm_staged(const GroupedArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)grouped_mm_grid(a));
-    if (mm_edge(a) == 64) hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 64>), grid, dim3(256), 0, s, a);
+static void mm_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t s) {
+    if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 64>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 128>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
-    if (mm_thin(a)) {
-        const dim3 grid((uint32_t)grouped_mm_grid(a));
+    const Kernel k = mm_kernel(a);
+    const int64_t tiles = grouped_mm_grid(a);
+    const dim3 grid((uint32_t)tiles);
+    if (k == Kernel::Thin) {
         if (trans_w) hipLaunchKernelGGL((grouped_mm_thin<true>), grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL((grouped_mm_thin<false>), grid, dim3(256), 0, s, a);
-    } else if (a.dtype == 0 && a.vec) {
-        const int64_t tiles = grouped_mm_grid(a);
-        const dim3 grid(big_grid(tiles));
-        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), grid, dim3(512), 0, s, a, (int)tiles);
-        else hipLaunchKernelGGL((grouped_big<0>), grid, dim3(512), 0, s, a, (int)tiles);
+    } else if (k == Kernel::Big) {
+        if (trans_w) hipLaunchKernelGGL((grouped_big<1>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
+        else hipLaunchKernelGGL((grouped_big<0>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
     } else if (a.dtype == 0) {
-        if (trans_w) mm_staged<0, true>(a, s);
-        else mm_staged<0, false>(a, s);
+        if (trans_w) mm_staged<0, true>(a, k, grid, s);
+        else mm_staged<0, false>(a, k, grid, s);
     } else {
-        if (trans_w) mm_staged<1, true>(a, s);
-        else mm_staged<1, false>(a, s);
+        if (trans_w) mm_staged<1, true>(a, k, grid, s);
+        else mm_staged<1, false>(a, k, grid, s);
     }
     return hipGetLastError();
 }
 
 template <int DT>
-static void wgrad_staged(const GroupedArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)grouped_wgrad_grid(a));
-    if (wgrad_edge(a) == 64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64>), grid, dim3(256), 0, s, a);
+static void wgrad_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t s) {
+    if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((grouped_wgrad_staged<DT, 128>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-    if (a.dtype == 0 && a.vec) {
-        const int64_t tiles = grouped_wgrad_grid(a);
+    const Kernel k = wgrad_kernel(a);
+    const int64_t tiles = grouped_wgrad_grid(a);
+    const dim3 grid((uint32_t)tiles);
+    if (k == Kernel::Big)
         hipLaunchKernelGGL((grouped_big<2>), dim3(big_grid(tiles)), dim3(512), 0, s, a, (int)tiles);
-    } else if (a.dtype == 0) {
-        wgrad_staged<0>(a, s);
-    } else {
-        wgrad_staged<1>(a, s);
-    }
+    else if (a.dtype == 0) wgrad_staged<0>(a, k, grid, s);
+    else wgrad_staged<1>(a, k, grid, s);
     return hipGetLastError();
 }
 
