@@ -334,6 +334,32 @@ def test_distill_absent_repeated_masked(cuda, dt, V, pad, shift):
             assert torch.isnan(v._base[:, :shift]).all() and torch.isnan(v._base[:, shift + V:]).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("threads,chunks", [(256, 1), (256, 2), (256, 3), (256, 4), (256, 6), (256, 8), (512, 6), (512, 8),
+                                            (1024, 6), (1024, 8), (1024, 12), (1024, 16), (1024, 18), (1024, 20)])
+def test_distill_row_sizes(cuda, threads, chunks, dt):
+    """Rows around the sizes that workgroups hold, on and off the 16-byte grid,
+    the gradient on the logits' grid and on another one; nothing outside it is
+    written."""
+    epc = 8 if dt == "bf16" else 4
+    N, full = 5, threads * chunks * epc
+    for V in (full - epc, full - epc - 3, full):
+        idx, t = teacher(N, V, 6, 90)
+        idx[1, 0], idx[2, 0] = 0, V - 1
+        z = logits(N, V, dt, 91)
+        w = torch.tensor([1.0, 0.5, 2.0, 0.0, 1.0])
+        loss, grad, lse, d, lb, gb = distill64(z, idx, t, 1.0, True, w)
+        tol = gb + ROUND[dt] * grad.abs() + 1e-38
+        for (zp, zs), (gp, gs) in (((epc, 0), (2 * epc, epc)), ((3, 1), (3, 1)), ((2, 1), (2, 1)), ((3, 1), (4, 2))):
+            print(f"distill {N}x{V} logits {zp} {zs} gradient {gp} {gs} {dt}", flush=True)
+            out = strided(torch.full((N, V), float("nan"), dtype=TYPES[dt]), gp, gs)
+            r = H.himuon_distill(strided(z, zp, zs), idx.cuda(), t.cuda(), weight=w.cuda(), grad=out)
+            near(r.loss, loss, lb, "loss")
+            near(r.lse.double().sum(1)[w != 0], lse[w != 0], d[w != 0], "lse")
+            near(out, grad, tol, "grad")
+            assert torch.isnan(out._base[:, :gs]).all() and torch.isnan(out._base[:, gs + V:]).all()
+
+
 def test_distill_extremes(cuda):
     """A masked logit under an entry gives the loss +inf and a finite gradient;
     NaN and +inf make their own row NaN; a row of the lowest value is uniform."""

@@ -536,34 +536,31 @@ __device__ __forceinline__ void segment_top(TopShared& sh, int top, const Row<DT
     for (int j = at + threadIdx.x; j < top; j += kThreads) emit(j, 0);   // fewer elements than that
 }
 
-// The `top` largest of the keys a workgroup holds (0: none), all different.
+// The `top` largest of the keys a workgroup holds (0: none), all different; the
+// bound as in segment_top, from the keys' logits.
 template <int U, typename Emit>
 __device__ __forceinline__ void keys_top(TopShared& sh, int top, const uint64_t (&key)[U], Emit emit) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t v = 0;
+    uint64_t most = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) v = v > key[u] ? v : key[u];
-    const uint64_t mine = v;
-    uint64_t low = 0;
+    for (int u = 0; u < U; ++u) most = most > key[u] ? most : key[u];
+    const float mine = most != 0 ? key_value(most) : kNegInf;
+    float v = mine, low = kNegInf;
     for (int i = 0; i < (top + 3) / 4; ++i) {
-        low = v;
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-            const uint64_t w = __shfl_xor((unsigned long long)low, o, 64);
-            low = low > w ? low : w;
-        }
-        if (v == low) v = 0;
+        low = wmax(v);
+        const unsigned long long at = __ballot(v == low);
+        if (at != 0 && lane == __builtin_ctzll(at)) v = __builtin_nanf("");   // passed over from here on
+        if (at == 0) low = kNegInf;
     }
     __syncthreads();   // sh may still be read from the last use
-    if (lane == 0) sh.best[wave] = low;
+    if (lane == 0) sh.low[wave] = low;
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) low = low < sh.best[w] ? low : sh.best[w];
+    low = fminf(fminf(sh.low[0], sh.low[1]), fminf(sh.low[2], sh.low[3]));
     if (mine >= low)
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (key[u] >= low && key[u] != 0) {
+            if (key[u] != 0 && key_value(key[u]) >= low) {
                 const int at = atomicAdd(&sh.count, 1);
                 if (at < kCand) sh.cand[at] = key[u];
             }
@@ -878,23 +875,45 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
 // holds its chunks packed in registers; as each is turned into its gradient and
 // stored, the next row's chunk is loaded in its place, so that one row's stores
 // and the next one's loads overlap the products between them.
-template <int DT, int NT, int U, bool FL>
+// GRID 0: rows of whole chunks; 1: rows that start or end inside a chunk, z and
+// dz on the same grid; 2: on different ones (stored element by element).  The
+// elements of a row's partial chunks are held one each by the first threads.
+// bf16, 64 entries a row: 2048 x 131072 in 272 us (3.9 TB/s; a large copy
+// reaches 4.9), 2048 x 65537 in 161 us (3.3 TB/s).
+template <int DT, int NT, int U, int GRID>
 __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
+    constexpr bool FL = GRID == 0;
     constexpr int EPC = kEpc<DT>, KE = kMaxEntries / NT;
     __shared__ float red1[NT / 64][3], red2[NT / 64][4];
     __shared__ int ids[kMaxEntries];
     __shared__ float ps[kMaxEntries];
     const float c = a.inv_temp * kLog2e;
     auto weight_of = [&](int64_t row) { return row < a.rows ? (a.weight ? a.weight[row] : 1.f) : 0.f; };
+    // whole chunk c of a row, -inf otherwise
+    auto load = [&](const Row<DT, FL>& z, int ch) __attribute__((always_inline)) {
+        const unsigned none = DT == 0 ? 0xff80ff80u : 0xff800000u;
+        return z.whole(ch) ? *reinterpret_cast<const u32x4*>(z.at(ch)) : u32x4{none, none, none, none};
+    };
+    // column this thread holds of the row's partial chunks (-1: none)
+    auto edge_of = [&](const Row<DT, FL>& z) {
+        if (FL || threadIdx.x >= 2 * EPC) return -1;
+        const int e = threadIdx.x % EPC, last = z.chunks() - 1;
+        const int ch = threadIdx.x < EPC ? 0 : last;
+        if (threadIdx.x >= EPC && last == 0) return -1;   // the first chunk is the last one
+        const int col = z.first(ch) + e;
+        return z.whole(ch) || col < 0 || col >= z.cols ? -1 : col;
+    };
 
     int64_t row = blockIdx.x;
-    float w = weight_of(row);
+    float w = weight_of(row), ez = kNegInf;
     u32x4 r[U];
     {
         // a row that counts nothing is not read: no columns
         const Row<DT, FL> z(a.z, a.z_ld, row, w != 0.f ? a.cols : 0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = z.load(u * NT + threadIdx.x);
+        for (int u = 0; u < U; ++u) r[u] = load(z, u * NT + threadIdx.x);
+        const int edge = edge_of(z);
+        if (edge >= 0) ez = z.load_elem(edge);
     }
     for (; row < a.rows; row += gridDim.x) {
         const Row<DT, FL> z(a.z, a.z_ld, row, a.cols), dz(a.dz, a.dz_ld, row, a.cols);
@@ -906,7 +925,7 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
         Entry x[KE];
 #pragma unroll
         for (int i = 0; i < KE; ++i) x[i] = {-1, kNegInf, 0.f};
-        float mx[3] = {kNegInf, 0.f, kNegInf};   // teacher's largest u, any entry, largest logit
+        float mx[3] = {kNegInf, 0.f, FL ? kNegInf : ez};   // teacher's largest u, any entry, largest logit
         if (w != 0.f) {
 #pragma unroll
             for (int i = 0; i < KE; ++i) {
@@ -944,6 +963,7 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
                 sum[2] += e * (x[i].u - M);
                 sum[3] += e * ((x[i].z - ref) * a.inv_temp);
             }
+            if (!FL) sum[0] = exp2_hw((ez - ref) * c);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -971,14 +991,28 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
         // ---- the gradient, and the next row's loads ----
         const Softmax q(a.inv_temp, l);
         const unsigned mask = live ? ~0u : 0u;   // a row that counts nothing gets zeros whatever it holds
+        const int edge = edge_of(z);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const int ch = u * NT + threadIdx.x;
             float g[EPC];
 #pragma unroll
             for (int e = 0; e < EPC; ++e) g[e] = scale * q(elem<DT>(r[u], e));
-            dz.store(u * NT + threadIdx.x, pack<DT>(g) & mask, z.mis);
-            r[u] = zn.load(u * NT + threadIdx.x);
+            if (z.whole(ch)) {
+                if constexpr (GRID == 2) {
+#pragma unroll
+                    for (int e = 0; e < EPC; ++e) dz.store_elem(z.first(ch) + e, live ? g[e] : 0.f);
+                } else {
+                    *reinterpret_cast<u32x4*>(dz.at(ch)) = pack<DT>(g) & mask;
+                }
+            }
+            r[u] = load(zn, ch);
             __builtin_amdgcn_sched_barrier(0);   // else all chunks of both rows are held at once
+        }
+        if (!FL) {
+            if (edge >= 0) dz.store_elem(edge, live ? scale * q(ez) : 0.f);
+            const int edge_next = edge_of(zn);
+            ez = edge_next >= 0 ? zn.load_elem(edge_next) : kNegInf;
         }
         __syncthreads();   // the row's stores before those of its entries; ids and ps are free
         if (live)
@@ -1045,23 +1079,52 @@ hipError_t grad(LogitsArgs a, hipStream_t s) {
     return flush(a) ? grad_fl<KIND, true>(a, s) : grad_fl<KIND, false>(a, s);
 }
 
-template <int DT, int NT, int U, bool FL>
+template <int DT, int NT, int U, int GRID>
 hipError_t row_launch(const LogitsArgs& a, hipStream_t s) {
     static const int cus = [] { const int c = device_cus(); return c > 0 ? c : 256; }();
-    const int64_t most = (int64_t)cus * (1024 / NT);
-    hipLaunchKernelGGL((distill_row_kernel<DT, NT, U, FL>), dim3((uint32_t)std::min<int64_t>(a.rows, most)), dim3(NT), 0, s, a);
+    // workgroups the chip holds at once (64 registers a thread up to four chunks, 128 above)
+    const int64_t most = (int64_t)cus * ((U <= 4 ? 2048 : 1024) / NT);
+    hipLaunchKernelGGL((distill_row_kernel<DT, NT, U, GRID>), dim3((uint32_t)std::min<int64_t>(a.rows, most)), dim3(NT),
+                       0, s, a);
     return hipGetLastError();
 }
 
-template <int DT, bool FL>
-hipError_t row_fl(const LogitsArgs& a, hipStream_t s) {
+// The fewest threads and chunks that hold a row: 2048 x 131071 in bf16, which
+// needs 17 chunks of 1024 threads, takes 321 us with 18 and 353 us with 20.
+template <int DT, int GRID>
+hipError_t row_size(const LogitsArgs& a, hipStream_t s) {
     const int64_t n = row_chunks(a);
-    if (n <= 256 * 2) return row_launch<DT, 256, 2, FL>(a, s);
-    if (n <= 256 * 8) return row_launch<DT, 256, 8, FL>(a, s);
-    if (n <= 512 * 8) return row_launch<DT, 512, 8, FL>(a, s);
-    if (n <= 1024 * 8) return row_launch<DT, 1024, 8, FL>(a, s);
-    if (n <= 1024 * 16) return row_launch<DT, 1024, 16, FL>(a, s);
-    return row_launch<DT, 1024, 20, FL>(a, s);
+    if constexpr (GRID == 2) {   // rare, and bound by its stores: fewer sizes
+        if (n <= 256 * 8) return row_launch<DT, 256, 8, GRID>(a, s);
+        if (n <= 1024 * 8) return row_launch<DT, 1024, 8, GRID>(a, s);
+        return row_launch<DT, 1024, 20, GRID>(a, s);
+    } else {
+        if (n <= 256 * 1) return row_launch<DT, 256, 1, GRID>(a, s);
+        if (n <= 256 * 2) return row_launch<DT, 256, 2, GRID>(a, s);
+        if (n <= 256 * 3) return row_launch<DT, 256, 3, GRID>(a, s);
+        if (n <= 256 * 4) return row_launch<DT, 256, 4, GRID>(a, s);
+        if (n <= 256 * 6) return row_launch<DT, 256, 6, GRID>(a, s);
+        if (n <= 256 * 8) return row_launch<DT, 256, 8, GRID>(a, s);
+        if (n <= 512 * 6) return row_launch<DT, 512, 6, GRID>(a, s);
+        if (n <= 512 * 8) return row_launch<DT, 512, 8, GRID>(a, s);
+        if (n <= 1024 * 6) return row_launch<DT, 1024, 6, GRID>(a, s);
+        if (n <= 1024 * 8) return row_launch<DT, 1024, 8, GRID>(a, s);
+        if (n <= 1024 * 12) return row_launch<DT, 1024, 12, GRID>(a, s);
+        if (n <= 1024 * 16) return row_launch<DT, 1024, 16, GRID>(a, s);
+        if (n <= 1024 * 18) return row_launch<DT, 1024, 18, GRID>(a, s);
+        return row_launch<DT, 1024, 20, GRID>(a, s);
+    }
+}
+template <int GRID>
+hipError_t row_dt(const LogitsArgs& a, hipStream_t s) {
+    return a.dtype == 0 ? row_size<0, GRID>(a, s) : row_size<1, GRID>(a, s);
+}
+
+// z's and dz's rows start at the same place of the 16-byte grid.
+bool same_grid(const LogitsArgs& a) {
+    const int epc = a.dtype == 0 ? 8 : 4;
+    const int64_t apart = reinterpret_cast<intptr_t>(a.z) - reinterpret_cast<intptr_t>(a.dz);
+    return apart % 16 == 0 && ((a.z_ld - a.dz_ld) % epc == 0 || a.rows == 1);
 }
 
 }  // namespace
@@ -1079,12 +1142,16 @@ SegPlan seg_plan(int32_t rows, int32_t cols, int32_t dtype) {
     return p;
 }
 
+// One pass over a row that fits 1024 threads x 20 chunks (of 128 registers a
+// thread 80), against a forward pass and a gradient: bf16 2048 x 131072 272
+// against 336 us, 2048 x 65537 161 against 188 us, 8192 x 10001 111 against
+// 160 us; at the upper end 2048 x 163000 361 against 390 us, and 163001, whose
+// rows are off the grid, 405 against 420 us.
 bool distill_on_chip(int32_t rows, int32_t cols, int32_t dtype) { return row_chunks(cols, dtype) <= 1024 * 20; }
 
 hipError_t launch_distill(const LogitsArgs& a, hipStream_t s) { return forward<0>(a, s); }
 hipError_t launch_distill_on_chip(const LogitsArgs& a, hipStream_t s) {
-    if (flush(a)) return a.dtype == 0 ? row_fl<0, true>(a, s) : row_fl<1, true>(a, s);
-    return a.dtype == 0 ? row_fl<0, false>(a, s) : row_fl<1, false>(a, s);
+    return flush(a) ? row_dt<0>(a, s) : same_grid(a) ? row_dt<1>(a, s) : row_dt<2>(a, s);
 }
 hipError_t launch_distill_grad(const LogitsArgs& a, hipStream_t s) { return grad<0>(a, s); }
 hipError_t launch_logprobs(const LogitsArgs& a, hipStream_t s) {
