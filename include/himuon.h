@@ -335,7 +335,9 @@ himuon_status_t himuon_pair_stats_workspace(const himuon_matrix_t* a, int32_t n,
  *   statistics, losses and log probabilities are fp32 for either type.
  * - Arrays named as device arrays are contiguous and aligned to their
  *   element.  Their contents are not validated on the host; the kernels clamp
- *   or skip as stated, and never access memory outside the operands.
+ *   or skip as stated, and never access memory outside the operands.  (An
+ *   operand reaches from its first element to its last: what lies between its
+ *   rows may be read, and is not used, but never written.)
  * - Results do not depend on scheduling: the same inputs give the same bits.
  * ========================================================================== */
 
