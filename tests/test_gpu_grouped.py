@@ -154,6 +154,40 @@ def test_nan_stays_with_its_expert(cuda, dt, K, N):
         close(g[e], *product(x[r].t(), d[r], dt))
 
 
+def guarded_block(rows, cols, dt, seed, before, after):
+    """A column block whose neighbours, and the rows around it, hold NaN."""
+    t = torch.full((rows + 2, before + cols + after), float("nan"), dtype=TYPES[dt], device="cuda")
+    v = t[1:rows + 1, before:before + cols]
+    v.copy_(randn((rows, cols), dt, seed))
+    return v
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("K,N", [(1, 3), (3, 1), (5, 7), (9, 2), (65, 66), (71, 67), (130, 39), (513, 65), (519, 5), (1030, 129),
+                                 (2047, 3)])
+def test_narrow_and_long(cuda, K, N, dt):
+    """Widths that end inside a 16-byte chunk or fall short of one, few tiles
+    with long sums (along K and along the rows), NaN around every operand."""
+    print(f"narrow {K}x{N} {dt}", flush=True)
+    counts = [70, 0, 1200, 2]
+    M, n = sum(counts), len(counts)
+    x, d = guarded_block(M, K, dt, 5, 3, 2), guarded_block(M, N, dt, 6, 1, 4)
+    w = [guarded_block(K, N, dt, 10 + e, 1, 4) for e in range(n)]
+    wt = [guarded_block(N, K, dt, 20 + e, 5, 2).t() for e in range(n)]
+    for ws in (w, wt):
+        y = guarded_block(M, N, dt, 7, 2, 3)
+        check_mm(x, ws, counts, dt, out=y)
+        base = y._base.clone()
+        base[1:M + 1, 2:2 + N] = float("nan")
+        assert torch.isnan(base).all()
+    g = [guarded_block(K, N, dt, 30 + e, 4, 1) for e in range(n)]
+    check_wgrad(x, d, counts, dt, out=g)
+    for v in g:
+        base = v._base.clone()
+        base[1:K + 1, 4:4 + N] = float("nan")
+        assert torch.isnan(base).all()
+
+
 def test_many_experts_and_no_rows(cuda):
     """More experts than one launch holds, and calls without a row."""
     n, K, N = 600, 40, 24

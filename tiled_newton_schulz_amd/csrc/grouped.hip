@@ -89,12 +89,19 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
 // ---------------------------------------------------------------------------
 // Any operand (fp32; bf16 rows and widths that are not whole 16-byte chunks):
 // tiles of 128 x 128 (four waves of 64 x 64 each) or, where those would leave
-// CUs idle, 64 x 64, k in steps of 64 (bf16) or 32 (fp32).  The next step's chunks are loaded into registers while the present
-// one is multiplied from LDS, then stored in the other LDS buffer.  Loads and
-// stores are 16 bytes wide at any alignment of the element; chunks at the
-// operand's ends are moved element by element.  An operand stays in LDS in its
-// own order, as below for the larger tiles; fp32 products take four k at a time
-// (lane group g holds k = 4 g .. 4 g + 3 of eight, for both operands alike).
+// CUs idle, 64 x 64, k in steps of 64 (bf16) or 32 (fp32).  The next step's
+// chunks are loaded into registers while the present one is multiplied from
+// LDS, then stored in the other LDS buffer.  Loads and stores are 16 bytes wide
+// at any alignment of the element.  A chunk that reaches past its row's end is
+// loaded from as much further left and shifted (element by element, a load's
+// latency each, the 39 columns of a 4528 x 925 x 39 gradient took 155 instead of
+// 35 us, and 8 x 2048 x 2047 x 2045 386 instead of 258 us).  An operand stays in
+// LDS in its own order, as below for the larger tiles; fp32 products take four k
+// at a time (lane group g holds k = 4 g .. 4 g + 3 of eight, for both operands
+// alike).
+// Where even the 64 x 64 tiles are fewer than the CUs, four parts of the
+// workgroup (SPLIT) take every fourth step each, and their sums are added in
+// order at the end.
 // ---------------------------------------------------------------------------
 template <int DT> struct Io;
 template <> struct Io<0> {
@@ -124,28 +131,35 @@ struct Staged {
     const T* p;
     int64_t ld;
     int side, kd;
+    int before;   // elements of a row before p (along k: 0)
 
+    // thread of its part of the workgroup
+    __device__ __forceinline__ static int tid() { return threadIdx.x & 255; }
     // bf16 along i: place of chunk c of k row k is c ^ swap(k), so that the four
     // rows and 32 columns that are read together lie on different banks
     __device__ __forceinline__ static int swap(int k) { return EDGE == 128 ? 4 * (k & 3) : 2 * (k & 2); }
     // chunk j of this thread at k0: row and first column of the stored matrix
     // (a row of k elements, or a k row)
     __device__ __forceinline__ void load(int k0, u32x4 (&r)[NCH]) const {
-        const int row0 = threadIdx.x / CPR, c = (threadIdx.x % CPR) * EPC;
+        const int row0 = tid() / CPR, c = (tid() % CPR) * EPC;
         const int rows = ALONG_K ? side : kd - k0, cols = ALONG_K ? kd - k0 : side;
         const T* q = p + (ALONG_K ? (int64_t)k0 : k0 * ld) + c;
+        // elements of the chunk past the row's end: it is loaded from as many
+        // before its place where the row has them, see put()
+        const int out = max(c + EPC - cols, 0);
+        const bool wide = out < EPC && (ALONG_K ? k0 : before) + c >= out;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             const int row = row0 + j * ROWS;
             const T* at = q + row * ld;
-            if (row < rows && c + EPC <= cols) {
-                r[j] = reinterpret_cast<const Loose16*>(at)->v;
+            if (row < rows && wide) {
+                r[j] = reinterpret_cast<const Loose16*>(at - out)->v;
                 continue;
             }
             uint64_t w[2] = {0, 0};
             if (row < rows)
 #pragma unroll 1
-                for (int e = 0; e < cols - c; ++e) {
+                for (int e = 0; e < cols - c; ++e) {   // a matrix narrower than a chunk
                     const uint64_t x = DT == 0 ? (uint64_t)reinterpret_cast<const unsigned short*>(at)[e]
                                                : (uint64_t)reinterpret_cast<const unsigned*>(at)[e];
                     const uint64_t y = x << (sizeof(T) * 8 * (e % (EPC / 2)));
@@ -155,8 +169,19 @@ struct Staged {
             r[j] = u32x4{(unsigned)w[0], (unsigned)(w[0] >> 32), (unsigned)w[1], (unsigned)(w[1] >> 32)};
         }
     }
-    __device__ __forceinline__ static void put(T* s, const u32x4 (&r)[NCH]) {
-        const int row0 = threadIdx.x / CPR, ch = threadIdx.x % CPR;
+    // stores the chunks that load(k0, r) has loaded
+    __device__ __forceinline__ void put(int k0, T* s, u32x4 (&r)[NCH]) const {
+        const int col = (tid() % CPR) * EPC, out = max(col + EPC - (ALONG_K ? kd - k0 : side), 0);
+        if (out > 0 && out < EPC && (ALONG_K ? k0 : before) + col >= out) {
+            const int by = out * (int)sizeof(T) * 8;   // 16 .. 112 bits
+#pragma unroll
+            for (int j = 0; j < NCH; ++j) {
+                const uint64_t lo = r[j][0] | (uint64_t)r[j][1] << 32, hi = r[j][2] | (uint64_t)r[j][3] << 32;
+                const uint64_t a = by < 64 ? lo >> by | hi << (64 - by) : hi >> (by - 64), b = by < 64 ? hi >> by : 0;
+                r[j] = u32x4{(unsigned)a, (unsigned)(a >> 32), (unsigned)b, (unsigned)(b >> 32)};
+            }
+        }
+        const int row0 = tid() / CPR, ch = tid() % CPR;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             const int row = row0 + j * ROWS;
@@ -191,15 +216,19 @@ struct Staged {
 
 // C = A B of one tile (operands exchanged in the MFMA, so that a lane holds
 // runs of four columns of one row).
-template <int DT, bool AK, bool BKK, int EDGE>
+template <int DT, bool AK, bool BKK, int EDGE, int SPLIT>
 __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE>& B,
                                             typename Io<DT>::T* C, int64_t ldc) {
     using T = typename Io<DT>::T;
     constexpr int WE = EDGE / 2, F = WE / 32;   // edge of a wave's part, in 32-wide blocks
     constexpr int BK = Io<DT>::BK, SUB = DT == 0 ? 16 : 8;
-    __shared__ __attribute__((aligned(16))) T sa[2][Staged<DT, AK, EDGE>::SIZE], sb[2][Staged<DT, BKK, EDGE>::SIZE];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int SA = Staged<DT, AK, EDGE>::SIZE, SB = Staged<DT, BKK, EDGE>::SIZE;
+    __shared__ __attribute__((aligned(16))) T buf_a[SPLIT][2][SA], buf_b[SPLIT][2][SB];
+    const int lane = threadIdx.x & 63, id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = id & 3, part = SPLIT > 1 ? id >> 2 : 0;
     const int l32 = lane & 31, gl = lane >> 5, wm = wave >> 1, wn = wave & 1;
+    T (&sa)[2][SA] = buf_a[part];
+    T (&sb)[2][SB] = buf_b[part];
     const bool work = wm * WE < A.side && wn * WE < B.side;
     f32x16 acc[F][F];
 #pragma unroll
@@ -208,18 +237,19 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
         for (int j = 0; j < F; ++j) acc[i][j] = f32x16{};
     if (A.kd > 0) {
         u32x4 ra[Staged<DT, AK, EDGE>::NCH], rb[Staged<DT, BKK, EDGE>::NCH];
-        A.load(0, ra);
-        B.load(0, rb);
-        Staged<DT, AK, EDGE>::put(sa[0], ra);
-        Staged<DT, BKK, EDGE>::put(sb[0], rb);
+        A.load(part * BK, ra);   // past kd: zeros
+        B.load(part * BK, rb);
+        A.put(part * BK, sa[0], ra);
+        B.put(part * BK, sb[0], rb);
         __syncthreads();
-        for (int k0 = 0, cur = 0; k0 < A.kd; k0 += BK, cur ^= 1) {
-            const bool more = k0 + BK < A.kd;
+        for (int k0 = 0, cur = 0; k0 < A.kd; k0 += SPLIT * BK, cur ^= 1) {   // the same number of steps in every part
+            const int next = k0 + (SPLIT + part) * BK;
+            const bool more = next < A.kd;
             if (more) {
-                A.load(k0 + BK, ra);
-                B.load(k0 + BK, rb);
+                A.load(next, ra);
+                B.load(next, rb);
             }
-            if (work) {
+            if (work && k0 + part * BK < A.kd) {
 #pragma unroll
                 for (int kk = 0; kk < BK / SUB; ++kk) {
                     u32x4 av[F], bv[F];
@@ -243,11 +273,24 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
                 }
             }
             if (more) {
-                Staged<DT, AK, EDGE>::put(sa[cur ^ 1], ra);
-                Staged<DT, BKK, EDGE>::put(sb[cur ^ 1], rb);
+                A.put(next, sa[cur ^ 1], ra);
+                B.put(next, sb[cur ^ 1], rb);
             }
             __syncthreads();
         }
+    }
+    if constexpr (SPLIT > 1) {
+        static_assert(F == 1 && sizeof(buf_a) >= (SPLIT - 1) * 4 * 64 * 16 * sizeof(float), "the parts' sums fit");
+        float* sums = reinterpret_cast<float*>(&buf_a[0][0][0]);   // no longer read (last barrier)
+        if (part > 0)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sums[(((part - 1) * 4 + wave) * 16 + e) * 64 + lane] = acc[0][0][e];
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int o = 0; o < SPLIT - 1; ++o)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[0][0][e] += sums[((o * 4 + wave) * 16 + e) * 64 + lane];
     }
 #pragma unroll
     for (int i = 0; i < F; ++i) {
@@ -279,27 +322,27 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
     }
 }
 
-template <int DT, bool WT, int EDGE>
-__global__ __launch_bounds__(256) void grouped_mm_staged(const GroupedArgs a) {
+template <int DT, bool WT, int EDGE, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT) void grouped_mm_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
     GroupTile t;
     if (!find_tile(a, EDGE, (a.ndim + EDGE - 1) / EDGE, t)) return;
     const int64_t m0 = (int64_t)t.row0 + t.mt * EDGE;
     const int n0 = t.nt * EDGE;
     Staged<DT, true, EDGE> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
-                       min(EDGE, t.rows - t.mt * EDGE), a.kdim};
-    Staged<DT, WT, EDGE> B{nullptr, 0, min(EDGE, a.ndim - n0), a.kdim};
+                             min(EDGE, t.rows - t.mt * EDGE), a.kdim, 0};
+    Staged<DT, WT, EDGE> B{nullptr, 0, min(EDGE, a.ndim - n0), a.kdim, n0};
     if (t.e < a.n) {
         B.ld = a.w_ld[t.e];
         B.p = reinterpret_cast<const T*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
     } else {
         A.kd = B.kd = 0;   // rows of no expert: zeros
     }
-    staged_tile<DT, true, WT, EDGE>(A, B, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
+    staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
 }
 
-template <int DT, int EDGE>
-__global__ __launch_bounds__(256) void grouped_wgrad_staged(const GroupedArgs a) {
+template <int DT, int EDGE, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT) void grouped_wgrad_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
     const int ntk = (a.kdim + EDGE - 1) / EDGE, ntn = (a.ndim + EDGE - 1) / EDGE;
     const int total = a.n * ntk * ntn, per = (total + 7) / 8;
@@ -311,9 +354,9 @@ __global__ __launch_bounds__(256) void grouped_wgrad_staged(const GroupedArgs a)
     slot_rows(a, e, lo, hi);
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int kd = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
-    const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(EDGE, a.kdim - i0), kd};
-    const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(EDGE, a.ndim - j0), kd};
-    staged_tile<DT, false, false, EDGE>(A, B, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
+    const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(EDGE, a.kdim - i0), kd, i0};
+    const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(EDGE, a.ndim - j0), kd, j0};
+    staged_tile<DT, false, false, EDGE, SPLIT>(A, B, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1000,19 +1043,29 @@ double mm_expect(const GroupedArgs& a, int edge) {
 // from three quarters of a tile a CU, else staged with tiles of 128 from one a
 // CU.  Weight gradients alike: 1 x 1024 x 1024 x 1024 (16 tiles of 256) 30
 // against 7 us staged, 1 x 256 x 4096 x 4096 (256 tiles) 19 against 27 us.
-enum class Kernel { Thin, Big, Staged128, Staged64 };
+enum class Kernel { Thin, Big, Staged128, Staged64, Split64 };
 bool enough_big(double tiles) { return tiles >= 0.75 * device_cus_or_256(); }
+// Four parts of a workgroup share a tile's steps; one such workgroup fits a CU.
+// In us without and with: weight gradients 2 x 4528 x 925 x 39 35 and 22, 1 x
+// 1024 x 512 x 512 11.9 and 9.4, 16 x 8192 x 256 x 256 (8 steps) 9.3 and 8.8;
+// products (rows of all experts) 4 x 300 x 4095 x 500 55 and 30, in fp32 129
+// and 93, with K = 512 in fp32 19.6 and 17.4.
+bool split(const GroupedArgs& a, double tiles, int64_t k) {
+    return tiles <= device_cus_or_256() && k >= 8 * (a.dtype == 0 ? Io<0>::BK : Io<1>::BK);
+}
 Kernel mm_kernel(const GroupedArgs& a) {
     if (a.dtype == 0 && a.vec) {
         const bool big = enough_big(mm_expect(a, kBig));
         if (a.rows <= (big ? 16 : 32) * (int64_t)a.n) return Kernel::Thin;
         if (big) return Kernel::Big;
     }
-    return mm_expect(a, 128) < device_cus_or_256() ? Kernel::Staged64 : Kernel::Staged128;
+    if (mm_expect(a, 128) >= device_cus_or_256()) return Kernel::Staged128;
+    return split(a, mm_expect(a, 64), a.kdim) ? Kernel::Split64 : Kernel::Staged64;
 }
 Kernel wgrad_kernel(const GroupedArgs& a) {
     if (a.dtype == 0 && a.vec && enough_big((double)wgrad_tiles(a, kBig))) return Kernel::Big;
-    return wgrad_tiles(a, 128) < device_cus_or_256() ? Kernel::Staged64 : Kernel::Staged128;
+    if (wgrad_tiles(a, 128) >= device_cus_or_256()) return Kernel::Staged128;
+    return split(a, (double)wgrad_tiles(a, 64), a.rows / a.n) ? Kernel::Split64 : Kernel::Staged64;
 }
 int edge_of(Kernel k) { return k == Kernel::Big ? kBig : k == Kernel::Staged128 ? 128 : 64; }
 
@@ -1030,8 +1083,9 @@ static uint32_t big_grid(int64_t tiles) { return (uint32_t)std::min<int64_t>(til
 
 template <int DT, bool WT>
 static void mm_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t s) {
-    if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 64>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 128>), grid, dim3(256), 0, s, a);
+    if (k == Kernel::Split64) hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 64, 4>), grid, dim3(1024), 0, s, a);
+    else if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 64, 1>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grouped_mm_staged<DT, WT, 128, 1>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) {
@@ -1056,8 +1110,9 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
 
 template <int DT>
 static void wgrad_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t s) {
-    if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grouped_wgrad_staged<DT, 128>), grid, dim3(256), 0, s, a);
+    if (k == Kernel::Split64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 4>), grid, dim3(1024), 0, s, a);
+    else if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 1>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grouped_wgrad_staged<DT, 128, 1>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
