@@ -361,7 +361,7 @@ himuon_status_t himuon_pair_stats_workspace(const himuon_matrix_t* a, int32_t n,
  * weights are K x N) a multiple of 8 take the fast path.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT (null pointer, n < 1, shapes that do not
  * match), HIMUON_ERR_UNSUPPORTED (dtype), HIMUON_ERR_LAYOUT (alignment, a side
- * above INT32_MAX, or more output tiles than a launch can hold),
+ * above INT32_MAX - 4096, or more output tiles than a launch can hold),
  * HIMUON_ERR_OVERLAP, HIMUON_ERR_HIP.
  */
 himuon_status_t himuon_grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, int32_t n, int32_t trans_w,
@@ -377,10 +377,20 @@ himuon_status_t himuon_grouped_mm(const himuon_matrix_t* X, const himuon_matrix_
  *            rows); they must not overlap each other, X or D.  For weights
  *            stored N x K, pass D as X and X as D.
  * ends     : as for himuon_grouped_mm; rows past ends[n-1] count nowhere.
- * Errors as for himuon_grouped_mm.
+ * workspace: device scratch of at least himuon_grouped_wgrad_workspace bytes,
+ *            16-byte aligned; may be NULL when that is 0.  Where G is small and
+ *            the rows are many, these are cut into parts whose sums are added in
+ *            order.
+ * Errors as for himuon_grouped_mm, and HIMUON_ERR_WORKSPACE.
  */
 himuon_status_t himuon_grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D, const int32_t* ends,
-                                     const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* stream);
+                                     const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace himuon_grouped_wgrad needs for operands of these shapes
+ * (the pointers are not read): at most 4 MiB.  Host-side only. */
+himuon_status_t himuon_grouped_wgrad_workspace(const himuon_matrix_t* X, const himuon_matrix_t* D, int32_t n,
+                                               himuon_dtype_t dt, size_t* bytes);
 
 /* Element type of a device array of vocabulary ids. */
 typedef enum himuon_index {

@@ -188,6 +188,29 @@ def test_narrow_and_long(cuda, K, N, dt):
         assert torch.isnan(base).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("counts,K,N", [([5000], 40, 48), ([9, 0, 6001, 2000], 130, 65), ([2100, 2100], 128, 256), ([12345], 8, 3),
+                                          ([9, 0, 13001, 5000], 130, 65)])
+def test_rows_in_parts(cuda, counts, K, N, dt):
+    """Weight gradients whose rows are cut into parts: experts with fewer rows
+    than parts, rows past the last expert, the workspace given or not, and no
+    write outside it."""
+    print(f"rows in parts {counts} {K}x{N} {dt}", flush=True)
+    M, n = sum(counts) + 77, len(counts)
+    x, d = randn((M, K), dt, 40), randn((M, N), dt, 41)
+    x[M - 77:] = float("nan")
+    need = H.himuon_grouped_wgrad_workspace(x, d, n)
+    first = check_wgrad(x, d, counts, dt)
+    if need == 0:   # too few rows an expert
+        assert M // n < 2560
+        return
+    ws = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    g = H.himuon_grouped_wgrad(x, d, ends_of(counts), workspace=ws)
+    assert torch.equal(g, first) and torch.all(ws[need:] == 0x5a)
+    with pytest.raises(H.HimuonError):
+        H.himuon_grouped_wgrad(x, d, ends_of(counts), workspace=ws[:need - 16])
+
+
 def test_many_experts_and_no_rows(cuda):
     """More experts than one launch holds, and calls without a row."""
     n, K, N = 600, 40, 24

@@ -28,9 +28,10 @@ def mm(x=sd(10, 64, ptr=at(0)), w=None, n=None, tr=0, ends=at(5), y=sd(10, 32, p
     return H.lib.himuon_grouped_mm(ref(x), mats(w) if w else None, len(w) if n is None else n, tr, ends, ref(y), dt, None)
 
 
-def wgrad(x=sd(10, 64, ptr=at(0)), d=sd(10, 32, ptr=at(1)), ends=at(5), g=None, n=None, dt=H.BF16):
+def wgrad(x=sd(10, 64, ptr=at(0)), d=sd(10, 32, ptr=at(1)), ends=at(5), g=None, n=None, dt=H.BF16, ws=None, nbytes=0):
     g = [sd(64, 32, ptr=at(2)), sd(64, 32, ptr=at(3))] if g is None else g
-    return H.lib.himuon_grouped_wgrad(ref(x), ref(d), ends, mats(g) if g else None, len(g) if n is None else n, dt, None)
+    return H.lib.himuon_grouped_wgrad(ref(x), ref(d), ends, mats(g) if g else None, len(g) if n is None else n, dt, ws,
+                                      nbytes, None)
 
 
 def test_grouped_refusals():
@@ -65,6 +66,19 @@ def test_wgrad_refusals():
     assert wgrad(g=[sd(64, 32, ptr=at(2) + 1)]) == LAYOUT
     assert wgrad(g=[sd(64, 32, ptr=at(2)), sd(64, 32, ptr=at(2) + 2048)]) == OVERLAP
     assert wgrad(g=[sd(64, 32, ptr=at(0))]) == wgrad(g=[sd(64, 32, ptr=at(1))]) == wgrad(g=[sd(64, 32, ptr=at(5))]) == OVERLAP
+    # many rows and a small gradient: parts of the rows in a workspace
+    rows = 1 << 16
+    need = ctypes.c_size_t(0)
+    size = lambda x, d, n, dt=H.BF16: H.lib.himuon_grouped_wgrad_workspace(ref(x), ref(d), n, dt, ctypes.byref(need))
+    x, d = sd(rows, 64, ptr=1 << 40), sd(rows, 32, ptr=1 << 41)
+    assert size(x, d, 2) == OK and 0 < need.value <= 4 << 20
+    assert wgrad(x=x, d=d) == wgrad(x=x, d=d, ws=at(7), nbytes=need.value - 1) == wgrad(x=x, d=d, nbytes=need.value) == WORKSPACE
+    assert wgrad(x=x, d=d, ws=at(7) + 8, nbytes=need.value) == LAYOUT
+    assert size(sd(10, 64), sd(10, 32), 2) == OK and need.value == 0
+    assert size(sd(0, 64), sd(0, 32), 2) == OK and need.value == 0
+    assert size(None, d, 2) == size(x, None, 2) == size(x, d, 0) == size(x, sd(10, 32), 2) == INVALID
+    assert size(sd((1 << 31) - 1, 64), sd((1 << 31) - 1, 32), 2) == LAYOUT
+    assert size(x, d, 2, H.BF16_PRECISE) == UNSUPPORTED
     # more output tiles than a launch can hold
     wide = (1 << 24) - 8
     assert wgrad(x=sd(1, wide, ptr=at(0)), d=sd(1, wide, ptr=at(9)), g=[sd(wide, wide, ptr=1 << 40)]) == LAYOUT

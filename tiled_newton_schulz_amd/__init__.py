@@ -29,7 +29,8 @@ NOALLOC_SCRATCH_BYTES = 128 << 20
 EXPORTS = ["himuon_plan", "himuon_workspace_size", "himuon_tiled_ns", "himuon_tiled_ns_noalloc",
            "himuon_tiled_ns_schedule",
            "himuon_muon_step", "himuon_gram_ns", "himuon_gram_ns_workspace", "himuon_pair_stats",
-           "himuon_pair_stats_workspace", "himuon_grouped_mm", "himuon_grouped_wgrad", "himuon_distill",
+           "himuon_pair_stats_workspace", "himuon_grouped_mm", "himuon_grouped_wgrad",
+           "himuon_grouped_wgrad_workspace", "himuon_distill",
            "himuon_distill_workspace", "himuon_distill_grad", "himuon_token_logprobs",
            "himuon_token_logprobs_workspace", "himuon_token_logprobs_grad", "himuon_status_string",
            "himuon_last_hip_error", "himuon_version"]
@@ -106,7 +107,8 @@ def _load():
     E = ctypes.c_int
     for name, args in {
             "himuon_grouped_mm": [M, M, I, I, V, M, E, V],
-            "himuon_grouped_wgrad": [M, M, V, M, I, E, V],
+            "himuon_grouped_wgrad": [M, M, V, M, I, E, V, Z, V],
+            "himuon_grouped_wgrad_workspace": [M, M, I, E, P(Z)],
             "himuon_distill": [M, V, E, M, F, I, V, V, V, M, E, V, Z, V],
             "himuon_distill_workspace": [M, E, I, P(Z)],
             "himuon_distill_grad": [M, V, E, M, F, I, V, V, M, E, V],
@@ -532,7 +534,17 @@ def himuon_grouped_mm(x, w, ends, out=None, stream=None):
     return out
 
 
-def himuon_grouped_wgrad(x, dy, ends, out=None, stream=None):
+def himuon_grouped_wgrad_workspace(x, dy, n: int) -> int:
+    """Workspace bytes himuon_grouped_wgrad needs for operands like x and dy and
+    n experts."""
+    need = ctypes.c_size_t(0)
+    a, b = _rows(x), _rows(dy)
+    _check(lib.himuon_grouped_wgrad_workspace(ctypes.byref(a), ctypes.byref(b), n, _dtype_code(x), ctypes.byref(need)),
+           "himuon_grouped_wgrad_workspace")
+    return need.value
+
+
+def himuon_grouped_wgrad(x, dy, ends, out=None, workspace=None, stream=None):
     """The weight gradients x_e^T dy_e of every expert, (n, K, N) or the given
     `out` (as matrices() takes them; transposed views are written as stored).
     Zero for an expert without rows."""
@@ -550,8 +562,11 @@ def himuon_grouped_wgrad(x, dy, ends, out=None, stream=None):
         if g.n != n or g.shape != (x.shape[1], dy.shape[1]):
             raise ValueError("out must hold one (K, N) matrix per expert")
         a, b = (_rows(dy), _rows(x)) if g.transposed else (_rows(x), _rows(dy))
-        _check(lib.himuon_grouped_wgrad(ctypes.byref(a), ctypes.byref(b), _ends(ends, n, x.device), g.array, n,
-                                        _dtype_code(x), s), "himuon_grouped_wgrad")
+        code = _dtype_code(x)
+        keep, wp, wb = _scratch(lib.himuon_grouped_wgrad_workspace, "himuon_grouped_wgrad_workspace", workspace,
+                                x.device, ctypes.byref(a), ctypes.byref(b), n, code)
+        _check(lib.himuon_grouped_wgrad(ctypes.byref(a), ctypes.byref(b), _ends(ends, n, x.device), g.array, n, code,
+                                        wp, wb, s), "himuon_grouped_wgrad")
     return out
 
 

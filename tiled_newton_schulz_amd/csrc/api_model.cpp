@@ -46,6 +46,18 @@ Extent array_extent(const void* p, int64_t bytes) {
     return extent_of(himuon_matrix_t{const_cast<void*>(p), 1, bytes, bytes}, 1, 0);
 }
 
+#define HIMUON_TRY(call)                           \
+    do {                                           \
+        const himuon_status_t st_ = (call);        \
+        if (st_ != HIMUON_OK) return st_;          \
+    } while (0)
+
+himuon_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (need == 0) return HIMUON_OK;
+    if (ws == nullptr || bytes < need) return HIMUON_ERR_WORKSPACE;
+    return aligned(ws, 16) ? HIMUON_OK : HIMUON_ERR_LAYOUT;
+}
+
 // ---- the experts' products ------------------------------------------------------
 // Checks of X, ends and n; fills the arguments every launch of the call shares.
 himuon_status_t grouped_args(const himuon_matrix_t* X, const himuon_matrix_t* W, int32_t n, const int32_t* ends,
@@ -60,6 +72,8 @@ himuon_status_t grouped_args(const himuon_matrix_t* X, const himuon_matrix_t* W,
         if ((st = check_matrix(W[e], es)) != HIMUON_OK) return st;
         if (W[e].rows != W[0].rows || W[e].cols != W[0].cols) return HIMUON_ERR_INVALID_ARGUMENT;
     }
+    for (const int64_t side : {X->rows, X->cols, W[0].rows, W[0].cols})
+        if (side > kMaxSide) return HIMUON_ERR_LAYOUT;
     a.x = X->ptr;
     a.x_ld = X->ld;
     a.ends = ends;
@@ -123,8 +137,20 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
     });
 }
 
+// Workspace of the launch that takes the most: the parts' sums.
+size_t wgrad_bytes(GroupedArgs a, int32_t n) {
+    int64_t most = 0;
+    for (const int32_t some : {std::min(kExperts, n), (n - 1) % kExperts + 1}) {
+        a.n = some;
+        const int64_t parts = a.rows > 0 ? grouped_wgrad_parts(a) : 1;
+        if (parts > 1) most = std::max(most, parts * grouped_wgrad_part_bytes(a));
+    }
+    return (size_t)most;
+}
+
 himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D, const int32_t* ends,
-                              const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* stream) {
+                              const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* workspace,
+                              size_t workspace_bytes, void* stream) {
     GroupedArgs a{};
     himuon_status_t st = grouped_args(X, G, n, ends, dt, a);
     if (st != HIMUON_OK) return st;
@@ -147,7 +173,10 @@ himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D
     a.vec = chunked(*X) && chunked(*D) && a.kdim % 8 == 0 && a.ndim % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(G[e]);
     if (!grids_fit(a, n, grouped_wgrad_grid)) return HIMUON_ERR_LAYOUT;
+    HIMUON_TRY(check_workspace(workspace, workspace_bytes, wgrad_bytes(a, n)));
+    a.sums = reinterpret_cast<float*>(workspace);
     return each_launch(a, G, n, [&] {
+        a.parts = grouped_wgrad_parts(a);
         const hipError_t e = launch_grouped_wgrad(a, reinterpret_cast<hipStream_t>(stream));
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);
     });
@@ -169,12 +198,6 @@ size_t keys_bytes(int64_t rows, const SegPlan& p, int32_t top) {
 size_t distill_bytes(int32_t rows, int32_t cols, int32_t dtype, bool with_grad) {
     if (rows == 0 || (with_grad && distill_on_chip(rows, cols, dtype))) return 0;
     return parts_bytes(rows, seg_plan(rows, cols, dtype)) + (with_grad ? (size_t)rows * 2 * sizeof(float) : 0);
-}
-
-himuon_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
-    if (need == 0) return HIMUON_OK;
-    if (ws == nullptr || bytes < need) return HIMUON_ERR_WORKSPACE;
-    return aligned(ws, 16) ? HIMUON_OK : HIMUON_ERR_LAYOUT;
 }
 
 // Shape checks of the workspace queries.
@@ -241,12 +264,6 @@ struct Arrays {
         return HIMUON_OK;
     }
 };
-
-#define HIMUON_TRY(call)                           \
-    do {                                           \
-        const himuon_status_t st_ = (call);        \
-        if (st_ != HIMUON_OK) return st_;          \
-    } while (0)
 
 himuon_status_t teacher_args(const himuon_matrix_t* Z, const void* idx, const himuon_matrix_t* T, int32_t normalize,
                              LogitsArgs& a, Arrays& arr) {
@@ -400,8 +417,25 @@ himuon_status_t himuon_grouped_mm(const himuon_matrix_t* X, const himuon_matrix_
 }
 
 himuon_status_t himuon_grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D, const int32_t* ends,
-                                     const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* stream) {
-    return guarded([&] { return grouped_wgrad(X, D, ends, G, n, dt, stream); });
+                                     const himuon_matrix_t* G, int32_t n, himuon_dtype_t dt, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    return guarded([&] { return grouped_wgrad(X, D, ends, G, n, dt, workspace, workspace_bytes, stream); });
+}
+
+himuon_status_t himuon_grouped_wgrad_workspace(const himuon_matrix_t* X, const himuon_matrix_t* D, int32_t n,
+                                               himuon_dtype_t dt, size_t* bytes) {
+    if (X == nullptr || D == nullptr || bytes == nullptr || n < 1) return HIMUON_ERR_INVALID_ARGUMENT;
+    if (X->rows < 0 || X->rows != D->rows || X->cols < 1 || D->cols < 1) return HIMUON_ERR_INVALID_ARGUMENT;
+    for (const int64_t side : {X->rows, X->cols, D->cols})
+        if (side > kMaxSide) return HIMUON_ERR_LAYOUT;
+    HIMUON_TRY(check_dtype(dt));
+    GroupedArgs a{};   // vec = 0: as many parts as any alignment may take
+    a.rows = (int32_t)X->rows;
+    a.kdim = (int32_t)X->cols;
+    a.ndim = (int32_t)D->cols;
+    a.dtype = dt == HIMUON_FP32 ? 1 : 0;
+    *bytes = wgrad_bytes(a, n);
+    return HIMUON_OK;
 }
 
 himuon_status_t himuon_distill(const himuon_matrix_t* Z, const void* idx, himuon_index_t it, const himuon_matrix_t* T,

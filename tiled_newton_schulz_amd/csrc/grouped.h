@@ -10,6 +10,9 @@ namespace himuon {
 // slot they fill four slots for each lane of a wave (find_tile in grouped.hip).
 constexpr int kExperts = 255;
 
+// Longest side: the kernels step past an end by less than this leaves to 2^31.
+constexpr int64_t kMaxSide = INT32_MAX - 4096;
+
 // One launch of Y = X W_e (or X W_e^T) or of G_e = X_e^T D_e.
 struct GroupedArgs {
     const void* x;           // M x K
@@ -23,6 +26,8 @@ struct GroupedArgs {
     int32_t last;            // product: this launch also zeroes the rows past the last expert
     int32_t dtype;           // 0 bf16, 1 fp32
     int32_t vec;             // rows and widths allow 16-byte chunks
+    float* sums;             // weight gradient: workspace of the parts' sums, or null
+    int32_t parts;           // weight gradient: parts an expert's rows are cut into
     void* w[kExperts];       // product: weights; weight gradient: results
     int64_t w_ld[kExperts];
 };
@@ -30,6 +35,10 @@ struct GroupedArgs {
 // Most tiles of a launch (checked before any launch).
 int64_t grouped_mm_grid(const GroupedArgs& a);
 int64_t grouped_wgrad_grid(const GroupedArgs& a);
+// Parts worth cutting the experts' rows of a weight gradient into (1: none), and
+// the workspace of a part.
+int32_t grouped_wgrad_parts(const GroupedArgs& a);
+int64_t grouped_wgrad_part_bytes(const GroupedArgs& a);
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s);
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
 

@@ -18,6 +18,8 @@
 namespace himuon {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 struct GroupTile {
     int e;          // slot of the launch (a.n: the rows that belong to no expert)
     int row0;       // first row of the expert
@@ -214,11 +216,47 @@ struct Staged {
     }
 };
 
-// C = A B of one tile (operands exchanged in the MFMA, so that a lane holds
-// runs of four columns of one row).
-template <int DT, bool AK, bool BKK, int EDGE, int SPLIT>
-__device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE>& B,
-                                            typename Io<DT>::T* C, int64_t ldc) {
+// Stores a wave's part of a tile: block (i, j) of rows and columns 32 i, 32 j
+// from (r0, c0), an element of C a lane and register as the MFMA leaves them.
+template <int DT, int F>
+__device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename Io<DT>::T* C, int64_t ldc, int rows,
+                                           int cols, int r0, int c0) {
+    using T = typename Io<DT>::T;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+        const int row = r0 + i * 32 + l32;
+        if (row >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int col = c0 + j * 32 + m * 8 + gl * 4;
+                T* at = C + row * ldc + col;
+                if (col + 4 <= cols) {
+                    if constexpr (DT == 0) {
+                        const Loose8 v = {u32x2{pack2(acc[i][j][4 * m], acc[i][j][4 * m + 1]),
+                                                pack2(acc[i][j][4 * m + 2], acc[i][j][4 * m + 3])}};
+                        *reinterpret_cast<Loose8*>(at) = v;
+                    } else {
+                        Loose16 v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v.v[e] = __float_as_uint(acc[i][j][4 * m + e]);
+                        *reinterpret_cast<Loose16*>(at) = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < cols) at[e] = Io<DT>::cv(acc[i][j][4 * m + e]);
+                }
+            }
+    }
+}
+
+// A B of one tile (operands exchanged in the MFMA, so that a lane holds runs of
+// four columns of one row): done(sums, wave) in each wave that ends with some.
+template <int DT, bool AK, bool BKK, int EDGE, int SPLIT, typename Done>
+__device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE>& B, Done done) {
     using T = typename Io<DT>::T;
     constexpr int WE = EDGE / 2, F = WE / 32;   // edge of a wave's part, in 32-wide blocks
     constexpr int BK = Io<DT>::BK, SUB = DT == 0 ? 16 : 8;
@@ -226,7 +264,7 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
     __shared__ __attribute__((aligned(16))) T buf_a[SPLIT][2][SA], buf_b[SPLIT][2][SB];
     const int lane = threadIdx.x & 63, id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = id & 3, part = SPLIT > 1 ? id >> 2 : 0;
-    const int l32 = lane & 31, gl = lane >> 5, wm = wave >> 1, wn = wave & 1;
+    const int wm = wave >> 1, wn = wave & 1;
     T (&sa)[2][SA] = buf_a[part];
     T (&sb)[2][SB] = buf_b[part];
     const bool work = wm * WE < A.side && wn * WE < B.side;
@@ -292,34 +330,7 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[0][0][e] += sums[((o * 4 + wave) * 16 + e) * 64 + lane];
     }
-#pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int row = wm * WE + i * 32 + l32;
-        if (row >= A.side) continue;
-#pragma unroll
-        for (int j = 0; j < F; ++j)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int col = wn * WE + j * 32 + m * 8 + gl * 4;
-                T* at = C + row * ldc + col;
-                if (col + 4 <= B.side) {
-                    if constexpr (DT == 0) {
-                        const Loose8 v = {u32x2{pack2(acc[i][j][4 * m], acc[i][j][4 * m + 1]),
-                                                pack2(acc[i][j][4 * m + 2], acc[i][j][4 * m + 3])}};
-                        *reinterpret_cast<Loose8*>(at) = v;
-                    } else {
-                        Loose16 v;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v.v[e] = __float_as_uint(acc[i][j][4 * m + e]);
-                        *reinterpret_cast<Loose16*>(at) = v;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < B.side) at[e] = Io<DT>::cv(acc[i][j][4 * m + e]);
-                }
-            }
-    }
+    done(acc, wave);
 }
 
 template <int DT, bool WT, int EDGE, int SPLIT>
@@ -338,25 +349,73 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_mm_staged(const GroupedAr
     } else {
         A.kd = B.kd = 0;   // rows of no expert: zeros
     }
-    staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld);
+    staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave) __attribute__((always_inline)) {
+        put_blocks<DT>(acc, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, A.side, B.side,
+                       (wave >> 1) * (EDGE / 2), (wave & 1) * (EDGE / 2));
+    });
 }
 
-template <int DT, int EDGE, int SPLIT>
+// PARTS: a workgroup takes one of the parts that an expert's rows are cut into,
+// and leaves its sums for grouped_wgrad_join.
+template <int DT, int EDGE, int SPLIT, bool PARTS>
 __global__ __launch_bounds__(256 * SPLIT) void grouped_wgrad_staged(const GroupedArgs a) {
     using T = typename Io<DT>::T;
+    constexpr int BK = Io<DT>::BK;
     const int ntk = (a.kdim + EDGE - 1) / EDGE, ntn = (a.ndim + EDGE - 1) / EDGE;
-    const int total = a.n * ntk * ntn, per = (total + 7) / 8;
+    const int tiles = a.n * ntk * ntn, total = PARTS ? tiles * a.parts : tiles, per = (total + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
-    const int e = id / (ntk * ntn), b = id % (ntk * ntn);
+    // the tiles of one part of an expert next to each other: they share its rows
+    const int e = id / (PARTS ? ntk * ntn * a.parts : ntk * ntn), b = id % (ntk * ntn);
     const int i0 = (b % ntk) * EDGE, j0 = (b / ntk) * EDGE;
     int lo, hi;
     slot_rows(a, e, lo, hi);
+    hi = max(lo, hi);
+    const int part = id / (ntk * ntn) % (PARTS ? a.parts : 1);
+    if (PARTS) {
+        const int64_t steps = (hi - lo + BK - 1) / BK;   // the host leaves room for such roundings
+        const int from = (int)(steps * part / a.parts) * BK, to = (int)(steps * (part + 1) / a.parts) * BK;
+        hi = min(hi, lo + to);
+        lo += from;
+    }
     lo = __builtin_amdgcn_readfirstlane(lo);
-    const int kd = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
+    const int kd = __builtin_amdgcn_readfirstlane(hi - lo);
     const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(EDGE, a.kdim - i0), kd, i0};
     const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(EDGE, a.ndim - j0), kd, j0};
-    staged_tile<DT, false, false, EDGE, SPLIT>(A, B, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e]);
+    staged_tile<DT, false, false, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave) __attribute__((always_inline)) {
+        if constexpr (PARTS) {
+            f32x4* to = reinterpret_cast<f32x4*>(a.sums + ((int64_t)part * tiles + e * ntk * ntn + b) * (EDGE * EDGE)) +
+                        wave * 256 + (threadIdx.x & 63);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                to[m * 64] = f32x4{acc[0][0][4 * m], acc[0][0][4 * m + 1], acc[0][0][4 * m + 2], acc[0][0][4 * m + 3]};
+        } else {
+            put_blocks<DT>(acc, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], A.side, B.side,
+                           (wave >> 1) * (EDGE / 2), (wave & 1) * (EDGE / 2));
+        }
+    });
+}
+
+// Adds the parts' sums of one 64 x 64 tile, in order.
+template <int DT>
+__global__ __launch_bounds__(256) void grouped_wgrad_join(const GroupedArgs a) {
+    using T = typename Io<DT>::T;
+    const int ntk = (a.kdim + 63) / 64, ntn = (a.ndim + 63) / 64, tiles = a.n * ntk * ntn;
+    const int id = blockIdx.x, e = id / (ntk * ntn), b = id % (ntk * ntn);
+    const int i0 = (b % ntk) * 64, j0 = (b / ntk) * 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const f32x4* from = reinterpret_cast<const f32x4*>(a.sums + (int64_t)id * 4096) + wave * 256 + lane;
+    f32x16 acc[1][1] = {};
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p, from += (int64_t)tiles * 1024)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 v = from[m * 64];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][0][4 * m + i] += v[i];
+        }
+    put_blocks<DT>(acc, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], min(64, a.kdim - i0),
+                   min(64, a.ndim - j0), (wave >> 1) * 32, (wave & 1) * 32);
 }
 
 // ---------------------------------------------------------------------------
@@ -909,7 +968,6 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
 // ---------------------------------------------------------------------------
 constexpr int kThinRows = 16, kThinCols = 64, kRing = 4, kThinK = 32;
 constexpr int kThinStage = (kThinRows + kThinCols) * kThinK;   // elements
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <bool WT>
 __global__ __launch_bounds__(256) void grouped_mm_thin(const GroupedArgs a) {
@@ -1078,6 +1136,21 @@ int64_t grouped_mm_grid(const GroupedArgs& a) {
 }
 int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, edge_of(wgrad_kernel(a))), 8) * 8; }
 
+// Where the tiles split in a workgroup are at most half the CUs, the rows are
+// cut into parts that fill them, of at least four rounds of a workgroup's four
+// steps each; not below the rows where joining the parts (a second launch) costs
+// what they gain.  In us without and with, 256 x 256: bf16 2048 rows 12.4 and
+// 11.8 on the device and 12.6 and 15.6 with the host's calls, 3000 rows 16.4 and
+// 13.8, 8192 rows 37 and 13.5; fp32 1024 rows 25 and 18, 4096 rows 85 and 20.
+// 32768 x 512 x 512 in bf16: 160 and 50.
+int32_t grouped_wgrad_parts(const GroupedArgs& a) {
+    if (wgrad_kernel(a) != Kernel::Split64) return 1;
+    const int64_t steps = a.rows / a.n / (a.dtype == 0 ? Io<0>::BK : Io<1>::BK);
+    if (steps < (a.dtype == 0 ? 40 : 32)) return 1;
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(device_cus_or_256() / wgrad_tiles(a, 64), steps / 16));
+}
+int64_t grouped_wgrad_part_bytes(const GroupedArgs& a) { return wgrad_tiles(a, 64) * 64 * 64 * 4; }
+
 // Workgroups of the 256 x 256 kernel for at most `tiles` tiles: one fits a CU.
 static uint32_t big_grid(int64_t tiles) { return (uint32_t)std::min<int64_t>(tiles, device_cus_or_256() / 8 * 8); }
 
@@ -1110,9 +1183,18 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
 
 template <int DT>
 static void wgrad_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t s) {
-    if (k == Kernel::Split64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 4>), grid, dim3(1024), 0, s, a);
-    else if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 1>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grouped_wgrad_staged<DT, 128, 1>), grid, dim3(256), 0, s, a);
+    if (k == Kernel::Split64 && a.parts > 1) {
+        const int64_t tiles = wgrad_tiles(a, 64);
+        hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 4, true>), dim3((uint32_t)(cdiv(tiles * a.parts, 8) * 8)),
+                           dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((grouped_wgrad_join<DT>), dim3((uint32_t)tiles), dim3(256), 0, s, a);
+    } else if (k == Kernel::Split64) {
+        hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 4, false>), grid, dim3(1024), 0, s, a);
+    } else if (k == Kernel::Staged64) {
+        hipLaunchKernelGGL((grouped_wgrad_staged<DT, 64, 1, false>), grid, dim3(256), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((grouped_wgrad_staged<DT, 128, 1, false>), grid, dim3(256), 0, s, a);
+    }
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
