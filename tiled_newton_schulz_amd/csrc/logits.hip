@@ -608,8 +608,11 @@ __device__ __forceinline__ void put_alternative(const LogitsArgs& a, int64_t row
 // ---- forward passes --------------------------------------------------------------
 // One workgroup per segment.  KIND 0: distillation, 1: log probabilities, 2:
 // the same with alternatives.
+// (Alternatives over bf16 logits are held to the registers of six waves a SIMD
+// instead of five: 4000 x 65537 with 5 of them 147 and 138 us, with 20 187 and 178.
+// In fp32 it spills more and loses: 2048 x 65536 with 5 of them 104 and 111 us.)
 template <int DT, int U, int KIND, bool FL>
-__global__ __launch_bounds__(kThreads) void forward_kernel(const LogitsArgs a) {
+__global__ __launch_bounds__(kThreads, KIND == 2 && DT == 0 ? 6 : 1) void forward_kernel(const LogitsArgs a) {
     __shared__ Stats part[4];
     const int64_t row = blockIdx.x / a.plan.segs;
     const int seg = blockIdx.x % a.plan.segs;
