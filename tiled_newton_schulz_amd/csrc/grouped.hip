@@ -453,6 +453,12 @@ __global__ __launch_bounds__(256) void grouped_wgrad_join(const GroupedArgs a) {
 // Both leave the 16 lanes that read together on 64 different banks.
 // The products run with the operands exchanged (columns as the MFMA's rows), so
 // that a lane ends with runs of four consecutive columns of one row.
+//
+// Measured: 8 experts of 2048 x 4096 x 4096 420 us either way (1.3 PFLOP/s; a
+// step takes 1.47 us, 82 % of the matrix rate at the clock the chip holds), their
+// weight gradients 460 us.  64 experts with ragged shares, 4096 x 1408: products
+// of 16384 rows 266 us, input gradients of 32768 rows 385 - 408 us, weight
+// gradients 450 us (0.74 GB of results).
 // ---------------------------------------------------------------------------
 constexpr int kBig = 256;                  // tile edge
 constexpr int kBK = 64;                    // k of a step
@@ -970,6 +976,7 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
 // columns of W, 5 KB), loaded straight from global memory: two workgroups hold
 // 120 KB a CU in flight, which covers the memory's latency.  In a larger tile
 // the same weights would wait for a pipeline's start and end at every tile.
+// 96 rows over 64 experts of 4096 x 1408: 107 us, 5.7 TB/s.
 //   along k: rows of four 16-byte chunks, chunk c of row r at c ^ ((r / 4) & 3)
 //   along i: 32 k rows of eight chunks, chunk c of row k at c ^ (2 (k & 2))
 // ---------------------------------------------------------------------------
