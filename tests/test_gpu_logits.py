@@ -197,6 +197,28 @@ def test_logprobs_nan_and_inf_stay_in_their_row(cuda):
     assert torch.isnan(g[1:4]).all() and torch.all(g[4] == 0) and torch.isfinite(g[keep]).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("V,top", [(600001, 64), (600001, 5), (131072, 64), (131071, 33), (40000, 64)])
+def test_many_segments_and_alternatives(cuda, V, top, dt):
+    """Rows of one value, of few, and masked but for some ids, next to ordinary
+    ones: the alternatives are those of a stable sort, whatever the segments."""
+    print(f"many segments {V} top {top} {dt}", flush=True)
+    z = logits(4, V, dt, 60)
+    z[1] = -2.5
+    z[2] = torch.round(z[2])
+    z[3] = -INF
+    z[3, 17::V // 40] = 1.0
+    r = H.himuon_token_logprobs(z.cuda(), top=top)
+    order = torch.sort(z.float(), dim=1, descending=True, stable=True).indices[:, :top]
+    assert torch.equal(r.top_idx.cpu().long(), order)
+    s = z.double()
+    want = (s - torch.logsumexp(s, 1, keepdim=True)).gather(1, order)
+    _, d = row_bound(s, V)
+    there = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(r.top_logp.cpu()), there)
+    near(r.top_logp[there.cuda()], want[there], d[:, None].expand_as(want)[there], "top")
+
+
 def test_logprobs_without_tokens_and_rows(cuda):
     z = logits(5, 777, "bf16", 10)
     r = H.himuon_token_logprobs(z.cuda(), top=3)
