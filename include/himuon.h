@@ -388,7 +388,7 @@ himuon_status_t himuon_grouped_wgrad(const himuon_matrix_t* X, const himuon_matr
                                      size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace himuon_grouped_wgrad needs for operands of these shapes
- * (the pointers are not read): at most 4 MiB.  Host-side only. */
+ * (the pointers are not read): at most 16 MiB.  Host-side only. */
 himuon_status_t himuon_grouped_wgrad_workspace(const himuon_matrix_t* X, const himuon_matrix_t* D, int32_t n,
                                                himuon_dtype_t dt, size_t* bytes);
 

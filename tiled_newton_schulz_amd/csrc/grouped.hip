@@ -1150,18 +1150,28 @@ int64_t grouped_mm_grid(const GroupedArgs& a) {
 }
 int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, edge_of(wgrad_kernel(a))), 8) * 8; }
 
-// Where the tiles split in a workgroup are at most half the CUs, the rows are
-// cut into parts that fill them, of at least four rounds of a workgroup's four
-// steps each; not below the rows where joining the parts (a second launch) costs
-// what they gain.  In us without and with, 256 x 256: bf16 2048 rows 12.4 and
-// 11.8 on the device and 12.6 and 15.6 with the host's calls, 3000 rows 16.4 and
-// 13.8, 8192 rows 37 and 13.5; fp32 1024 rows 25 and 18, 4096 rows 85 and 20.
-// 32768 x 512 x 512 in bf16: 160 and 50.
+// Where the tiles split in a workgroup are few and the rows many, the rows are cut
+// into the parts that should take the least time: rounds of one workgroup a CU, at
+// 1.1 us (fp32: 2.6) for a workgroup's four steps, at least four times these a
+// part; 5 us for the join, and its bytes.  In us without and with, 256 x 256: bf16
+// 2048 rows 12.4 and 11.8 on the device and 12.6 and 15.6 with the host's calls
+// (so not cut), 3000 rows 16.4 and 13.8, 8192 rows 37 and 13.5; fp32 1024 rows 25
+// and 18, 4096 rows 85 and 20.  32768 x 512 x 512 in bf16: 160 and 50.
+constexpr int64_t kMostParts = 1024;   // of all tiles: 16 MiB
 int32_t grouped_wgrad_parts(const GroupedArgs& a) {
     if (wgrad_kernel(a) != Kernel::Split64) return 1;
-    const int64_t steps = a.rows / a.n / (a.dtype == 0 ? Io<0>::BK : Io<1>::BK);
-    if (steps < (a.dtype == 0 ? 40 : 32)) return 1;
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(device_cus_or_256() / wgrad_tiles(a, 64), steps / 16));
+    const int64_t steps = a.rows / a.n / (a.dtype == 0 ? Io<0>::BK : Io<1>::BK), tiles = wgrad_tiles(a, 64);
+    int64_t best = 1;
+    double least = 1e30;
+    for (int64_t p = 1; p == 1 || (p <= steps / 16 && p * tiles <= kMostParts); ++p) {
+        const double rounds = (double)cdiv(tiles * p, device_cus_or_256()) * (double)steps / (4.0 * (double)p);
+        const double t = rounds * (a.dtype == 0 ? 1.1 : 2.6) + (p > 1 ? 5.0 + 0.0067 * (double)(p * tiles) : 0.0);
+        if (t < least) {
+            least = t;
+            best = p;
+        }
+    }
+    return (int32_t)best;
 }
 int64_t grouped_wgrad_part_bytes(const GroupedArgs& a) { return wgrad_tiles(a, 64) * 64 * 64 * 4; }
 
