@@ -117,7 +117,6 @@ template <> struct Io<1> {
     __device__ static T cv(float f) { return f; }
 };
 struct __attribute__((packed, aligned(2))) Loose16 { u32x4 v; };   // 16 bytes at an element's alignment
-struct __attribute__((packed, aligned(2))) Loose8 { u32x2 v; };
 
 // One operand of a tile: `side` rows (or columns) of the tile by kd.
 template <int DT, bool ALONG_K, int EDGE>
@@ -217,44 +216,57 @@ struct Staged {
 };
 
 // Stores a wave's part of a tile: block (i, j) of rows and columns 32 i, 32 j
-// from (r0, c0), an element of C a lane and register as the MFMA leaves them.
+// from (r0, c0).  A lane holds runs of four columns of a row; through the wave's
+// own 32 x 32 elements of LDS (chunk c of row r at c ^ (r / 2 & 3), fp32 c ^ (r &
+// 7)) neighbouring lanes store whole rows of a block.  (Stored from registers in
+// runs of four, the 0.13 GB of gradients of 4 rows over 15 experts of 1340 x 3339
+// took 59 instead of 37 us.)
 template <int DT, int F>
-__device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename Io<DT>::T* C, int64_t ldc, int rows,
-                                           int cols, int r0, int c0) {
+__device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename Io<DT>::T* scratch,
+                                           typename Io<DT>::T* C, int64_t ldc, int rows, int cols, int r0, int c0) {
     using T = typename Io<DT>::T;
+    constexpr int EPC = Io<DT>::EPC, CPR = 32 / EPC, RPP = 64 / CPR;   // chunks of a row, rows stored at a time
     const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+    auto at = [&](int r, int c) { return scratch + r * 32 + (c ^ ((DT == 0 ? r >> 1 : r) & (CPR - 1))) * EPC; };
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int row = r0 + i * 32 + l32;
-        if (row >= rows) continue;
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j)
+        for (int j = 0; j < F; ++j) {
+            const int br = r0 + i * 32, bc = c0 + j * 32;
+            if (br >= rows || bc >= cols) continue;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const int col = c0 + j * 32 + m * 8 + gl * 4;
-                T* at = C + row * ldc + col;
-                if (col + 4 <= cols) {
-                    if constexpr (DT == 0) {
-                        const Loose8 v = {u32x2{pack2(acc[i][j][4 * m], acc[i][j][4 * m + 1]),
-                                                pack2(acc[i][j][4 * m + 2], acc[i][j][4 * m + 3])}};
-                        *reinterpret_cast<Loose8*>(at) = v;
-                    } else {
-                        Loose16 v;
+                const auto& v = acc[i][j];
+                if constexpr (DT == 0)
+                    *reinterpret_cast<u32x2*>(at(l32, m) + 4 * gl) =
+                        u32x2{pack2(v[4 * m], v[4 * m + 1]), pack2(v[4 * m + 2], v[4 * m + 3])};
+                else
+                    *reinterpret_cast<f32x4*>(at(l32, 2 * m + gl)) =
+                        f32x4{v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]};
+            }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v.v[e] = __float_as_uint(acc[i][j][4 * m + e]);
-                        *reinterpret_cast<Loose16*>(at) = v;
-                    }
+            for (int p = 0; p < 32 / RPP; ++p) {
+                const int r = p * RPP + lane / CPR, c = lane % CPR, col = bc + c * EPC;
+                if (br + r >= rows || col >= cols) continue;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, c));
+                T* to = C + (br + r) * ldc + col;
+                if (col + EPC <= cols) {
+                    *reinterpret_cast<Loose16*>(to) = Loose16{v};
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < cols) at[e] = Io<DT>::cv(acc[i][j][4 * m + e]);
+                    for (int e = 0; e < EPC - 1; ++e)
+                        if (col + e < cols) {
+                            if constexpr (DT == 0) to[e] = (unsigned short)(v[e >> 1] >> (16 * (e & 1)));
+                            else to[e] = __uint_as_float(v[e]);
+                        }
                 }
             }
-    }
+        }
 }
 
 // A B of one tile (operands exchanged in the MFMA, so that a lane holds runs of
-// four columns of one row): done(sums, wave) in each wave that ends with some.
+// four columns of one row): done(sums, wave, its scratch) in each wave that ends
+// with some.
 template <int DT, bool AK, bool BKK, int EDGE, int SPLIT, typename Done>
 __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE>& B, Done done) {
     using T = typename Io<DT>::T;
@@ -330,7 +342,9 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[0][0][e] += sums[((o * 4 + wave) * 16 + e) * 64 + lane];
     }
-    done(acc, wave);
+    // (buf_b is no longer read either)
+    static_assert(sizeof(buf_b) >= 4 * 32 * 32 * sizeof(T), "the waves' scratch fits");
+    done(acc, wave, &buf_b[0][0][0] + wave * (32 * 32));
 }
 
 template <int DT, bool WT, int EDGE, int SPLIT>
@@ -349,8 +363,8 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_mm_staged(const GroupedAr
     } else {
         A.kd = B.kd = 0;   // rows of no expert: zeros
     }
-    staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave) __attribute__((always_inline)) {
-        put_blocks<DT>(acc, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, A.side, B.side,
+    staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
+        put_blocks<DT>(acc, scratch, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, A.side, B.side,
                        (wave >> 1) * (EDGE / 2), (wave & 1) * (EDGE / 2));
     });
 }
@@ -380,9 +394,11 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_wgrad_staged(const Groupe
     }
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int kd = __builtin_amdgcn_readfirstlane(hi - lo);
-    const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld, min(EDGE, a.kdim - i0), kd, i0};
-    const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld, min(EDGE, a.ndim - j0), kd, j0};
-    staged_tile<DT, false, false, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave) __attribute__((always_inline)) {
+    const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld,
+                                    min(EDGE, a.kdim - i0), kd, i0};
+    const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld,
+                                    min(EDGE, a.ndim - j0), kd, j0};
+    staged_tile<DT, false, false, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
         if constexpr (PARTS) {
             f32x4* to = reinterpret_cast<f32x4*>(a.sums + ((int64_t)part * tiles + e * ntk * ntn + b) * (EDGE * EDGE)) +
                         wave * 256 + (threadIdx.x & 63);
@@ -390,8 +406,8 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_wgrad_staged(const Groupe
             for (int m = 0; m < 4; ++m)
                 to[m * 64] = f32x4{acc[0][0][4 * m], acc[0][0][4 * m + 1], acc[0][0][4 * m + 2], acc[0][0][4 * m + 3]};
         } else {
-            put_blocks<DT>(acc, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], A.side, B.side,
-                           (wave >> 1) * (EDGE / 2), (wave & 1) * (EDGE / 2));
+            put_blocks<DT>(acc, scratch, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], A.side,
+                           B.side, (wave >> 1) * (EDGE / 2), (wave & 1) * (EDGE / 2));
         }
     });
 }
@@ -414,8 +430,9 @@ __global__ __launch_bounds__(256) void grouped_wgrad_join(const GroupedArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[0][0][4 * m + i] += v[i];
         }
-    put_blocks<DT>(acc, reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e], min(64, a.kdim - i0),
-                   min(64, a.ndim - j0), (wave >> 1) * 32, (wave & 1) * 32);
+    __shared__ __attribute__((aligned(16))) T scratch[4][32 * 32];
+    put_blocks<DT>(acc, scratch[wave], reinterpret_cast<T*>(a.w[e]) + i0 * a.w_ld[e] + j0, a.w_ld[e],
+                   min(64, a.kdim - i0), min(64, a.ndim - j0), (wave >> 1) * 32, (wave & 1) * 32);
 }
 
 // ---------------------------------------------------------------------------
