@@ -421,6 +421,8 @@ typedef enum himuon_index {
  * lse      : device array of N x 2 fp32, written, or NULL: log sum exp of s
  *            rounded to fp32, and what that rounding lost (a row masked by the
  *            type's lowest value would lose it all), for himuon_distill_grad.
+ *            The row's largest s enters as the fp32 product of the logit and
+ *            1 / temperature, held to fp32's finite range.
  * dZ       : N x V in dt, written, or NULL.  It may be Z itself (the same
  *            pointer and ld); any other overlap is refused.
  * workspace: device scratch of at least himuon_distill_workspace bytes,

@@ -465,3 +465,96 @@ def test_same_bits_streams_graph(cuda, N, V):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(calls(), got))
+
+
+# ---- logits of large magnitude ---------------------------------------------------------
+# Differences of equal logits are exactly zero whatever their size, and the next
+# other value of the rows below is so far off that its q is 0 in fp32.  So q is
+# 1 / n over the n largest, and the bounds are those of a row with A = 0.
+FAR = {"-1e9": -1e9, "1e9": 1e9, "lowest": None}
+
+
+def far_rows(V, dt, base):
+    """All at base; one id far above; two values, the larger one on a third of
+    the ids (both past fp32's range under a temperature below 1 for the lowest
+    value); base among -inf; an ordinary row."""
+    low = torch.finfo(TYPES[dt]).min
+    b = low if base is None else base
+    z = torch.full((5, V), b)
+    z[1, V // 2] = 2.0 if b < 0 else 1.5 * b
+    z[2] = b * (0.875 if b < 0 else 1.25)
+    z[2, torch.arange(V) % 3 != 0] = b
+    z[3, torch.arange(V) % 7 != 0] = -INF
+    z[4] = torch.randn(V, generator=gen(200)) * 3
+    return z.to(TYPES[dt])
+
+
+def far_softmax(z, tau):
+    """log q and q in fp64, from differences."""
+    x = z.double()
+    s = (x - x.amax(1, keepdim=True)) / tau
+    lq = s - torch.logsumexp(s, 1, keepdim=True)
+    return lq, torch.exp(lq)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.5])
+@pytest.mark.parametrize("base", list(FAR))
+@pytest.mark.parametrize("V", [1000, 40001])
+def test_gradients_of_far_logits(cuda, V, base, tau, dt):
+    print(f"far logits {V} {base} {tau} {dt}", flush=True)
+    z = far_rows(V, dt, FAR[base])
+    N, k = z.shape[0], 4
+    zg = z.cuda()
+    lq, q = far_softmax(z, tau)
+    d = 2.0 ** -20 * (8 + math.log(V) + 40) + (V / 64 + 64) * 2.0 ** -24   # 40: the ordinary row's s
+    # entries among the largest logits of each row (other losses are as large as the logits)
+    best = torch.sort(z.float(), dim=1, descending=True, stable=True).indices[:, :k]
+    best[1, 1:] = -1
+    t = torch.randn((N, k), generator=gen(201))
+    w = torch.rand(N, generator=gen(202)) + 0.5
+    there = best >= 0
+    u = torch.where(there, t.double() / tau, -INF)
+    lp = torch.log_softmax(u, 1)
+    p = torch.exp(lp)
+    pick = lq.gather(1, best.clamp(min=0))
+    loss = w.double() * torch.where(there, p * (lp - pick), 0.0).sum(1)
+    dp = 2.0 ** -20 * 16 + 65 * 2.0 ** -24
+    gap = torch.where(there, lp.abs() + pick.abs(), 0.0).amax(1)
+    lb = w.double() * (d + dp * (1 + gap))
+    dense = torch.zeros_like(q).scatter_add_(1, best.clamp(min=0), torch.where(there, p, 0.0))
+    c = (w.double() / tau)[:, None]
+    grad = c * (q - dense)
+    gb = c * (q * (d + dp) + dense * dp) + ROUND[dt] * grad.abs() + 1e-38
+    args = (zg, best.cuda(), t.cuda())
+    fused = H.himuon_distill(*args, tau, weight=w.cuda(), grad=True)
+    apart = H.himuon_distill(*args, tau, weight=w.cuda())
+    g2 = H.himuon_distill_grad(*args, apart.lse, w.cuda(), tau)
+    in_place = zg.clone()
+    H.himuon_distill_grad(in_place, best.cuda(), t.cuda(), apart.lse, w.cuda(), tau, out=in_place)
+    assert torch.equal(in_place, g2)
+    for r in (fused, apart):
+        near(r.loss, loss, lb, "loss")
+        assert torch.isfinite(r.lse).all()
+    near(fused.grad, grad, gb, "fused gradient")
+    near(g2, grad, gb, "gradient")
+
+    tokens = best[:, 0].clone()
+    r = H.himuon_token_logprobs(zg, tokens.cuda(), top=4, temperature=tau)
+    Hq = -torch.where(q > 0, q * lq, 0.0).sum(1)
+    dH = d * (8 + math.log(V) + 40)
+    near(r.logp, lq.gather(1, tokens[:, None])[:, 0], d, "logp")
+    near(r.entropy, Hq, dH, "entropy")
+    gl, gh = torch.randn(N, generator=gen(203)), torch.randn(N, generator=gen(204))
+    hot = torch.zeros_like(q)
+    hot[torch.arange(N), tokens] = 1.0
+    qlq = torch.where(q > 0, q * lq, 0.0)
+    for a, b in ((gl, gh), (gl, None), (None, gh)):
+        got = H.himuon_token_logprobs_grad(zg, tokens.cuda(), r.lse, r.entropy, None if a is None else a.cuda(),
+                                           None if b is None else b.cuda(), temperature=tau)
+        A = torch.zeros(N).double() if a is None else a.double()
+        B = torch.zeros(N).double() if b is None else b.double()
+        want = (A[:, None] * (hot - q) - B[:, None] * (qlq + q * Hq[:, None])) / tau
+        err = (A.abs()[:, None] * (q * d + 2.0 ** -22 * (hot + q))
+               + B.abs()[:, None] * (q * (d + dH) + (qlq.abs() + q * Hq[:, None]) * (d + 2.0 ** -21))) / tau
+        near(got, want, err + ROUND[dt] * want.abs() + 1e-38, "gradient of logp and entropy")

@@ -4,7 +4,8 @@
 //     S = sum exp(s - s_m),  E = sum exp(s - s_m) (z - m),
 //     lse = s_m + log S,     entropy = log S - E / (S temperature),
 // all in fp32.  The differences are taken before they are scaled, so a row
-// masked by the type's lowest value loses nothing.
+// masked by the type's lowest value loses nothing; a gradient from a known lse
+// takes s rounded as the lse has it, and the differences after (Softmax).
 //
 // The work is a stream over the logits (HBM bound, a read for a forward pass, a
 // read and a write for a gradient), so rows move in 16-byte chunks and stay
@@ -184,34 +185,52 @@ __device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
 
 // log sum exp of a row as hi + lo: hi is its fp32 value and lo what that
 // rounding lost, which counts where it is large (a row masked by the lowest
-// value would lose log S altogether).
+// value would lose log S altogether).  The largest s enters as the rounded
+// product, held to fp32's range: where it reaches +-kFltMax, hi does not say
+// which logit was the largest (Softmax::far).
+constexpr float kFltMax = 3.40282346638528859812e38f;
 struct Lse {
     float hi, lo;
 };
 __device__ __forceinline__ Lse make_lse(const Stats& st, float inv_temp) {
+#pragma clang fp contract(off)
     if (st.s == 0.f) return {kNegInf, 0.f};   // -inf only
-    const float m = st.m * inv_temp, l = ln_hw(st.s), hi = m + l;
+    const float m = fminf(fmaxf(st.m * inv_temp, -kFltMax), kFltMax), l = ln_hw(st.s), hi = m + l;
     const float lo = fabsf(m) >= fabsf(l) ? (m - hi) + l : (l - hi) + m;
     return {hi, lo};
 }
 __device__ __forceinline__ float entropy_of(const Stats& st, float inv_temp) {
     return st.s == 0.f ? 0.f : ln_hw(st.s) - inv_temp * (st.e / st.s);
 }
-// log q of a logit.
-__device__ __forceinline__ float log_q(float z, float inv_temp, Lse l) {
-    const float s = z * inv_temp;
-    if (s == kNegInf && l.hi == l.hi) return kNegInf;
-    return (s - l.hi) - l.lo;
+// log q of a logit of a row with these statistics.
+__device__ __forceinline__ float log_q(float z, float inv_temp, const Stats& st) {
+    if (z == kNegInf && st.s == st.s) return kNegInf;
+    return (z - st.m) * inv_temp - ln_hw(st.s);
 }
-// q = exp2(fma(fma(z, inv_temp, -hi), log2 e, -lo log2 e)); a row of -inf only
-// takes hi = 0 and has q = 0.
+// q and log q of the logits of a row from its lse alone:
+//     d = z mul - sub,   log q = slope d - lo,   q = exp2(d k - lo log2 e).
+// With mul = inv_temp, sub = hi the product is rounded before hi is taken off, as
+// make_lse rounds the largest one (unrounded it would be off from it by half a
+// unit of s, 32 where |s| is 1e9, whatever the logits' differences are).  A far
+// row takes m, its largest logit, in hi's place: mul = 1, sub = m.  A row of -inf
+// only takes sub = 0 and has q = 0.
 struct Softmax {
-    float inv_temp, neg_hi, neg_lo2;
-    __device__ __forceinline__ Softmax(float it, Lse l)
-        : inv_temp(it), neg_hi(l.hi == kNegInf ? 0.f : -l.hi), neg_lo2(-l.lo * kLog2e) {}
-    __device__ __forceinline__ float operator()(float z) const {
-        return exp2_hw(__builtin_fmaf(__builtin_fmaf(z, inv_temp, neg_hi), kLog2e, neg_lo2));
+    float mul, sub, slope, k, lo, neg_lo2;
+    __device__ __forceinline__ static bool far(Lse l) { return fabsf(l.hi) == kFltMax; }
+    __device__ __forceinline__ Softmax(float inv_temp, Lse l)
+        : mul(inv_temp), sub(l.hi == kNegInf ? 0.f : l.hi), slope(1.f), k(kLog2e), lo(l.lo), neg_lo2(-l.lo * kLog2e) {}
+    __device__ __forceinline__ void set_far(float inv_temp, float m) {
+        mul = 1.f;
+        sub = m;
+        slope = inv_temp;
+        k = inv_temp * kLog2e;
     }
+    __device__ __forceinline__ float diff(float z) const {
+#pragma clang fp contract(off)
+        return z * mul - sub;
+    }
+    __device__ __forceinline__ float at(float d) const { return exp2_hw(__builtin_fmaf(d, k, neg_lo2)); }
+    __device__ __forceinline__ float operator()(float z) const { return at(diff(z)); }
 };
 
 __device__ __forceinline__ void put_lse(const LogitsArgs& a, int64_t row, Lse l) {
@@ -325,9 +344,9 @@ struct Sum {
     __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
 };
 
-// Loss of a row whose lse is known.  NT 256: a workgroup; 64: a wave (k <= 64).
+// Loss of a row whose statistics are known.  NT 256: a workgroup; 64: a wave (k <= 64).
 template <int DT, bool FL, int NT>
-__device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, Lse l) {
+__device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, const Stats& st, Lse l) {
     constexpr int KE = NT == 64 ? 1 : kMaxEntries / NT;
     const int tid = threadIdx.x % NT;
     const Row<DT, FL> z(a.z, a.z_ld, row, a.cols);
@@ -361,7 +380,7 @@ __device__ __forceinline__ void distill_loss(const LogitsArgs& a, int64_t row, L
         if (e == 0.f) continue;   // adds nothing, whatever the student has there
         sum[0] += e;
         sum[1] += e * (x[i].u - M);
-        sum[2] += e * log_q(x[i].z, a.inv_temp, l);
+        sum[2] += e * log_q(x[i].z, a.inv_temp, st);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) sum[i] = wsum(sum[i]);
@@ -583,7 +602,7 @@ __device__ __forceinline__ void keys_top(TopShared& sh, int top, const uint64_t 
 // Results of a row of log probabilities.
 template <int DT, bool FL>
 __device__ __forceinline__ void put_logprobs(const LogitsArgs& a, int64_t row, int tok, const Stats& st, Lse l) {
-    if (a.logp) a.logp[row] = log_q(Row<DT, FL>(a.z, a.z_ld, row, a.cols).load_elem(tok), a.inv_temp, l);
+    if (a.logp) a.logp[row] = log_q(Row<DT, FL>(a.z, a.z_ld, row, a.cols).load_elem(tok), a.inv_temp, st);
     if (a.entropy) a.entropy[row] = st.s == st.s ? entropy_of(st, a.inv_temp) : st.s;
     put_lse(a, row, l);
 }
@@ -600,9 +619,10 @@ __device__ __forceinline__ void skip_logprobs(const LogitsArgs& a, int64_t row) 
         a.top_logp[row * a.top + j] = kNegInf;
     }
 }
-__device__ __forceinline__ void put_alternative(const LogitsArgs& a, int64_t row, Lse l, int rank, uint64_t key) {
+__device__ __forceinline__ void put_alternative(const LogitsArgs& a, int64_t row, const Stats& st, int rank,
+                                                uint64_t key) {
     a.top_idx[row * a.top + rank] = key_id(key);
-    a.top_logp[row * a.top + rank] = log_q(key_value(key), a.inv_temp, l);
+    a.top_logp[row * a.top + rank] = log_q(key_value(key), a.inv_temp, st);
 }
 
 // ---- forward passes --------------------------------------------------------------
@@ -652,13 +672,13 @@ __global__ __launch_bounds__(kThreads, KIND == 2 && DT == 0 ? 6 : 1) void forwar
     if (!alone && threadIdx.x == 0) a.part[row * a.plan.segs + seg] = {st.m, st.s, st.e, 0.f};
     const Lse l = make_lse(st, a.inv_temp);
     if constexpr (KIND == 0) {
-        if (alone) distill_loss<DT, FL, kThreads>(a, row, l);
+        if (alone) distill_loss<DT, FL, kThreads>(a, row, st, l);
     } else {
         if (alone && threadIdx.x == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
         if constexpr (KIND == 2) {
             __shared__ TopShared sh;
             segment_top<DT, FL, U>(sh, a.top, z, c0, cn, cm, mine, [&](int rank, uint64_t key) {
-                if (alone) put_alternative(a, row, l, rank, key);
+                if (alone) put_alternative(a, row, st, rank, key);
                 else a.keys[(row * a.plan.segs + seg) * a.top + rank] = key;
             });
         }
@@ -705,7 +725,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
     }
     const Lse l = make_lse(st, a.inv_temp);
     if constexpr (KIND == 0) {
-        distill_loss<DT, FL, NT>(a, row, l);
+        distill_loss<DT, FL, NT>(a, row, st, l);
     } else {
         if (threadIdx.x % NT == 0) put_logprobs<DT, FL>(a, row, tok, st, l);
         if constexpr (KIND == 2) {
@@ -719,7 +739,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
                                        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), j) << 32;
                     rank += o > key ? 1 : 0;
                 }
-                if (key != 0 && rank < a.top) put_alternative(a, row, l, rank, key);
+                if (key != 0 && rank < a.top) put_alternative(a, row, st, rank, key);
             } else {
                 __shared__ TopShared sh;
                 __shared__ uint64_t carry[kMaxTop];
@@ -747,7 +767,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
                 __syncthreads();
                 const int found = sh.count;
                 if (found <= kCand) {
-                    auto put = [&](int rank, uint64_t k) { put_alternative(a, row, l, rank, k); };
+                    auto put = [&](int rank, uint64_t k) { put_alternative(a, row, st, rank, k); };
                     rank_candidates(sh, found, a.top, put);
                     for (int j = found + threadIdx.x; j < a.top; j += kThreads) put(j, 0);
                     return;
@@ -765,7 +785,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
                     const bool last = b + batch >= n;
                     __syncthreads();
                     keys_top(sh, a.top, key, [&](int rank, uint64_t k) {
-                        if (last) put_alternative(a, row, l, rank, k);
+                        if (last) put_alternative(a, row, st, rank, k);
                         else carry[rank] = k;
                     });
                     __syncthreads();
@@ -780,13 +800,28 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(const LogitsArgs a) {
 // In place each chunk is read before its own element is written, and the
 // entries' logits before any.  HBM bound: fp32 1024 x 65536 82 us (6.5 TB/s), bf16
 // 2048 x 131072 223 us (4.8 TB/s).
+// A far row (Softmax::far: s past fp32's range, or fp32 rows of the lowest value
+// only) is left to the workgroup of its first segment, which looks for the
+// largest logit first.
 template <int DT, int KIND, bool FL>
 __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
     constexpr int U = 4, EPC = kEpc<DT>;
     const int64_t row = blockIdx.x / a.plan.segs;
     const int seg = blockIdx.x % a.plan.segs;
     const Row<DT, FL> z(a.z, a.z_ld, row, a.cols), dz(a.dz, a.dz_ld, row, a.cols);
-    const int c0 = seg * a.plan.chunks, c1 = min(z.chunks(), c0 + a.plan.chunks);
+    int c0 = seg * a.plan.chunks, c1 = min(z.chunks(), c0 + a.plan.chunks);
+    const Lse l = get_lse(a, row);
+    Softmax q(a.inv_temp, l);
+    if (Softmax::far(l)) {
+        if (seg > 0) return;
+        c1 = z.chunks();
+        float m[1] = {kNegInf};
+        for (int v = threadIdx.x; v < a.cols; v += kThreads) m[0] = fmaxf(m[0], z.load_elem(v));
+        m[0] = wmax(m[0]);
+        __shared__ float red0[4][1];
+        block_join<kThreads>(m, red0, kNegInf, Max());
+        q.set_far(a.inv_temp, m[0]);
+    }
     const int v_lo = max(0, z.first(c0)), v_hi = min(a.cols, z.first(c1));   // this segment's columns
 
     // ---- what the row's gradient is made of ----
@@ -796,14 +831,12 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
     int fix_id[KE];
     float fix[KE];
     bool live = true;
-    Lse l = {0.f, 0.f};
     if constexpr (KIND == 1) {
         if (a.tokens) tok = load_id(a.tokens, a.idx64, row, a.cols);
         gl = a.g_logp ? a.g_logp[row] * a.inv_temp : 0.f;
         gh = a.g_entropy ? a.g_entropy[row] * a.inv_temp : 0.f;
         if (a.tokens && tok < 0) gl = gh = 0.f;
         live = !(gl == 0.f && gh == 0.f);
-        if (live) l = get_lse(a, row);
     } else {
         __shared__ float red1[4][2], red2[4][1];
         __shared__ int ids[kMaxEntries];
@@ -824,7 +857,6 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
             block_join<kThreads>(mx, red1, kNegInf, Max());
             live = mx[1] != 0.f;
             if (live) {
-                l = get_lse(a, row);
                 const float M = a.normalize ? mx[0] : 0.f;
                 float sum[1] = {0.f};
 #pragma unroll
@@ -842,7 +874,6 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
                 const float P = a.normalize ? 1.f : sum[0], r = a.normalize ? 1.f / sum[0] : 1.f;
                 const float cw = w * a.inv_temp;
                 scale = cw * P;
-                const Softmax q(a.inv_temp, l);
 #pragma unroll
                 for (int i = 0; i < KE; ++i) {
                     fix_id[i] = x[i].id >= v_lo && x[i].id < v_hi ? x[i].id : -1;
@@ -859,10 +890,9 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
         return;
     }
 
-    const Softmax q(a.inv_temp, l);
-    // log probabilities: dz = -q (gl + gh (s - lse + H)), and gl more at the token
+    // log probabilities: dz = -q (gl + gh (log q + H)), and gl more at the token
     const float H = KIND == 1 && gh != 0.f ? a.entropy[row] : 0.f;
-    const float slope = a.inv_temp * gh, at0 = gl + (gh != 0.f ? gh * ((H - l.hi) - l.lo) : 0.f);
+    const float slope = q.slope * gh, at0 = gl + (gh != 0.f ? gh * (H - q.lo) : 0.f);
     for (int b = c0; b < c1; b += kThreads * U) {
         u32x4 r[U];
 #pragma unroll
@@ -877,13 +907,13 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
             float g[EPC];
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
-                const float x = elem<DT>(r[u], e), p = q(x);
+                const float d = q.diff(elem<DT>(r[u], e)), p = q.at(d);
                 if constexpr (KIND == 0) {
                     g[e] = scale * p;
                 } else if (gh == 0.f) {
                     g[e] = -gl * p;
                 } else {
-                    const float t = __builtin_fmaf(x, slope, at0);
+                    const float t = __builtin_fmaf(d, slope, at0);
                     g[e] = p == 0.f ? 0.f : -p * t;
                 }
             }
@@ -983,7 +1013,9 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
         const float ref = mx[2] == kNegInf ? 0.f : mx[2], M = a.normalize ? mx[0] : 0.f;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};   // S of the row; S, E, G of the teacher
         Lse l = {0.f, 0.f};
-        float scale = 0.f, loss = 0.f, fix[KE];
+        float scale = 0.f, loss = 0.f, lg = 0.f, fix[KE];   // lg: log2 S
+        // from the largest logit, which is at hand here
+        auto q = [&](float v) { return exp2_hw(__builtin_fmaf(v - ref, c, -lg)); };
         if (live) {
 #pragma unroll
             for (int i = 0; i < KE; ++i) {
@@ -1009,10 +1041,10 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
             l = make_lse(Stats{mx[2], sum[0], 0.f}, a.inv_temp);
             const TeacherSums t = teacher_sums(a, sum[1], sum[2], sum[3]);
             // b is relative to the row's largest logit: B = -log S
-            loss = w * (t.loss + (sum[0] == 0.f ? 0.f : t.P * ln_hw(sum[0])));
+            if (sum[0] != 0.f) lg = __builtin_amdgcn_logf(sum[0]);
+            loss = w * (t.loss + t.P * (lg * kLn2));
             const float cw = w * a.inv_temp;
             scale = cw * t.P;
-            const Softmax q(a.inv_temp, l);
 #pragma unroll
             for (int i = 0; i < KE; ++i)
                 fix[i] = x[i].id >= 0 ? cw * (t.P * q(x[i].z) - t.scale * mass_at(ids, ps, a.k, x[i].id)) : 0.f;
@@ -1024,7 +1056,6 @@ __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
         stay_packed(r);
 
         // ---- the gradient, and the next row's loads ----
-        const Softmax q(a.inv_temp, l);
         const unsigned mask = live ? ~0u : 0u;   // a row that counts nothing gets zeros whatever it holds
         const int edge = edge_of(z);
 #pragma unroll
