@@ -427,8 +427,9 @@ typedef enum himuon_index {
  *            pointer and ld); any other overlap is refused.
  * workspace: device scratch of at least himuon_distill_workspace bytes,
  *            16-byte aligned; may be NULL when that is 0.
- * A row whose weight is 0, or that has no entry with p_j > 0, counts nothing:
- * its loss, lse and gradient are 0 whatever it holds.  In the other rows a logit
+ * A row whose weight is 0, or that has no entry with p_j > 0 (in fp32:
+ * exp(t_j) is 0 from about -104 down), counts nothing: its loss, lse and
+ * gradient are 0 whatever it holds.  In the other rows a logit
  * of -inf has q = 0 (an entry there gives the loss +inf); NaN or +inf logits
  * make that row's results NaN.  k up to HIMUON_MAX_ENTRIES, V up to 2^29.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (dtype, index

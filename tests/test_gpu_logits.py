@@ -558,3 +558,32 @@ def test_gradients_of_far_logits(cuda, V, base, tau, dt):
         err = (A.abs()[:, None] * (q * d + 2.0 ** -22 * (hot + q))
                + B.abs()[:, None] * (q * (d + dH) + (qlq.abs() + q * Hq[:, None]) * (d + 2.0 ** -21))) / tau
         near(got, want, err + ROUND[dt] * want.abs() + 1e-38, "gradient of logp and entropy")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [700, 60000])
+def test_teacher_without_probability(cuda, V, dt):
+    """Teacher's log probabilities whose exponentials are 0 in fp32: the row has
+    no entry with p > 0 and counts nothing, whatever its logits are; next to an
+    entry that counts they add nothing."""
+    print(f"teacher without probability {V} {dt}", flush=True)
+    N, k = 6, 5
+    z = logits(N, V, dt, 210)
+    z[1, 7] = float("nan")
+    z[2, 7] = INF
+    z[3] = -INF
+    idx, t = teacher(N, V, k, 211)
+    t = torch.log_softmax(t, 1)
+    t[:4] = torch.tensor([-200.0, -1e4, -1e30, -INF, -150.0])
+    t[4, 2:] = -300.0
+    w = torch.ones(N)
+    args = (z.cuda(), idx.cuda(), t.cuda(), 1.0, False)
+    fused = H.himuon_distill(*args, w.cuda(), grad=True)
+    apart = H.himuon_distill(*args, w.cuda())
+    g2 = H.himuon_distill_grad(z.cuda(), idx.cuda(), t.cuda(), apart.lse, w.cuda(), 1.0, False)
+    loss, grad, lse, d, lb, gb = distill64(z[4:], idx[4:], t[4:], 1.0, False, w[4:])
+    for r, g in ((fused, fused.grad), (apart, g2)):
+        assert torch.all(r.loss[:4] == 0) and torch.all(r.lse[:4] == 0) and torch.all(g[:4] == 0)
+        near(r.loss[4:], loss, lb, "loss")
+        near(r.lse[4:].double().sum(1), lse, d, "lse")
+        near(g[4:], grad, gb + ROUND[dt] * grad.abs() + 1e-38, "grad")

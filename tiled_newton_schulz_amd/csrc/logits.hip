@@ -301,6 +301,8 @@ __device__ __forceinline__ Entry load_entry(const LogitsArgs& a, const Row<DT, F
     if (x.id < 0) return x;
     const float t = a.t[row * a.t_ld + j];
     x.u = a.normalize ? t * a.inv_temp : t;
+    // no probability in fp32: as if it were -inf (a row of such entries counts nothing)
+    if (!a.normalize && exp2_hw(t * kLog2e) == 0.f) x.u = kNegInf;
     x.z = z.load_elem(x.id);
     return x;
 }
