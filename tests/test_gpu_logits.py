@@ -587,3 +587,37 @@ def test_teacher_without_probability(cuda, V, dt):
         near(r.loss[4:], loss, lb, "loss")
         near(r.lse[4:].double().sum(1), lse, d, "lse")
         near(g[4:], grad, gb + ROUND[dt] * grad.abs() + 1e-38, "grad")
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_more_rows_than_a_launch_holds(cuda, shift):
+    """A row a workgroup of 256 threads: 2^24 rows and a few take two launches,
+    whose results and skipped rows meet where the first ends."""
+    N, V, cut = (1 << 24) + 300, 8, (1 << 24) - 1
+    print(f"{N} rows, shift {shift}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(220)
+    z = torch.randn((N, V + shift), generator=g, device="cuda").bfloat16()[:, shift:]
+    tokens = torch.randint(0, V, (N,), generator=g, device="cuda")
+    tokens[cut + 1], tokens[cut + 7] = -1, V
+    idx = torch.randint(0, V, (N, 1), generator=g, device="cuda")
+    t = torch.rand((N, 1), generator=g, device="cuda") - 1.0
+    gl, gh = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    r = H.himuon_token_logprobs(z, tokens, top=2)
+    dz = H.himuon_token_logprobs_grad(z, tokens, r.lse, r.entropy, gl, gh)
+    a = H.himuon_distill(z, idx, t, normalize=False, weight=gl)
+    da = H.himuon_distill_grad(z, idx, t, a.lse, gl, normalize=False)
+    f = H.himuon_distill(z, idx, t, normalize=False, weight=gl, grad=True)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 1000), slice(cut - 500, cut + 500), slice(N - 200, N)):
+        zz, tk, ll, hh = z[rows].cpu(), tokens[rows].cpu(), gl[rows].cpu(), gh[rows].cpu()
+        part = type(r)(*[x[rows] for x in r])
+        _, ref = check_logprobs(zz, None, tk, 2, 1.0, "bf16", r=part)
+        want = H.himuon_token_logprobs_grad(z[rows], tokens[rows], part.lse.contiguous(), part.entropy.contiguous(),
+                                            gl[rows], gh[rows])
+        assert torch.equal(dz[rows], want)
+        check_logprobs_grad(zz, z[rows], tk, 1.0, "bf16", part, ref, ll, hh)
+        loss, grad, lse, d, lb, gb = distill64(zz, idx[rows].cpu(), t[rows].cpu(), 1.0, False, ll)
+        for res, dres in ((a, da), (f, f.grad)):
+            near(res.loss[rows], loss, lb, "loss")
+            near(res.lse[rows].double().sum(1), lse, d, "lse")
+            near(dres[rows], grad, gb + ROUND["bf16"] * grad.abs() + 1e-38, "grad")

@@ -20,6 +20,7 @@
 // and the elements of its first and last chunk are moved one by one.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_util.h"
 #include "logits.h"
@@ -1111,6 +1112,46 @@ bool flush(const LogitsArgs& a) {
     return a.cols % epc == 0 && on(a.z, a.z_ld) && (a.dz == nullptr || on(a.dz, a.dz_ld));
 }
 
+// The call's rows [r, r + n).
+LogitsArgs rows_of(const LogitsArgs& a, int64_t r, int32_t n) {
+    LogitsArgs b = a;
+    b.rows = n;
+    auto on = [&](auto& p, int64_t bytes) {
+        using P = std::remove_reference_t<decltype(p)>;
+        if (p != nullptr) p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)(r * bytes));
+    };
+    const int64_t es = a.dtype == 0 ? 2 : 4, id = a.idx64 ? 8 : 4;
+    on(b.z, a.z_ld * es);
+    on(b.dz, a.dz_ld * es);
+    on(b.idx, a.k * id);
+    on(b.t, a.t_ld * 4);
+    on(b.weight, 4);
+    on(b.loss, 4);
+    on(b.lse, 8);
+    on(b.tokens, id);
+    on(b.logp, 4);
+    on(b.entropy, 4);
+    on(b.top_idx, a.top * 4);
+    on(b.top_logp, a.top * 4);
+    on(b.g_logp, 4);
+    on(b.g_entropy, 4);
+    on(b.part, a.plan.segs * (int64_t)sizeof(SegStats));
+    on(b.keys, a.plan.segs * (int64_t)sizeof(uint64_t) * a.top);
+    return b;
+}
+// Launches f over all rows: a launch holds at most 2^32 - 1 threads, so rows
+// past that follow in further ones.
+template <typename F>
+hipError_t in_launches(const LogitsArgs& a, F f) {
+    const int64_t most = std::max<int64_t>(1, UINT32_MAX / kThreads / a.plan.segs);
+    if (a.rows <= most) return f(a);
+    for (int64_t r = 0; r < a.rows; r += most) {
+        const hipError_t e = f(rows_of(a, r, (int32_t)std::min<int64_t>(most, a.rows - r)));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <int DT, int KIND, bool FL>
 hipError_t forward_fl(const LogitsArgs& a, hipStream_t s) {
     const dim3 grid((uint32_t)((int64_t)a.rows * a.plan.segs)), block(kThreads);
@@ -1130,8 +1171,11 @@ hipError_t forward_fl(const LogitsArgs& a, hipStream_t s) {
 
 template <int KIND>
 hipError_t forward(const LogitsArgs& a, hipStream_t s) {
-    if (flush(a)) return a.dtype == 0 ? forward_fl<0, KIND, true>(a, s) : forward_fl<1, KIND, true>(a, s);
-    return a.dtype == 0 ? forward_fl<0, KIND, false>(a, s) : forward_fl<1, KIND, false>(a, s);
+    const bool fl = flush(a);
+    return in_launches(a, [&](const LogitsArgs& b) {
+        if (fl) return b.dtype == 0 ? forward_fl<0, KIND, true>(b, s) : forward_fl<1, KIND, true>(b, s);
+        return b.dtype == 0 ? forward_fl<0, KIND, false>(b, s) : forward_fl<1, KIND, false>(b, s);
+    });
 }
 
 template <int KIND, bool FL>
@@ -1144,7 +1188,10 @@ hipError_t grad_fl(const LogitsArgs& a, hipStream_t s) {
 template <int KIND>
 hipError_t grad(LogitsArgs a, hipStream_t s) {
     a.plan = seg_plan(a.rows, a.cols, a.dtype);
-    return flush(a) ? grad_fl<KIND, true>(a, s) : grad_fl<KIND, false>(a, s);
+    const bool fl = flush(a);
+    return in_launches(a, [&](const LogitsArgs& b) {
+        return fl ? grad_fl<KIND, true>(b, s) : grad_fl<KIND, false>(b, s);
+    });
 }
 
 template <int DT, int NT, int U, int GRID>
