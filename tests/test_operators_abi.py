@@ -163,3 +163,14 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         H.matrices([])
     with pytest.raises(ValueError):
         H.matrices(torch.zeros(2, 8, 8, 2)[..., 0].transpose(0, 1))
+
+
+def test_products_of_more_tiles_than_a_launch_holds():
+    """A workgroup of 256 threads a tile of 128 x 128 or 64 x 64, and at most
+    2^32 - 1 threads a launch: refused as more tiles than it can hold."""
+    rows = (1 << 31) - 1 - 4096   # 16,777,183 row tiles of 128, one more for each of 40 experts
+    far = [1 << 40, 1 << 45]
+    w = [sd(1, 1, ptr=at(2)) for _ in range(40)]
+    assert mm(x=sd(rows, 1, ptr=far[0]), w=w, y=sd(rows, 1, ptr=far[1])) == LAYOUT
+    g = [sd(1, rows, ptr=far[0]), sd(1, rows, ptr=far[1])]
+    assert wgrad(x=sd(1, 1, ptr=at(0)), d=sd(1, rows, ptr=1 << 50), g=g) == LAYOUT

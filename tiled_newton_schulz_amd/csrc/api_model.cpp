@@ -84,10 +84,10 @@ himuon_status_t grouped_args(const himuon_matrix_t* X, const himuon_matrix_t* W,
 }
 
 // True if every launch of the call has a grid that fits (the full ones and the last).
-bool grids_fit(GroupedArgs a, int32_t n, int64_t (*grid)(const GroupedArgs&)) {
+bool grids_fit(GroupedArgs a, int32_t n, bool (*fits)(const GroupedArgs&)) {
     for (const int32_t part : {std::min(kExperts, n), (n - 1) % kExperts + 1}) {
         a.n = part;
-        if (grid(a) > INT32_MAX / 2) return false;
+        if (!fits(a)) return false;
     }
     return true;
 }
@@ -130,7 +130,7 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
     a.ndim = (int32_t)N;
     a.vec = chunked(*X) && chunked(*Y) && K % 8 == 0 && N % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(W[e]);
-    if (!grids_fit(a, n, grouped_mm_grid)) return HIMUON_ERR_LAYOUT;
+    if (!grids_fit(a, n, grouped_mm_fits)) return HIMUON_ERR_LAYOUT;
     return each_launch(a, W, n, [&] {
         const hipError_t e = launch_grouped_mm(a, trans_w != 0, reinterpret_cast<hipStream_t>(stream));
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);
@@ -172,7 +172,7 @@ himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D
     a.ndim = (int32_t)D->cols;
     a.vec = chunked(*X) && chunked(*D) && a.kdim % 8 == 0 && a.ndim % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(G[e]);
-    if (!grids_fit(a, n, grouped_wgrad_grid)) return HIMUON_ERR_LAYOUT;
+    if (!grids_fit(a, n, grouped_wgrad_fits)) return HIMUON_ERR_LAYOUT;
     HIMUON_TRY(check_workspace(workspace, workspace_bytes, wgrad_bytes(a, n)));
     a.sums = reinterpret_cast<float*>(workspace);
     return each_launch(a, G, n, [&] {

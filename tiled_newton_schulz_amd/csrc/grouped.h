@@ -32,9 +32,9 @@ struct GroupedArgs {
     int64_t w_ld[kExperts];
 };
 
-// Most tiles of a launch (checked before any launch).
-int64_t grouped_mm_grid(const GroupedArgs& a);
-int64_t grouped_wgrad_grid(const GroupedArgs& a);
+// True if a launch can hold the tiles (checked before any launch).
+bool grouped_mm_fits(const GroupedArgs& a);
+bool grouped_wgrad_fits(const GroupedArgs& a);
 // Parts worth cutting the experts' rows of a weight gradient into (1: none), and
 // the workspace of a part.
 int32_t grouped_wgrad_parts(const GroupedArgs& a);

@@ -1158,14 +1158,25 @@ Kernel wgrad_kernel(const GroupedArgs& a) {
 }
 int edge_of(Kernel k) { return k == Kernel::Big ? kBig : k == Kernel::Staged128 ? 128 : 64; }
 
-}  // namespace
-
+// Most tiles of a launch, whole rounds of the XCDs.
 int64_t grouped_mm_grid(const GroupedArgs& a) {
     const Kernel k = mm_kernel(a);
     if (k == Kernel::Thin) return cdiv((a.rows / kThinRows + a.n + 1) * cdiv(a.ndim, kThinCols), 8) * 8;
     return cdiv(mm_tiles(a, edge_of(k)), 8) * 8;
 }
 int64_t grouped_wgrad_grid(const GroupedArgs& a) { return cdiv(wgrad_tiles(a, edge_of(wgrad_kernel(a))), 8) * 8; }
+
+// A workgroup a tile, and at most 2^32 - 1 threads a launch; the 256-tiles have
+// workgroups of their own number and count tiles in an int.
+bool fits(Kernel k, int64_t tiles) {
+    if (k == Kernel::Big) return tiles <= INT32_MAX / 2;
+    return tiles <= UINT32_MAX / (k == Kernel::Split64 ? 1024 : 256);
+}
+
+}  // namespace
+
+bool grouped_mm_fits(const GroupedArgs& a) { return fits(mm_kernel(a), grouped_mm_grid(a)); }
+bool grouped_wgrad_fits(const GroupedArgs& a) { return fits(wgrad_kernel(a), grouped_wgrad_grid(a)); }
 
 // Where the tiles split in a workgroup are few and the rows many, the rows are cut
 // into the parts that should take the least time: rounds of one workgroup a CU, at
