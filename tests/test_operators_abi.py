@@ -174,3 +174,19 @@ def test_products_of_more_tiles_than_a_launch_holds():
     assert mm(x=sd(rows, 1, ptr=far[0]), w=w, y=sd(rows, 1, ptr=far[1])) == LAYOUT
     g = [sd(1, rows, ptr=far[0]), sd(1, rows, ptr=far[1])]
     assert wgrad(x=sd(1, 1, ptr=at(0)), d=sd(1, rows, ptr=1 << 50), g=g) == LAYOUT
+
+
+def test_assembly_names_the_registers_it_writes():
+    """Inline assembly that sets m0 says so: the compiler sets it itself, for
+    instructions of its own."""
+    import glob
+    import os
+    import re
+    seen = 0
+    for path in glob.glob(os.path.join(os.path.dirname(H.__file__), "csrc", "*")):
+        text = open(path).read()
+        for block in re.findall(r"\basm\b[^;]*?\(.*?\)\s*;", text, re.S):
+            if re.search(r"s_mov_b32\s+m0\b", block):
+                seen += 1
+                assert '"m0"' in block.split(":")[-1], (path, block)
+    assert seen > 0

@@ -510,7 +510,7 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* p, int64_t bytes) {
 // register result, so nothing can be read or reused too early.
 __device__ __forceinline__ void dma16(i32x4 r, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(r) : "memory");
+                 :: "s"(lds), "v"(off), "s"(r) : "m0", "memory");
 }
 // Ends a reading slot: all but this wave's newest loads have landed and its LDS
 // reads are done; then the same of all waves.  The half that the next reading
