@@ -190,3 +190,28 @@ def test_assembly_names_the_registers_it_writes():
                 seen += 1
                 assert '"m0"' in block.split(":")[-1], (path, block)
     assert seen > 0
+
+
+def test_workspace_is_memory_of_the_operands_gpu():
+    """A workspace on another device, or one whose elements share memory (less
+    of it than its size), is refused before its address is used."""
+    torch = pytest.importorskip("torch")
+    size = lambda need: 0
+    gpu0, gpu1 = torch.device("cuda:0"), torch.device("cuda:1")
+
+    class Workspace:   # a GPU tensor's stand-in
+        is_cuda = True
+
+        def __init__(self, t, device):
+            self.t, self.device = t, device
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    whole = torch.zeros(4096, dtype=torch.uint8)
+    kept, ptr, nbytes = H._scratch(size, "test", Workspace(whole, gpu0), gpu0)
+    assert ptr.value == whole.data_ptr() and nbytes == 4096
+    for bad in (Workspace(whole, gpu1), Workspace(torch.zeros(1, dtype=torch.uint8).expand(4096), gpu0),
+                Workspace(whole[::2], gpu0), whole):
+        with pytest.raises(ValueError):
+            H._scratch(size, "test", bad, gpu0)

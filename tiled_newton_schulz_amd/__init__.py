@@ -616,7 +616,9 @@ def _scratch(size_fn, where, workspace, device, *args):
         if need.value == 0:
             return None, None, 0
         workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-    _need_gpu(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        # (an expanded tensor has less memory than elements)
+        raise ValueError("workspace must be contiguous, on the operands' GPU")
     return workspace, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
 
 
