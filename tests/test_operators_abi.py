@@ -215,3 +215,33 @@ def test_workspace_is_memory_of_the_operands_gpu():
                 Workspace(whole[::2], gpu0), whole):
         with pytest.raises(ValueError):
             H._scratch(size, "test", bad, gpu0)
+
+
+def test_described_matrices_refuse_moved_tensors():
+    """Descriptors hold addresses: they are not used once a tensor has other
+    memory than it was described with, and follow changes of its values."""
+    torch = pytest.importorskip("torch")
+
+    def described(tensors):
+        first = tensors[0]
+        arr = mats([sd(8, 4, ptr=t.data_ptr()) for t in tensors])
+        return H.Matrices(arr, len(arr), (8, 4), False, first.dtype, first.device, tensors)
+
+    stack = torch.zeros(3, 8, 4)
+    for tensors in (stack, list(torch.zeros(3, 8, 4)), [torch.zeros(8, 4) for _ in range(3)]):
+        m = described(tensors)
+        assert H.matrices(m) is m
+        tensors[1].fill_(2.0)
+        assert H.matrices(m) is m
+    moved = m.tensors[2]
+    moved.data = torch.zeros(8, 4)
+    with pytest.raises(ValueError):
+        H.matrices(m)
+    m = described(stack)
+    stack.set_(torch.zeros(3, 8, 4))
+    with pytest.raises(ValueError):
+        H.matrices(m)
+    m = described(stack)
+    stack.untyped_storage().resize_(0)
+    with pytest.raises(ValueError):
+        H.matrices(m)

@@ -386,13 +386,27 @@ def himuon_pair_stats(a: Sequence, b: Sequence, out=None, workspace=None, stream
 # ---- the experts' products -------------------------------------------------------
 class Matrices:
     """Descriptors of the weight matrices of a layer's experts, made once and
-    used for any number of calls; keeps the tensors alive."""
+    used for any number of calls.  It keeps the tensors, whose values may change
+    but not their place: one that was given other memory (t.data = ..., set_, a
+    storage resized) makes the next call raise ValueError."""
 
     is_cuda = True   # checked when they are made
 
     def __init__(self, array, n, shape, transposed, dtype, device, tensors):
         self.array, self.n, self.shape, self.transposed = array, n, shape, transposed
         self.dtype, self.device, self.tensors = dtype, device, tensors
+        self.places = self._places()
+
+    def _places(self):
+        if isinstance(self.tensors, list):
+            return [t.data_ptr() for t in self.tensors]
+        return self.tensors.data_ptr()
+
+    def in_place(self):
+        """Itself, if the tensors are still where they were described."""
+        if self._places() != self.places:
+            raise ValueError("matrices were described before their tensors got other memory: describe them again")
+        return self
 
     def __len__(self):
         return self.n
@@ -413,7 +427,7 @@ def matrices(w) -> Matrices:
     row-major or all transposed views of row-major matrices."""
     import torch
     if isinstance(w, Matrices):
-        return w
+        return w.in_place()
     if isinstance(w, torch.Tensor):
         if w.dim() != 3:
             raise ValueError("stacked matrices must be a 3-D tensor")
