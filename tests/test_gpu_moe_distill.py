@@ -69,3 +69,24 @@ def test_command(cuda, capsys):
     moe_distill.main(["--steps", "2", "--tokens", "64", "--vocab", "500", "--dim", "64", "--hidden", "64", "--experts", "4",
                       "--top", "4", "--tile", "32"])
     assert capsys.readouterr().out.count("loss") == 2
+
+
+def test_replaced_weights_are_used(cuda):
+    """Weights given to a model after it was made are those of its products,
+    and of the step that trains them."""
+    vocab, dim, hidden, experts = 400, 64, 96, 4
+    teacher, student = pair(vocab, dim, hidden, experts, torch.float32)
+    d = moe_distill.Distiller(student, teacher, top=5, tile=32)
+    other = moe_distill.Moe(vocab, dim, hidden, experts, torch.float32, seed=9)
+    ids = torch.arange(100, device="cuda")
+    student.up, student.down, student.head = (w.clone() for w in (other.up, other.down, other.head))
+    other.embed, other.route = student.embed, student.route
+    assert torch.equal(student.forward(ids)[0], other.forward(ids)[0])
+    targets = d.targets(ids)
+    want = moe_distill.Distiller(other, teacher, top=5, tile=32).gradients(ids, *targets)
+    got = d.gradients(ids, *targets)
+    assert torch.equal(got[0], want[0]) and all(torch.equal(a, b) for a, b in zip(got[1], want[1]))
+    before = [w.clone() for w in (student.up, student.down, student.head)]
+    d.step(ids)
+    for a, b in zip((student.up, student.down, student.head), before):
+        assert not torch.equal(a, b)

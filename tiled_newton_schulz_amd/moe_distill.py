@@ -27,8 +27,7 @@ from __future__ import annotations
 
 import argparse
 
-from . import (himuon_distill, himuon_grouped_mm, himuon_grouped_wgrad, himuon_muon_step, himuon_token_logprobs,
-               matrices)
+from . import himuon_distill, himuon_grouped_mm, himuon_grouped_wgrad, himuon_muon_step, himuon_token_logprobs
 
 
 class Moe:
@@ -47,9 +46,6 @@ class Moe:
         self.up = normal(experts, dim, hidden, scale=dim ** -0.5)
         self.down = normal(experts, hidden, dim, scale=hidden ** -0.5)
         self.head = normal(dim, vocab, scale=2 * dim ** -0.5)
-        # descriptors of the experts' weights, and of their transposes for the backward pass
-        self.up_w, self.down_w = matrices(self.up), matrices(self.down)
-        self.up_t, self.down_t = matrices(self.up.transpose(1, 2)), matrices(self.down.transpose(1, 2))
 
     def forward(self, tokens):
         """(logits, what the backward pass needs)."""
@@ -59,9 +55,9 @@ class Moe:
         order = torch.argsort(expert, stable=True)
         ends = torch.searchsorted(expert[order], torch.arange(len(self.up), device=x.device), right=True).int()
         xs = x[order]
-        pre = himuon_grouped_mm(xs, self.up_w, ends)
+        pre = himuon_grouped_mm(xs, self.up, ends)
         act = torch.relu(pre).square()
-        h = x.index_add(0, order, himuon_grouped_mm(act, self.down_w, ends))
+        h = x.index_add(0, order, himuon_grouped_mm(act, self.down, ends))
         return h @ self.head, (order, ends, xs, pre, act, h)
 
     def backward(self, kept, dlogits):
@@ -69,7 +65,7 @@ class Moe:
         import torch
         order, ends, xs, pre, act, h = kept
         dy = (dlogits @ self.head.t())[order]
-        dact = himuon_grouped_mm(dy, self.down_t, ends)
+        dact = himuon_grouped_mm(dy, self.down.transpose(1, 2), ends)
         dpre = dact * (2 * torch.relu(pre))
         g_up, g_down = torch.empty_like(self.up), torch.empty_like(self.down)
         himuon_grouped_wgrad(xs, dpre, ends, g_up)
@@ -83,8 +79,7 @@ class Distiller:
         import torch
         self.student, self.teacher = student, teacher
         self.top, self.temperature, self.tile, self.eta, self.head_rate = top, temperature, tile, eta, head_rate
-        self.weights = list(student.up) + list(student.down)
-        self.momenta = [torch.zeros_like(w) for w in self.weights]
+        self.momenta = [torch.zeros_like(w) for w in (*student.up, *student.down)]
 
     def targets(self, tokens):
         """(ids, log probabilities) of the teacher's top entries, best first."""
@@ -106,7 +101,8 @@ class Distiller:
     def step(self, tokens):
         """Trains on a batch of tokens; the mean loss before the update (on the device)."""
         loss, (g_up, g_down, g_head) = self.gradients(tokens, *self.targets(tokens))
-        himuon_muon_step(self.weights, self.momenta, list(g_up) + list(g_down), self.tile, 5, eta=self.eta)
+        weights = [*self.student.up, *self.student.down]
+        himuon_muon_step(weights, self.momenta, [*g_up, *g_down], self.tile, 5, eta=self.eta)
         self.student.head.sub_(self.head_rate * g_head)
         return loss.sum()
 
