@@ -245,3 +245,19 @@ def test_described_matrices_refuse_moved_tensors():
     stack.untyped_storage().resize_(0)
     with pytest.raises(ValueError):
         H.matrices(m)
+
+
+def test_plan_of_many_experts():
+    """Experts past those of one launch are planned by their share of the rows:
+    256 rows an expert are too few to cut into parts, however few experts the
+    last launch holds."""
+    need = ctypes.c_size_t(0)
+
+    def size(n, rows):
+        assert H.lib.himuon_grouped_wgrad_workspace(ref(sd(n * rows, 64)), ref(sd(n * rows, 64)), n, H.BF16,
+                                                    ctypes.byref(need)) == OK
+        return need.value
+
+    for n in (128, 255, 256, 257, 300, 510, 511, 600):
+        assert size(n, 256) == 0, n
+    assert size(1, 65536) > 0

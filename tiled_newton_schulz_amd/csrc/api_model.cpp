@@ -80,14 +80,16 @@ himuon_status_t grouped_args(const himuon_matrix_t* X, const himuon_matrix_t* W,
     a.rows = (int32_t)X->rows;
     a.kdim = (int32_t)X->cols;
     a.dtype = dt == HIMUON_FP32 ? 1 : 0;
+    a.total = n;
     return HIMUON_OK;
 }
 
-// True if every launch of the call has a grid that fits (the full ones and the last).
-bool grids_fit(GroupedArgs a, int32_t n, bool (*fits)(const GroupedArgs&)) {
-    for (const int32_t part : {std::min(kExperts, n), (n - 1) % kExperts + 1}) {
+// True if f holds for every launch of the call (the full ones and the last).
+template <typename F>
+bool all_launches(GroupedArgs a, F f) {
+    for (const int32_t part : {std::min(kExperts, a.total), (a.total - 1) % kExperts + 1}) {
         a.n = part;
-        if (!fits(a)) return false;
+        if (!f(a)) return false;
     }
     return true;
 }
@@ -130,7 +132,7 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
     a.ndim = (int32_t)N;
     a.vec = chunked(*X) && chunked(*Y) && K % 8 == 0 && N % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(W[e]);
-    if (!grids_fit(a, n, grouped_mm_fits)) return HIMUON_ERR_LAYOUT;
+    if (!all_launches(a, grouped_mm_fits)) return HIMUON_ERR_LAYOUT;
     return each_launch(a, W, n, [&] {
         const hipError_t e = launch_grouped_mm(a, trans_w != 0, reinterpret_cast<hipStream_t>(stream));
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);
@@ -138,13 +140,13 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
 }
 
 // Workspace of the launch that takes the most: the parts' sums.
-size_t wgrad_bytes(GroupedArgs a, int32_t n) {
+size_t wgrad_bytes(const GroupedArgs& a) {
     int64_t most = 0;
-    for (const int32_t some : {std::min(kExperts, n), (n - 1) % kExperts + 1}) {
-        a.n = some;
-        const int64_t parts = a.rows > 0 ? grouped_wgrad_parts(a) : 1;
-        if (parts > 1) most = std::max(most, parts * grouped_wgrad_part_bytes(a));
-    }
+    all_launches(a, [&](const GroupedArgs& l) {
+        const int64_t parts = l.rows > 0 ? grouped_wgrad_parts(l) : 1;
+        if (parts > 1) most = std::max(most, parts * grouped_wgrad_part_bytes(l));
+        return true;
+    });
     return (size_t)most;
 }
 
@@ -172,8 +174,8 @@ himuon_status_t grouped_wgrad(const himuon_matrix_t* X, const himuon_matrix_t* D
     a.ndim = (int32_t)D->cols;
     a.vec = chunked(*X) && chunked(*D) && a.kdim % 8 == 0 && a.ndim % 8 == 0;
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(G[e]);
-    if (!grids_fit(a, n, grouped_wgrad_fits)) return HIMUON_ERR_LAYOUT;
-    HIMUON_TRY(check_workspace(workspace, workspace_bytes, wgrad_bytes(a, n)));
+    if (!all_launches(a, grouped_wgrad_fits)) return HIMUON_ERR_LAYOUT;
+    HIMUON_TRY(check_workspace(workspace, workspace_bytes, wgrad_bytes(a)));
     a.sums = reinterpret_cast<float*>(workspace);
     return each_launch(a, G, n, [&] {
         a.parts = grouped_wgrad_parts(a);
@@ -434,7 +436,8 @@ himuon_status_t himuon_grouped_wgrad_workspace(const himuon_matrix_t* X, const h
     a.kdim = (int32_t)X->cols;
     a.ndim = (int32_t)D->cols;
     a.dtype = dt == HIMUON_FP32 ? 1 : 0;
-    *bytes = wgrad_bytes(a, n);
+    a.total = n;
+    *bytes = wgrad_bytes(a);
     return HIMUON_OK;
 }
 

@@ -23,6 +23,7 @@ struct GroupedArgs {
     int32_t rows;            // M
     int32_t kdim, ndim;      // K, N
     int32_t e0, n;           // experts [e0, e0 + n) of the call
+    int32_t total;           // experts of the call
     int32_t last;            // product: this launch also zeroes the rows past the last expert
     int32_t dtype;           // 0 bf16, 1 fp32
     int32_t vec;             // rows and widths allow 16-byte chunks

@@ -1115,9 +1115,13 @@ int64_t mm_tiles(const GroupedArgs& a, int edge) {
 int64_t wgrad_tiles(const GroupedArgs& a, int edge) { return cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n; }
 
 // Tiles to expect: the host knows the rows and the experts, not which expert has
-// how many; half a partial row tile each.
+// how many; half a partial row tile each.  Of the whole call: where it takes more
+// than one launch they all run the same kernel.  (The last launch of 256 experts
+// holds one: planned by its share of the rows, calls of 1024 x 512 took 60 instead
+// of 72 us at 32 rows an expert, but 148 instead of 132 us at 256, as its grid has
+// to hold all rows and nearly all of it is empty.)
 double mm_expect(const GroupedArgs& a, int edge) {
-    return ((double)a.rows / edge + 0.5 * a.n) * (double)cdiv(a.ndim, edge);
+    return ((double)a.rows / edge + 0.5 * a.total) * (double)cdiv(a.ndim, edge);
 }
 
 // Which kernel.  Measured in us, experts x rows x K x N (K x N stored, bf16):
@@ -1145,7 +1149,7 @@ bool split(const GroupedArgs& a, double tiles, int64_t k) {
 Kernel mm_kernel(const GroupedArgs& a) {
     if (a.dtype == 0 && a.vec) {
         const bool big = enough_big(mm_expect(a, kBig));
-        if (a.rows <= (big ? 16 : 32) * (int64_t)a.n) return Kernel::Thin;
+        if (a.rows <= (big ? 16 : 32) * (int64_t)a.total) return Kernel::Thin;
         if (big) return Kernel::Big;
     }
     if (mm_expect(a, 128) >= device_cus_or_256()) return Kernel::Staged128;
@@ -1154,7 +1158,7 @@ Kernel mm_kernel(const GroupedArgs& a) {
 Kernel wgrad_kernel(const GroupedArgs& a) {
     if (a.dtype == 0 && a.vec && enough_big((double)wgrad_tiles(a, kBig))) return Kernel::Big;
     if (wgrad_tiles(a, 128) >= device_cus_or_256()) return Kernel::Staged128;
-    return split(a, (double)wgrad_tiles(a, 64), a.rows / a.n) ? Kernel::Split64 : Kernel::Staged64;
+    return split(a, (double)wgrad_tiles(a, 64), a.rows / a.total) ? Kernel::Split64 : Kernel::Staged64;
 }
 int edge_of(Kernel k) { return k == Kernel::Big ? kBig : k == Kernel::Staged128 ? 128 : 64; }
 
@@ -1188,7 +1192,7 @@ bool grouped_wgrad_fits(const GroupedArgs& a) { return fits(wgrad_kernel(a), gro
 constexpr int64_t kMostParts = 1024;   // of all tiles: 16 MiB
 int32_t grouped_wgrad_parts(const GroupedArgs& a) {
     if (wgrad_kernel(a) != Kernel::Split64) return 1;
-    const int64_t steps = a.rows / a.n / (a.dtype == 0 ? Io<0>::BK : Io<1>::BK), tiles = wgrad_tiles(a, 64);
+    const int64_t steps = a.rows / a.total / (a.dtype == 0 ? Io<0>::BK : Io<1>::BK), tiles = wgrad_tiles(a, 64);
     int64_t best = 1;
     double least = 1e30;
     for (int64_t p = 1; p == 1 || (p <= steps / 16 && p * tiles <= kMostParts); ++p) {
