@@ -415,7 +415,7 @@ typedef enum himuon_index {
  * idx      : device array N x k of ids, of type it.  An id outside [0, V)
  *            marks an absent entry.  An id may occur more than once in a row.
  * T        : N x k fp32 teacher values (row stride T->ld).  -inf is p_j = 0.
- * temperature : > 0, finite.
+ * temperature : finite, above 4.3e-39.
  * weight   : device array of N fp32, or NULL (all 1).
  * loss     : device array of N fp32, written.
  * lse      : device array of N x 2 fp32, written, or NULL: log sum exp of s

@@ -261,3 +261,10 @@ def test_plan_of_many_experts():
     for n in (128, 255, 256, 257, 300, 510, 511, 600):
         assert size(n, 256) == 0, n
     assert size(1, 65536) > 0
+
+
+def test_temperatures_whose_exponent_factor_overflows():
+    """The kernels take exponents times log2(e) / temperature: a temperature that
+    leaves it infinite would make every row NaN."""
+    for tau in (3.5e-39, 4.2e-39):
+        assert distill(tau=tau) == distill_grad(tau=tau) == logprobs(tau=tau) == logprobs_grad(tau=tau) == INVALID

@@ -218,7 +218,8 @@ himuon_status_t logits_args(const himuon_matrix_t* Z, himuon_index_t it, float t
     if (Z == nullptr) return HIMUON_ERR_INVALID_ARGUMENT;
     if ((st = check_rows(*Z, elem_size(dt))) != HIMUON_OK) return st;
     if (Z->cols > kMaxCols) return HIMUON_ERR_LAYOUT;
-    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    // (the kernels scale exponents by log2(e) / temperature)
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.4426951f * (1.f / temperature)))
         return HIMUON_ERR_INVALID_ARGUMENT;
     a.z = Z->ptr;
     a.z_ld = Z->ld;
