@@ -621,3 +621,156 @@ def test_more_rows_than_a_launch_holds(cuda, shift):
             near(res.loss[rows], loss, lb, "loss")
             near(res.lse[rows].double().sum(1), lse, d, "lse")
             near(dres[rows], grad, gb + ROUND["bf16"] * grad.abs() + 1e-38, "grad")
+
+
+# ---- sizes at which a workgroup takes several rows, or long segments ----------------------
+# Every row against fp64 on the GPU, in blocks of rows.
+def on_gpu(got, want, bound, what):
+    got = got.double()
+    ok = (got == want) | (torch.isnan(got) & torch.isnan(want)) | ((got - want).abs() <= bound)
+    assert torch.all(ok), (what, float(torch.where(ok, 0.0, (got - want).abs() - bound).nan_to_num(9e99).max()))
+
+
+def gpu_logits(N, V, dt, seed, shift):
+    """(logits on the GPU inside a wider tensor of NaN if shift, else contiguous)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.full((N, V + 2 * shift), float("nan"), dtype=TYPES[dt], device="cuda")[:, shift:shift + V]
+    for r in range(0, N, 256):
+        z[r:r + 256] = torch.randn((min(256, N - r), V), generator=g, device="cuda") * 3
+    return z, g
+
+
+def gpu_teacher(N, V, k, g):
+    """Ids spread over the row, all different; some absent."""
+    at = torch.rand((N, k), generator=g, device="cuda")
+    idx = ((torch.arange(k, device="cuda") + at) * (V / k)).long().clamp(max=V - 1)
+    idx[torch.rand((N, k), generator=g, device="cuda") < 0.1] = -1
+    idx[::11] = V
+    return idx, torch.randn((N, k), generator=g, device="cuda") * 3
+
+
+def gpu_weights(N, g):
+    w = torch.rand(N, generator=g, device="cuda") + 0.5
+    w[torch.arange(N, device="cuda") % 7 == 3] = 0.0
+    return w
+
+
+@pytest.mark.parametrize("N,V,dt,shift,out_shift", [
+    (700, 70000, "bf16", 0, 0), (700, 70001, "bf16", 1, 1), (700, 70001, "bf16", 1, 2), (600, 131072, "bf16", 0, 0),
+    (600, 40000, "fp32", 0, 0), (600, 40003, "fp32", 1, 1), (600, 40003, "fp32", 1, 2),
+    (5000, 1003, "bf16", 1, 1), (5000, 3000, "bf16", 0, 0), (5000, 1003, "fp32", 1, 2), (5000, 3000, "fp32", 0, 0)])
+def test_distill_several_rows_a_workgroup(cuda, N, V, dt, shift, out_shift):
+    """More rows than workgroups: rows of weight 0 over NaN and rows without an
+    entry between the others, apart and in place."""
+    print(f"several rows {N}x{V} {dt} {shift} {out_shift}", flush=True)
+    z, g = gpu_logits(N, V, dt, 300 + N, shift)
+    idx, t = gpu_teacher(N, V, 9, g)
+    w = gpu_weights(N, g)
+    z[w == 0] = float("nan")
+    out = torch.full((N, V + 2 * out_shift), float("nan"), dtype=TYPES[dt], device="cuda")[:, out_shift:out_shift + V]
+    r = H.himuon_distill(z, idx, t, 1.5, weight=w, grad=out)
+    torch.cuda.synchronize()
+    for r0 in range(0, N, 200):
+        rows = slice(r0, min(N, r0 + 200))
+        zz = torch.where((w[rows] == 0)[:, None], torch.zeros((), dtype=z.dtype, device="cuda"), z[rows])
+        loss, grad, lse, d, lb, gb = distill64(zz, idx[rows], t[rows], 1.5, True, w[rows])
+        on_gpu(r.loss[rows], loss, lb, "loss")
+        on_gpu(r.lse[rows].double().sum(1), lse, d, "lse")
+        on_gpu(out[rows], grad, gb + ROUND[dt] * grad.abs() + 1e-38, "gradient")
+    base = out._base
+    assert torch.isnan(base[:, :out_shift]).all() and torch.isnan(base[:, out_shift + V:]).all()
+    if shift == out_shift:
+        again = H.himuon_distill(z, idx, t, 1.5, weight=w, grad=z)
+        assert torch.equal(z, out) and torch.equal(again.loss, r.loss) and torch.equal(again.lse, r.lse)
+        base = z._base
+        assert torch.isnan(base[:, :shift]).all() and torch.isnan(base[:, shift + V:]).all()
+
+
+LONG = [(1100, 16000, "bf16", 0), (600, 16000, "bf16", 0), (1100, 20001, "bf16", 1), (1100, 8000, "fp32", 0),
+        (600, 8000, "fp32", 0), (1100, 20001, "fp32", 1), (1030, 70000, "bf16", 0)]
+
+
+@pytest.mark.parametrize("top", [0, 5, 40])
+@pytest.mark.parametrize("N,V,dt,shift", LONG)
+def test_logprobs_of_long_segments(cuda, N, V, dt, shift, top):
+    """Segments of four and eight chunks a thread: rows of one value, of few,
+    ascending and descending, masked but for some ids, low in the chunks of one
+    wave (the others' all lie above its bound), and ordinary ones."""
+    print(f"long segments {N}x{V} {dt} {shift} top {top}", flush=True)
+    z, g = gpu_logits(N, V, dt, 400 + N, shift)
+    v = torch.arange(V, device="cuda")
+    epc = 8 if dt == "bf16" else 4
+    for r in (1, 333, N - 1):   # (each kind in several rows)
+        z[r] = -2.5
+    z[2] = torch.round(z[2])
+    z[4], z[5] = v / 64, -(v / 64)
+    z[6] = -INF
+    z[6, 17::V // 60] = 1.0
+    z[7] = torch.finfo(TYPES[dt]).min
+    z[7, V // 3] = 2.0
+    for r in (8, N // 2):
+        z[r] = torch.where(v // epc % 256 < 64, z[r].float() - 50.0, z[r].float())
+    z[9] = (v * 37 % 1009) / 16
+    tokens = torch.randint(0, V, (N,), generator=g, device="cuda")
+    tokens[6] = 17
+    tokens[torch.arange(N, device="cuda") % 13 == 3] = -1
+    tau = 1.3
+    r = H.himuon_token_logprobs(z, tokens, top=top, temperature=tau)
+    gl, gh = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    dz = H.himuon_token_logprobs_grad(z, tokens, r.lse, r.entropy, gl, gh, temperature=tau)
+    torch.cuda.synchronize()
+    for r0 in range(0, N, 200):
+        rows = slice(r0, min(N, r0 + 200))
+        zz, tok = z[rows], tokens[rows]
+        live = tok >= 0
+        s, lse, lq, q = softmax64(zz, tau)
+        # (logits masked by the lowest value: their q is 0, and their own log q
+        # carries the relative error of s)
+        A, d = row_bound(torch.where(s < -1e30, 0.0, s), V)
+        ids = tok.clamp(min=0)[:, None]
+        own = torch.where(lq < -1e30, 2.0 ** -20 * lq.abs(), 0.0)
+        on_gpu(r.logp[rows], torch.where(live, lq.gather(1, ids)[:, 0], 0.0), d + own.gather(1, ids)[:, 0], "logp")
+        qlq = torch.where(q > 0, q * lq, 0.0)
+        Hq = -qlq.sum(1)
+        dH = d * (2 * A + 8 + math.log(V))
+        on_gpu(r.entropy[rows], torch.where(live, Hq, 0.0), dH, "entropy")
+        on_gpu(r.lse[rows].double().sum(1), torch.where(live, lse, 0.0), d, "lse")
+        if top:
+            order = torch.sort(zz.float(), dim=1, descending=True, stable=True).indices[:, :top]
+            assert torch.equal(r.top_idx[rows].long()[live], order[live])
+            got = r.top_logp[rows].double()
+            on_gpu(got[live], lq.gather(1, order)[live], (d[:, None] + own.gather(1, order))[live], "alternatives")
+            assert torch.all(r.top_idx[rows][~live] == -1) and torch.all(got[~live] == -INF)
+        a, b = torch.where(live, gl[rows], 0.0).double()[:, None], torch.where(live, gh[rows], 0.0).double()[:, None]
+        hot = torch.zeros_like(q).scatter_(1, ids, 1.0)
+        want = (a * (hot - q) - b * (qlq + q * Hq[:, None])) / tau
+        # (a q below 2^-126 may be 0, and |q log q| is below 88 2^-126 there)
+        err = (a.abs() * (q * d[:, None] + 2.0 ** -22 * (hot + q) + 2.0 ** -126)
+               + b.abs() * (q * (d + dH)[:, None] + (qlq.abs() + q * Hq[:, None].abs()) * (d[:, None] + 2.0 ** -21)
+                            + 2.0 ** -126 * (88 + Hq[:, None]))) / tau
+        on_gpu(dz[rows], want, err + ROUND[dt] * want.abs() + 1e-38, "gradient")
+    H.himuon_token_logprobs_grad(z, tokens, r.lse, r.entropy, gl, gh, temperature=tau, out=z)
+    assert torch.equal(z, dz)
+
+
+@pytest.mark.parametrize("N,V,dt,shift", LONG)
+def test_distill_of_long_segments_in_two_calls(cuda, N, V, dt, shift):
+    """The loss, and from its lse the gradient, apart and in place."""
+    print(f"two calls {N}x{V} {dt} {shift}", flush=True)
+    z, g = gpu_logits(N, V, dt, 500 + N, shift)
+    w = gpu_weights(N, g)
+    z[w == 0] = float("nan")
+    for k in (9, 70):
+        idx, t = gpu_teacher(N, V, k, g)
+        t = torch.log_softmax(t, 1) - 0.1
+        r = H.himuon_distill(z, idx, t, 0.7, False, w)
+        dz = H.himuon_distill_grad(z, idx, t, r.lse, w, 0.7, False)
+        for r0 in range(0, N, 200):
+            rows = slice(r0, min(N, r0 + 200))
+            zz = torch.where((w[rows] == 0)[:, None], torch.zeros((), dtype=z.dtype, device="cuda"), z[rows])
+            loss, grad, lse, d, lb, gb = distill64(zz, idx[rows], t[rows], 0.7, False, w[rows])
+            on_gpu(r.loss[rows], loss, lb, "loss")
+            on_gpu(r.lse[rows].double().sum(1), lse, d, "lse")
+            on_gpu(dz[rows], grad, gb + ROUND[dt] * grad.abs() + 1e-38, "gradient")
+    H.himuon_distill_grad(z, idx, t, r.lse, w, 0.7, False, out=z)
+    assert torch.equal(z, dz)
