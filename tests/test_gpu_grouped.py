@@ -374,3 +374,77 @@ def test_many_tiles_strided_and_repeated(cuda):
     d = randn((M, N), "bf16", 46)
     g = check_wgrad(x, d, counts, "bf16")
     assert torch.equal(g, H.himuon_grouped_wgrad(x, d, ends))
+
+
+def test_difference_quotients_tightly(cuda):
+    """<Y, R> is linear in X and in W, so its difference along a direction differs
+    from <gradient, direction> by roundings alone.  An element of Y is off by at
+    most 2 K 2^-24 sum |x w| (as above), the gradients alike over N and over the
+    rows; each is multiplied by its partner and summed in fp64."""
+    counts, K, N = [40, 0, 77], 48, 56
+    M = sum(counts)
+    x, w, R = randn((M, K), "fp32", 20), randn((3, K, N), "fp32", 21), randn((M, N), "fp32", 22)
+    u, v = randn((M, K), "fp32", 23), randn((3, K, N), "fp32", 24)
+    ends = ends_of(counts)
+    expert = torch.repeat_interleave(torch.arange(3), torch.tensor(counts))
+
+    def loss(x, w):
+        """(<Y, R>, bound of its error)"""
+        y = H.himuon_grouped_mm(x, w, ends).double().cpu()
+        size = torch.bmm(x.double().cpu().abs()[:, None], w.double().cpu().abs()[expert])[:, 0]
+        r = R.double().cpu()
+        return float((y * r).sum()), (2 * K * 2.0 ** -24) * float((size * r.abs()).sum())
+
+    dx = H.himuon_grouped_mm(R, w.transpose(1, 2), ends).double().cpu()
+    dw = H.himuon_grouped_wgrad(x, R, ends).double().cpu()
+    wa, ra, xa = w.double().cpu().abs(), R.double().cpu().abs(), x.double().cpu().abs()
+    bx = 2 * N * 2.0 ** -24 * float((torch.bmm(ra[:, None], wa.transpose(1, 2).contiguous()[expert])[:, 0] * u.double().cpu().abs()).sum())
+    bw, r = 0.0, 0
+    for e, c in enumerate(counts):
+        bw += 2 * max(c, 1) * 2.0 ** -24 * float(((xa[r:r + c].t() @ ra[r:r + c]) * v[e].double().cpu().abs()).sum())
+        r += c
+    # the sums x + u and w + v are rounded to fp32 as well
+    for up, down, grad, along, bound in ((loss(x + u, w), loss(x - u, w), dx, u, bx), (loss(x, w + v), loss(x, w - v), dw, v, bw)):
+        diff = (up[0] - down[0]) / 2
+        tol = (up[1] + down[1]) / 2 + bound + (up[1] + down[1]) / (2 * 2 * K)
+        assert abs(diff - float((grad * along.double().cpu()).sum())) <= tol
+
+
+@pytest.mark.parametrize("dt,K,N", [("bf16", 4096, 4096), ("bf16", 4095, 4097), ("fp32", 2048, 4100)])
+def test_operands_past_2_to_the_31_elements(cuda, dt, K, N):
+    """Rows and results whose offsets pass 32 bits: sampled rows and columns
+    against fp64."""
+    M = (1 << 31) // min(K, N) + 5000
+    counts = [M // 3, 5, M - M // 3 - 5 - 100]
+    print(f"past 2^31: {M} rows {K}x{N} {dt}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(50)
+
+    def big(rows, cols):
+        t = torch.empty((rows, cols), dtype=TYPES[dt], device="cuda")
+        for r in range(0, rows, 1 << 16):
+            t[r:r + (1 << 16)] = torch.randn((min(1 << 16, rows - r), cols), generator=g, device="cuda")
+        return t
+
+    x, w = big(M, K), big(3 * K, N).view(3, K, N)
+    ends = ends_of(counts)
+    sample = torch.tensor([0, M // 3 - 1, M // 3, M // 3 + 5, M // 2, M - 102, M - 101])
+    for weights in (w, w.transpose(1, 2).contiguous().transpose(1, 2)):
+        y = H.himuon_grouped_mm(x, weights, ends)
+        for r in sample.tolist():
+            e = int((ends.cpu() <= r).sum())
+            close(y[r:r + 1], *product(x[r:r + 1], w[e], dt))
+        assert torch.all(y[M - 100:] == 0)
+        del weights
+    d = y
+    for r in range(0, M, 1 << 16):
+        d[r:r + (1 << 16)] = torch.randn((min(1 << 16, M - r), N), generator=g, device="cuda")
+    got = H.himuon_grouped_wgrad(x, d, ends)
+    r = 0
+    for e, c in enumerate(counts):
+        rows = slice(r, r + c)
+        for i in (0, K // 2, K - 1):
+            a, b = x[rows, i].double(), d[rows][:, [0, 255, 256, N - 1]]
+            want = torch.stack([(a * b[:, j].double()).sum() for j in range(4)]).cpu()
+            size = torch.stack([(a.abs() * b[:, j].double().abs()).sum() for j in range(4)]).cpu()
+            close(got[e, i, [0, 255, 256, N - 1]], want, 2 * c * 2.0 ** -24 * size + ROUND[dt] * want.abs())
+        r += c

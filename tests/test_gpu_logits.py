@@ -774,3 +774,36 @@ def test_distill_of_long_segments_in_two_calls(cuda, N, V, dt, shift):
             on_gpu(dz[rows], grad, gb + ROUND[dt] * grad.abs() + 1e-38, "gradient")
     H.himuon_distill_grad(z, idx, t, r.lse, w, 0.7, False, out=z)
     assert torch.equal(z, dz)
+
+
+@pytest.mark.parametrize("V", [131072, 131073])
+def test_logits_past_2_to_the_32_elements(cuda, V):
+    """Rows whose offsets pass 32 bits, in bytes and in elements, on and off the
+    16-byte grid, the gradients in place: sampled rows against fp64."""
+    N, k = 33000, 5
+    print(f"{N}x{V}", flush=True)
+    assert N * V > 1 << 32
+    z, g = gpu_logits(N, V, "bf16", 600, 0)
+    rows = torch.tensor([0, 16383, 16384, 32767, 32768, N - 2, N - 1], device="cuda")
+    zz = z[rows].cpu()
+    idx, t = gpu_teacher(N, V, k, g)
+    tokens = torch.randint(0, V, (N,), generator=g, device="cuda")
+    w = torch.rand(N, generator=g, device="cuda") + 0.5
+    r = H.himuon_token_logprobs(z, tokens, top=3)
+    part = type(r)(*[x[rows] for x in r])
+    _, ref = check_logprobs(zz, None, tokens[rows].cpu(), 3, 1.0, "bf16", r=part)
+    loss, grad, lse, d, lb, gb = distill64(zz, idx[rows].cpu(), t[rows].cpu(), 1.0, True, w[rows].cpu())
+    a = H.himuon_distill(z, idx, t, weight=w)
+    near(a.loss[rows], loss, lb, "loss")
+    kept = z.clone()
+    H.himuon_distill_grad(kept, idx, t, a.lse, w, out=kept)
+    near(kept[rows], grad, gb + ROUND["bf16"] * grad.abs() + 1e-38, "gradient")
+    kept.copy_(z)
+    f = H.himuon_distill(kept, idx, t, weight=w, grad=kept)
+    near(f.loss[rows], loss, lb, "fused loss")
+    near(kept[rows], grad, gb + ROUND["bf16"] * grad.abs() + 1e-38, "fused gradient")
+    gl, gh = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    want = H.himuon_token_logprobs_grad(z[rows], tokens[rows], part.lse.contiguous(), part.entropy.contiguous(), gl[rows], gh[rows])
+    check_logprobs_grad(zz, z[rows], tokens[rows].cpu(), 1.0, "bf16", part, ref, gl[rows].cpu(), gh[rows].cpu())
+    H.himuon_token_logprobs_grad(z, tokens, r.lse, r.entropy, gl, gh, out=z)
+    assert torch.equal(z[rows], want)
