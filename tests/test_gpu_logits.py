@@ -15,6 +15,7 @@ P (d + d_p (1 + max |log p - log q|)), the gradient by
 c (P q (d + d_p) + p d_p), c = |weight| / temperature, before it is rounded to
 its type: 2^-8 (bf16), 2^-22 (fp32) of itself.
 """
+import ctypes
 import math
 
 import pytest
@@ -807,3 +808,64 @@ def test_logits_past_2_to_the_32_elements(cuda, V):
     check_logprobs_grad(zz, z[rows], tokens[rows].cpu(), 1.0, "bf16", part, ref, gl[rows].cpu(), gh[rows].cpu())
     H.himuon_token_logprobs_grad(z, tokens, r.lse, r.entropy, gl, gh, out=z)
     assert torch.equal(z[rows], want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [3000, 170001, 170008])
+def test_distill_without_weights_or_lse(cuda, V, dt):
+    """No weights are weights of 1, and no lse wanted changes nothing else,
+    whether a row is kept on chip or read twice."""
+    print(f"distill without weights {V} {dt}", flush=True)
+    N, k = 5, 6
+    z = logits(N, V, dt, 700)
+    idx, t = teacher(N, V, k, 701)
+    idx[2] = -1
+    zg, ig, tg = z.cuda(), idx.cuda(), t.cuda()
+    loss, grad, lse, d, lb, gb = distill64(z, idx, t, 1.5, True, torch.ones(N))
+    tol = gb + ROUND[dt] * grad.abs() + 1e-38
+    r = H.himuon_distill(zg, ig, tg, 1.5, grad=True)
+    near(r.loss, loss, lb, "loss")
+    near(r.lse.double().sum(1), lse, d, "lse")
+    near(r.grad, grad, tol, "grad")
+    ones = H.himuon_distill(zg, ig, tg, 1.5, weight=torch.ones(N, device="cuda"), grad=True)
+    assert torch.equal(ones.loss, r.loss) and torch.equal(ones.grad, r.grad)
+    in_place = zg.clone()
+    H.himuon_distill(in_place, ig, tg, 1.5, grad=in_place)
+    assert torch.equal(in_place, r.grad)
+    # the C entry without lse
+    got, l2 = torch.empty_like(zg), torch.empty(N, device="cuda")
+    ws = torch.empty(max(H.himuon_distill_workspace(zg, True), 16), dtype=torch.uint8, device="cuda")
+    dz, do, dt_ = H._rows(zg), H._rows(got), H._rows(tg)
+    at = lambda x: ctypes.c_void_p(x.data_ptr())
+    code = H.lib.himuon_distill(ctypes.byref(dz), at(ig), H.I64, ctypes.byref(dt_), 1.5, 1, None, at(l2), None,
+                                ctypes.byref(do), H._dtype_code(zg), at(ws), ws.numel(),
+                                ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert code == 0 and torch.equal(got, r.grad) and torch.equal(l2, r.loss)
+
+
+@pytest.mark.parametrize("V", [1000, 60000])
+def test_logprobs_optional_results(cuda, V):
+    """Each result of the C entry may be left out; the others stay the same."""
+    N, top = 6, 4
+    print(f"optional results {V}", flush=True)
+    zg = logits(N, V, "bf16", 710).cuda()
+    tokens = torch.randint(0, V, (N,), generator=gen(711)).cuda()
+    tokens[2] = -1
+    want = H.himuon_token_logprobs(zg, tokens, top=top)
+    ws = torch.empty(max(H.himuon_token_logprobs_workspace(zg, top), 16), dtype=torch.uint8, device="cuda")
+    dz = H._rows(zg)
+    for left_out in range(4):
+        res = [torch.full_like(x, 7) for x in want]
+        at = [None if i == left_out else ctypes.c_void_p(x.data_ptr()) for i, x in enumerate(res)]
+        code = H.lib.himuon_token_logprobs(ctypes.byref(dz), ctypes.c_void_p(tokens.data_ptr()), H.I64, 1.0,
+                                           0 if left_out == 3 else top, at[0], at[1], at[2], at[3],
+                                           None if left_out == 3 else at[4], H.BF16, ctypes.c_void_p(ws.data_ptr()), ws.numel(),
+                                           ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        assert code == 0
+        for i, (x, y) in enumerate(zip(res, want)):
+            if i == left_out or (left_out == 3 and i == 4):
+                assert torch.all(x == 7)
+            else:
+                assert torch.equal(x, y)

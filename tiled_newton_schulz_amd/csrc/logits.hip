@@ -844,7 +844,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
         __shared__ float red1[4][2], red2[4][1];
         __shared__ int ids[kMaxEntries];
         __shared__ float ps[kMaxEntries];
-        const float w = a.weight[row];
+        const float w = a.weight ? a.weight[row] : 1.f;   // (none: the second pass of a call without weights)
         live = w != 0.f;
         if (live) {
             Entry x[KE];
