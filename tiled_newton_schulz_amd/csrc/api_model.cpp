@@ -198,7 +198,7 @@ size_t keys_bytes(int64_t rows, const SegPlan& p, int32_t top) {
 // Distillation with a gradient where rows are not kept on chip: the sums, and
 // the lse between the passes.
 size_t distill_bytes(int32_t rows, int32_t cols, int32_t dtype, bool with_grad) {
-    if (rows == 0 || (with_grad && distill_on_chip(rows, cols, dtype))) return 0;
+    if (rows == 0 || (with_grad && distill_on_chip(cols, dtype))) return 0;
     return parts_bytes(rows, seg_plan(rows, cols, dtype)) + (with_grad ? (size_t)rows * 2 * sizeof(float) : 0);
 }
 
@@ -309,7 +309,7 @@ himuon_status_t distill(const himuon_matrix_t* Z, const void* idx, himuon_index_
     a.lse = lse;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     hipError_t e;
-    if (dZ != nullptr && distill_on_chip(a.rows, a.cols, a.dtype)) {
+    if (dZ != nullptr && distill_on_chip(a.cols, a.dtype)) {
         e = launch_distill_on_chip(a, s);
     } else {
         a.part = reinterpret_cast<SegStats*>(workspace);

@@ -58,7 +58,7 @@ struct LogitsArgs {
 SegPlan seg_plan(int32_t rows, int32_t cols, int32_t dtype);
 // True if himuon_distill with a gradient keeps every row on chip (one launch,
 // one pass over the logits).
-bool distill_on_chip(int32_t rows, int32_t cols, int32_t dtype);
+bool distill_on_chip(int32_t cols, int32_t dtype);
 
 hipError_t launch_distill(const LogitsArgs& a, hipStream_t s);         // loss (and lse)
 hipError_t launch_distill_on_chip(const LogitsArgs& a, hipStream_t s); // loss, lse and gradient

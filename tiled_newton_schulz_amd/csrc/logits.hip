@@ -433,7 +433,9 @@ __device__ __forceinline__ void rank_candidates(const TopShared& sh, int n, int 
     }
 }
 // Searches each rank in turn: the largest key below the last one.  all(f) calls
-// f(key) on every element of this thread.
+// f(key) on every element of this thread.  Slow, and rare: in bf16, 1024 rows of
+// 65536 that ascend take 1.5 ms with 20 alternatives and 4.6 ms with 64, against
+// 58 and 62 us of rows in any order (fp32: 0.5 ms either way, against 66 and 87).
 template <typename All, typename Emit>
 __device__ __forceinline__ void search_ranks(TopShared& sh, int top, All all, Emit emit) {
     uint64_t below = ~0ull;
@@ -946,8 +948,10 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const LogitsArgs a) {
 // GRID 0: rows of whole chunks; 1: rows that start or end inside a chunk, z and
 // dz on the same grid; 2: on different ones (stored element by element).  The
 // elements of a row's partial chunks are held one each by the first threads.
-// bf16, 64 entries a row: 2048 x 131072 in 272 us (3.9 TB/s; a large copy
-// reaches 4.9), 2048 x 65537 in 161 us (3.3 TB/s).
+// bf16, 64 entries a row: 2048 x 131072 in 256 us (4.2 TB/s; a large copy
+// reaches 4.9), 2048 x 65537 in 159 us (3.4 TB/s); fp32 2048 x 65536 in 236 us
+// (4.5 TB/s).  16, 18 and 20 chunks of 1024 threads spill 12, 56 and 104 bytes a
+// thread, off the grid 80, 132 and 204: 2048 x 131071 takes 318 us (3.4 TB/s).
 template <int DT, int NT, int U, int GRID>
 __global__ __launch_bounds__(NT) void distill_row_kernel(const LogitsArgs a) {
     constexpr bool FL = GRID == 0;
@@ -1258,11 +1262,13 @@ SegPlan seg_plan(int32_t rows, int32_t cols, int32_t dtype) {
 }
 
 // One pass over a row that fits 1024 threads x 20 chunks (of 128 registers a
-// thread 80), against a forward pass and a gradient: bf16 2048 x 131072 272
-// against 336 us, 2048 x 65537 161 against 188 us, 8192 x 10001 111 against
-// 160 us; at the upper end 2048 x 163000 361 against 390 us, and 163001, whose
-// rows are off the grid, 405 against 420 us.
-bool distill_on_chip(int32_t rows, int32_t cols, int32_t dtype) { return row_chunks(cols, dtype) <= 1024 * 20; }
+// thread 80), against a forward pass and a gradient, on the device: bf16 2048 x
+// 131072 256 against 326 us, 2048 x 65537 159 against 196 us, 8192 x 10001 109
+// against 135 us, 1 to 256 x 32000 8 to 11 against 12 to 20 us; at the upper end
+// 2048 x 163000 357 against 405 us, and 163001, whose rows are off the grid, 409
+// against 429 us.  A few long rows lose by it: 1, 16, 64 and 128 x 131072 18, 19, 21
+// and 24 against 12, 15, 21 and 29 us, within the 17 us the host takes for a call.
+bool distill_on_chip(int32_t cols, int32_t dtype) { return row_chunks(cols, dtype) <= 1024 * 20; }
 
 hipError_t launch_distill(const LogitsArgs& a, hipStream_t s) { return forward<0>(a, s); }
 hipError_t launch_distill_on_chip(const LogitsArgs& a, hipStream_t s) {
