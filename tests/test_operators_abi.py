@@ -268,3 +268,37 @@ def test_temperatures_whose_exponent_factor_overflows():
     leaves it infinite would make every row NaN."""
     for tau in (3.5e-39, 4.2e-39):
         assert distill(tau=tau) == distill_grad(tau=tau) == logprobs(tau=tau) == logprobs_grad(tau=tau) == INVALID
+
+
+@pytest.mark.parametrize("call", ["tiled_ns", "schedule", "muon", "gram", "pair_stats"])
+def test_workspace_of_the_step_has_the_memory_it_states(call, monkeypatch):
+    """The step's entries refuse a workspace on another device than the matrices,
+    and one with less memory than the bytes stated or than it has elements,
+    before the library is called; others pass as they are."""
+    torch = pytest.importorskip("torch")
+    called = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith(("_workspace", "_workspace_size")):
+                return lambda *a: 0
+            return lambda *a: called.append(name) or 0
+
+    monkeypatch.setattr(H, "lib", Library())
+    m = [torch.zeros(8, 8)]
+    run = {"tiled_ns": lambda **k: H.himuon_tiled_ns(m, 8, 1, stream=1, **k),
+           "schedule": lambda **k: H.himuon_tiled_ns_schedule(m, [8], stream=1, **k),
+           "muon": lambda **k: H.himuon_muon_step(m, m, m, 8, 1, stream=1, **k),
+           "gram": lambda **k: H.himuon_gram_ns(m, 1, stream=1, **k),
+           "pair_stats": lambda **k: H.himuon_pair_stats(m, m, stream=1, **k)}[call]
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    for good in (ws, ws[256:], ws[::2], ws[:0]):
+        run(workspace=good)
+    assert len(called) == 4
+    bad = [dict(workspace=ws[:1].expand(8192)), dict(workspace=torch.zeros(16, dtype=torch.uint8, device="meta"))]
+    if call != "pair_stats":
+        bad += [dict(workspace=ws, workspace_bytes=4097), dict(workspace=ws[256:], workspace_bytes=4096)]
+    for k in bad:
+        with pytest.raises(ValueError):
+            run(**k)
+    assert len(called) == 4

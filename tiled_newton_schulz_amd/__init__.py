@@ -216,11 +216,20 @@ def himuon_workspace_size(mats: Sequence, T: int, dtype: int | None = None) -> t
     return full.value, mn.value
 
 
+def _in_memory(workspace, nbytes, device):
+    """nbytes, if the workspace has as many from its first element on, on the device."""
+    if workspace.device != device:
+        raise ValueError("workspace must be on the matrices' GPU")
+    if nbytes > workspace.untyped_storage().nbytes() - workspace.storage_offset() * workspace.element_size():
+        raise ValueError("workspace is smaller than its stated size")
+    return nbytes
+
+
 def _workspace(mats, T, dtype, workspace, workspace_bytes, device):
     import torch
     if workspace is not None:
         nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-        return workspace, workspace.data_ptr(), nbytes
+        return workspace, workspace.data_ptr(), _in_memory(workspace, nbytes, device)
     full, mn = himuon_workspace_size(mats, T, dtype)
     if full == 0:
         return None, None, 0
@@ -281,6 +290,8 @@ def himuon_tiled_ns_schedule(mats: Sequence, Ts: Sequence[int], abc=(3.4445, -4.
             workspace_bytes = need
     ptr = workspace.data_ptr() if workspace is not None else None
     nbytes = 0 if workspace is None else (workspace.numel() if workspace_bytes is None else workspace_bytes)
+    if workspace is not None:
+        _in_memory(workspace, nbytes, mats[0].device)
     code = lib.himuon_tiled_ns_schedule(d, len(mats), ts, K, coeff_array(abc, K), dtype, eps,
                                         ctypes.c_void_p(ptr), nbytes, _stream_handle(stream))
     _check(code, "himuon_tiled_ns_schedule")
@@ -331,8 +342,10 @@ def himuon_gram_ns(mats: Sequence, K: int, abc=(3.4445, -4.7750, 2.0315), restar
             import torch
             workspace = torch.empty(cap, dtype=torch.uint8, device=mats[0].device)
         workspace_bytes = cap
-    elif workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+    else:
+        if workspace_bytes is None:
+            workspace_bytes = workspace.numel() * workspace.element_size()
+        _in_memory(workspace, workspace_bytes, mats[0].device)
     ptr = workspace.data_ptr() if workspace is not None else None
     code = lib.himuon_gram_ns(d, len(mats), K, coeff_array(abc, K), restart, dtype, eps,
                               ctypes.c_void_p(ptr), workspace_bytes, _stream_handle(stream))
@@ -376,7 +389,7 @@ def himuon_pair_stats(a: Sequence, b: Sequence, out=None, workspace=None, stream
         out = torch.empty((n, 3), dtype=torch.float64, device=dev)
     if workspace is None:
         workspace = torch.empty(max(himuon_pair_stats_workspace(a), 8), dtype=torch.uint8, device=dev)
-    nbytes = workspace.numel() * workspace.element_size()
+    nbytes = _in_memory(workspace, workspace.numel() * workspace.element_size(), dev)
     code = lib.himuon_pair_stats(da, db, n, dtype, ctypes.c_void_p(out.data_ptr()),
                                  ctypes.c_void_p(workspace.data_ptr()), nbytes, _stream_handle(stream))
     _check(code, "himuon_pair_stats")
