@@ -359,8 +359,8 @@ himuon_status_t himuon_pair_stats_workspace(const himuon_matrix_t* a, int32_t n,
  * stream   : hipStream_t to enqueue on.
  * One launch per 255 experts.  The fast paths are for bf16 operands of 16-byte
  * chunks: K and N multiples of 8, every matrix at a 16-byte aligned address with
- * a row stride that is a multiple of 8, at most 2^22.  Other bf16
- * operands are multiplied at about half their rate.
+ * a row stride that is a multiple of 8, at most 2^22.  Other bf16 operands are
+ * multiplied at about half their rate.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT (null pointer, n < 1, shapes that do not
  * match), HIMUON_ERR_UNSUPPORTED (dtype), HIMUON_ERR_LAYOUT (alignment, a side
  * above INT32_MAX - 4096, or more output tiles than a launch can hold),
