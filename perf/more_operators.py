@@ -304,17 +304,17 @@ def _dither(state, device):
     widths = torch.tensor([-(-s // BLOCK) * BLOCK for s in state["sizes"]], device=device)
     i = torch.arange(total, device=device) - torch.repeat_interleave(starts, widths, output_size=total)
     low = 0xFFFFFFFF
-    h = ((i >> 1) * 0x9E3779B1 + _key(state["case"]["step"])) & low
-    h = ((h ^ (h >> 15)) * 0x2C1B3C6D) & low
-    h = ((h ^ (h >> 13)) * 0x297A2D39) & low
+    h = ((i >> 1) * 0xB890E049 + _key(state["case"]["step"])) & low
+    h = ((h ^ (h >> 15)) * 0xB4A1B41D) & low
+    h = ((h ^ (h >> 13)) * 0xF5BBB081) & low
     u = torch.where((i & 1) == 0, h & 0xFFFF, h >> 16)
     return u, ((u << 8) | (u >> 8)) & 0xFFFF
 
 
 def _key(step):
     low = 0xFFFFFFFF
-    k = (step * 0x85EBCA77 + 0x165667B1) & low
-    return ((k ^ (k >> 16)) * 0xC2B2AE3D) & low
+    k = (step * 0x9AD24435 + 0xB3B07CC5) & low
+    return ((k ^ (k >> 16)) * 0xB06A350D) & low
 
 
 def _plain_codes(y, u):
