@@ -514,6 +514,162 @@ himuon_status_t himuon_token_logprobs_grad(const himuon_matrix_t* Z, const void*
                                            const float* g_logp, const float* g_entropy, const himuon_matrix_t* dZ,
                                            himuon_dtype_t dt, void* stream);
 
+/* Activation of a gated block. */
+typedef enum himuon_activation {
+    HIMUON_SILU = 0,        /* x / (1 + exp(-x))                                          */
+    HIMUON_GELU = 1,        /* x (1 + erf(x / sqrt 2)) / 2                                */
+    HIMUON_GELU_TANH = 2,   /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2          */
+    HIMUON_RELU = 3         /* max(x, 0), with slope 0 at 0                               */
+} himuon_activation_t;
+
+/*
+ * himuon_grouped_gated_mm - the gated experts' block up to its down product:
+ * both projections, the activation and the product in one kernel.
+ *
+ *     [G | U] = X[r, :] W_e,   H[r, :] = act(G) * U     for every row r of expert e
+ *
+ * X, ends  : as for himuon_grouped_mm (a block without experts is n = 1 with
+ *            ends[0] = M).
+ * W, n     : n >= 1 matrices of one shape, K x 2N: the gate's projection in the
+ *            first N columns, the up projection in the others.  2N x K when
+ *            trans_w is not 0.
+ * H        : M x N, written.
+ * P        : M x 2N, written with [G | U] in dt, for himuon_grouped_gated_mm_grad,
+ *            or NULL.
+ * Rows past ends[n-1] become zero in both.  H is computed from G and U before
+ * they are rounded to dt.  H and P must not overlap each other, X, any W or ends.
+ * The fast paths are those of himuon_grouped_mm, with N a multiple of 8.
+ * Errors: as for himuon_grouped_mm (HIMUON_ERR_UNSUPPORTED also for the
+ * activation).
+ */
+himuon_status_t himuon_grouped_gated_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, int32_t n, int32_t trans_w,
+                                        const int32_t* ends, const himuon_matrix_t* H, const himuon_matrix_t* P,
+                                        himuon_activation_t act, himuon_dtype_t dt, void* stream);
+
+/*
+ * himuon_grouped_gated_mm_grad - back through the down product and the gate in
+ * one kernel: with Y = H W_e the block's down product and dY its gradient,
+ *
+ *     dH = dY W_e^T,   D = [dH * U * act'(G) | dH * act(G)],   H = act(G) * U
+ *
+ * The rest of the block's gradients are the experts' products with D: its
+ * input's is himuon_grouped_mm of D with the projections' W transposed, the
+ * projections' is himuon_grouped_wgrad of X and D, and the down product's is
+ * himuon_grouped_wgrad of H and dY.
+ *
+ * dY       : M x K, rows sorted by expert.
+ * W, n     : the down product's n matrices, N x K as Y = H W_e has them, or
+ *            K x N when trans_w is not 0.
+ * ends     : as for himuon_grouped_mm.
+ * P        : M x 2N, [G | U] as the forward pass left them.
+ * D        : M x 2N, written; it may be P itself (the same pointer and ld), any
+ *            other overlap is refused.
+ * H        : M x N, written, or NULL: the block's H again, so that it need not be
+ *            kept from the forward pass (from the rounded G and U).
+ * Rows past ends[n-1] become zero in D and H, whatever P holds there.
+ * Errors: as for himuon_grouped_gated_mm.
+ */
+himuon_status_t himuon_grouped_gated_mm_grad(const himuon_matrix_t* dY, const himuon_matrix_t* W, int32_t n,
+                                             int32_t trans_w, const int32_t* ends, const himuon_matrix_t* P,
+                                             const himuon_matrix_t* D, const himuon_matrix_t* H,
+                                             himuon_activation_t act, himuon_dtype_t dt, void* stream);
+
+/*
+ * himuon_layer_norm - layer normalisation of rows.
+ *
+ *     y = (x - mean) rstd w + b,   mean and var over the D columns of a row,
+ *     rstd = 1 / sqrt(var + eps)
+ *
+ * X, Y     : N x D, D up to HIMUON_MAX_NORM_COLS; Y is written and may be X
+ *            itself (the same pointer and ld).  N may be 0.
+ * weight, bias : device arrays of D elements of type dt, or NULL (1 and 0).
+ * eps      : finite, >= 0 (with 0, a row of equal values gives NaN).
+ * stats    : device array of N x 2 fp32, written, or NULL: mean and rstd, for
+ *            himuon_layer_norm_grad.
+ * Statistics and sums are fp32 for either type, the variance from the
+ * differences to the mean; y is rounded once.  A NaN or infinity makes its row NaN.
+ * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (dtype, D above the
+ * maximum), HIMUON_ERR_LAYOUT, HIMUON_ERR_OVERLAP, HIMUON_ERR_HIP.
+ */
+#define HIMUON_MAX_NORM_COLS 32768
+himuon_status_t himuon_layer_norm(const himuon_matrix_t* X, const void* weight, const void* bias, float eps,
+                                  const himuon_matrix_t* Y, float* stats, himuon_dtype_t dt, void* stream);
+
+/*
+ * himuon_layer_norm_grad - its gradients, with x_hat = (x - mean) rstd:
+ *
+ *     dx = rstd (dy w - mean(dy w) - x_hat mean(dy w x_hat))
+ *     dweight = sum over rows of dy x_hat,   dbias = sum over rows of dy
+ *
+ * X, weight: of the forward call (weight may be NULL: 1).
+ * stats    : as the forward call wrote it.
+ * dY       : N x D.
+ * dX       : N x D, written, or NULL; it may be dY or X itself (the same pointer
+ *            and ld).
+ * dweight, dbias : device arrays of D elements of type dt, written (zeros where N
+ *            is 0), or NULL.
+ * workspace: device scratch of at least himuon_layer_norm_grad_workspace bytes,
+ *            16-byte aligned; may be NULL when neither dweight nor dbias is asked
+ *            for.  The sums over rows are fp32, added in an order that depends on
+ *            the shape alone.
+ * Errors: as for himuon_layer_norm, and HIMUON_ERR_WORKSPACE.
+ */
+himuon_status_t himuon_layer_norm_grad(const himuon_matrix_t* X, const void* weight, const float* stats,
+                                       const himuon_matrix_t* dY, const himuon_matrix_t* dX, void* dweight,
+                                       void* dbias, himuon_dtype_t dt, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Bytes of workspace himuon_layer_norm_grad needs for rows of this shape (the
+ * pointer is not read) where dweight or dbias is asked for: at most 512
+ * workgroups' 2 D fp32 sums.  Host-side only. */
+himuon_status_t himuon_layer_norm_grad_workspace(const himuon_matrix_t* X, himuon_dtype_t dt, size_t* bytes);
+
+/* State of one tensor in himuon_adamw_step: device arrays for its rows * cols
+ * elements in row order (without gaps, whatever the tensor's stride). */
+typedef struct himuon_adamw_state {
+    void*  m;         /* 32 bits: fp32; 8 bits: e4m3 codes, one byte each               */
+    void*  v;         /* 32 bits: fp32; 8 bits: e4m3 codes of sqrt(v)                   */
+    float* m_scale;   /* 8 bits: ceil(elements / HIMUON_ADAMW_BLOCK); 32 bits: NULL     */
+    float* v_scale;
+} himuon_adamw_state_t;
+
+/*
+ * himuon_adamw_step - one AdamW step on n tensors at once, in place: for what
+ * himuon_muon_step does not treat (weights of norms, biases, embeddings, heads).
+ * With g = grad_scale * G:
+ *
+ *     m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *     W <- (1 - lr weight_decay) W
+ *          - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps)
+ *
+ * W, G     : n >= 0 tensors as matrices (a tensor without gaps may be given as
+ *            one row); W[i] and G[i] of equal rows and cols.  W is written.
+ * S        : n states, written; zeros at the start.
+ * bits     : 32 or 8: how the states are held.  In 8 bits a state is code times
+ *            scale; after the step each block's largest code is 448 (the scale is
+ *            at least 1e-30 / 448), codes are rounded up or down by random bits
+ *            that are a function of step and of the element's place in its tensor,
+ *            and sqrt(v) above 0 keeps a code above 0.
+ * lr, beta1, beta2, eps, weight_decay : finite, 0 <= beta < 1, eps at least
+ *            1.2e-38.
+ * step     : >= 1, one more in every step; all tensors of a call share it.
+ * grad_scale : device scalar (fp32) the gradients are multiplied by, or NULL (1).
+ * w_dt, g_dt : types of W and of G, each HIMUON_BF16 or HIMUON_FP32.
+ * States and update are computed in fp32 and W is rounded once; the update is
+ * taken from m and v before they are rounded to 8 bits.  A NaN or infinity in G
+ * stays in its element (a state that is not finite is held as NaN in 8 bits).
+ * No tensor or state of the call may overlap another one, or G.
+ * One launch per 256 tensors.  lr, step and the rest are values of the call: a
+ * captured one repeats them (grad_scale is read anew).
+ * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (types, bits),
+ * HIMUON_ERR_LAYOUT, HIMUON_ERR_OVERLAP, HIMUON_ERR_HIP.
+ */
+#define HIMUON_ADAMW_BLOCK 256
+himuon_status_t himuon_adamw_step(const himuon_matrix_t* W, const himuon_matrix_t* G, const himuon_adamw_state_t* S,
+                                  int32_t n, int32_t bits, double lr, double beta1, double beta2, double eps,
+                                  double weight_decay, int64_t step, const float* grad_scale, himuon_dtype_t w_dt,
+                                  himuon_dtype_t g_dt, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* himuon_status_string(himuon_status_t s);
 

@@ -22,6 +22,9 @@ I32, I64 = 0, 1      # element types of id arrays
 MAX_STEPS = 16
 MAX_ENTRIES = 1024   # teacher entries of a row (himuon_distill)
 MAX_TOP = 64         # alternatives of a row (himuon_token_logprobs)
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}   # of a gated block
+MAX_NORM_COLS = 32768
+ADAMW_BLOCK = 256    # elements that share a scale in 8-bit states
 
 STATUS = {0: "HIMUON_OK", 1: "HIMUON_ERR_INVALID_ARGUMENT", 2: "HIMUON_ERR_UNSUPPORTED",
           3: "HIMUON_ERR_LAYOUT", 4: "HIMUON_ERR_OVERLAP", 5: "HIMUON_ERR_WORKSPACE", 6: "HIMUON_ERR_HIP"}
@@ -30,7 +33,9 @@ EXPORTS = ["himuon_plan", "himuon_workspace_size", "himuon_tiled_ns", "himuon_ti
            "himuon_tiled_ns_schedule",
            "himuon_muon_step", "himuon_gram_ns", "himuon_gram_ns_workspace", "himuon_pair_stats",
            "himuon_pair_stats_workspace", "himuon_grouped_mm", "himuon_grouped_wgrad",
-           "himuon_grouped_wgrad_workspace", "himuon_distill",
+           "himuon_grouped_wgrad_workspace", "himuon_grouped_gated_mm", "himuon_grouped_gated_mm_grad",
+           "himuon_layer_norm", "himuon_layer_norm_grad", "himuon_layer_norm_grad_workspace", "himuon_adamw_step",
+           "himuon_distill",
            "himuon_distill_workspace", "himuon_distill_grad", "himuon_token_logprobs",
            "himuon_token_logprobs_workspace", "himuon_token_logprobs_grad", "himuon_status_string",
            "himuon_last_hip_error", "himuon_version"]
@@ -39,6 +44,11 @@ EXPORTS = ["himuon_plan", "himuon_workspace_size", "himuon_tiled_ns", "himuon_ti
 class himuon_matrix_t(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("ld", ctypes.c_int64)]
+
+
+class himuon_adamw_state_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 class himuon_plan_info_t(ctypes.Structure):
@@ -104,11 +114,17 @@ def _load():
     L.himuon_pair_stats_workspace.argtypes = [P(himuon_matrix_t), ctypes.c_int32, P(ctypes.c_size_t)]
     L.himuon_pair_stats_workspace.restype = ctypes.c_int
     M, V, I, F, Z = P(himuon_matrix_t), ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
-    E = ctypes.c_int
+    E, D, A = ctypes.c_int, ctypes.c_double, P(himuon_adamw_state_t)
     for name, args in {
             "himuon_grouped_mm": [M, M, I, I, V, M, E, V],
             "himuon_grouped_wgrad": [M, M, V, M, I, E, V, Z, V],
             "himuon_grouped_wgrad_workspace": [M, M, I, E, P(Z)],
+            "himuon_grouped_gated_mm": [M, M, I, I, V, M, M, E, E, V],
+            "himuon_grouped_gated_mm_grad": [M, M, I, I, V, M, M, M, E, E, V],
+            "himuon_layer_norm": [M, V, V, F, M, V, E, V],
+            "himuon_layer_norm_grad": [M, V, V, M, M, V, V, E, V, Z, V],
+            "himuon_layer_norm_grad_workspace": [M, E, P(Z)],
+            "himuon_adamw_step": [M, M, A, I, I, D, D, D, D, D, ctypes.c_int64, V, E, E, V],
             "himuon_distill": [M, V, E, M, F, I, V, V, V, M, E, V, Z, V],
             "himuon_distill_workspace": [M, E, I, P(Z)],
             "himuon_distill_grad": [M, V, E, M, F, I, V, V, M, E, V],
@@ -595,6 +611,311 @@ def himuon_grouped_wgrad(x, dy, ends, out=None, workspace=None, stream=None):
         _check(lib.himuon_grouped_wgrad(ctypes.byref(a), ctypes.byref(b), _ends(ends, n, x.device), g.array, n, code,
                                         wp, wb, s), "himuon_grouped_wgrad")
     return out
+
+
+class Gated(NamedTuple):
+    h: object
+    pre: object = None
+
+
+class GatedGrad(NamedTuple):
+    grad: object
+    h: object = None
+
+
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _filled(t, rows, cols, like, what):
+    """t, or a new tensor, of the given shape, with the type and place of `like`."""
+    import torch
+    if t is None:
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what} must have the operands' dtype")
+    if t.shape != (rows, cols) or t.device != like.device:
+        raise ValueError(f"{what} must be of shape {(rows, cols)}, on the operands' GPU")
+    return t
+
+
+def himuon_grouped_gated_mm(x, w, ends, act: str = "silu", keep=False, out=None, stream=None) -> Gated:
+    """The gated experts' block up to its down product: with [g | u] = x[r] @ w[e]
+    for the rows r of expert e, h = act(g) * u, in one kernel.
+
+    x: (M, K), rows sorted by expert.  w: the experts' (K, 2 N) weights as
+    matrices() takes them, the gate's projection in the first N columns.  ends: as
+    for himuon_grouped_mm.  act: silu, gelu, gelu_tanh or relu.  keep: also
+    [g | u] (M, 2 N), for the gradient: True, or the tensor to write.  out:
+    optional (M, N) tensor.  Returns (h, pre)."""
+    w = matrices(w)
+    K, N2 = w.shape
+    _need_gpu(x, w, ends)
+    if x.dtype != w.dtype:
+        raise TypeError("x and w must have one dtype")
+    if N2 % 2:
+        raise ValueError("w must hold as many gate as up columns")
+    code = _activation(act)
+    with _placed(x.device, stream) as s:
+        M = x.shape[0]
+        h = _filled(out, M, N2 // 2, x, "out")
+        pre = dp = None
+        if keep is not False and keep is not None:
+            pre = _filled(None if keep is True else keep, M, N2, x, "keep")
+            dp = _rows(pre)
+        dx, dh = _rows(x), _rows(h)
+        _check(lib.himuon_grouped_gated_mm(ctypes.byref(dx), w.array, w.n, int(w.transposed), _ends(ends, w.n, x.device),
+                                           ctypes.byref(dh), None if dp is None else ctypes.byref(dp), code,
+                                           _dtype_code(x), s), "himuon_grouped_gated_mm")
+    return Gated(h, pre)
+
+
+def himuon_grouped_gated_mm_grad(dy, w, ends, pre, act: str = "silu", hidden=False, out=None, stream=None) -> GatedGrad:
+    """Back through the block's down product y = h @ w[e] and its gate in one
+    kernel: from dy (M, K) and the forward pass's pre = [g | u] (M, 2 N) the
+    gradient of pre.
+
+    w: the down product's (N, K) weights as matrices() takes them.  hidden: also h
+    again (M, N), for the gradient of w: True, or the tensor to write.  out: the
+    tensor to write, which may be pre itself.  Returns (grad, h).  The block's other
+    gradients are himuon_grouped_mm(grad, w_in.transpose(1, 2), ends),
+    himuon_grouped_wgrad(x, grad, ends) and himuon_grouped_wgrad(h, dy, ends)."""
+    w = matrices(w)
+    N, K = w.shape
+    _need_gpu(dy, w, ends, pre)
+    if dy.dtype != w.dtype or pre.dtype != dy.dtype:
+        raise TypeError("dy, w and pre must have one dtype")
+    code = _activation(act)
+    with _placed(dy.device, stream) as s:
+        M = dy.shape[0]
+        grad = _filled(out, M, 2 * N, dy, "out")
+        h = dh = None
+        if hidden is not False and hidden is not None:
+            h = _filled(None if hidden is True else hidden, M, N, dy, "hidden")
+            dh = _rows(h)
+        dd, dp, dg = _rows(dy), _rows(pre), _rows(grad)
+        _check(lib.himuon_grouped_gated_mm_grad(ctypes.byref(dd), w.array, w.n, int(w.transposed),
+                                                _ends(ends, w.n, dy.device), ctypes.byref(dp), ctypes.byref(dg),
+                                                None if dh is None else ctypes.byref(dh), code, _dtype_code(dy), s),
+               "himuon_grouped_gated_mm_grad")
+    return GatedGrad(grad, h)
+
+
+# ---- layer normalisation -----------------------------------------------------------
+class Normed(NamedTuple):
+    y: object
+    stats: object = None
+
+
+class NormGrad(NamedTuple):
+    dx: object = None
+    dweight: object = None
+    dbias: object = None
+
+
+def _columns(t, x, what):
+    if t is None:
+        return None
+    if t.dtype != x.dtype:
+        raise TypeError(f"{what} must have the rows' dtype")
+    if t.shape != (x.shape[1],) or not t.is_contiguous() or t.device != x.device:
+        raise ValueError(f"{what} must be contiguous with one entry per column, on the rows' GPU")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def himuon_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True, out=None,
+                      stream=None) -> Normed:
+    """Layer normalisation of the rows of x (N, D): (x - mean) / sqrt(var + eps) *
+    weight + bias.  weight, bias: (D,) of x's type, or None.  out: the tensor to
+    write, which may be x.  Returns (y, stats), stats (N, 2) float32, mean and 1 /
+    sqrt(var + eps), for himuon_layer_norm_grad (None with stats=False)."""
+    import torch
+    _need_gpu(x)
+    dx = _rows(x)
+    with _placed(x.device, stream) as s:
+        y = _filled(out, x.shape[0], x.shape[1], x, "out")
+        st = torch.empty((x.shape[0], 2), dtype=torch.float32, device=x.device) if stats else None
+        dy = _rows(y)
+        _check(lib.himuon_layer_norm(ctypes.byref(dx), _columns(weight, x, "weight"), _columns(bias, x, "bias"), eps,
+                                     ctypes.byref(dy), None if st is None else ctypes.c_void_p(st.data_ptr()),
+                                     _dtype_code(x), s), "himuon_layer_norm")
+    return Normed(y, st)
+
+
+def himuon_layer_norm_grad_workspace(x) -> int:
+    """Workspace bytes himuon_layer_norm_grad needs for rows like x."""
+    need = ctypes.c_size_t(0)
+    dx = _rows(x)
+    _check(lib.himuon_layer_norm_grad_workspace(ctypes.byref(dx), _dtype_code(x), ctypes.byref(need)),
+           "himuon_layer_norm_grad_workspace")
+    return need.value
+
+
+def himuon_layer_norm_grad(x, weight, stats, dy, dx=True, dweight=True, dbias=True, workspace=None,
+                           stream=None) -> NormGrad:
+    """Gradients of himuon_layer_norm's x, weight and bias from dy (N, D) and the
+    stats of the forward call.  dx, dweight, dbias: True, the tensor to write (dx may
+    be dy or x), or False.  Returns (dx, dweight, dbias)."""
+    import torch
+    _need_gpu(x, stats, dy)
+    if dy.dtype != x.dtype:
+        raise TypeError("x and dy must have one dtype")
+    N, D = x.shape
+    sp = _vector(stats, N, "stats", x.device, 2)
+    wanted = lambda t: t is not None and t is not False
+    with _placed(x.device, stream) as s:
+        gx = _filled(None if dx is True else dx, N, D, x, "dx") if wanted(dx) else None
+        vec = lambda t: torch.empty(D, dtype=x.dtype, device=x.device) if t is True else t
+        gw, gb = vec(dweight) if wanted(dweight) else None, vec(dbias) if wanted(dbias) else None
+        a, b, c = _rows(x), _rows(dy), None if gx is None else _rows(gx)
+        code = _dtype_code(x)
+        keep, wp, wb = None, None, 0
+        if gw is not None or gb is not None:
+            keep, wp, wb = _scratch(lib.himuon_layer_norm_grad_workspace, "himuon_layer_norm_grad_workspace", workspace,
+                                    x.device, ctypes.byref(a), code)
+        _check(lib.himuon_layer_norm_grad(ctypes.byref(a), _columns(weight, x, "weight"), sp, ctypes.byref(b),
+                                          None if c is None else ctypes.byref(c), _columns(gw, x, "dweight"),
+                                          _columns(gb, x, "dbias"), code, wp, wb, s), "himuon_layer_norm_grad")
+    return NormGrad(gx, gw, gb)
+
+
+# ---- AdamW -------------------------------------------------------------------------
+class Tensors:
+    """Descriptors of tensors of any shapes, made once and used for any number of
+    calls.  It keeps the tensors, whose values may change but not their place (see
+    Matrices)."""
+
+    def __init__(self, array, tensors, dtype, device, shapes):
+        self.array, self.tensors, self.dtype, self.device, self.shapes = array, tensors, dtype, device, shapes
+        self.places = [t.data_ptr() for t in tensors]
+
+    def in_place(self):
+        """Itself, if the tensors are still where they were described."""
+        if [t.data_ptr() for t in self.tensors] != self.places:
+            raise ValueError("tensors were described before they got other memory: describe them again")
+        return self
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def tensors(ts) -> Tensors:
+    """Descriptors of bf16 or fp32 tensors of one type on one GPU: contiguous ones
+    of any shape, or 2-D ones with unit stride along the rows."""
+    if isinstance(ts, Tensors):
+        return ts.in_place()
+    ts = list(ts)
+    arr = (himuon_matrix_t * max(len(ts), 1))()
+    if not ts:
+        return Tensors(arr, ts, None, None, [])
+    first = ts[0]
+    if not first.is_cuda:
+        raise ValueError("tensors must be on one GPU")
+    dtype, device = first.dtype, first.device
+    _dtype_code(first)
+    for i, t in enumerate(ts):
+        if t.dtype != dtype:
+            raise TypeError("tensors must have one dtype")
+        if t.device != device:
+            raise ValueError("tensors must be on one GPU")
+        n = t.numel()
+        if n == 0:
+            raise ValueError("tensors must not be empty")
+        if t.is_contiguous():
+            cols = t.shape[-1] if t.dim() else 1
+            arr[i] = himuon_matrix_t(t.data_ptr(), n // cols, cols, cols)
+        elif t.dim() <= 2:
+            arr[i] = _rows(t if t.dim() == 2 else t.unsqueeze(0))
+        else:
+            raise ValueError("tensors must be contiguous, or 2-D with unit stride along the rows")
+    return Tensors(arr, ts, dtype, device, [tuple(t.shape) for t in ts])
+
+
+class AdamWState:
+    """States of an AdamW step for given tensors, zero at first.  m and v are flat,
+    each tensor's part beginning at a multiple of ADAMW_BLOCK elements (`starts`):
+    float32 (bits=32), or float8_e4m3fn codes of m and of sqrt(v) with one float32
+    scale for each block, m_scale and v_scale (bits=8)."""
+
+    def __init__(self, like: Tensors, bits: int):
+        import numpy as np
+        import torch
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32")
+        self.bits, self.shapes, self.device = bits, like.shapes, like.device
+        n = len(like)
+        sizes = np.array([like.array[i].rows * like.array[i].cols for i in range(n)], dtype=np.int64)
+        blocks = -(-sizes // ADAMW_BLOCK)
+        firsts = np.concatenate([[0], np.cumsum(blocks)]).astype(np.int64)
+        self.starts = (firsts[:-1] * ADAMW_BLOCK).tolist()
+        total = int(firsts[-1])
+        dtype = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        flat = lambda: torch.zeros(total * ADAMW_BLOCK, dtype=torch.float32 if bits == 32 else torch.uint8,
+                                   device=like.device).view(dtype)
+        self.m, self.v = flat(), flat()
+        self.m_scale = self.v_scale = None
+        if bits == 8:
+            self.m_scale, self.v_scale = (torch.zeros(total, dtype=torch.float32, device=like.device) for _ in range(2))
+        es = self.m.element_size()
+        a = np.zeros((max(n, 1), 4), dtype=np.int64)
+        if n:
+            a[:, 0] = self.m.data_ptr() + firsts[:-1] * (ADAMW_BLOCK * es)
+            a[:, 1] = self.v.data_ptr() + firsts[:-1] * (ADAMW_BLOCK * es)
+            if bits == 8:
+                a[:, 2] = self.m_scale.data_ptr() + firsts[:-1] * 4
+                a[:, 3] = self.v_scale.data_ptr() + firsts[:-1] * 4
+        self.array = (himuon_adamw_state_t * max(n, 1)).from_buffer(a)
+        self.places = self._places()
+
+    def _places(self):
+        return [t.data_ptr() for t in (self.m, self.v, self.m_scale, self.v_scale) if t is not None]
+
+    def in_place(self):
+        """Itself, if its tensors are still where they were made (load saved states
+        with copy_)."""
+        if self._places() != self.places:
+            raise ValueError("states got other memory: copy into them instead")
+        return self
+
+
+def adamw_state(like, bits: int = 32) -> AdamWState:
+    """New (zero) states for tensors as himuon_adamw_step takes them."""
+    import torch
+    like = tensors(like)
+    if like.device is None:
+        return AdamWState(like, bits)
+    with torch.cuda.device(like.device):
+        return AdamWState(like, bits)
+
+
+def himuon_adamw_step(w, g, state: AdamWState, lr: float, step: int, betas=(0.9, 0.999), eps: float = 1e-8,
+                      weight_decay: float = 0.0, grad_scale=None, stream=None):
+    """One AdamW step on all tensors of w at once, in place, from gradients g and
+    the states adamw_state(w) made.  w, g: lists of tensors (bf16 or fp32, each list
+    of one type, which may differ), or what tensors() made of them once.  step: 1 in
+    the first step.  grad_scale: float32 tensor of one element on the GPU that the
+    gradients are multiplied by.  A captured call repeats its lr and step."""
+    import torch
+    w, g = tensors(w), tensors(g)
+    state.in_place()
+    if w.shapes != g.shapes or w.shapes != state.shapes:
+        raise ValueError("weights, gradients and states must agree in number and shapes")
+    if len(w) == 0:
+        return
+    if g.device != w.device or state.device != w.device:
+        raise ValueError("tensors must be on one GPU")
+    sp = None
+    if grad_scale is not None:
+        if grad_scale.dtype != torch.float32:
+            raise TypeError("grad_scale must be float32")
+        if grad_scale.numel() != 1 or grad_scale.device != w.device:
+            raise ValueError("grad_scale must be one element, on the tensors' GPU")
+        sp = ctypes.c_void_p(grad_scale.data_ptr())
+    with _placed(w.device, stream) as s:
+        _check(lib.himuon_adamw_step(w.array, g.array, state.array, len(w), state.bits, lr, betas[0], betas[1], eps,
+                                     weight_decay, step, sp, _dtype_code(w), _dtype_code(g), s), "himuon_adamw_step")
 
 
 # ---- losses over logits ------------------------------------------------------------

@@ -2,8 +2,6 @@
 // products and the losses over logits.  Argument checks and launches; see
 // include/himuon.h for the contract.
 #include <cmath>
-#include <new>
-#include <stdexcept>
 
 #include "api_util.h"
 #include "grouped.h"
@@ -12,51 +10,6 @@
 using namespace himuon;
 
 namespace {
-
-// No exception crosses the C interface: the checks below sort descriptor lists
-// in host memory, which can run out.
-template <typename F>
-himuon_status_t guarded(F f) {
-    try {
-        return f();
-    } catch (const std::bad_alloc&) {
-    } catch (const std::length_error&) {
-    }
-    return hip_fail(hipErrorOutOfMemory);
-}
-
-himuon_status_t check_dtype(himuon_dtype_t dt) {
-    return dt == HIMUON_BF16 || dt == HIMUON_FP32 ? HIMUON_OK : HIMUON_ERR_UNSUPPORTED;
-}
-
-// A matrix whose rows are tokens: as check_matrix, but it may have no rows.
-himuon_status_t check_rows(const himuon_matrix_t& d, size_t es) {
-    if (d.rows != 0) return check_matrix(d, es);
-    if (d.cols < 1 || d.ld < d.cols) return HIMUON_ERR_INVALID_ARGUMENT;
-    return d.cols > INT32_MAX ? HIMUON_ERR_LAYOUT : HIMUON_OK;
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// Rows of whole 16-byte chunks, and 256 of them within 32-bit byte offsets.
-bool chunked(const himuon_matrix_t& d) { return aligned(d.ptr, 16) && d.ld % 8 == 0 && d.ld <= (1 << 22); }
-
-// Byte range of a contiguous device array, as an extent of one row.
-Extent array_extent(const void* p, int64_t bytes) {
-    return extent_of(himuon_matrix_t{const_cast<void*>(p), 1, bytes, bytes}, 1, 0);
-}
-
-#define HIMUON_TRY(call)                           \
-    do {                                           \
-        const himuon_status_t st_ = (call);        \
-        if (st_ != HIMUON_OK) return st_;          \
-    } while (0)
-
-himuon_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
-    if (need == 0) return HIMUON_OK;
-    if (ws == nullptr || bytes < need) return HIMUON_ERR_WORKSPACE;
-    return aligned(ws, 16) ? HIMUON_OK : HIMUON_ERR_LAYOUT;
-}
 
 // ---- the experts' products ------------------------------------------------------
 // Checks of X, ends and n; fills the arguments every launch of the call shares.
@@ -135,6 +88,78 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
     if (!all_launches(a, grouped_mm_fits)) return HIMUON_ERR_LAYOUT;
     return each_launch(a, W, n, [&] {
         const hipError_t e = launch_grouped_mm(a, trans_w != 0, reinterpret_cast<hipStream_t>(stream));
+        return e == hipSuccess ? HIMUON_OK : hip_fail(e);
+    });
+}
+
+// ---- the gated block --------------------------------------------------------------
+himuon_status_t activation(himuon_activation_t act, GroupedArgs& a) {
+    const float slope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+    switch (act) {
+        case HIMUON_SILU: a.k0 = 1.f; return HIMUON_OK;
+        case HIMUON_GELU: a.erf = 1; return HIMUON_OK;
+        case HIMUON_GELU_TANH: a.k0 = slope; a.k1 = slope * 0.044715f; return HIMUON_OK;
+        case HIMUON_RELU: a.relu = 1; return HIMUON_OK;
+    }
+    return HIMUON_ERR_UNSUPPORTED;
+}
+
+// Both passes: Y is H (forward) or D, P = [G | U], H (of a gradient) may be null.
+himuon_status_t gated(Gate gate, const himuon_matrix_t* X, const himuon_matrix_t* W, int32_t n, bool stored_nk,
+                      const int32_t* ends, const himuon_matrix_t* Y, const himuon_matrix_t* P,
+                      const himuon_matrix_t* H, himuon_activation_t act, himuon_dtype_t dt, void* stream) {
+    GroupedArgs a{};
+    HIMUON_TRY(grouped_args(X, W, n, ends, dt, a));
+    a.gate = gate;
+    HIMUON_TRY(activation(act, a));
+    const bool forward = gate == Gate::Forward;
+    if (Y == nullptr || (P == nullptr && !forward)) return HIMUON_ERR_INVALID_ARGUMENT;
+    const size_t es = elem_size(dt);
+    const int64_t K = stored_nk ? W[0].cols : W[0].rows, wide = stored_nk ? W[0].rows : W[0].cols;
+    if (forward && wide % 2 != 0) return HIMUON_ERR_INVALID_ARGUMENT;
+    const int64_t N = forward ? wide / 2 : wide;
+    if (X->cols != K) return HIMUON_ERR_INVALID_ARGUMENT;
+    const auto rows_of = [&](const himuon_matrix_t* m, int64_t cols) {
+        if (m == nullptr) return HIMUON_OK;
+        HIMUON_TRY(check_rows(*m, es));
+        if (m->cols > kMaxSide) return HIMUON_ERR_LAYOUT;
+        return m->rows == X->rows && m->cols == cols ? HIMUON_OK : HIMUON_ERR_INVALID_ARGUMENT;
+    };
+    HIMUON_TRY(rows_of(Y, forward ? N : 2 * N));
+    HIMUON_TRY(rows_of(P, 2 * N));
+    HIMUON_TRY(rows_of(H, N));
+    if (a.rows == 0) return HIMUON_OK;
+    // what is written lies apart from all else (but D may be P)
+    std::vector<Extent> out{extent_of(*Y, es, 0)};
+    if (forward && P != nullptr) out.push_back(extent_of(*P, es, 0));
+    if (H != nullptr) out.push_back(extent_of(*H, es, 0));
+    if (out.size() == 2 && share_element(out[0], out[1])) return HIMUON_ERR_OVERLAP;
+    const bool in_place = !forward && P->ptr == Y->ptr && P->ld == Y->ld;
+    for (size_t i = 0; i < out.size(); ++i) {
+        if (share_element(out[i], extent_of(*X, es, 0)) || share_element(out[i], array_extent(ends, 4 * (int64_t)n)))
+            return HIMUON_ERR_OVERLAP;
+        for (int32_t e = 0; e < n; ++e)
+            if (share_element(out[i], extent_of(W[e], es, 0))) return HIMUON_ERR_OVERLAP;
+        if (!forward && !(i == 0 && in_place) && share_element(out[i], extent_of(*P, es, 0))) return HIMUON_ERR_OVERLAP;
+    }
+    a.y = Y->ptr;
+    a.y_ld = Y->ld;
+    a.ndim = (int32_t)N;
+    a.vec = chunked(*X) && chunked(*Y) && K % 8 == 0 && N % 8 == 0;
+    if (P != nullptr) {
+        a.p = P->ptr;
+        a.p_ld = P->ld;
+        a.vec = a.vec && chunked(*P);
+    }
+    if (H != nullptr) {
+        a.h = H->ptr;
+        a.h_ld = H->ld;
+        a.vec = a.vec && chunked(*H);
+    }
+    for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(W[e]);
+    if (!all_launches(a, grouped_mm_fits)) return HIMUON_ERR_LAYOUT;
+    return each_launch(a, W, n, [&] {
+        const hipError_t e = launch_grouped_gated(a, stored_nk, reinterpret_cast<hipStream_t>(stream));
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);
     });
 }
@@ -243,30 +268,6 @@ himuon_status_t grad_arg(const himuon_matrix_t* Z, const himuon_matrix_t* dZ, si
     if (Z->rows == 0 || (dZ->ptr == Z->ptr && dZ->ld == Z->ld)) return HIMUON_OK;
     return share_element(extent_of(*dZ, es, 0), extent_of(*Z, es, 0)) ? HIMUON_ERR_OVERLAP : HIMUON_OK;
 }
-
-// Device arrays of a call: none written may share memory with another one, or
-// with the matrices.
-struct Arrays {
-    std::vector<Extent> written, read;
-    himuon_status_t add(const void* p, int64_t count, size_t es, bool write) {
-        if (p == nullptr || count == 0) return HIMUON_OK;
-        if (!aligned(p, es)) return HIMUON_ERR_LAYOUT;
-        (write ? written : read).push_back(array_extent(p, count * (int64_t)es));
-        return HIMUON_OK;
-    }
-    void add(const himuon_matrix_t* m, size_t es, bool write) {
-        if (m != nullptr && m->rows > 0) (write ? written : read).push_back(extent_of(*m, es, 0));
-    }
-    himuon_status_t check() const {
-        for (size_t i = 0; i < written.size(); ++i) {
-            for (size_t j = i + 1; j < written.size(); ++j)
-                if (share_element(written[i], written[j])) return HIMUON_ERR_OVERLAP;
-            for (const Extent& r : read)
-                if (share_element(written[i], r)) return HIMUON_ERR_OVERLAP;
-        }
-        return HIMUON_OK;
-    }
-};
 
 himuon_status_t teacher_args(const himuon_matrix_t* Z, const void* idx, const himuon_matrix_t* T, int32_t normalize,
                              LogitsArgs& a, Arrays& arr) {
@@ -440,6 +441,20 @@ himuon_status_t himuon_grouped_wgrad_workspace(const himuon_matrix_t* X, const h
     a.total = n;
     *bytes = wgrad_bytes(a);
     return HIMUON_OK;
+}
+
+himuon_status_t himuon_grouped_gated_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, int32_t n, int32_t trans_w,
+                                        const int32_t* ends, const himuon_matrix_t* H, const himuon_matrix_t* P,
+                                        himuon_activation_t act, himuon_dtype_t dt, void* stream) {
+    return guarded([&] { return gated(Gate::Forward, X, W, n, trans_w != 0, ends, H, P, nullptr, act, dt, stream); });
+}
+
+himuon_status_t himuon_grouped_gated_mm_grad(const himuon_matrix_t* dY, const himuon_matrix_t* W, int32_t n,
+                                             int32_t trans_w, const int32_t* ends, const himuon_matrix_t* P,
+                                             const himuon_matrix_t* D, const himuon_matrix_t* H,
+                                             himuon_activation_t act, himuon_dtype_t dt, void* stream) {
+    // (W as Y = H W_e has it is N x K: the product with its transpose)
+    return guarded([&] { return gated(Gate::Grad, dY, W, n, trans_w == 0, ends, D, P, H, act, dt, stream); });
 }
 
 himuon_status_t himuon_distill(const himuon_matrix_t* Z, const void* idx, himuon_index_t it, const himuon_matrix_t* T,

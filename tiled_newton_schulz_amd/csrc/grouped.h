@@ -13,6 +13,13 @@ constexpr int kExperts = 255;
 // Longest side: the kernels step past an end by less than this leaves to 2^31.
 constexpr int64_t kMaxSide = INT32_MAX - 4096;
 
+// A product's part in a gated block (grouped.hip).
+enum class Gate : int32_t {
+    None,       // Y = X W_e
+    Forward,    // W_e holds the gate's and the up projection: Y = act(G) * U
+    Grad        // X W_e^T is the gradient of that Y: gradients of G and U
+};
+
 // One launch of Y = X W_e (or X W_e^T) or of G_e = X_e^T D_e.
 struct GroupedArgs {
     const void* x;           // M x K
@@ -29,6 +36,13 @@ struct GroupedArgs {
     int32_t vec;             // rows and widths allow 16-byte chunks
     float* sums;             // weight gradient: workspace of the parts' sums, or null
     int32_t parts;           // weight gradient: parts an expert's rows are cut into
+    // gated block: N = ndim is the width of H; y is H (Forward) or D (Grad, M x 2N)
+    Gate gate;
+    void* p;                 // [G | U], M x 2N: written by Forward (or null), read by Grad
+    void* h;                 // Grad: H, or null
+    int64_t p_ld, h_ld;
+    float k0, k1;            // act(g) = g s(g): s = sigmoid(k0 g + k1 g^3),
+    int32_t relu, erf;       // or 1 above 0, or the normal distribution's integral
     void* w[kExperts];       // product: weights; weight gradient: results
     int64_t w_ld[kExperts];
 };
@@ -42,5 +56,7 @@ int32_t grouped_wgrad_parts(const GroupedArgs& a);
 int64_t grouped_wgrad_part_bytes(const GroupedArgs& a);
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s);
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
+// a.gate != None; trans_w: W_e is stored N x K (2N x K).
+hipError_t launch_grouped_gated(const GroupedArgs& a, bool trans_w, hipStream_t s);
 
 }  // namespace himuon

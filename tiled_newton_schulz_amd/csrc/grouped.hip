@@ -119,7 +119,11 @@ template <> struct Io<1> {
 struct __attribute__((packed, aligned(2))) Loose16 { u32x4 v; };   // 16 bytes at an element's alignment
 
 // One operand of a tile: `side` rows (or columns) of the tile by kd.
-template <int DT, bool ALONG_K, int EDGE>
+// PAIR: the weights of a gated block, whose N gate columns are followed by N up
+// columns.  The panel's 32-wide blocks alternate between the two: block 2 b holds
+// gate columns 32 b .. 32 b + 31 of the tile and block 2 b + 1 the same up columns;
+// `side` counts the columns of one of them.
+template <int DT, bool ALONG_K, int EDGE, bool PAIR = false>
 struct Staged {
     using T = typename Io<DT>::T;
     static constexpr int EPC = Io<DT>::EPC, BK = Io<DT>::BK;
@@ -133,17 +137,28 @@ struct Staged {
     int64_t ld;
     int side, kd;
     int before;   // elements of a row before p (along k: 0)
+    int up;       // PAIR: N
 
+    // PAIR: a place of the panel as columns from the tile's first of its half, and
+    // as columns of the stored matrix from p
+    __device__ __forceinline__ static int in_half(int i) { return (i >> 6) * 32 + (i & 31); }
+    __device__ __forceinline__ int64_t stored(int i) const { return in_half(i) + (i & 32 ? (int64_t)up : 0); }
     // thread of its part of the workgroup
     __device__ __forceinline__ static int tid() { return threadIdx.x & 255; }
     // bf16 along i: place of chunk c of k row k is c ^ swap(k), so that the four
     // rows and 32 columns that are read together lie on different banks
     __device__ __forceinline__ static int swap(int k) { return EDGE == 128 ? 4 * (k & 3) : 2 * (k & 2); }
+    // elements of a stored row from p (along k: from k0) on that may be loaded
+    __device__ __forceinline__ int row_end(int k0) const {
+        return ALONG_K ? kd - k0 : PAIR ? (int)(2 * (int64_t)up - before) : side;
+    }
     // chunk j of this thread at k0: row and first column of the stored matrix
     // (a row of k elements, or a k row)
     __device__ __forceinline__ void load(int k0, u32x4 (&r)[NCH]) const {
-        const int row0 = tid() / CPR, c = (tid() % CPR) * EPC;
-        const int rows = ALONG_K ? side : kd - k0, cols = ALONG_K ? kd - k0 : side;
+        const int row0 = tid() / CPR, c0 = (tid() % CPR) * EPC;
+        const bool split = PAIR && !ALONG_K;
+        const int c = split ? (int)stored(c0) : c0;
+        const int rows = split && in_half(c0) >= side ? 0 : ALONG_K ? side : kd - k0, cols = row_end(k0);
         const T* q = p + (ALONG_K ? (int64_t)k0 : k0 * ld) + c;
         // elements of the chunk past the row's end: it is loaded from as many
         // before its place where the row has them, see put()
@@ -151,8 +166,8 @@ struct Staged {
         const bool wide = out < EPC && (ALONG_K ? k0 : before) + c >= out;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            const int row = row0 + j * ROWS;
-            const T* at = q + row * ld;
+            const int row = PAIR && ALONG_K ? in_half(row0 + j * ROWS) : row0 + j * ROWS;
+            const T* at = q + (PAIR && ALONG_K ? stored(row0 + j * ROWS) : row) * ld;
             if (row < rows && wide) {
                 r[j] = reinterpret_cast<const Loose16*>(at - out)->v;
                 continue;
@@ -172,7 +187,8 @@ struct Staged {
     }
     // stores the chunks that load(k0, r) has loaded
     __device__ __forceinline__ void put(int k0, T* s, u32x4 (&r)[NCH]) const {
-        const int col = (tid() % CPR) * EPC, out = max(col + EPC - (ALONG_K ? kd - k0 : side), 0);
+        const int c0 = (tid() % CPR) * EPC, col = PAIR && !ALONG_K ? (int)stored(c0) : c0;
+        const int out = max(col + EPC - row_end(k0), 0);
         if (out > 0 && out < EPC && (ALONG_K ? k0 : before) + col >= out) {
             const int by = out * (int)sizeof(T) * 8;   // 16 .. 112 bits
 #pragma unroll
@@ -221,54 +237,128 @@ struct Staged {
 // 7)) neighbouring lanes store whole rows of a block.  (Stored from registers in
 // runs of four, the 0.13 GB of gradients of 4 rows over 15 experts of 1340 x 3339
 // took 59 instead of 37 us.)
+template <int DT>
+struct BlockIo {
+    using T = typename Io<DT>::T;
+    static constexpr int EPC = Io<DT>::EPC, CPR = 32 / EPC, RPP = 64 / CPR;   // chunks of a row, rows moved at a time
+    __device__ __forceinline__ static T* at(T* scratch, int r, int c) {
+        return scratch + r * 32 + (c ^ ((DT == 0 ? r >> 1 : r) & (CPR - 1))) * EPC;
+    }
+    // the block at (br, bc) of C, which has `rows` by `cols` elements
+    __device__ __forceinline__ static void put(const f32x16& v, T* scratch, T* C, int64_t ldc, int rows, int cols,
+                                               int br, int bc) {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (DT == 0)
+                *reinterpret_cast<u32x2*>(at(scratch, l32, m) + 4 * gl) =
+                    u32x2{pack2(v[4 * m], v[4 * m + 1]), pack2(v[4 * m + 2], v[4 * m + 3])};
+            else
+                *reinterpret_cast<f32x4*>(at(scratch, l32, 2 * m + gl)) =
+                    f32x4{v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]};
+        }
+#pragma unroll
+        for (int p = 0; p < 32 / RPP; ++p) {
+            const int r = p * RPP + lane / CPR, c = lane % CPR, col = bc + c * EPC;
+            if (br + r >= rows || col >= cols) continue;
+            const u32x4 w = *reinterpret_cast<const u32x4*>(at(scratch, r, c));
+            T* to = C + (br + r) * ldc + col;
+            if (col + EPC <= cols) {
+                *reinterpret_cast<Loose16*>(to) = Loose16{w};
+            } else {
+#pragma unroll
+                for (int e = 0; e < EPC - 1; ++e)
+                    if (col + e < cols) {
+                        if constexpr (DT == 0) to[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+                        else to[e] = __uint_as_float(w[e]);
+                    }
+            }
+        }
+    }
+    // the other way: a block of C into the lanes that hold its sums (zeros outside)
+    __device__ __forceinline__ static f32x16 get(T* scratch, const T* C, int64_t ldc, int rows, int cols, int br, int bc) {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+        for (int p = 0; p < 32 / RPP; ++p) {
+            const int r = p * RPP + lane / CPR, c = lane % CPR, col = bc + c * EPC;
+            u32x4 w = {0, 0, 0, 0};
+            const T* from = C + (br + r) * ldc + col;
+            if (br + r < rows && col + EPC <= cols) {
+                w = reinterpret_cast<const Loose16*>(from)->v;
+            } else if (br + r < rows) {
+#pragma unroll
+                for (int e = 0; e < EPC - 1; ++e)
+                    if (col + e < cols) {
+                        if constexpr (DT == 0) w[e >> 1] |= (unsigned)from[e] << (16 * (e & 1));
+                        else w[e] = __float_as_uint(from[e]);
+                    }
+            }
+            *reinterpret_cast<u32x4*>(at(scratch, r, c)) = w;
+        }
+        f32x16 v;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (DT == 0) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(at(scratch, l32, m) + 4 * gl);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * m + e] = (e & 1) ? hi_f(w[e >> 1]) : lo_f(w[e >> 1]);
+            } else {
+                const f32x4 w = *reinterpret_cast<const f32x4*>(at(scratch, l32, 2 * m + gl));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * m + e] = w[e];
+            }
+        }
+        return v;
+    }
+};
 template <int DT, int F>
 __device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename Io<DT>::T* scratch,
                                            typename Io<DT>::T* C, int64_t ldc, int rows, int cols, int r0, int c0) {
-    using T = typename Io<DT>::T;
-    constexpr int EPC = Io<DT>::EPC, CPR = 32 / EPC, RPP = 64 / CPR;   // chunks of a row, rows stored at a time
-    const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
-    auto at = [&](int r, int c) { return scratch + r * 32 + (c ^ ((DT == 0 ? r >> 1 : r) & (CPR - 1))) * EPC; };
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < F; ++j) {
             const int br = r0 + i * 32, bc = c0 + j * 32;
-            if (br >= rows || bc >= cols) continue;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const auto& v = acc[i][j];
-                if constexpr (DT == 0)
-                    *reinterpret_cast<u32x2*>(at(l32, m) + 4 * gl) =
-                        u32x2{pack2(v[4 * m], v[4 * m + 1]), pack2(v[4 * m + 2], v[4 * m + 3])};
-                else
-                    *reinterpret_cast<f32x4*>(at(l32, 2 * m + gl)) =
-                        f32x4{v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]};
-            }
-#pragma unroll
-            for (int p = 0; p < 32 / RPP; ++p) {
-                const int r = p * RPP + lane / CPR, c = lane % CPR, col = bc + c * EPC;
-                if (br + r >= rows || col >= cols) continue;
-                const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, c));
-                T* to = C + (br + r) * ldc + col;
-                if (col + EPC <= cols) {
-                    *reinterpret_cast<Loose16*>(to) = Loose16{v};
-                } else {
-#pragma unroll
-                    for (int e = 0; e < EPC - 1; ++e)
-                        if (col + e < cols) {
-                            if constexpr (DT == 0) to[e] = (unsigned short)(v[e >> 1] >> (16 * (e & 1)));
-                            else to[e] = __uint_as_float(v[e]);
-                        }
-                }
-            }
+            if (br < rows && bc < cols) BlockIo<DT>::put(acc[i][j], scratch, C, ldc, rows, cols, br, bc);
         }
+}
+
+// ---- gated block: act(g) = g s(g) -----------------------------------------------
+// silu: s = sigmoid(g); gelu (tanh): (1 + tanh z) / 2 = sigmoid(2 z), so both are
+// sigmoid(k0 g + k1 g^3); relu: s is 0 or 1; gelu (erf): the normal distribution's
+// integral.  FAST: the hardware's exp2 and reciprocal, a few 2^-23 of the result
+// (for results rounded to bf16).
+template <bool ERF, bool FAST>
+__device__ __forceinline__ float gate_share(const GroupedArgs& a, float g) {
+    if constexpr (ERF) {
+        return 0.5f * erfcf(g * -0.70710678118654752f);
+    } else {
+        const float z = g * (a.k0 + a.k1 * fminf(g * g, 1e30f));   // (an infinite square times k1 = 0 were NaN)
+        float s;
+        if constexpr (FAST) s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+        else s = 1.f / (1.f + expf(-z));
+        return a.relu ? (g <= 0.f ? 0.f : 1.f) : s;
+    }
+}
+// (where s has underflowed, act(g) = 0: -inf gives no NaN)
+__device__ __forceinline__ float gate_act(float g, float s) { return s == 0.f ? 0.f : g * s; }
+// act'(g) = s + g s' (far out, where s' has underflowed, s: 0 or 1)
+template <bool ERF, bool FAST>
+__device__ __forceinline__ float gate_slope(const GroupedArgs& a, float g, float s) {
+    if constexpr (ERF) {
+        const float e = FAST ? __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f) : expf(-0.5f * g * g);
+        return s + (e == 0.f ? 0.f : g * (e * 0.39894228040143268f));
+    } else {
+        const float t = s * (1.f - s);
+        return s + (t == 0.f ? 0.f : g * t * (a.k0 + 3.f * a.k1 * g * g));
+    }
 }
 
 // A B of one tile (operands exchanged in the MFMA, so that a lane holds runs of
 // four columns of one row): done(sums, wave, its scratch) in each wave that ends
 // with some.
-template <int DT, bool AK, bool BKK, int EDGE, int SPLIT, typename Done>
-__device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE>& B, Done done) {
+template <int DT, bool AK, bool BKK, int EDGE, int SPLIT, bool PAIR = false, typename Done>
+__device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const Staged<DT, BKK, EDGE, PAIR>& B, Done done) {
     using T = typename Io<DT>::T;
     constexpr int WE = EDGE / 2, F = WE / 32;   // edge of a wave's part, in 32-wide blocks
     constexpr int BK = Io<DT>::BK, SUB = DT == 0 ? 16 : 8;
@@ -279,7 +369,7 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
     const int wm = wave >> 1, wn = wave & 1;
     T (&sa)[2][SA] = buf_a[part];
     T (&sb)[2][SB] = buf_b[part];
-    const bool work = wm * WE < A.side && wn * WE < B.side;
+    const bool work = wm * WE < A.side && (PAIR ? wn * (F - 1) * 32 : wn * WE) < B.side;
     f32x16 acc[F][F];
 #pragma unroll
     for (int i = 0; i < F; ++i)
@@ -355,8 +445,8 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_mm_staged(const GroupedAr
     const int64_t m0 = (int64_t)t.row0 + t.mt * EDGE;
     const int n0 = t.nt * EDGE;
     Staged<DT, true, EDGE> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
-                             min(EDGE, t.rows - t.mt * EDGE), a.kdim, 0};
-    Staged<DT, WT, EDGE> B{nullptr, 0, min(EDGE, a.ndim - n0), a.kdim, n0};
+                             min(EDGE, t.rows - t.mt * EDGE), a.kdim, 0, 0};
+    Staged<DT, WT, EDGE> B{nullptr, 0, min(EDGE, a.ndim - n0), a.kdim, n0, 0};
     if (t.e < a.n) {
         B.ld = a.w_ld[t.e];
         B.p = reinterpret_cast<const T*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
@@ -366,6 +456,121 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_mm_staged(const GroupedAr
     staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
         put_blocks<DT>(acc, scratch, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, A.side, B.side,
                        (wave >> 1) * (EDGE / 2), (wave & 1) * (EDGE / 2));
+    });
+}
+
+// The gated block's forward pass: a tile has EDGE / 2 columns of H.  In the 128-tiles
+// a wave holds the gate's and the up projection's block of the same columns; in the
+// 64-tiles neighbouring waves do, and the second hands its sums over through LDS.
+template <int DT, bool WT, int EDGE, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT) void grouped_gated_staged(const GroupedArgs a) {
+    using T = typename Io<DT>::T;
+    constexpr int HALF = EDGE / 2, F = EDGE / 64;
+    GroupTile t;
+    if (!find_tile(a, EDGE, (a.ndim + HALF - 1) / HALF, t)) return;
+    const int64_t m0 = (int64_t)t.row0 + t.mt * EDGE;
+    const int n0 = t.nt * HALF;
+    Staged<DT, true, EDGE> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
+                             min(EDGE, t.rows - t.mt * EDGE), a.kdim, 0, 0};
+    Staged<DT, WT, EDGE, true> B{nullptr, 0, min(HALF, a.ndim - n0), a.kdim, n0, a.ndim};
+    if (t.e < a.n) {
+        B.ld = a.w_ld[t.e];
+        B.p = reinterpret_cast<const T*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
+    } else {
+        A.kd = B.kd = 0;   // rows of no expert: zeros
+    }
+    staged_tile<DT, true, WT, EDGE, SPLIT, true>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
+        const int wm = wave >> 1, wn = wave & 1, lane = threadIdx.x & 63;
+        f32x16 up[F];
+        if constexpr (F == 1) {
+            float* swap = reinterpret_cast<float*>(scratch - wn * 32 * 32);   // of both waves
+            if (wn == 1)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) swap[e * 64 + lane] = acc[0][0][e];
+            __syncthreads();
+            if (wn == 1) return;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) up[0][e] = swap[e * 64 + lane];
+        } else {
+#pragma unroll
+            for (int i = 0; i < F; ++i) up[i] = acc[i][F - 1];
+        }
+        const int bc = F == 1 ? 0 : wn * 32;
+        if (bc >= B.side) return;
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int br = wm * (EDGE / 2) + i * 32;
+            if (br >= A.side) continue;
+            const f32x16 g = acc[i][0];
+            f32x16 h;
+            const auto gate = [&](auto erf) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    h[e] = gate_act(g[e], gate_share<decltype(erf)::value, DT == 0>(a, g[e])) * up[i][e];
+            };
+            if (a.erf) gate(std::true_type{});
+            else gate(std::false_type{});
+            BlockIo<DT>::put(h, scratch, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, A.side, B.side, br, bc);
+            if (a.p == nullptr) continue;
+            T* P = reinterpret_cast<T*>(a.p) + m0 * a.p_ld + n0;
+            BlockIo<DT>::put(g, scratch, P, a.p_ld, A.side, B.side, br, bc);
+            BlockIo<DT>::put(up[i], scratch, P + a.ndim, a.p_ld, A.side, B.side, br, bc);
+        }
+    });
+}
+
+// Back through the down product and the gate: the product as above, then G and U
+// are read into the lanes that hold the sums.
+template <int DT, bool WT, int EDGE, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT) void grouped_gated_grad_staged(const GroupedArgs a) {
+    using T = typename Io<DT>::T;
+    constexpr int F = EDGE / 64;
+    GroupTile t;
+    if (!find_tile(a, EDGE, (a.ndim + EDGE - 1) / EDGE, t)) return;
+    const int64_t m0 = (int64_t)t.row0 + t.mt * EDGE;
+    const int n0 = t.nt * EDGE;
+    Staged<DT, true, EDGE> A{reinterpret_cast<const T*>(a.x) + m0 * a.x_ld, a.x_ld,
+                             min(EDGE, t.rows - t.mt * EDGE), a.kdim, 0, 0};
+    Staged<DT, WT, EDGE> B{nullptr, 0, min(EDGE, a.ndim - n0), a.kdim, n0, 0};
+    const bool owned = t.e < a.n;
+    if (owned) {
+        B.ld = a.w_ld[t.e];
+        B.p = reinterpret_cast<const T*>(a.w[t.e]) + (WT ? n0 * B.ld : n0);
+    } else {
+        A.kd = B.kd = 0;   // rows of no expert: zeros
+    }
+    staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
+        const T* P = reinterpret_cast<const T*>(a.p) + m0 * a.p_ld + n0;
+        T* D = reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0;
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j) {
+                const int br = (wave >> 1) * (EDGE / 2) + i * 32, bc = (wave & 1) * (EDGE / 2) + j * 32;
+                if (br >= A.side || bc >= B.side) continue;
+                f32x16 dg = {}, du = {}, h = {};
+                if (owned) {
+                    const f32x16 g = BlockIo<DT>::get(scratch, P, a.p_ld, A.side, B.side, br, bc);
+                    const f32x16 u = BlockIo<DT>::get(scratch, P + a.ndim, a.p_ld, A.side, B.side, br, bc);
+                    const auto gate = [&](auto erf) __attribute__((always_inline)) {
+                        constexpr bool ERF = decltype(erf)::value;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float s = gate_share<ERF, DT == 0>(a, g[e]), act = gate_act(g[e], s);
+                            dg[e] = acc[i][j][e] * u[e] * gate_slope<ERF, DT == 0>(a, g[e], s);
+                            du[e] = acc[i][j][e] * act;
+                            h[e] = act * u[e];
+                        }
+                    };
+                    if (a.erf) gate(std::true_type{});
+                    else gate(std::false_type{});
+                }
+                BlockIo<DT>::put(dg, scratch, D, a.y_ld, A.side, B.side, br, bc);
+                BlockIo<DT>::put(du, scratch, D + a.ndim, a.y_ld, A.side, B.side, br, bc);
+                if (a.h != nullptr)
+                    BlockIo<DT>::put(h, scratch, reinterpret_cast<T*>(a.h) + m0 * a.h_ld + n0, a.h_ld, A.side, B.side, br,
+                                     bc);
+            }
     });
 }
 
@@ -395,9 +600,9 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_wgrad_staged(const Groupe
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int kd = __builtin_amdgcn_readfirstlane(hi - lo);
     const Staged<DT, false, EDGE> A{reinterpret_cast<const T*>(a.x) + lo * a.x_ld + i0, a.x_ld,
-                                    min(EDGE, a.kdim - i0), kd, i0};
+                                    min(EDGE, a.kdim - i0), kd, i0, 0};
     const Staged<DT, false, EDGE> B{reinterpret_cast<const T*>(a.d) + lo * a.d_ld + j0, a.d_ld,
-                                    min(EDGE, a.ndim - j0), kd, j0};
+                                    min(EDGE, a.ndim - j0), kd, j0, 0};
     staged_tile<DT, false, false, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
         if constexpr (PARTS) {
             f32x4* to = reinterpret_cast<f32x4*>(a.sums + ((int64_t)part * tiles + e * ntk * ntn + b) * (EDGE * EDGE)) +
@@ -1108,9 +1313,11 @@ int device_cus_or_256() {
     return cus;
 }
 
+// Column tiles: in a gated block's forward pass half a tile's columns are the gate's.
+int64_t col_tiles(const GroupedArgs& a, int edge) { return cdiv(a.ndim, a.gate == Gate::Forward ? edge / 2 : edge); }
 int64_t mm_tiles(const GroupedArgs& a, int edge) {
     // every slot ends in at most one partial row tile
-    return (a.rows / edge + a.n + 1) * cdiv(a.ndim, edge);
+    return (a.rows / edge + a.n + 1) * col_tiles(a, edge);
 }
 int64_t wgrad_tiles(const GroupedArgs& a, int edge) { return cdiv(a.kdim, edge) * cdiv(a.ndim, edge) * a.n; }
 
@@ -1121,7 +1328,7 @@ int64_t wgrad_tiles(const GroupedArgs& a, int edge) { return cdiv(a.kdim, edge) 
 // of 72 us at 32 rows an expert, but 148 instead of 132 us at 256, as its grid has
 // to hold all rows and nearly all of it is empty.)
 double mm_expect(const GroupedArgs& a, int edge) {
-    return ((double)a.rows / edge + 0.5 * a.total) * (double)cdiv(a.ndim, edge);
+    return ((double)a.rows / edge + 0.5 * a.total) * (double)col_tiles(a, edge);
 }
 
 // Which kernel.  Measured in us, experts x rows x K x N (K x N stored, bf16):
@@ -1147,7 +1354,7 @@ bool split(const GroupedArgs& a, double tiles, int64_t k) {
     return tiles <= device_cus_or_256() && k >= 8 * (a.dtype == 0 ? Io<0>::BK : Io<1>::BK);
 }
 Kernel mm_kernel(const GroupedArgs& a) {
-    if (a.dtype == 0 && a.vec) {
+    if (a.dtype == 0 && a.vec && a.gate == Gate::None) {
         const bool big = enough_big(mm_expect(a, kBig));
         if (a.rows <= (big ? 16 : 32) * (int64_t)a.total) return Kernel::Thin;
         if (big) return Kernel::Big;
@@ -1233,6 +1440,32 @@ hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s) 
     } else {
         if (trans_w) mm_staged<1, true>(a, k, grid, s);
         else mm_staged<1, false>(a, k, grid, s);
+    }
+    return hipGetLastError();
+}
+
+template <int DT, bool WT>
+static void gated_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t s) {
+    if (a.gate == Gate::Forward) {
+        if (k == Kernel::Split64) hipLaunchKernelGGL((grouped_gated_staged<DT, WT, 64, 4>), grid, dim3(1024), 0, s, a);
+        else if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_gated_staged<DT, WT, 64, 1>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((grouped_gated_staged<DT, WT, 128, 1>), grid, dim3(256), 0, s, a);
+    } else {
+        if (k == Kernel::Split64) hipLaunchKernelGGL((grouped_gated_grad_staged<DT, WT, 64, 4>), grid, dim3(1024), 0, s, a);
+        else if (k == Kernel::Staged64) hipLaunchKernelGGL((grouped_gated_grad_staged<DT, WT, 64, 1>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((grouped_gated_grad_staged<DT, WT, 128, 1>), grid, dim3(256), 0, s, a);
+    }
+}
+
+hipError_t launch_grouped_gated(const GroupedArgs& a, bool trans_w, hipStream_t s) {
+    const Kernel k = mm_kernel(a);
+    const dim3 grid((uint32_t)grouped_mm_grid(a));
+    if (a.dtype == 0) {
+        if (trans_w) gated_staged<0, true>(a, k, grid, s);
+        else gated_staged<0, false>(a, k, grid, s);
+    } else {
+        if (trans_w) gated_staged<1, true>(a, k, grid, s);
+        else gated_staged<1, false>(a, k, grid, s);
     }
     return hipGetLastError();
 }
