@@ -41,8 +41,8 @@ struct GroupedArgs {
     void* p;                 // [G | U], M x 2N: written by Forward (or null), read by Grad
     void* h;                 // Grad: H, or null
     int64_t p_ld, h_ld;
-    float k0, k1;            // act(g) = g s(g): s = sigmoid(k0 g + k1 g^3),
-    int32_t relu, erf;       // or 1 above 0, or the normal distribution's integral
+    float k0, k1, k2;        // act(g) = g s(g): s = sigmoid(k0 g + k1 g^3 + k2),
+    int32_t erf;             // or the normal distribution's integral
     void* w[kExperts];       // product: weights; weight gradient: results
     int64_t w_ld[kExperts];
 };

@@ -325,32 +325,34 @@ __device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename I
 
 // ---- gated block: act(g) = g s(g) -----------------------------------------------
 // silu: s = sigmoid(g); gelu (tanh): (1 + tanh z) / 2 = sigmoid(2 z), so both are
-// sigmoid(k0 g + k1 g^3); relu: s is 0 or 1; gelu (erf): the normal distribution's
-// integral.  FAST: the hardware's exp2 and reciprocal, a few 2^-23 of the result
-// (for results rounded to bf16).
+// sigmoid(k0 g + k1 g^3); relu: s is 0 or 1, as a sigmoid so steep (10^30 g - 200) that
+// only gates below 10^-27 tell the two apart; gelu (erf): the normal distribution's
+// integral.  FAST: the hardware's exp2 and reciprocal, a few 2^-23 of the result (for
+// results rounded to bf16).  No branches: with one for each element the gradient's
+// results took longer than the products.
+__device__ __forceinline__ float gate_inner(float g) { return __builtin_amdgcn_fmed3f(g, -1e18f, 1e18f); }
 template <bool ERF, bool FAST>
 __device__ __forceinline__ float gate_share(const GroupedArgs& a, float g) {
     if constexpr (ERF) {
         return 0.5f * erfcf(g * -0.70710678118654752f);
     } else {
-        const float z = g * (a.k0 + a.k1 * fminf(g * g, 1e30f));   // (an infinite square times k1 = 0 were NaN)
-        float s;
-        if constexpr (FAST) s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
-        else s = 1.f / (1.f + expf(-z));
-        return a.relu ? (g <= 0.f ? 0.f : 1.f) : s;
+        const float x = gate_inner(g), z = x * (a.k0 + a.k1 * x * x) + a.k2;   // (of finite terms)
+        const float s = FAST ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f))
+                             : 1.f / (1.f + expf(-z));
+        return g != g ? g : s;
     }
 }
-// (where s has underflowed, act(g) = 0: -inf gives no NaN)
-__device__ __forceinline__ float gate_act(float g, float s) { return s == 0.f ? 0.f : g * s; }
+// (where s is 0, -inf gives 0)
+__device__ __forceinline__ float gate_act(float g, float s) { return fmaxf(g, -3.402823466e38f) * s; }
 // act'(g) = s + g s' (far out, where s' has underflowed, s: 0 or 1)
 template <bool ERF, bool FAST>
 __device__ __forceinline__ float gate_slope(const GroupedArgs& a, float g, float s) {
+    const float x = gate_inner(g);
     if constexpr (ERF) {
-        const float e = FAST ? __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f) : expf(-0.5f * g * g);
-        return s + (e == 0.f ? 0.f : g * (e * 0.39894228040143268f));
+        const float e = FAST ? __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f) : expf(-0.5f * x * x);
+        return s + x * (e * 0.39894228040143268f);
     } else {
-        const float t = s * (1.f - s);
-        return s + (t == 0.f ? 0.f : g * t * (a.k0 + 3.f * a.k1 * g * g));
+        return s + x * (s - s * s) * (a.k0 + 3.f * a.k1 * x * x);
     }
 }
 
@@ -741,7 +743,9 @@ __device__ __forceinline__ void end_multiply() {
 // The loads of one operand, step by step.  An instruction of the workgroup
 // fills 64 rows of 128 bytes (along k) or 32 rows of 256 bytes (along i); a half
 // takes two.
-template <bool ALONG_K>
+// PAIR (a gated block's weights): half 0 is 128 gate columns, half 1 the same columns
+// of the up projection, `up` bytes further on.
+template <bool ALONG_K, bool PAIR = false>
 struct Feed {
     uint64_t at;        // first byte of the step
     int64_t rest;       // bytes from there to the operand's end (the end of the last row that counts)
@@ -749,6 +753,7 @@ struct Feed {
     int left;           // k from the step on
     uint32_t v, first;  // this lane's byte offset in an instruction; first k element of its chunk
     uint32_t off[2][2]; // byte offset of instruction j of half h
+    uint64_t up;        // PAIR
 
     // p: element (0, 0) of the tile at k = 0; side: its rows (or columns) inside
     // the operand; kd: length of k (0: all zeros)
@@ -772,9 +777,11 @@ struct Feed {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                off[h][j] = ALONG_K ? (h * 128 + j * 64) * ld2
-                                    : h * 128 < side ? h * 256 + j * 32 * ld2 : kNowhere;
+            for (int j = 0; j < 2; ++j) {
+                const int half = PAIR ? 0 : h;
+                off[h][j] = ALONG_K ? (half * 128 + j * 64) * ld2
+                                    : half * 128 < side ? half * 256 + j * 32 * ld2 : kNowhere;
+            }
     }
     __device__ __forceinline__ void next() {
         at += move;
@@ -783,7 +790,7 @@ struct Feed {
     }
     // half h into LDS byte address lds (this wave's part)
     __device__ __forceinline__ void load(int h, uint32_t lds) const {
-        const i32x4 r = rsrc_words(reinterpret_cast<const void*>(at), left > 0 ? rest : 0);
+        const i32x4 r = rsrc_words(reinterpret_cast<const void*>(PAIR && h ? at + up : at), left > 0 ? rest : 0);
         // a last step that k does not fill: chunks along k past its end would
         // read the next row
         const uint32_t u = ALONG_K && (int)first >= left ? kNowhere : v;
@@ -831,6 +838,13 @@ struct Frag {
     }
 };
 
+// Two stores that are dropped (as assembly, so that neither is removed).
+__device__ __forceinline__ void drop_stores() {
+    const i32x4 none = {0, 0, 0, 0x00020000};
+    asm volatile("buffer_store_dword %0, %0, %1, 0 offen\n\tbuffer_store_dword %0, %0, %1, 0 offen"
+                 :: "v"(kNowhere), "s"(none) : "memory");
+}
+
 // Half h of the result tile (rows 128 h ..): C[r][c] with r = (2 i + wm) 32 + l32
 // and c = (4 j + wn) 32 + 8 m + 4 gl + e is acc[i][j][4 m + e] of lane
 // 32 gl + l32.  Each 32 x 32 block goes through the wave's own LDS scratch, so
@@ -856,11 +870,7 @@ __device__ __forceinline__ void put_result(const f32x16 (&acc)[AM][FN], int h, u
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (i >= AM || j >= FN) {
-                // nothing there: two stores that are dropped (as assembly, so
-                // that neither is removed)
-                const i32x4 none = {0, 0, 0, 0x00020000};
-                asm volatile("buffer_store_dword %0, %0, %1, 0 offen\n\tbuffer_store_dword %0, %0, %1, 0 offen"
-                             :: "v"(kNowhere), "s"(none) : "memory");
+                drop_stores();   // nothing there
                 continue;
             }
             const auto& v = acc[i < AM ? i : 0][j < FN ? j : 0];
@@ -879,9 +889,149 @@ __device__ __forceinline__ void put_result(const f32x16 (&acc)[AM][FN], int h, u
     }
 }
 
+// A 32 x 32 block in bf16 as the lanes hold its sums: words m are columns 8 m + 4 gl
+// and the three after it, of row l32.
+struct Packed {
+    u32x2 w[4];
+};
+__device__ __forceinline__ Packed packed(const f32x16& v) {
+    Packed p;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) p.w[m] = u32x2{pack2(v[4 * m], v[4 * m + 1]), pack2(v[4 * m + 2], v[4 * m + 3])};
+    return p;
+}
+// It goes through the wave's scratch: into 64-byte pieces of rows ...
+__device__ __forceinline__ void store_block(const Packed& p, unsigned short* scratch, __amdgpu_buffer_rsrc_t to,
+                                            uint32_t off, uint32_t half, int lane) {
+    const int l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) *reinterpret_cast<u32x2*>(&scratch[l32 * kScratchLd + m * 8 + gl * 4]) = p.w[m];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            *reinterpret_cast<const u32x4*>(&scratch[(s * 16 + (lane >> 2)) * kScratchLd + (lane & 3) * 8]), to,
+            off + s * half, 0, 0);
+}
+// ... and back.
+__device__ __forceinline__ Packed spread_block(const u32x4 (&w)[2], unsigned short* scratch, int lane) {
+    const int l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        *reinterpret_cast<u32x4*>(&scratch[(s * 16 + (lane >> 2)) * kScratchLd + (lane & 3) * 8]) = w[s];
+    Packed p;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) p.w[m] = *reinterpret_cast<const u32x2*>(&scratch[l32 * kScratchLd + m * 8 + gl * 4]);
+    return p;
+}
+// Buffer of rows 64 i on of a tile's block at element `at` of a matrix: `rows` rows of
+// which the last ends `width` elements after its first.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const void* base, int64_t at, int64_t ld, int i, int rows,
+                                                            int64_t width) {
+    const int64_t down = (int64_t)i * 64 * ld;
+    const int64_t bytes = i * 64 < rows ? 2 * ((int64_t)(rows - 1) * ld + width - down) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void*>(reinterpret_cast<uint64_t>(base) + 2 * (at + down)), (short)0,
+        (int)min(bytes, (int64_t)0x7fffff00), 0x00020000);
+}
+// A gated tile's result: acc[i][0] is the gate's and acc[i][1] the up projection's
+// block of the same rows and columns.  24 stores with [G | U], else 8.
+template <int AM, bool KEEP, bool ERF>
+__device__ __forceinline__ void put_gated(const GroupedArgs& a, const f32x16 (&acc)[AM][2], unsigned short* scratch,
+                                          int64_t m0, int n0, int rows, int cols, int wm, int wn, int lane) {
+    asm volatile("" : "+v"(lane));   // (what follows from it is not kept in registers over the products)
+    const int r0 = wm * 32 + (lane >> 2), c0 = wn * 32 + (lane & 3) * 8;
+    const bool in = c0 < cols;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i >= AM) {
+#pragma unroll
+            for (int k = 0; k < (KEEP ? 3 : 1); ++k) drop_stores();
+            continue;
+        }
+        const f32x16 &g = acc[i < AM ? i : 0][0], &u = acc[i < AM ? i : 0][1];
+        f32x16 v;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = gate_act(g[e], gate_share<ERF, true>(a, g[e])) * u[e];
+        const uint32_t hl = (uint32_t)a.y_ld * 2u;
+        store_block(packed(v), scratch, tile_rows(a.y, m0 * a.y_ld + n0, a.y_ld, i, rows, cols),
+                    in ? r0 * hl + c0 * 2u : kNowhere, hl * 16u, lane);
+        if constexpr (KEEP) {
+            const uint32_t pl = (uint32_t)a.p_ld * 2u, at = in ? r0 * pl + c0 * 2u : kNowhere;
+            const auto P = tile_rows(a.p, m0 * a.p_ld + n0, a.p_ld, i, rows, (int64_t)a.ndim + cols);
+            store_block(packed(g), scratch, P, at, pl * 16u, lane);
+            store_block(packed(u), scratch, P, in ? at + 2u * (uint32_t)a.ndim : kNowhere, pl * 16u, lane);
+        }
+    }
+}
+
+// A tile of the gate's gradient, acc the gradient of H.  G and U of kAhead blocks are
+// on their way while one is worked on.  At least 16 loads and stores in all, whatever
+// the tile's size.
+template <int AM, int FN, bool ERF>
+__device__ __forceinline__ void put_gate_grad(const GroupedArgs& a, const f32x16 (&acc)[AM][FN], unsigned short* scratch,
+                                              int64_t m0, int n0, int rows, int cols, bool owned, int wm, int wn, int lane) {
+    asm volatile("" : "+v"(lane));   // (what follows from it is not kept in registers over the products)
+    constexpr int kAhead = 2, kBlocks = AM * FN;
+    const int r0 = wm * 32 + (lane >> 2), c0 = wn * 32 + (lane & 3) * 8;
+    const uint32_t pl = (uint32_t)a.p_ld * 2u, dl = (uint32_t)a.y_ld * 2u, hl = (uint32_t)a.h_ld * 2u, up = 2u * (uint32_t)a.ndim;
+    u32x4 gw[kAhead][2], uw[kAhead][2];
+    const auto load = [&](int b) __attribute__((always_inline)) {
+        const int i = b / FN, c = c0 + (b % FN) * 128;
+        // (rows of no expert: zeros for whatever P holds)
+        const auto P = tile_rows(a.p, m0 * a.p_ld + n0, a.p_ld, i, owned ? rows : 0, (int64_t)a.ndim + cols);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t at = c < cols ? r0 * pl + c * 2u + s * 16u * pl : kNowhere;
+            gw[b % kAhead][s] = __builtin_amdgcn_raw_buffer_load_b128(P, at, 0, 0);
+            uw[b % kAhead][s] = __builtin_amdgcn_raw_buffer_load_b128(P, c < cols ? at + up : kNowhere, 0, 0);
+        }
+    };
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b)
+        if (b < kBlocks) load(b);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        __builtin_amdgcn_sched_barrier(0);   // (blocks worked on at once would not fit the registers)
+        const int i = b / FN, c = c0 + (b % FN) * 128;
+        const auto& dh = acc[i][b % FN];
+        const bool in = c < cols;
+        // kept packed: g becomes the up projection's gradient, u the gate's
+        Packed g = spread_block(gw[b % kAhead], scratch, lane), u = spread_block(uw[b % kAhead], scratch, lane), v;
+        if (b + kAhead < kBlocks) load(b + kAhead);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float dg[2], du[2], hv[2];
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const float x = o ? hi_f(g.w[m][k]) : lo_f(g.w[m][k]), y = o ? hi_f(u.w[m][k]) : lo_f(u.w[m][k]);
+                    const float d = dh[4 * m + 2 * k + o], s = gate_share<ERF, true>(a, x), act = gate_act(x, s);
+                    hv[o] = act * y;
+                    dg[o] = d * y * gate_slope<ERF, true>(a, x, s);
+                    du[o] = d * act;
+                }
+                v.w[m][k] = pack2(hv[0], hv[1]);
+                u.w[m][k] = pack2(dg[0], dg[1]);
+                g.w[m][k] = pack2(du[0], du[1]);
+            }
+        const uint32_t at = r0 * dl + c * 2u;
+        const auto D = tile_rows(a.y, m0 * a.y_ld + n0, a.y_ld, i, rows, (int64_t)a.ndim + cols);
+        store_block(u, scratch, D, in ? at : kNowhere, dl * 16u, lane);
+        store_block(g, scratch, D, in ? at + up : kNowhere, dl * 16u, lane);
+        if (a.h != nullptr)
+            store_block(v, scratch, tile_rows(a.h, m0 * a.h_ld + n0, a.h_ld, i, rows, cols), in ? r0 * hl + c * 2u : kNowhere,
+                        hl * 16u, lane);
+    }
+    static_assert(kBlocks >= 1, "8 loads and stores a block");
+    if (kBlocks < 2)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) drop_stores();
+}
+
 // One output tile.
 struct Job {
-    uint64_t a, b, c;    // element (0, 0) of its operands (at k = 0) and result
+    uint64_t a, b, c;    // element (0, 0) of its operands (at k = 0) and result; gated: c = its first row and column
     int w_ld;            // row stride of the expert's matrix
     int rows, cols;      // size of the tile
     int kd;              // length of k (0: the result is zero)
@@ -903,11 +1053,12 @@ struct GroupTable {
 // x 4096: 443 us without bands, 411 with; weight gradient of 64 experts of 512 x
 // 4096 x 1408: 450 and 434).
 constexpr int kBand = 8;
-template <int MODE>
+template <int MODE, Gate GATE = Gate::None>
 struct Grid {
+    static constexpr int kWide = GATE == Gate::Forward ? kBig / 2 : kBig;   // columns of a tile's result
     const GroupedArgs& a;
     int ntn;   // column tiles
-    __device__ __forceinline__ explicit Grid(const GroupedArgs& x) : a(x), ntn((x.ndim - 1) / kBig + 1) {}
+    __device__ __forceinline__ explicit Grid(const GroupedArgs& x) : a(x), ntn((x.ndim - 1) / kWide + 1) {}
     __device__ __forceinline__ int row_tiles(int rows) const {
         const int h = MODE == 2 ? a.kdim : rows;
         return h > 0 ? (h - 1) / kBig + 1 : 0;
@@ -928,10 +1079,10 @@ struct Grid {
         const int R = row_tiles(t.rows[e]), off = id - t.first[e];
         // bands of eight row tiles, column by column
         const int band = off / (kBand * ntn), in = off - band * kBand * ntn, high = min(kBand, R - band * kBand);
-        const int m = (band * kBand + in % high) * kBig, n0 = in / high * kBig;
+        const int m = (band * kBand + in % high) * kBig, n0 = in / high * kWide;
         Job j;
         const unsigned short* x = reinterpret_cast<const unsigned short*>(a.x);
-        j.cols = min(kBig, a.ndim - n0);
+        j.cols = min(kWide, a.ndim - n0);
         if constexpr (MODE == 2) {
             j.a = reinterpret_cast<uint64_t>(x + t.lo[e] * a.x_ld + m);
             j.b = reinterpret_cast<uint64_t>(reinterpret_cast<const unsigned short*>(a.d) + t.lo[e] * a.d_ld + n0);
@@ -942,7 +1093,9 @@ struct Grid {
         } else {
             const int64_t m0 = (int64_t)t.lo[e] + m;
             j.a = reinterpret_cast<uint64_t>(x + m0 * a.x_ld);
-            j.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0);
+            if constexpr (GATE == Gate::None)
+                j.c = reinterpret_cast<uint64_t>(reinterpret_cast<unsigned short*>(a.y) + m0 * a.y_ld + n0);
+            else j.c = (uint64_t)m0 << 32 | (uint32_t)n0;
             j.rows = min(kBig, t.rows[e] - m);
             j.b = 0;
             j.w_ld = 0;
@@ -960,8 +1113,8 @@ struct Grid {
 
 // Fills the table (one wave).  `most`: the tiles the launch was made for (end
 // rows that decrease could count more; those are cut off).
-template <int MODE>
-__device__ __forceinline__ void fill_table(const GroupedArgs& a, const Grid<MODE>& g, GroupTable& t, int most) {
+template <int MODE, Gate GATE>
+__device__ __forceinline__ void fill_table(const GroupedArgs& a, const Grid<MODE, GATE>& g, GroupTable& t, int most) {
     const int lane = threadIdx.x, slots = a.n + (MODE != 2 && a.last ? 1 : 0);
     float c[4], csum = 0.f;
     int n[4], nsum = 0;
@@ -1021,9 +1174,16 @@ __device__ __forceinline__ int share(const GroupTable& t, int x) {
     return t.first[e] + (c > 0.f ? max(0, min(n, (int)((at - t.cost[e]) / c * n))) : 0);
 }
 
-template <int MODE>
+// GATE: the two passes of a gated block; KEEP: the forward one also stores [G | U].
+template <int MODE, Gate GATE = Gate::None, bool KEEP = false, bool ERF = false>
 __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const int most) {
     constexpr bool AK = MODE != 2, BKK = MODE == 1;   // operands stored along k
+    constexpr bool PAIR = GATE == Gate::Forward;
+    constexpr int kPuts = PAIR ? (KEEP ? 12 : 4) : 8;   // (at least) stores of half a result
+    // A gated block's results take many loads and stores and much arithmetic, so both
+    // groups work on them at a time: at a tile's end the first one lets the other's
+    // products pass, and falls a slot ahead again in the next tile.
+    constexpr bool kTogether = GATE != Gate::None;
     __shared__ __attribute__((aligned(1024))) unsigned short sbuf[4 * kPanel];
     __shared__ __attribute__((aligned(16))) unsigned short scratch[8 * kScratch];
     __shared__ __attribute__((aligned(16))) Job jobs[kJobs];
@@ -1034,8 +1194,8 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
     // ---- this workgroup's tiles.  Each XCD (workgroup ids go round the eight)
     //      takes a run of tiles, so that what they share sits in one L2, and
     //      deals them out to its workgroups in turn
-    const Grid<MODE> grid(a);
-    if (wave == 0) fill_table<MODE>(a, grid, table, most);
+    const Grid<MODE, GATE> grid(a);
+    if (wave == 0) fill_table(a, grid, table, most);
     __syncthreads();
     const int stride = gridDim.x >> 3;
     const int end = uniform(share(table, (blockIdx.x & 7) + 1));
@@ -1053,7 +1213,7 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
 
     // ---- loads, ahead of the products: tile `in` ----
     Feed<AK> feed_a;
-    Feed<BKK> feed_b;
+    Feed<BKK, PAIR> feed_b;
     int in = 0;
     auto start_feed = [&]() __attribute__((always_inline)) {
         const Job j = jobs[min(in, count - 1)];
@@ -1061,6 +1221,7 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
         const int64_t w_ld = uniform(j.w_ld);
         feed_a.start(uniform(j.a), a.x_ld, uniform(j.rows), kd, wave, lane);
         feed_b.start(uniform(j.b), MODE == 2 ? a.d_ld : w_ld, uniform(j.cols), kd, wave, lane);
+        if constexpr (PAIR) feed_b.up = 2 * (uint64_t)a.ndim * (BKK ? w_ld : 1);
     };
     auto advance = [&]() __attribute__((always_inline)) {
         feed_a.next();
@@ -1091,6 +1252,16 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
         feed_a.load(0, ldsA + q * (2 * kPanel));
         feed_b.load(0, ldsB + q * (2 * kPanel));
         feed_b.load(1, ldsB + q * (2 * kPanel));
+    };
+    // the tile's result
+    auto put = [&](const auto& acc) __attribute__((always_inline)) {
+        constexpr int AM = std::extent_v<std::remove_reference_t<decltype(acc)>>;
+        constexpr int FN = std::extent_v<std::remove_reference_t<decltype(acc[0])>>;
+        unsigned short* mine = scratch + wave * kScratch;
+        const int64_t m0 = (int64_t)(C >> 32);
+        const int n0 = (int)(uint32_t)C;
+        if constexpr (PAIR) put_gated<AM, KEEP, ERF>(a, acc, mine, m0, n0, rows, cols, wm, wn, lane);
+        else put_gate_grad<AM, FN, ERF>(a, acc, mine, m0, n0, rows, cols, kd > 0, wm, wn, lane);
     };
     int after = 0;   // the tile's first step comes after another tile's
     int p = 0;       // parity of the step
@@ -1127,28 +1298,35 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
                         }
             __builtin_amdgcn_s_setprio(0);
         };
+        if (kTogether && wm == 1) end_multiply();   // one slot behind
         for (int k = 0;; ++k) {
             const int last = (k + 1) * kBK >= kd;
             read_a(0);
             read_b(0);
             if (FN > 1) read_b(1);
             load_a1();
-            end_read<16>(after);
+            end_read<2 * kPuts>(after);
             multiply(0);
             end_multiply();
             if (AM > 2) read_a(1);
-            if (last) put_result(acc, 0, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
+            if (!kTogether && last) put_result(acc, 0, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
             load_rest();
             fa.flip(p);
             fb.flip(p);
-            end_read<8>(after | last);
+            if (kTogether) end_read<2 * kPuts>(after);
+            else end_read<kPuts>(after | last);
             if (AM > 2) multiply(1);
             end_multiply();
             p ^= 1;
             after = 0;
             if (last) break;
         }
-        put_result(acc, 1, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
+        if constexpr (kTogether) {
+            if (wm == 0) end_multiply();   // the other group multiplies
+            put(acc);
+        } else {
+            put_result(acc, 1, scratch + wave * kScratch, C, ldc, rows, cols, wm, wn, lane);
+        }
     };
 
     // the first step, and the second but for A1
@@ -1160,7 +1338,7 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
     load_rest();
     start_tile();
     asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
-    if (wm == 1) end_multiply();   // one slot behind
+    if (!kTogether && wm == 1) end_multiply();   // one slot behind
 
     for (;;) {
         const int am = (rows + 63) >> 6;
@@ -1168,12 +1346,12 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
         constexpr std::integral_constant<int, 2> c2{};
         constexpr std::integral_constant<int, 3> c3{};
         constexpr std::integral_constant<int, 4> c4{};
-        if (cols > 128) {
+        if (PAIR || cols > 128) {
             if (am == 4) run(c4, c2);
             else if (am == 3) run(c3, c2);
             else if (am == 2) run(c2, c2);
             else run(c1, c2);
-        } else {
+        } else if constexpr (!PAIR) {
             if (am == 4) run(c4, c1);
             else if (am == 3) run(c3, c1);
             else if (am == 2) run(c2, c1);
@@ -1183,7 +1361,7 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
         start_tile();
         after = 1;
     }
-    if (wm == 0) end_multiply();   // as many barriers as the others
+    if (!kTogether && wm == 0) end_multiply();   // as many barriers as the others
     // the loads past the last tile still write (zeros) into this workgroup's LDS
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -1354,9 +1532,9 @@ bool split(const GroupedArgs& a, double tiles, int64_t k) {
     return tiles <= device_cus_or_256() && k >= 8 * (a.dtype == 0 ? Io<0>::BK : Io<1>::BK);
 }
 Kernel mm_kernel(const GroupedArgs& a) {
-    if (a.dtype == 0 && a.vec && a.gate == Gate::None) {
+    if (a.dtype == 0 && a.vec) {
         const bool big = enough_big(mm_expect(a, kBig));
-        if (a.rows <= (big ? 16 : 32) * (int64_t)a.total) return Kernel::Thin;
+        if (a.rows <= (big ? 16 : 32) * (int64_t)a.total && a.gate == Gate::None) return Kernel::Thin;
         if (big) return Kernel::Big;
     }
     if (mm_expect(a, 128) >= device_cus_or_256()) return Kernel::Staged128;
@@ -1457,10 +1635,22 @@ static void gated_staged(const GroupedArgs& a, Kernel k, dim3 grid, hipStream_t 
     }
 }
 
+template <int MODE, bool ERF>
+static void gated_big(const GroupedArgs& a, int tiles, hipStream_t s) {
+    const dim3 grid(big_grid(tiles)), threads(512);
+    if (a.gate == Gate::Grad) hipLaunchKernelGGL((grouped_big<MODE, Gate::Grad, false, ERF>), grid, threads, 0, s, a, tiles);
+    else if (a.p != nullptr) hipLaunchKernelGGL((grouped_big<MODE, Gate::Forward, true, ERF>), grid, threads, 0, s, a, tiles);
+    else hipLaunchKernelGGL((grouped_big<MODE, Gate::Forward, false, ERF>), grid, threads, 0, s, a, tiles);
+}
+
 hipError_t launch_grouped_gated(const GroupedArgs& a, bool trans_w, hipStream_t s) {
     const Kernel k = mm_kernel(a);
-    const dim3 grid((uint32_t)grouped_mm_grid(a));
-    if (a.dtype == 0) {
+    const int64_t tiles = grouped_mm_grid(a);
+    const dim3 grid((uint32_t)tiles);
+    if (k == Kernel::Big) {
+        if (trans_w) a.erf ? gated_big<1, true>(a, (int)tiles, s) : gated_big<1, false>(a, (int)tiles, s);
+        else a.erf ? gated_big<0, true>(a, (int)tiles, s) : gated_big<0, false>(a, (int)tiles, s);
+    } else if (a.dtype == 0) {
         if (trans_w) gated_staged<0, true>(a, k, grid, s);
         else gated_staged<0, false>(a, k, grid, s);
     } else {
