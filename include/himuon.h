@@ -621,7 +621,7 @@ himuon_status_t himuon_layer_norm_grad(const himuon_matrix_t* X, const void* wei
 
 /* Bytes of workspace himuon_layer_norm_grad needs for rows of this shape (the
  * pointer is not read) where dweight or dbias is asked for: at most 512
- * workgroups' 2 D fp32 sums.  Host-side only. */
+ * workgroups' 2 D fp32 sums (256 on an MI355X).  Host-side only. */
 himuon_status_t himuon_layer_norm_grad_workspace(const himuon_matrix_t* X, himuon_dtype_t dt, size_t* bytes);
 
 /* State of one tensor in himuon_adamw_step: device arrays for its rows * cols

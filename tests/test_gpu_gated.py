@@ -242,7 +242,7 @@ def ragged(n, most, seed, none=0.1):
 
 # tiles enough for every kernel: experts, most rows of one, K, N
 TILED = [(64, 300, 200, 264), (20, 700, 1032, 392), (300, 40, 264, 72), (64, 130, 264, 320), (40, 16, 520, 200), (9, 2100, 72, 520),
-         (64, 3, 1096, 136)]
+         (64, 3, 1096, 136), (64, 4, 200, 328), (5, 30, 456, 4104), (70, 20, 40, 264)]
 
 
 @pytest.mark.parametrize("stored", ["kn", "nk"])

@@ -111,6 +111,7 @@ himuon_status_t gated(Gate gate, const himuon_matrix_t* X, const himuon_matrix_t
     GroupedArgs a{};
     HIMUON_TRY(grouped_args(X, W, n, ends, dt, a));
     a.gate = gate;
+    a.nk = stored_nk;
     HIMUON_TRY(activation(act, a));
     const bool forward = gate == Gate::Forward;
     if (Y == nullptr || (P == nullptr && !forward)) return HIMUON_ERR_INVALID_ARGUMENT;

@@ -1,4 +1,5 @@
-// Internal declarations of the experts' products (api_model.cpp, grouped.hip).
+// Internal declarations of the experts' products (api_model.cpp,
+// grouped.hip, gated.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -38,6 +39,7 @@ struct GroupedArgs {
     int32_t parts;           // weight gradient: parts an expert's rows are cut into
     // gated block: N = ndim is the width of H; y is H (Forward) or D (Grad, M x 2N)
     Gate gate;
+    int32_t nk;              // weights stored N x K (2N x K)
     void* p;                 // [G | U], M x 2N: written by Forward (or null), read by Grad
     void* h;                 // Grad: H, or null
     int64_t p_ld, h_ld;
@@ -46,6 +48,14 @@ struct GroupedArgs {
     void* w[kExperts];       // product: weights; weight gradient: results
     int64_t w_ld[kExperts];
 };
+
+// Which kernel a product takes (rules and measurements: grouped.hip), the most
+// workgroups or tiles of its launch, and the workgroups of the 256 x 256 kernel.
+enum class GroupedKernel { Thin, Big, Staged128, Staged64, Split64 };
+GroupedKernel grouped_mm_kernel(const GroupedArgs& a);
+int grouped_thin_cols(const GroupedArgs& a);   // of a tile's result (Thin)
+int64_t grouped_mm_grid(const GroupedArgs& a);
+uint32_t grouped_big_grid(int64_t tiles);
 
 // True if a launch can hold the tiles (checked before any launch).
 bool grouped_mm_fits(const GroupedArgs& a);

@@ -13,6 +13,7 @@
 // adds in order (no atomics: the same inputs give the same bits).
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_util.h"
 #include "norm.h"
@@ -37,35 +38,59 @@ template <> struct Elem<1> {
 };
 struct __attribute__((packed, aligned(2))) Loose16 { u32x4 v; };   // 16 bytes at an element's alignment
 
-// A row's chunk at element `at` (zeros from `cols` on).
-template <int DT>
+// `by` bits (less than 128) out of the low end.
+__device__ __forceinline__ u32x4 shift_down(const u32x4& v, int by) {
+    const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    const uint64_t a = by == 0 ? lo : by < 64 ? lo >> by | hi << (64 - by) : hi >> (by - 64), b = by < 64 ? hi >> by : 0;
+    return u32x4{(unsigned)a, (unsigned)(a >> 32), (unsigned)b, (unsigned)(b >> 32)};
+}
+
+// A row's chunk at element `at` (zeros from `cols` on).  WHOLE: rows of whole chunks.  A
+// chunk that the row's end cuts is loaded from as much further left and shifted.
+template <int DT, bool WHOLE>
 __device__ __forceinline__ u32x4 load_chunk(const typename Elem<DT>::T* row, int at, int cols) {
     constexpr int EPC = Elem<DT>::EPC;
-    if (at + EPC <= cols) return reinterpret_cast<const Loose16*>(row + at)->v;
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < EPC - 1; ++e)
-        if (at + e < cols) {
-            if constexpr (DT == 0) v[e >> 1] |= (unsigned)row[at + e] << (16 * (e & 1));
-            else v[e] = __float_as_uint(row[at + e]);
-        }
-    return v;
+    if (at >= cols) return u32x4{0, 0, 0, 0};
+    const int over = WHOLE ? 0 : max(at + EPC - cols, 0);
+    if (WHOLE || cols >= EPC) {
+        const u32x4 v = reinterpret_cast<const Loose16*>(row + at - over)->v;
+        return over > 0 ? shift_down(v, over * (128 / EPC)) : v;
+    }
+    uint64_t w[2] = {0, 0};
+#pragma unroll 1
+    for (int e = 0; e < cols; ++e) {   // a row narrower than a chunk
+        uint64_t x;
+        if constexpr (DT == 0) x = row[e];
+        else x = __float_as_uint(row[e]);
+        w[e / (EPC / 2)] |= x << (128 / EPC * (e % (EPC / 2)));
+    }
+    return u32x4{(unsigned)w[0], (unsigned)(w[0] >> 32), (unsigned)w[1], (unsigned)(w[1] >> 32)};
 }
-template <int DT>
+template <int DT, bool WHOLE>
 __device__ __forceinline__ void store_chunk(typename Elem<DT>::T* row, int at, int cols,
                                             const float (&f)[Elem<DT>::EPC]) {
     constexpr int EPC = Elem<DT>::EPC;
-    if (at + EPC <= cols) {
-        u32x4 v;
+    u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = DT == 0 ? pack2(f[(2 * i) % EPC], f[(2 * i + 1) % EPC]) : __float_as_uint(f[i]);
+    for (int i = 0; i < 4; ++i)
+        v[i] = DT == 0 ? pack2(f[(2 * i) % EPC], f[(2 * i + 1) % EPC]) : __float_as_uint(f[i]);
+    if (WHOLE || at + EPC <= cols) {
         reinterpret_cast<Loose16*>(row + at)->v = v;
         return;
     }
+#pragma unroll 1
+    for (int e = 0; at + e < cols; ++e) {
+        const u32x4 x = shift_down(v, e * (128 / EPC));
+        if constexpr (DT == 0) row[at + e] = (unsigned short)x[0];
+        else row[at + e] = __uint_as_float(x[0]);
+    }
+}
+// Values that are unpacked again where they are used next (unpacked once, the rows would
+// take twice the registers).
+template <int N>
+__device__ __forceinline__ void stay_packed(u32x4 (&v)[N]) {
 #pragma unroll
-    for (int e = 0; e < EPC - 1; ++e)
-        if (at + e < cols) row[at + e] = Elem<DT>::down(f[e]);
+    for (int c = 0; c < N; ++c) asm volatile("" : "+v"(v[c]));
 }
 
 template <int CTRL>
@@ -77,14 +102,10 @@ template <int L>
 __device__ __forceinline__ float lane_sum(float v) {
     v += dpp<0xB1>(v);                   // neighbours
     v += dpp<0x4E>(v);                   // pairs of a quad
-    if (L >= 16) {
-        v += dpp<0x141>(v);              // quads of eight lanes (mirrored)
-        v += dpp<0x140>(v);              // eights of sixteen lanes (mirrored)
-    }
-    if (L >= 64) {
-        v += __shfl_xor(v, 16, 64);
-        v += __shfl_xor(v, 32, 64);
-    }
+    if (L >= 8) v += dpp<0x141>(v);      // quads of eight lanes (mirrored)
+    if (L >= 16) v += dpp<0x140>(v);     // eights of sixteen lanes (mirrored)
+    if (L >= 32) v += __shfl_xor(v, 16, 64);
+    if (L >= 64) v += __shfl_xor(v, 32, 64);
     return v;
 }
 // Sums of a and b over the L threads of a row.  slots: LDS of the workgroup, two
@@ -95,10 +116,9 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2 (*slots)[16]
     b = lane_sum<(L < 64 ? L : 64)>(b);
     if constexpr (L > 64) {
         constexpr int W = L / 64;
-        float2* s = slots[turn];
+        float2* s = slots[turn] + threadIdx.x / L * W;   // of the row's waves
         turn ^= 1;
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) s[wave] = make_float2(a, b);
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x % L >> 6] = make_float2(a, b);
         __syncthreads();
         a = s[0].x;
         b = s[0].y;
@@ -110,10 +130,10 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2 (*slots)[16]
     }
 }
 
-// Threads of a workgroup that holds rows with L threads each.
+// Threads of a forward pass's workgroup that holds rows with L threads each.
 template <int L> constexpr int kGroup = L > 256 ? L : 256;
 
-template <int DT, int L, int CH>
+template <int DT, int L, int CH, bool WHOLE>
 __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int EPC = Elem<DT>::EPC, G = kGroup<L> / L;
@@ -129,24 +149,27 @@ __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
         const int cols = live ? a.cols : 0;
         u32x4 v[CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) v[c] = load_chunk<DT>(x, (c * L + l) * EPC, cols);
+        for (int c = 0; c < CH; ++c) v[c] = load_chunk<DT, WHOLE>(x, (c * L + l) * EPC, cols);
         float sum = 0.f, none = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int e = 0; e < EPC; ++e) sum += Elem<DT>::get(v[c], e);
+        stay_packed(v);
         row_sum2<L>(sum, none, slots, turn);
         const float mean = sum / n;   // (exact where all values are equal)
         float var = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int at = (c * L + l) * EPC;
+            const int in = cols - (c * L + l) * EPC;
+            if (in <= 0) continue;
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
                 const float d = Elem<DT>::get(v[c], e) - mean;
-                var += at + e < cols ? d * d : 0.f;
+                var += WHOLE || e < in ? d * d : 0.f;
             }
         }
+        stay_packed(v);
         row_sum2<L>(var, none, slots, turn);
         const float r = 1.f / sqrtf(var / n + a.eps);
         if (!live) continue;   // (no barrier below)
@@ -160,24 +183,30 @@ __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
 #pragma unroll
             for (int e = 0; e < EPC; ++e) f[e] = (Elem<DT>::get(v[c], e) - mean) * r;
             if (a.weight != nullptr) {
-                const u32x4 w = load_chunk<DT>(reinterpret_cast<const T*>(a.weight), at, cols);
+                const u32x4 w = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.weight), at, cols);
 #pragma unroll
                 for (int e = 0; e < EPC; ++e) f[e] *= Elem<DT>::get(w, e);
             }
             if (a.bias != nullptr) {
-                const u32x4 b = load_chunk<DT>(reinterpret_cast<const T*>(a.bias), at, cols);
+                const u32x4 b = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.bias), at, cols);
 #pragma unroll
                 for (int e = 0; e < EPC; ++e) f[e] += Elem<DT>::get(b, e);
             }
-            store_chunk<DT>(y, at, cols, f);
+            store_chunk<DT, WHOLE>(y, at, cols, f);
         }
     }
 }
 
-template <int DT, int L, int CH>
-__global__ __launch_bounds__(kGroup<L>) void norm_backward(const NormArgs a) {
+// A workgroup of 1024 threads goes through 1024 / L rows at a time, the next ones loaded
+// while those are worked on (AHEAD; not where the registers would not hold both).  Rows
+// too long to be held beside their sums (HOLD = false) are read again for dx, from L2.
+constexpr int kBackward = 1024;
+template <int DT, int L, int CH, bool WHOLE>
+__global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
     using T = typename Elem<DT>::T;
-    constexpr int EPC = Elem<DT>::EPC, G = kGroup<L> / L;
+    constexpr int EPC = Elem<DT>::EPC, G = kBackward / L;
+    constexpr bool AHEAD = CH * EPC <= 8, HOLD = CH <= 2;
+    constexpr int N = HOLD ? CH : 1;
     __shared__ float2 slots[2][16];
     int turn = 0;
     const int l = threadIdx.x % L;
@@ -187,54 +216,83 @@ __global__ __launch_bounds__(kGroup<L>) void norm_backward(const NormArgs a) {
     for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int e = 0; e < EPC; ++e) dw[c][e] = db[c][e] = 0.f;
-    const int64_t step = (int64_t)gridDim.x * G;
-    for (int64_t first = (int64_t)blockIdx.x * G; first < a.rows; first += step) {
-        const int64_t row = first + threadIdx.x / L;
+    struct Rows {
+        u32x4 x[N], g[N];
+        float2 st;
+    };
+    u32x4 wv[N];
+    const auto load_w = [&](int c) __attribute__((always_inline)) {
+        constexpr unsigned kOne = DT == 0 ? 0x3f803f80u : 0x3f800000u;
+        wv[c % N] = a.weight != nullptr ? load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.weight), (c * L + l) * EPC, a.cols)
+                                        : u32x4{kOne, kOne, kOne, kOne};
+    };
+    const auto load_chunks = [&](int64_t row, int c, Rows& p) __attribute__((always_inline)) {
         const bool live = row < a.rows;
-        const T* x = reinterpret_cast<const T*>(a.x) + (live ? row * a.x_ld : 0);
-        const T* dy = reinterpret_cast<const T*>(a.dy) + (live ? row * a.dy_ld : 0);
-        const int cols = live ? a.cols : 0;
-        const float2 st = live ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
-        u32x4 xv[CH], gv[CH];
+        p.x[c % N] = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.x) + (live ? row * a.x_ld : 0), (c * L + l) * EPC,
+                                           live ? a.cols : 0);
+        p.g[c % N] = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.dy) + (live ? row * a.dy_ld : 0), (c * L + l) * EPC,
+                                           live ? a.cols : 0);
+    };
+    const auto load = [&](int64_t row, Rows& p) __attribute__((always_inline)) {
+        p.st = row < a.rows ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
+        if (HOLD)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            xv[c] = load_chunk<DT>(x, (c * L + l) * EPC, cols);
-            gv[c] = load_chunk<DT>(dy, (c * L + l) * EPC, cols);
-        }
+            for (int c = 0; c < CH; ++c) load_chunks(row, c, p);
+    };
+    if (HOLD)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) load_w(c);
+    const int64_t step = (int64_t)gridDim.x * G, mine = threadIdx.x / L;
+    Rows p;
+    load((int64_t)blockIdx.x * G + mine, p);
+    for (int64_t first = (int64_t)blockIdx.x * G; first < a.rows; first += step) {   // the same in all threads
+        const int64_t row = first + mine;
+        Rows q;
+        if (AHEAD) load(row + step, q);
         float s1 = 0.f, s2 = 0.f;
-        u32x4 wv[CH];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            if (a.weight != nullptr) wv[c] = load_chunk<DT>(reinterpret_cast<const T*>(a.weight), (c * L + l) * EPC, cols);
+            if (!HOLD) {
+                load_chunks(row, c, p);
+                load_w(c);
+            }
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
-                const float g = Elem<DT>::get(gv[c], e), xh = (Elem<DT>::get(xv[c], e) - st.x) * st.y;
+                const float g = Elem<DT>::get(p.g[c % N], e), xh = (Elem<DT>::get(p.x[c % N], e) - p.st.x) * p.st.y;
                 db[c][e] += g;
                 dw[c][e] += g * xh;   // (past the row's end g is 0)
-                const float gw = a.weight != nullptr ? g * Elem<DT>::get(wv[c], e) : g;
+                const float gw = g * Elem<DT>::get(wv[c % N], e);
                 s1 += gw;
                 s2 += gw * xh;
             }
         }
-        if (a.dx == nullptr) continue;
-        row_sum2<L>(s1, s2, slots, turn);
-        s1 *= inv;
-        s2 *= inv;
-        if (!live) continue;   // (no barrier below)
-        T* dx = reinterpret_cast<T*>(a.dx) + row * a.dx_ld;
+        stay_packed(p.x);
+        stay_packed(p.g);
+        stay_packed(wv);
+        if (a.dx != nullptr) {
+            row_sum2<L>(s1, s2, slots, turn);
+            s1 *= inv;
+            s2 *= inv;
+            T* dx = reinterpret_cast<T*>(a.dx) + row * a.dx_ld;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int at = (c * L + l) * EPC;
-            if (at >= cols) continue;
-            float f[EPC];
+            for (int c = 0; c < CH; ++c) {
+                if (!HOLD) {
+                    load_chunks(row, c, p);
+                    load_w(c);
+                }
+                const int at = (c * L + l) * EPC;
+                if (row >= a.rows || at >= a.cols) continue;
+                float f[EPC];
 #pragma unroll
-            for (int e = 0; e < EPC; ++e) {
-                const float g = Elem<DT>::get(gv[c], e), xh = (Elem<DT>::get(xv[c], e) - st.x) * st.y;
-                const float gw = a.weight != nullptr ? g * Elem<DT>::get(wv[c], e) : g;
-                f[e] = st.y * (gw - s1 - xh * s2);
+                for (int e = 0; e < EPC; ++e) {
+                    const float g = Elem<DT>::get(p.g[c % N], e), xh = (Elem<DT>::get(p.x[c % N], e) - p.st.x) * p.st.y;
+                    f[e] = p.st.y * (g * Elem<DT>::get(wv[c % N], e) - s1 - xh * s2);
+                }
+                store_chunk<DT, WHOLE>(dx, at, a.cols, f);
             }
-            store_chunk<DT>(dx, at, cols, f);
         }
+        if (AHEAD) p = q;
+        else if (first + step < a.rows) load(row + step, p);
     }
     if (a.part == nullptr) return;
     // ---- the workgroup's sums: its groups of threads in order, dw then db
@@ -261,9 +319,8 @@ __global__ __launch_bounds__(kGroup<L>) void norm_backward(const NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < EPC; ++e) sums[group][(c * L + l) * EPC + e] = k ? db[c][e] : dw[c][e];
             __syncthreads();
-            for (int i = threadIdx.x; i < a.cols; i += kGroup<L>) {
+            for (int i = threadIdx.x; i < a.cols; i += kBackward) {
                 float s = sums[0][i];
-#pragma unroll
                 for (int g = 1; g < G; ++g) s += sums[g][i];
                 to[k * a.cols + i] = s;
             }
@@ -304,7 +361,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How rows are held: L threads of CH chunks.
 struct Shape { int l, ch; };
-Shape shape_of(int32_t cols, int32_t dtype) {
+Shape forward_shape(int32_t cols, int32_t dtype) {
     const int64_t c = cdiv(cols, dtype == 0 ? 8 : 4);   // chunks of a row
     if (c <= 4) return {4, 1};
     if (c <= 16) return {16, 1};
@@ -317,50 +374,78 @@ Shape shape_of(int32_t cols, int32_t dtype) {
     if (c <= 4096) return {1024, 4};
     return {1024, 8};
 }
-
-// Workgroups of a gradient: two on a CU, and no more than have rows.
-int64_t backward_groups(int32_t rows, const Shape& s) {
-    const int64_t g = s.l > 256 ? 1 : 256 / s.l;
-    return std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, g), 2 * cus_or_256()));
+// (one chunk a thread: with two, the sums and the next rows' chunks spill)
+Shape backward_shape(int32_t cols, int32_t dtype) {
+    const int64_t c = cdiv(cols, dtype == 0 ? 8 : 4);
+    int l = 4;
+    while (l < c && l < kBackward) l *= 2;
+    int ch = 1;
+    while ((int64_t)l * ch < c) ch *= 2;
+    return {l, ch};
 }
 
-template <int DT, typename F>
-hipError_t with_shape(const Shape& s, F f) {
-#define HIMUON_SHAPE(L, CH) \
-    if (s.l == L && s.ch == CH) return f(std::integral_constant<int, L>{}, std::integral_constant<int, CH>{})
-    HIMUON_SHAPE(4, 1);
-    HIMUON_SHAPE(16, 1);
-    HIMUON_SHAPE(64, 1);
-    HIMUON_SHAPE(64, 2);
-    HIMUON_SHAPE(64, 4);
-    HIMUON_SHAPE(64, 8);
-    HIMUON_SHAPE(256, 4);
-    HIMUON_SHAPE(256, 8);
-    HIMUON_SHAPE(1024, 4);
-    if constexpr (DT == 1) HIMUON_SHAPE(1024, 8);
-#undef HIMUON_SHAPE
+// Workgroups of a gradient: one on a CU, and no more than have rows.
+int64_t backward_groups(int32_t rows, const Shape& s) {
+    return std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, kBackward / s.l), cus_or_256()));
+}
+
+template <int DT, int L, int CH>
+hipError_t forward_of(const NormArgs& a, hipStream_t s) {
+    constexpr int G = kGroup<L> / L;
+    const dim3 grid((uint32_t)std::min<int64_t>(cdiv(a.rows, G), (int64_t)cus_or_256() * 64)), threads(kGroup<L>);
+    if (a.cols % Elem<DT>::EPC == 0) hipLaunchKernelGGL((norm_forward<DT, L, CH, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((norm_forward<DT, L, CH, false>), grid, threads, 0, s, a);
+    return hipGetLastError();
+}
+template <int DT>
+hipError_t forward(const NormArgs& a, hipStream_t s) {
+    const Shape sh = forward_shape(a.cols, DT);
+    switch (sh.l * 16 + sh.ch) {
+        case 4 * 16 + 1: return forward_of<DT, 4, 1>(a, s);
+        case 16 * 16 + 1: return forward_of<DT, 16, 1>(a, s);
+        case 64 * 16 + 1: return forward_of<DT, 64, 1>(a, s);
+        case 64 * 16 + 2: return forward_of<DT, 64, 2>(a, s);
+        case 64 * 16 + 4: return forward_of<DT, 64, 4>(a, s);
+        case 64 * 16 + 8: return forward_of<DT, 64, 8>(a, s);
+        case 256 * 16 + 4: return forward_of<DT, 256, 4>(a, s);
+        case 256 * 16 + 8: return forward_of<DT, 256, 8>(a, s);
+        case 1024 * 16 + 4: return forward_of<DT, 1024, 4>(a, s);
+    }
+    if constexpr (DT == 1) return forward_of<DT, 1024, 8>(a, s);
     return hipErrorInvalidValue;
 }
 
-template <int DT>
-hipError_t forward(const NormArgs& a, hipStream_t s) {
-    return with_shape<DT>(shape_of(a.cols, DT), [&](auto l, auto ch) {
-        constexpr int L = decltype(l)::value, CH = decltype(ch)::value, G = kGroup<L> / L;
-        const int64_t groups = std::min<int64_t>(cdiv(a.rows, G), (int64_t)cus_or_256() * 64);
-        hipLaunchKernelGGL((norm_forward<DT, L, CH>), dim3((uint32_t)groups), dim3(kGroup<L>), 0, s, a);
-        return hipGetLastError();
-    });
+template <int DT, int L, int CH>
+hipError_t backward_of(const NormArgs& a, uint32_t groups, hipStream_t s) {
+    if (a.cols % Elem<DT>::EPC == 0) hipLaunchKernelGGL((norm_backward<DT, L, CH, true>), dim3(groups), dim3(kBackward), 0, s, a);
+    else hipLaunchKernelGGL((norm_backward<DT, L, CH, false>), dim3(groups), dim3(kBackward), 0, s, a);
+    return hipGetLastError();
 }
-
+template <int DT>
+hipError_t backward_rows(const NormArgs& a, const Shape& sh, uint32_t g, hipStream_t s) {
+    if (sh.ch == 1) {
+        switch (sh.l) {
+            case 4: return backward_of<DT, 4, 1>(a, g, s);
+            case 8: return backward_of<DT, 8, 1>(a, g, s);
+            case 16: return backward_of<DT, 16, 1>(a, g, s);
+            case 32: return backward_of<DT, 32, 1>(a, g, s);
+            case 64: return backward_of<DT, 64, 1>(a, g, s);
+            case 128: return backward_of<DT, 128, 1>(a, g, s);
+            case 256: return backward_of<DT, 256, 1>(a, g, s);
+            case 512: return backward_of<DT, 512, 1>(a, g, s);
+            default: return backward_of<DT, 1024, 1>(a, g, s);
+        }
+    }
+    if (sh.ch == 2) return backward_of<DT, 1024, 2>(a, g, s);
+    if (sh.ch == 4) return backward_of<DT, 1024, 4>(a, g, s);
+    if constexpr (DT == 1) return backward_of<DT, 1024, 8>(a, g, s);
+    return hipErrorInvalidValue;
+}
 template <int DT>
 hipError_t backward(const NormArgs& a, hipStream_t s) {
-    const Shape sh = shape_of(a.cols, DT);
-    const int64_t groups = backward_groups(a.rows, sh);
-    const hipError_t e = with_shape<DT>(sh, [&](auto l, auto ch) {
-        constexpr int L = decltype(l)::value, CH = decltype(ch)::value;
-        hipLaunchKernelGGL((norm_backward<DT, L, CH>), dim3((uint32_t)groups), dim3(kGroup<L>), 0, s, a);
-        return hipGetLastError();
-    });
+    const Shape sh = backward_shape(a.cols, DT);
+    const uint32_t groups = (uint32_t)backward_groups(a.rows, sh);
+    const hipError_t e = backward_rows<DT>(a, sh, groups, s);
     if (e != hipSuccess || a.part == nullptr) return e;
     hipLaunchKernelGGL((norm_join<DT>), dim3((uint32_t)cdiv(2 * (int64_t)a.cols, 64)), dim3(1024), 0, s, a, (int)groups);
     return hipGetLastError();
@@ -369,7 +454,7 @@ hipError_t backward(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 int64_t norm_grad_bytes(int32_t rows, int32_t cols, int32_t dtype) {
-    return backward_groups(rows, shape_of(cols, dtype)) * 2 * cols * (int64_t)sizeof(float);
+    return backward_groups(rows, backward_shape(cols, dtype)) * 2 * cols * (int64_t)sizeof(float);
 }
 
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s) { return a.dtype == 0 ? forward<0>(a, s) : forward<1>(a, s); }
