@@ -68,20 +68,27 @@ __device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&f)
 }
 
 // Eight elements of a tensor from flat index `at`, `here` of them (0 to 8) inside.
+// WHOLE: all of the unit's are, in one run of memory.
+template <bool WHOLE>
 struct Place {
     int64_t at;
     int here;
     int64_t row, col;   // where the rows have gaps
-    __device__ __forceinline__ Place(const AdamwTensor& t, int64_t i) : at(i), row(0), col(0) {
-        here = (int)max((int64_t)0, min((int64_t)8, t.numel - i));
+    __device__ __forceinline__ Place(const AdamwTensor& t, int64_t base, int in) : at(base + in), here(8), row(0), col(0) {
+        if (WHOLE) return;
+        here = (int)max((int64_t)0, min((int64_t)8, t.numel - at));
         if (t.cols != 0) {
-            row = i / t.cols;
-            col = i - row * t.cols;
+            row = at / t.cols;
+            col = at - row * t.cols;
         }
     }
     // in one run of memory: the offset of its first element
-    __device__ __forceinline__ bool run(const AdamwTensor& t) const { return here == 8 && (t.cols == 0 || col + 8 <= t.cols); }
-    __device__ __forceinline__ int64_t offset(const AdamwTensor& t, int64_t ld) const { return t.cols == 0 ? at : row * ld + col; }
+    __device__ __forceinline__ bool run(const AdamwTensor& t) const {
+        return WHOLE || (here == 8 && (t.cols == 0 || col + 8 <= t.cols));
+    }
+    __device__ __forceinline__ int64_t offset(const AdamwTensor& t, int64_t ld) const {
+        return WHOLE || t.cols == 0 ? at : row * ld + col;
+    }
     __device__ __forceinline__ int64_t offset(const AdamwTensor& t, int64_t ld, int e) const {
         if (t.cols == 0) return at + e;
         int64_t r = row, c = col + e;
@@ -92,8 +99,9 @@ struct Place {
         return r * ld + c;
     }
 };
-template <int DT>
-__device__ __forceinline__ void load_part(const AdamwTensor& t, const void* base, int64_t ld, const Place& p, float (&f)[8]) {
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void load_part(const AdamwTensor& t, const void* base, int64_t ld, const Place<WHOLE>& p,
+                                          float (&f)[8]) {
     using T = typename Elem<DT>::T;
     const T* q = reinterpret_cast<const T*>(base);
     if (p.run(t)) {
@@ -103,8 +111,9 @@ __device__ __forceinline__ void load_part(const AdamwTensor& t, const void* base
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = e < p.here ? Elem<DT>::up(q[p.offset(t, ld, e)]) : 0.f;
 }
-template <int DT>
-__device__ __forceinline__ void store_part(const AdamwTensor& t, void* base, int64_t ld, const Place& p, const float (&f)[8]) {
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void store_part(const AdamwTensor& t, void* base, int64_t ld, const Place<WHOLE>& p,
+                                           const float (&f)[8]) {
     using T = typename Elem<DT>::T;
     T* q = reinterpret_cast<T*>(base);
     if (p.run(t)) {
@@ -116,7 +125,8 @@ __device__ __forceinline__ void store_part(const AdamwTensor& t, void* base, int
         if (e < p.here) q[p.offset(t, ld, e)] = Elem<DT>::down(f[e]);
 }
 
-__device__ __forceinline__ u32x2 load_codes(const void* base, const Place& p) {
+template <bool WHOLE>
+__device__ __forceinline__ u32x2 load_codes(const void* base, const Place<WHOLE>& p) {
     const unsigned char* q = reinterpret_cast<const unsigned char*>(base) + p.at;
     if (p.here == 8) return reinterpret_cast<const Loose8*>(q)->v;
     u32x2 c = {0, 0};
@@ -125,7 +135,8 @@ __device__ __forceinline__ u32x2 load_codes(const void* base, const Place& p) {
         if (e < p.here) c[e >> 2] |= (unsigned)q[e] << (8 * (e & 3));
     return c;
 }
-__device__ __forceinline__ void store_codes(void* base, const Place& p, u32x2 c) {
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(void* base, const Place<WHOLE>& p, u32x2 c) {
     unsigned char* q = reinterpret_cast<unsigned char*>(base) + p.at;
     if (p.here == 8) {
         reinterpret_cast<Loose8*>(q)->v = c;
@@ -145,35 +156,180 @@ __device__ __forceinline__ void decode8(u32x2 c, float scale, float (&f)[8]) {
         f[4 * h + 3] = b[1] * scale;
     }
 }
-// e4m3 code of y, 0 to 448: the value at or below y + u / 65536 of the step
-// between codes there.  Below 2^-6 codes are 2^-9 apart, as they are from 2^-6 to
-// 2^-5, to where such a y is moved.
+// e4m3 code of y, 0 to 448 (and at most 2^-21 of that more): the value at or below y +
+// u / 65536 of the step between codes there.  Below 2^-6 codes are 2^-9 apart, as they
+// are from 2^-6 to 2^-5, to where such a y is moved.
 __device__ __forceinline__ unsigned encode(float y, unsigned u) {
     const bool small = y < 0.015625f;
     const float z = small ? y + 0.015625f : y;
-    return min(((__float_as_uint(z) + (u << 4)) >> 20) - (small ? 968u : 960u), 126u);
+    return ((__float_as_uint(z) + (u << 4)) >> 20) - (small ? 968u : 960u);
 }
 // Largest over 32 lanes (a block's), the same in each of them.
 template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+__device__ __forceinline__ unsigned dpp(unsigned v) {
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
-__device__ __forceinline__ float block_max(float v) {
-    v = fmaxf(v, dpp<0xB1>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x140>(v));
-    return fmaxf(v, __shfl_xor(v, 16, 64));
+__device__ __forceinline__ unsigned block_max(unsigned v) {
+    v = max(v, dpp<0xB1>(v));
+    v = max(v, dpp<0x4E>(v));
+    v = max(v, dpp<0x141>(v));
+    v = max(v, dpp<0x140>(v));
+    return max(v, (unsigned)__shfl_xor((int)v, 16, 64));
 }
-constexpr float kLargest = 3.402823466e38f;
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= kLargest; }
+// A float without its sign, as a number: these compare as the floats do, infinity and
+// NaN above the finite ones.
+__device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr unsigned kInfinity = 0x7f800000u, kLeast = 0x0da24260u;   // of 1e-30
 
-template <int WT, int GT, int BITS>
-__global__ __launch_bounds__(256) void adamw_kernel(const AdamwArgs a) {
+// A block's largest finite magnitude, at least 1e-30; `odd`: the block holds others too.
+__device__ __forceinline__ float largest(const float (&x)[8], bool& odd) {
+    unsigned most = kLeast;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = max(most, magnitude(x[e]));
+    most = block_max(most);
+    odd = most >= kInfinity;
+    if (odd) {
+        asm volatile("");   // (a branch that is hardly ever taken, not selects that always run)
+        most = kLeast;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = max(most, magnitude(x[e]) < kInfinity ? magnitude(x[e]) : 0u);
+        most = block_max(most);
+    }
+    return __uint_as_float(most);
+}
+
+// sqrt(v): the hardware's reciprocal root and a Newton step, which leaves nearly every
+// result rounded correctly at two thirds of sqrtf's instructions (arithmetic bounds the
+// step in 8 bits; with the hardware's root alone more codes fell on the wrong side).
+__device__ __forceinline__ float root(float v) {
+    const float s = fminf(__builtin_amdgcn_rsqf(v), 1e30f), r = v * s;   // (v = 0: 0, not 0 times infinity)
+    return fmaf(fmaf(-r, r, v), 0.5f * s, r);
+}
+
+// 1 / x likewise, for x from 1e-30 to 8e37 (above, where v overflows, 0).
+__device__ __forceinline__ float reciprocal(float x) {
+    const float s = __builtin_amdgcn_rcpf(x);
+    return fmaf(fmaf(-x, s, 1.f), s, s);
+}
+__device__ __forceinline__ unsigned at_most_1(unsigned x) {   // (the compiler makes a test and a select of min)
+    unsigned r;
+    asm("v_min_u32 %0, 1, %1" : "=v"(r) : "v"(x));
+    return r;
+}
+
+// One unit of a tensor, from element `base`.
+template <int WT, int GT, int BITS, bool WHOLE>
+__device__ __forceinline__ void step_unit(const AdamwArgs& a, const AdamwTensor& t, int64_t base, float gs) {
 #pragma clang fp contract(off)
     // (the states are rounded after every operation, as the codes' rounding is a
     // function of their last bits)
     constexpr int U = (int)(kAdamwUnit / (256 * 8));
+    float w[U][8], g[U][8], m[U][8], v[U][8];
+    u32x2 mc[U], vc[U];
+    float ms[U], vs[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Place<WHOLE> p(t, base, u * 2048 + (int)threadIdx.x * 8);
+        load_part<WT>(t, t.w, t.w_ld, p, w[u]);
+        load_part<GT>(t, t.g, t.g_ld, p, g[u]);
+        if constexpr (BITS == 32) {
+            if (p.here == 8) {
+                load8<1>(reinterpret_cast<const float*>(t.m) + p.at, m[u]);
+                load8<1>(reinterpret_cast<const float*>(t.v) + p.at, v[u]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    m[u][e] = e < p.here ? reinterpret_cast<const float*>(t.m)[p.at + e] : 0.f;
+                    v[u][e] = e < p.here ? reinterpret_cast<const float*>(t.v)[p.at + e] : 0.f;
+                }
+            }
+        } else {
+            mc[u] = load_codes(t.m, p);
+            vc[u] = load_codes(t.v, p);
+            const int64_t block = p.at / kAdamwBlock;
+            const bool there = WHOLE || block * kAdamwBlock < t.numel;
+            ms[u] = there ? t.m_scale[block] : 0.f;
+            vs[u] = there ? t.v_scale[block] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Place<WHOLE> p(t, base, u * 2048 + (int)threadIdx.x * 8);
+        if constexpr (BITS == 8) {
+            decode8(mc[u], ms[u], m[u]);
+            decode8(vc[u], vs[u], v[u]);
+        }
+        float r[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = g[u][e] * gs;
+            if constexpr (BITS == 8) v[u][e] = v[u][e] * v[u][e];
+            m[u][e] = m[u][e] * a.beta1 + x * a.rest1;
+            v[u][e] = v[u][e] * a.beta2 + (x * x) * a.rest2;
+            r[e] = BITS == 8 ? root(v[u][e]) : sqrtf(v[u][e]);
+            const float up = m[u][e] * __builtin_amdgcn_rcpf(fmaf(r[e], a.root, a.eps));
+            w[u][e] = fmaf(-a.rate, up, w[u][e] * a.keep);
+        }
+        store_part<WT>(t, t.w, t.w_ld, p, w[u]);
+        if constexpr (BITS == 32) {
+            if (p.here == 8) {
+                store8<1>(reinterpret_cast<float*>(t.m) + p.at, m[u]);
+                store8<1>(reinterpret_cast<float*>(t.v) + p.at, v[u]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < p.here) {
+                        reinterpret_cast<float*>(t.m)[p.at + e] = m[u][e];
+                        reinterpret_cast<float*>(t.v)[p.at + e] = v[u][e];
+                    }
+            }
+        } else {
+            bool m_odd, r_odd;
+            const float m_max = largest(m[u], m_odd), r_max = largest(r, r_odd);
+            const float mi = reciprocal(m_max) * 448.f, ri = reciprocal(r_max) * 448.f;
+            unsigned cm[8], cv[8];
+            const unsigned first = (uint32_t)(p.at >> 1) * 0xB890E049u + a.key;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                unsigned h = first + (unsigned)k * 0xB890E049u;   // of elements 2 k and 2 k + 1
+                h = (h ^ (h >> 15)) * 0xB4A1B41Du;
+                h = (h ^ (h >> 13)) * 0xF5BBB081u;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int e = 2 * k + o;
+                    const unsigned uv = o ? h >> 16 : h & 0xffffu;
+                    const unsigned um = __builtin_amdgcn_perm(0u, uv, 0x0c0c0001u);   // its two bytes exchanged
+                    cm[e] = encode(fabsf(m[u][e]) * mi, um) | ((__float_as_uint(m[u][e]) >> 24) & 128u);
+                    cv[e] = max(encode(r[e] * ri, uv), at_most_1(__float_as_uint(r[e])));   // not 0 where r is not
+                }
+            }
+            if (m_odd || r_odd) {
+                asm volatile("");   // (as above)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (magnitude(m[u][e]) >= kInfinity) cm[e] = 127u;
+                    if (magnitude(r[e]) >= kInfinity) cv[e] = 127u;
+                }
+            }
+            u32x2 mo, vo;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mo[k] = cm[4 * k] | cm[4 * k + 1] << 8 | cm[4 * k + 2] << 16 | cm[4 * k + 3] << 24;
+                vo[k] = cv[4 * k] | cv[4 * k + 1] << 8 | cv[4 * k + 2] << 16 | cv[4 * k + 3] << 24;
+            }
+            store_codes(t.m, p, mo);
+            store_codes(t.v, p, vo);
+            if (p.here > 0 && (threadIdx.x & 31) == 0) {
+                const int64_t block = p.at / kAdamwBlock;
+                t.m_scale[block] = m_max * (1.f / 448.f);
+                t.v_scale[block] = r_max * (1.f / 448.f);
+            }
+        }
+    }
+}
+
+template <int WT, int GT, int BITS>
+__global__ __launch_bounds__(256) void adamw_kernel(const AdamwArgs a) {
     const float gs = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
     int id = 0;
     for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
@@ -189,99 +345,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwArgs a) {
         }
         id = __builtin_amdgcn_readfirstlane(id);
         const AdamwTensor& t = a.t[id];
-        const int64_t base = (int64_t)(unit - t.first) * kAdamwUnit + threadIdx.x * 8;
-        float w[U][8], g[U][8], m[U][8], v[U][8];
-        u32x2 mc[U], vc[U];
-        float ms[U], vs[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const Place p(t, base + u * 2048);
-            load_part<WT>(t, t.w, t.w_ld, p, w[u]);
-            load_part<GT>(t, t.g, t.g_ld, p, g[u]);
-            if constexpr (BITS == 32) {
-                if (p.here == 8) {
-                    load8<1>(reinterpret_cast<const float*>(t.m) + p.at, m[u]);
-                    load8<1>(reinterpret_cast<const float*>(t.v) + p.at, v[u]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        m[u][e] = e < p.here ? reinterpret_cast<const float*>(t.m)[p.at + e] : 0.f;
-                        v[u][e] = e < p.here ? reinterpret_cast<const float*>(t.v)[p.at + e] : 0.f;
-                    }
-                }
-            } else {
-                mc[u] = load_codes(t.m, p);
-                vc[u] = load_codes(t.v, p);
-                const int64_t block = p.at / kAdamwBlock;
-                const bool there = block * kAdamwBlock < t.numel;
-                ms[u] = there ? t.m_scale[block] : 0.f;
-                vs[u] = there ? t.v_scale[block] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const Place p(t, base + u * 2048);
-            if constexpr (BITS == 8) {
-                decode8(mc[u], ms[u], m[u]);
-                decode8(vc[u], vs[u], v[u]);
-            }
-            float m_max = 1e-30f, r_max = 1e-30f;
-            float r[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = g[u][e] * gs;
-                if constexpr (BITS == 8) v[u][e] = v[u][e] * v[u][e];
-                m[u][e] = m[u][e] * a.beta1 + x * a.rest1;
-                v[u][e] = v[u][e] * a.beta2 + (x * x) * a.rest2;
-                r[e] = sqrtf(v[u][e]);
-                w[u][e] = w[u][e] * a.keep - a.rate * m[u][e] * __builtin_amdgcn_rcpf(r[e] * a.root + a.eps);
-                m_max = fmaxf(m_max, finite(m[u][e]) ? fabsf(m[u][e]) : 0.f);
-                r_max = fmaxf(r_max, finite(r[e]) ? r[e] : 0.f);
-            }
-            store_part<WT>(t, t.w, t.w_ld, p, w[u]);
-            if constexpr (BITS == 32) {
-                if (p.here == 8) {
-                    store8<1>(reinterpret_cast<float*>(t.m) + p.at, m[u]);
-                    store8<1>(reinterpret_cast<float*>(t.v) + p.at, v[u]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < p.here) {
-                            reinterpret_cast<float*>(t.m)[p.at + e] = m[u][e];
-                            reinterpret_cast<float*>(t.v)[p.at + e] = v[u][e];
-                        }
-                }
-            } else {
-                m_max = block_max(m_max);
-                r_max = block_max(r_max);
-                const float mi = 1.f / m_max * 448.f, ri = 1.f / r_max * 448.f;
-                u32x2 mo = {0, 0}, vo = {0, 0};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    unsigned h = ((uint32_t)(p.at >> 1) + k) * 0xB890E049u + a.key;
-                    h = (h ^ (h >> 15)) * 0xB4A1B41Du;
-                    h = (h ^ (h >> 13)) * 0xF5BBB081u;
-#pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        const int e = 2 * k + o;
-                        const unsigned uv = o ? h >> 16 : h & 0xffffu, um = ((uv << 8) | (uv >> 8)) & 0xffffu;
-                        unsigned c = finite(m[u][e]) ? encode(fabsf(m[u][e]) * mi, um) : 127u;
-                        if (m[u][e] < 0.f) c |= 128u;
-                        mo[e >> 2] |= c << (8 * (e & 3));
-                        c = finite(r[e]) ? encode(r[e] * ri, uv) : 127u;
-                        if (r[e] > 0.f) c = max(c, 1u);
-                        vo[e >> 2] |= c << (8 * (e & 3));
-                    }
-                }
-                store_codes(t.m, p, mo);
-                store_codes(t.v, p, vo);
-                if (p.here > 0 && (threadIdx.x & 31) == 0) {
-                    const int64_t block = p.at / kAdamwBlock;
-                    t.m_scale[block] = m_max * (1.f / 448.f);
-                    t.v_scale[block] = r_max * (1.f / 448.f);
-                }
-            }
-        }
+        const int64_t base = (int64_t)(unit - t.first) * kAdamwUnit;
+        if (t.cols == 0 && base + kAdamwUnit <= t.numel) step_unit<WT, GT, BITS, true>(a, t, base, gs);
+        else step_unit<WT, GT, BITS, false>(a, t, base, gs);
     }
 }
 

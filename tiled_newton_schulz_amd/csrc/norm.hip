@@ -199,49 +199,44 @@ __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
 
 // A workgroup of 1024 threads goes through 1024 / L rows at a time, the next ones loaded
 // while those are worked on (AHEAD; not where the registers would not hold both).  Rows
-// too long to be held beside their sums (HOLD = false) are read again for dx, from L2.
+// of more than two chunks a thread leave no room for their sums (SUMS = false): those
+// are norm_columns' (2048 x 32768 in bf16 with the sums here 325 us).
 constexpr int kBackward = 1024;
 template <int DT, int L, int CH, bool WHOLE>
 __global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int EPC = Elem<DT>::EPC, G = kBackward / L;
-    constexpr bool AHEAD = CH * EPC <= 8, HOLD = CH <= 2;
-    constexpr int N = HOLD ? CH : 1;
+    constexpr bool AHEAD = CH * EPC <= 8, SUMS = CH <= 2;
     __shared__ float2 slots[2][16];
     int turn = 0;
     const int l = threadIdx.x % L;
     const float inv = 1.f / (float)a.cols;
-    float dw[CH][EPC], db[CH][EPC];
+    float dw[SUMS ? CH : 1][EPC], db[SUMS ? CH : 1][EPC];
+    u32x4 wv[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+        constexpr unsigned kOne = DT == 0 ? 0x3f803f80u : 0x3f800000u;
+        wv[c] = a.weight != nullptr ? load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.weight), (c * L + l) * EPC, a.cols)
+                                    : u32x4{kOne, kOne, kOne, kOne};
+        if (SUMS)
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) dw[c][e] = db[c][e] = 0.f;
+            for (int e = 0; e < EPC; ++e) dw[c][e] = db[c][e] = 0.f;
+    }
     struct Rows {
-        u32x4 x[N], g[N];
+        u32x4 x[CH], g[CH];
         float2 st;
     };
-    u32x4 wv[N];
-    const auto load_w = [&](int c) __attribute__((always_inline)) {
-        constexpr unsigned kOne = DT == 0 ? 0x3f803f80u : 0x3f800000u;
-        wv[c % N] = a.weight != nullptr ? load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.weight), (c * L + l) * EPC, a.cols)
-                                        : u32x4{kOne, kOne, kOne, kOne};
-    };
-    const auto load_chunks = [&](int64_t row, int c, Rows& p) __attribute__((always_inline)) {
-        const bool live = row < a.rows;
-        p.x[c % N] = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.x) + (live ? row * a.x_ld : 0), (c * L + l) * EPC,
-                                           live ? a.cols : 0);
-        p.g[c % N] = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.dy) + (live ? row * a.dy_ld : 0), (c * L + l) * EPC,
-                                           live ? a.cols : 0);
-    };
     const auto load = [&](int64_t row, Rows& p) __attribute__((always_inline)) {
-        p.st = row < a.rows ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
-        if (HOLD)
+        const bool live = row < a.rows;
+        const T* x = reinterpret_cast<const T*>(a.x) + (live ? row * a.x_ld : 0);
+        const T* dy = reinterpret_cast<const T*>(a.dy) + (live ? row * a.dy_ld : 0);
+        p.st = live ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) load_chunks(row, c, p);
+        for (int c = 0; c < CH; ++c) {
+            p.x[c] = load_chunk<DT, WHOLE>(x, (c * L + l) * EPC, live ? a.cols : 0);
+            p.g[c] = load_chunk<DT, WHOLE>(dy, (c * L + l) * EPC, live ? a.cols : 0);
+        }
     };
-    if (HOLD)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) load_w(c);
     const int64_t step = (int64_t)gridDim.x * G, mine = threadIdx.x / L;
     Rows p;
     load((int64_t)blockIdx.x * G + mine, p);
@@ -252,16 +247,14 @@ __global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            if (!HOLD) {
-                load_chunks(row, c, p);
-                load_w(c);
-            }
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
-                const float g = Elem<DT>::get(p.g[c % N], e), xh = (Elem<DT>::get(p.x[c % N], e) - p.st.x) * p.st.y;
-                db[c][e] += g;
-                dw[c][e] += g * xh;   // (past the row's end g is 0)
-                const float gw = g * Elem<DT>::get(wv[c % N], e);
+                const float g = Elem<DT>::get(p.g[c], e), xh = (Elem<DT>::get(p.x[c], e) - p.st.x) * p.st.y;
+                if (SUMS) {
+                    db[c][e] += g;
+                    dw[c][e] += g * xh;   // (past the row's end g is 0)
+                }
+                const float gw = g * Elem<DT>::get(wv[c], e);
                 s1 += gw;
                 s2 += gw * xh;
             }
@@ -276,17 +269,13 @@ __global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
             T* dx = reinterpret_cast<T*>(a.dx) + row * a.dx_ld;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                if (!HOLD) {
-                    load_chunks(row, c, p);
-                    load_w(c);
-                }
                 const int at = (c * L + l) * EPC;
                 if (row >= a.rows || at >= a.cols) continue;
                 float f[EPC];
 #pragma unroll
                 for (int e = 0; e < EPC; ++e) {
-                    const float g = Elem<DT>::get(p.g[c % N], e), xh = (Elem<DT>::get(p.x[c % N], e) - p.st.x) * p.st.y;
-                    f[e] = p.st.y * (g * Elem<DT>::get(wv[c % N], e) - s1 - xh * s2);
+                    const float g = Elem<DT>::get(p.g[c], e), xh = (Elem<DT>::get(p.x[c], e) - p.st.x) * p.st.y;
+                    f[e] = p.st.y * (g * Elem<DT>::get(wv[c], e) - s1 - xh * s2);
                 }
                 store_chunk<DT, WHOLE>(dx, at, a.cols, f);
             }
@@ -297,7 +286,8 @@ __global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
     if (a.part == nullptr) return;
     // ---- the workgroup's sums: its groups of threads in order, dw then db
     float* to = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-    if constexpr (G == 1) {
+    if constexpr (!SUMS) {
+    } else if constexpr (G == 1) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -326,6 +316,55 @@ __global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
             }
         }
     }
+}
+
+// The sums over rows alone, of 256 chunks of columns (blockIdx.x) and one of gridDim.y
+// parts of the rows, the next rows loaded while kRows are added.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(256) void norm_columns(const NormArgs a) {
+    using T = typename Elem<DT>::T;
+    constexpr int EPC = Elem<DT>::EPC, kRows = 4;
+    const int at = (int)(blockIdx.x * 256 + threadIdx.x) * EPC;
+    const int64_t from = (int64_t)a.rows * blockIdx.y / gridDim.y, to = (int64_t)a.rows * (blockIdx.y + 1) / gridDim.y;
+    float dw[EPC], db[EPC];
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) dw[e] = db[e] = 0.f;
+    struct Rows {
+        u32x4 x[kRows], g[kRows];
+        float2 st[kRows];
+    };
+    const auto load = [&](int64_t row, Rows& p) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const bool live = row + k < to;
+            const int64_t r = live ? row + k : 0;
+            p.x[k] = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.x) + r * a.x_ld, at, live ? a.cols : 0);
+            p.g[k] = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.dy) + r * a.dy_ld, at, live ? a.cols : 0);
+            p.st[k] = live ? *reinterpret_cast<const float2*>(a.stats + 2 * r) : make_float2(0.f, 0.f);
+        }
+    };
+    Rows p;
+    load(from, p);
+    for (int64_t row = from; row < to; row += kRows) {
+        Rows q;
+        load(row + kRows, q);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) {
+                const float g = Elem<DT>::get(p.g[k], e);
+                db[e] += g;
+                dw[e] += g * ((Elem<DT>::get(p.x[k], e) - p.st[k].x) * p.st[k].y);
+            }
+        p = q;
+    }
+    float* out = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+#pragma unroll
+    for (int e = 0; e < EPC; ++e)
+        if (at + e < a.cols) {
+            out[at + e] = dw[e];
+            out[a.cols + at + e] = db[e];
+        }
 }
 
 // Adds the workgroups' sums in order: 64 of the 2 D columns by 16 runs of
@@ -361,8 +400,11 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How rows are held: L threads of CH chunks.
 struct Shape { int l, ch; };
-Shape forward_shape(int32_t cols, int32_t dtype) {
+// Few rows take more threads each (4 x 4096 in bf16 with 64 threads a row FEW us, with
+// 256 MANY).
+Shape forward_shape(int32_t rows, int32_t cols, int32_t dtype) {
     const int64_t c = cdiv(cols, dtype == 0 ? 8 : 4);   // chunks of a row
+    if (rows <= 4 * cus_or_256() && c > 64 && c <= 512) return {256, c <= 256 ? 1 : 2};
     if (c <= 4) return {4, 1};
     if (c <= 16) return {16, 1};
     if (c <= 64) return {64, 1};
@@ -384,8 +426,12 @@ Shape backward_shape(int32_t cols, int32_t dtype) {
     return {l, ch};
 }
 
-// Workgroups of a gradient: one on a CU, and no more than have rows.
+// Whether the sums over rows are a launch of their own.
+bool apart(const Shape& s) { return s.ch > 2; }
+// Workgroups of a gradient: one on a CU, and no more than have rows (apart: parts of the
+// rows, of which there are four workgroups on a CU with the slabs of columns).
 int64_t backward_groups(int32_t rows, const Shape& s) {
+    if (apart(s)) return std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, 4), cus_or_256() / s.ch));
     return std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, kBackward / s.l), cus_or_256()));
 }
 
@@ -399,7 +445,7 @@ hipError_t forward_of(const NormArgs& a, hipStream_t s) {
 }
 template <int DT>
 hipError_t forward(const NormArgs& a, hipStream_t s) {
-    const Shape sh = forward_shape(a.cols, DT);
+    const Shape sh = forward_shape(a.rows, a.cols, DT);
     switch (sh.l * 16 + sh.ch) {
         case 4 * 16 + 1: return forward_of<DT, 4, 1>(a, s);
         case 16 * 16 + 1: return forward_of<DT, 16, 1>(a, s);
@@ -407,6 +453,8 @@ hipError_t forward(const NormArgs& a, hipStream_t s) {
         case 64 * 16 + 2: return forward_of<DT, 64, 2>(a, s);
         case 64 * 16 + 4: return forward_of<DT, 64, 4>(a, s);
         case 64 * 16 + 8: return forward_of<DT, 64, 8>(a, s);
+        case 256 * 16 + 1: return forward_of<DT, 256, 1>(a, s);
+        case 256 * 16 + 2: return forward_of<DT, 256, 2>(a, s);
         case 256 * 16 + 4: return forward_of<DT, 256, 4>(a, s);
         case 256 * 16 + 8: return forward_of<DT, 256, 8>(a, s);
         case 1024 * 16 + 4: return forward_of<DT, 1024, 4>(a, s);
@@ -445,8 +493,22 @@ template <int DT>
 hipError_t backward(const NormArgs& a, hipStream_t s) {
     const Shape sh = backward_shape(a.cols, DT);
     const uint32_t groups = (uint32_t)backward_groups(a.rows, sh);
-    const hipError_t e = backward_rows<DT>(a, sh, groups, s);
-    if (e != hipSuccess || a.part == nullptr) return e;
+    if (!apart(sh)) {
+        const hipError_t e = backward_rows<DT>(a, sh, groups, s);
+        if (e != hipSuccess || a.part == nullptr) return e;
+    } else {
+        if (a.part != nullptr) {   // first, as dx may be written over dy or x
+            const dim3 grid((uint32_t)cdiv(a.cols, 256 * Elem<DT>::EPC), groups);
+            if (a.cols % Elem<DT>::EPC == 0) hipLaunchKernelGGL((norm_columns<DT, true>), grid, dim3(256), 0, s, a);
+            else hipLaunchKernelGGL((norm_columns<DT, false>), grid, dim3(256), 0, s, a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        if (a.dx != nullptr && a.rows > 0) {
+            const hipError_t e = backward_rows<DT>(a, sh, (uint32_t)std::min<int64_t>(a.rows, 2 * cus_or_256()), s);
+            if (e != hipSuccess || a.part == nullptr) return e;
+        }
+    }
     hipLaunchKernelGGL((norm_join<DT>), dim3((uint32_t)cdiv(2 * (int64_t)a.cols, 64)), dim3(1024), 0, s, a, (int)groups);
     return hipGetLastError();
 }
