@@ -788,12 +788,17 @@ class Tensors:
     Matrices)."""
 
     def __init__(self, array, tensors, dtype, device, shapes):
-        self.array, self.tensors, self.dtype, self.device, self.shapes = array, tensors, dtype, device, shapes
-        self.places = [t.data_ptr() for t in tensors]
+        self.array, self.tensors, self.dtype, self.device = array, tensors, dtype, device
+        self.shapes, self.key = shapes, repr(shapes).encode()   # (bytes compare at once)
+        self.places = self._places()
+
+    def _places(self):
+        import torch
+        return list(map(torch.Tensor.data_ptr, self.tensors))
 
     def in_place(self):
         """Itself, if the tensors are still where they were described."""
-        if [t.data_ptr() for t in self.tensors] != self.places:
+        if self._places() != self.places:
             raise ValueError("tensors were described before they got other memory: describe them again")
         return self
 
@@ -844,7 +849,7 @@ class AdamWState:
         import torch
         if bits not in (8, 32):
             raise ValueError("bits must be 8 or 32")
-        self.bits, self.shapes, self.device = bits, like.shapes, like.device
+        self.bits, self.shapes, self.key, self.device = bits, like.shapes, like.key, like.device
         n = len(like)
         sizes = np.array([like.array[i].rows * like.array[i].cols for i in range(n)], dtype=np.int64)
         blocks = -(-sizes // ADAMW_BLOCK)
@@ -900,7 +905,7 @@ def himuon_adamw_step(w, g, state: AdamWState, lr: float, step: int, betas=(0.9,
     import torch
     w, g = tensors(w), tensors(g)
     state.in_place()
-    if w.shapes != g.shapes or w.shapes != state.shapes:
+    if w.key != g.key or w.key != state.key:
         raise ValueError("weights, gradients and states must agree in number and shapes")
     if len(w) == 0:
         return
