@@ -326,3 +326,99 @@ def test_block_gradients_against_differences(cuda):
                 # chain of three fp32 products of at most 20 terms is off by 2^-18 of its terms' sum
                 size = (got[i].double().abs() * v.abs()).sum()
                 assert abs((got[i].double() * v).sum() - slope) <= 1e-6 + 2.0 ** -14 * size, (act, i)
+
+
+@pytest.mark.parametrize("dt,K,N", [("bf16", 512, 4096), ("bf16", 511, 4097), ("fp32", 256, 2049)])
+def test_operands_past_2_to_the_31_elements(cuda, dt, K, N):
+    """[G | U] of more than 2^31 elements, and weights of as many bytes: the first and
+    the last rows of the first and the last experts."""
+    M = (1 << 31) // (2 * N) + 700
+    n = max(3, (1 << 31) // (2 * K * N) // (2 if dt == "fp32" else 1))
+    print(f"gated {M} rows, {n} experts of {K} x {2 * N} {dt}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((M, K), device=cuda, generator=gen).to(TYPES[dt])
+    w = torch.empty((n, K, 2 * N), dtype=TYPES[dt], device=cuda).normal_(generator=gen).mul_(K ** -0.5)
+    counts = [M // n] * (n - 1) + [M - (n - 1) * (M // n)]
+    r = H.himuon_grouped_gated_mm(x, w, ends_of(counts), keep=True)
+    starts = [sum(counts[:e]) for e in range(n)]
+    picks = [(0, 0), (0, counts[0] - 1), (n - 1, starts[-1]), (n - 1, M - 1)]
+    for e, row in picks:
+        pre, off = accumulated(x[row:row + 1], w[e])
+        g, u, eg, eu = pre[:, :N], pre[:, N:], off[:, :N], off[:, N:]
+        _, a, _, _ = share("silu", g)
+        da = 1.2 * eg + (a.abs() + 1.2 * eg) * rel(g)
+        close(r.h[row:row + 1], a * u, u.abs() * da + a.abs() * eu + da * eu + 2.0 ** -23 * (a * u).abs(), dt, "h")
+        close(r.pre[row:row + 1], pre, off, dt, "pre")
+    del w, r
+    torch.cuda.empty_cache()
+    pre = torch.empty((M, 2 * N), dtype=TYPES[dt], device=cuda).normal_(generator=gen)
+    keep = {row: pre[row:row + 1].double() for _, row in picks}
+    w = torch.empty((n, N, K), dtype=TYPES[dt], device=cuda).normal_(generator=gen).mul_(N ** -0.5)
+    r = H.himuon_grouped_gated_mm_grad(x, w, ends_of(counts), pre, out=pre)
+    for e, row in picks:
+        dh, off = accumulated(x[row:row + 1], w[e].t())
+        g, u = keep[row][:, :N], keep[row][:, N:]
+        s, a, slope, p = share("silu", g)
+        ds = rel(g) * (s + (a * (1 - s) * p).abs() + (slope - s).abs()) + 2.0 ** -23 * (a * p).abs()
+        close(r.grad[row:row + 1, :N], dh * u * slope,
+              (u * slope).abs() * off + (dh.abs() + off) * u.abs() * ds + 2.0 ** -22 * (dh * u * slope).abs(), dt, "gate")
+        close(r.grad[row:row + 1, N:], dh * a,
+              a.abs() * off + (dh.abs() + off) * a.abs() * rel(g) + 2.0 ** -22 * (dh * a).abs(), dt, "up")
+
+
+def test_two_streams_at_once(cuda):
+    """Two blocks on two streams, each filling the chip, and their gradients."""
+    print("gated blocks on two streams", flush=True)
+    counts, K, N = ragged(40, 500, 5), 520, 328
+    M, n = sum(counts), len(counts)
+    ends, sides, sets = ends_of(counts), [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for k in range(2):
+        x, dy = randn((M, K), "bf16", 10 * k), randn((M, K), "bf16", 10 * k + 1)
+        sets.append((x, weights(n, K, 2 * N, "kn", "bf16", 10 * k + 2), dy, weights(n, N, K, "kn", "bf16", 10 * k + 3)))
+
+    def block(x, w, dy, wd):
+        r = H.himuon_grouped_gated_mm(x, w, ends, keep=True)
+        return (*r, *H.himuon_grouped_gated_mm_grad(dy, wd, ends, r.pre, hidden=True))
+
+    want = [block(*s) for s in sets]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for k in range(2):
+            with torch.cuda.stream(sides[k]):
+                got[k] = block(*sets[k])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_refusals_in_python(cuda):
+    x, w, ends = randn((10, 16), "bf16", 1), randn((2, 16, 24), "bf16", 2), ends_of([4, 6])
+    r = H.himuon_grouped_gated_mm(x, w, ends, keep=True)
+    wd, dy = randn((2, 12, 16), "bf16", 3), randn((10, 16), "bf16", 4)
+    for bad in (dict(act="tanh"), dict(out=r.pre), dict(keep=r.h), dict(out=r.h.cpu())):
+        with pytest.raises(ValueError):
+            H.himuon_grouped_gated_mm(x, w, ends, **bad)
+    for bad in (dict(out=r.h.float()), dict(keep=r.pre.float())):
+        with pytest.raises(TypeError):
+            H.himuon_grouped_gated_mm(x, w, ends, **bad)
+    with pytest.raises(ValueError):
+        H.himuon_grouped_gated_mm(x, w[:, :, :23], ends)
+    with pytest.raises(TypeError):
+        H.himuon_grouped_gated_mm(x.float(), w, ends)
+    with pytest.raises(TypeError):
+        H.himuon_grouped_gated_mm(x, w, ends.long())
+    with pytest.raises(ValueError):
+        H.himuon_grouped_gated_mm(x, w, ends.cpu())
+    with pytest.raises(H.HimuonError):
+        H.himuon_grouped_gated_mm(x[:, :8], w, ends)
+    with pytest.raises(H.HimuonError):   # [g | u] over x
+        both = randn((10, 24), "bf16", 5)
+        H.himuon_grouped_gated_mm(both[:, :16], w, ends, keep=both)
+    for bad in (r.pre[:, :22], r.pre[:9], r.h):
+        with pytest.raises(H.HimuonError):
+            H.himuon_grouped_gated_mm_grad(dy, wd, ends, bad)
+    with pytest.raises(TypeError):
+        H.himuon_grouped_gated_mm_grad(dy, wd, ends, r.pre.float())
+    with pytest.raises(ValueError):
+        H.himuon_grouped_gated_mm_grad(dy, wd, ends, r.pre.cpu())

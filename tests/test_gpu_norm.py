@@ -33,9 +33,14 @@ def close(got, want, off, dt, what):
 
 
 def check_forward(x, w, b, eps, dt, **more):
-    x64 = x.double()
     r = H.himuon_layer_norm(x, w, b, eps=eps, **more)
     torch.cuda.synchronize()
+    check_rows(x, w, b, eps, dt, r.y, r.stats)
+    return r
+
+
+def check_rows(x, w, b, eps, dt, got, stats):
+    x64 = x.double()
     mean = x64.mean(1, keepdim=True)
     d = x64 - mean
     var = d.square().mean(1, keepdim=True)
@@ -46,17 +51,21 @@ def check_forward(x, w, b, eps, dt, **more):
     b64 = torch.zeros((), device=x.device).double() if b is None else b.double()
     y = d * rstd * w64 + b64
     off = abs(w64) * (rstd * em + (d * rstd).abs() * (rr + 4 * U)) + 2 * U * (y.abs() + b64.abs())
-    close(r.y, y, off, dt, "y")
-    if r.stats is not None:
-        s = r.stats.double()
+    close(got, y, off, dt, "y")
+    if stats is not None:
+        s = stats.double()
         assert torch.all((s[:, :1] - mean).abs() <= em + 1e-37) and torch.all((s[:, 1:] / rstd - 1).abs() <= rr)
-    return r
 
 
 def check_grad(x, w, stats, dy, dt, **more):
-    x64, g = x.double(), dy.double()
     r = H.himuon_layer_norm_grad(x, w, stats, dy, **more)
     torch.cuda.synchronize()
+    check_grads(x, w, stats, dy, dt, r)
+    return r
+
+
+def check_grads(x, w, stats, dy, dt, r):
+    x64, g = x.double(), dy.double()
     N, s = x.shape[0], stats.double()
     xh = (x64 - s[:, :1]) * s[:, 1:]
     gw = g if w is None else g * w.double()
@@ -71,7 +80,6 @@ def check_grad(x, w, stats, dy, dt, **more):
         close(r.dweight, (g * xh).sum(0), (chain + 4 * U) * (g * xh).abs().sum(0), dt, "dweight")
     if r.dbias is not None:
         close(r.dbias, g.sum(0), chain * g.abs().sum(0), dt, "dbias")
-    return r
 
 
 # around every size at which rows are held in another way, and odd ones
@@ -219,3 +227,76 @@ def test_gradients_against_differences(cuda):
             slope = (value(*up) - value(*down)) / 2e-5
             # h^2 / 6 = 2e-11 of the third derivative; the gradients within 100 u of their terms
             assert abs((g[i].double() * v).sum() - slope) <= 1e-7 + 400 * U * (g[i].double().abs() * v.abs()).sum() + 400 * U * c.abs().sum()
+
+
+@pytest.mark.parametrize("dt,cols", [("bf16", 4096), ("fp32", 2047), ("bf16", 32760)])
+def test_rows_past_2_to_the_31_elements(cuda, dt, cols):
+    rows = (1 << 31) // cols + 301
+    print(f"layer norm {rows} x {cols} {dt}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((rows, cols), dtype=TYPES[dt], device=cuda).normal_(generator=gen)
+    w = randn((cols,), dt, 2)
+    r = H.himuon_layer_norm(x, w)
+    ends = (slice(0, 40), slice(rows - 40, rows))
+    for part in ends:
+        check_rows(x[part], w, None, 1e-5, dt, r.y[part], r.stats[part])
+    dy = r.y   # (any gradient)
+    kept = [dy[part].clone() for part in ends]
+    g = H.himuon_layer_norm_grad(x, w, r.stats, dy, dx=dy)
+    for part, k in zip(ends, kept):
+        check_grads(x[part], w, r.stats[part], k, dt, H.NormGrad(g.dx[part]))
+    # the sums over all rows, from sums over blocks of them in fp64
+    sums, size = torch.zeros(cols, dtype=torch.float64, device=cuda), torch.zeros(cols, dtype=torch.float64, device=cuda)
+    again = H.himuon_layer_norm(x, w).y
+    for block in again.split(4096):
+        sums += block.double().sum(0)
+        size += block.double().abs().sum(0)
+    close(g.dbias, sums, (rows / 256 + 128) * U * size, dt, "dbias")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 20000), (3, 17000), (37, 30001), (0, 32768), (130, 24576)])
+def test_wide_rows(cuda, rows, cols, dt):
+    """Rows whose sums are a launch of their own; dx over dy and over x."""
+    print(f"layer norm {rows} x {cols} {dt}", flush=True)
+    x, w, dy = randn((rows, cols), dt, 1), randn((cols,), dt, 2), randn((rows, cols), dt, 3)
+    r = check_forward(x, w, None, 1e-5, dt)
+    g = check_grad(x, w, r.stats, dy, dt) if rows else H.himuon_layer_norm_grad(x, w, r.stats, dy)
+    if rows == 0:
+        assert torch.all(g.dweight == 0) and torch.all(g.dbias == 0)
+    for over in (x.clone(), dy.clone()):
+        args = (over, dy) if torch.equal(over, x) else (x, over)
+        h = H.himuon_layer_norm_grad(args[0], w, r.stats, args[1], dx=over)
+        assert all(torch.equal(p, q) for p, q in zip(h, g))
+
+
+def test_refusals_in_python(cuda):
+    x, w = randn((4, 16), "bf16", 1), randn((16,), "bf16", 2)
+    r = H.himuon_layer_norm(x, w)
+    for bad in (dict(weight=w[:8]), dict(weight=w.cpu()), dict(bias=torch.cat([w, w])[::2]), dict(out=r.y[:3]), dict(out=r.y.cpu())):
+        with pytest.raises(ValueError):
+            H.himuon_layer_norm(x, **bad)
+    for bad in (dict(weight=w.float()), dict(out=r.y.float())):
+        with pytest.raises(TypeError):
+            H.himuon_layer_norm(x, **bad)
+    with pytest.raises(ValueError):
+        H.himuon_layer_norm(x.cpu(), w.cpu())
+    with pytest.raises(ValueError):
+        H.himuon_layer_norm(x.t())
+    with pytest.raises(H.HimuonError):
+        H.himuon_layer_norm(x, w, eps=-1.0)
+    with pytest.raises(H.HimuonError):
+        H.himuon_layer_norm(randn((2, H.MAX_NORM_COLS + 1), "bf16", 3))
+    with pytest.raises(TypeError):
+        H.himuon_layer_norm_grad(x, w, r.stats.double(), x)
+    with pytest.raises(ValueError):
+        H.himuon_layer_norm_grad(x, w, r.stats[:3], x)
+    with pytest.raises(TypeError):
+        H.himuon_layer_norm_grad(x, w, r.stats, x.float())
+    with pytest.raises(H.HimuonError):
+        H.himuon_layer_norm_grad(x, w, r.stats, x[:3])
+    with pytest.raises(H.HimuonError):   # one vector for both sums
+        v = w.clone()
+        H.himuon_layer_norm_grad(x, w, r.stats, r.y, dweight=v, dbias=v)
+    with pytest.raises(H.HimuonError):   # a workspace that is too small
+        H.himuon_layer_norm_grad(x, w, r.stats, r.y, workspace=torch.empty(16, device=cuda))
