@@ -630,15 +630,16 @@ def _activation(act):
 
 
 def _filled(t, rows, cols, like, what):
-    """t, or a new tensor, of the given shape, with the type and place of `like`."""
-    import torch
+    """t, or a new tensor, of the given shape, with the type and place of `like`, and
+    its descriptor."""
     if t is None:
-        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+        t = like.new_empty((rows, cols))
+        return t, himuon_matrix_t(t.data_ptr(), rows, cols, cols)
     if t.dtype != like.dtype:
         raise TypeError(f"{what} must have the operands' dtype")
     if t.shape != (rows, cols) or t.device != like.device:
         raise ValueError(f"{what} must be of shape {(rows, cols)}, on the operands' GPU")
-    return t
+    return t, _rows(t)
 
 
 def himuon_grouped_gated_mm(x, w, ends, act: str = "silu", keep=False, out=None, stream=None) -> Gated:
@@ -660,12 +661,11 @@ def himuon_grouped_gated_mm(x, w, ends, act: str = "silu", keep=False, out=None,
     code = _activation(act)
     with _placed(x.device, stream) as s:
         M = x.shape[0]
-        h = _filled(out, M, N2 // 2, x, "out")
+        h, dh = _filled(out, M, N2 // 2, x, "out")
         pre = dp = None
         if keep is not False and keep is not None:
-            pre = _filled(None if keep is True else keep, M, N2, x, "keep")
-            dp = _rows(pre)
-        dx, dh = _rows(x), _rows(h)
+            pre, dp = _filled(None if keep is True else keep, M, N2, x, "keep")
+        dx = _rows(x)
         _check(lib.himuon_grouped_gated_mm(ctypes.byref(dx), w.array, w.n, int(w.transposed), _ends(ends, w.n, x.device),
                                            ctypes.byref(dh), None if dp is None else ctypes.byref(dp), code,
                                            _dtype_code(x), s), "himuon_grouped_gated_mm")
@@ -690,12 +690,11 @@ def himuon_grouped_gated_mm_grad(dy, w, ends, pre, act: str = "silu", hidden=Fal
     code = _activation(act)
     with _placed(dy.device, stream) as s:
         M = dy.shape[0]
-        grad = _filled(out, M, 2 * N, dy, "out")
+        grad, dg = _filled(out, M, 2 * N, dy, "out")
         h = dh = None
         if hidden is not False and hidden is not None:
-            h = _filled(None if hidden is True else hidden, M, N, dy, "hidden")
-            dh = _rows(h)
-        dd, dp, dg = _rows(dy), _rows(pre), _rows(grad)
+            h, dh = _filled(None if hidden is True else hidden, M, N, dy, "hidden")
+        dd, dp = _rows(dy), _rows(pre)
         _check(lib.himuon_grouped_gated_mm_grad(ctypes.byref(dd), w.array, w.n, int(w.transposed),
                                                 _ends(ends, w.n, dy.device), ctypes.byref(dp), ctypes.byref(dg),
                                                 None if dh is None else ctypes.byref(dh), code, _dtype_code(dy), s),
@@ -722,7 +721,7 @@ def _columns(t, x, what):
         raise TypeError(f"{what} must have the rows' dtype")
     if t.shape != (x.shape[1],) or not t.is_contiguous() or t.device != x.device:
         raise ValueError(f"{what} must be contiguous with one entry per column, on the rows' GPU")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def himuon_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True, out=None,
@@ -735,12 +734,11 @@ def himuon_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool 
     _need_gpu(x)
     dx = _rows(x)
     with _placed(x.device, stream) as s:
-        y = _filled(out, x.shape[0], x.shape[1], x, "out")
-        st = torch.empty((x.shape[0], 2), dtype=torch.float32, device=x.device) if stats else None
-        dy = _rows(y)
+        y, dy = _filled(out, dx.rows, dx.cols, x, "out")
+        st = torch.empty((dx.rows, 2), dtype=torch.float32, device=x.device) if stats else None
         _check(lib.himuon_layer_norm(ctypes.byref(dx), _columns(weight, x, "weight"), _columns(bias, x, "bias"), eps,
-                                     ctypes.byref(dy), None if st is None else ctypes.c_void_p(st.data_ptr()),
-                                     _dtype_code(x), s), "himuon_layer_norm")
+                                     ctypes.byref(dy), None if st is None else st.data_ptr(), _dtype_code(x), s),
+               "himuon_layer_norm")
     return Normed(y, st)
 
 
@@ -766,10 +764,10 @@ def himuon_layer_norm_grad(x, weight, stats, dy, dx=True, dweight=True, dbias=Tr
     sp = _vector(stats, N, "stats", x.device, 2)
     wanted = lambda t: t is not None and t is not False
     with _placed(x.device, stream) as s:
-        gx = _filled(None if dx is True else dx, N, D, x, "dx") if wanted(dx) else None
-        vec = lambda t: torch.empty(D, dtype=x.dtype, device=x.device) if t is True else t
+        gx, c = _filled(None if dx is True else dx, N, D, x, "dx") if wanted(dx) else (None, None)
+        vec = lambda t: x.new_empty(D) if t is True else t
         gw, gb = vec(dweight) if wanted(dweight) else None, vec(dbias) if wanted(dbias) else None
-        a, b, c = _rows(x), _rows(dy), None if gx is None else _rows(gx)
+        a, b = _rows(x), _rows(dy)
         code = _dtype_code(x)
         keep, wp, wb = None, None, 0
         if gw is not None or gb is not None:
