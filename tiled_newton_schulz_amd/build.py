@@ -19,8 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libhimuon.so")
 OBJDIR = os.path.join(ROOT, "_build")
-SOURCES = ["resident.hip", "resident32.hip", "resident_f32.hip", "resident256.hip", "stepwise.hip", "pair_stats.hip", "static_scratch.hip", "grouped.hip", "gated.hip", "logits.hip", "norm.hip", "adamw.hip", "api.cpp", "api_model.cpp",
-           "api_train.cpp"]
+SOURCES = ["resident.hip", "resident32.hip", "resident_f32.hip", "resident256.hip", "stepwise.hip", "pair_stats.hip",
+           "static_scratch.hip", "grouped.hip", "gated.hip", "gated_grad.hip", "logits.hip", "norm.hip", "adamw.hip", "api.cpp",
+           "api_model.cpp", "api_train.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -96,10 +96,10 @@ himuon_status_t grouped_mm(const himuon_matrix_t* X, const himuon_matrix_t* W, i
 himuon_status_t activation(himuon_activation_t act, GroupedArgs& a) {
     const float slope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
     switch (act) {
-        case HIMUON_SILU: a.k0 = 1.f; return HIMUON_OK;
-        case HIMUON_GELU: a.erf = 1; return HIMUON_OK;
-        case HIMUON_GELU_TANH: a.k0 = slope; a.k1 = slope * 0.044715f; return HIMUON_OK;
-        case HIMUON_RELU: a.k0 = 1e30f; a.k2 = -200.f; return HIMUON_OK;   // 0 or 1
+        case HIMUON_SILU: a.kind = GateKind::Linear; a.k0 = 1.f; return HIMUON_OK;
+        case HIMUON_GELU: a.kind = GateKind::Erf; return HIMUON_OK;
+        case HIMUON_GELU_TANH: a.kind = GateKind::Cubic; a.k0 = slope; a.k1 = slope * 0.044715f; return HIMUON_OK;
+        case HIMUON_RELU: a.kind = GateKind::Linear; a.k0 = 1e30f; a.k2 = -200.f; return HIMUON_OK;   // 0 or 1
     }
     return HIMUON_ERR_UNSUPPORTED;
 }
@@ -160,7 +160,8 @@ himuon_status_t gated(Gate gate, const himuon_matrix_t* X, const himuon_matrix_t
     for (int32_t e = 0; e < n; ++e) a.vec = a.vec && chunked(W[e]);
     if (!all_launches(a, grouped_mm_fits)) return HIMUON_ERR_LAYOUT;
     return each_launch(a, W, n, [&] {
-        const hipError_t e = launch_grouped_gated(a, stored_nk, reinterpret_cast<hipStream_t>(stream));
+        const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        const hipError_t e = forward ? launch_grouped_gated(a, s) : launch_grouped_gated_grad(a, s);
         return e == hipSuccess ? HIMUON_OK : hip_fail(e);
     });
 }

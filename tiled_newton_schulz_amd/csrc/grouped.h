@@ -1,5 +1,5 @@
 // Internal declarations of the experts' products (api_model.cpp,
-// grouped.hip, gated.hip).
+// grouped.hip, gated.hip, gated_grad.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -20,6 +20,10 @@ enum class Gate : int32_t {
     Forward,    // W_e holds the gate's and the up projection: Y = act(G) * U
     Grad        // X W_e^T is the gradient of that Y: gradients of G and U
 };
+
+// What s is in act(g) = g s(g): sigmoid(k0 g + k2), sigmoid(k0 g + k1 g^3), or the
+// integral of the normal distribution.
+enum class GateKind : int32_t { Linear, Cubic, Erf };
 
 // One launch of Y = X W_e (or X W_e^T) or of G_e = X_e^T D_e.
 struct GroupedArgs {
@@ -43,8 +47,8 @@ struct GroupedArgs {
     void* p;                 // [G | U], M x 2N: written by Forward (or null), read by Grad
     void* h;                 // Grad: H, or null
     int64_t p_ld, h_ld;
-    float k0, k1, k2;        // act(g) = g s(g): s = sigmoid(k0 g + k1 g^3 + k2),
-    int32_t erf;             // or the normal distribution's integral
+    GateKind kind;           // act(g) = g s(g), with k0, k1, k2
+    float k0, k1, k2;
     void* w[kExperts];       // product: weights; weight gradient: results
     int64_t w_ld[kExperts];
 };
@@ -66,7 +70,8 @@ int32_t grouped_wgrad_parts(const GroupedArgs& a);
 int64_t grouped_wgrad_part_bytes(const GroupedArgs& a);
 hipError_t launch_grouped_mm(const GroupedArgs& a, bool trans_w, hipStream_t s);
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
-// a.gate != None; trans_w: W_e is stored N x K (2N x K).
-hipError_t launch_grouped_gated(const GroupedArgs& a, bool trans_w, hipStream_t s);
+// a.gate == Forward; a.gate == Grad.
+hipError_t launch_grouped_gated(const GroupedArgs& a, hipStream_t s);
+hipError_t launch_grouped_gated_grad(const GroupedArgs& a, hipStream_t s);
 
 }  // namespace himuon

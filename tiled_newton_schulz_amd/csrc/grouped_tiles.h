@@ -1,5 +1,5 @@
 // Device code of the experts' products and of the gated block (grouped.hip,
-// gated.hip): tiles of ragged groups of rows.
+// gated.hip, gated_grad.hip): tiles of ragged groups of rows.
 //
 // One launch covers up to 255 experts.  A workgroup takes its output tile from
 // a linear id: every wave reads the experts' end rows (four slots a lane),
@@ -328,32 +328,45 @@ __device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename I
 // sigmoid(k0 g + k1 g^3); relu: s is 0 or 1, as a sigmoid so steep (10^30 g - 200) that
 // only gates below 10^-27 tell the two apart; gelu (erf): the normal distribution's
 // integral.  FAST: the hardware's exp2 and reciprocal, a few 2^-23 of the result (for
-// results rounded to bf16).  No branches: with one for each element the gradient's
-// results took longer than the products.
+// results rounded to bf16).  The kinds are kernels of their own (told apart for each
+// element, gelu's gradient took 357 instead of 316 us), and silu's and relu's has no
+// branches and no cubic: with both, results of short products took 3 to 8 % longer.
 __device__ __forceinline__ float gate_inner(float g) { return __builtin_amdgcn_fmed3f(g, -1e18f, 1e18f); }
-template <bool ERF, bool FAST>
+template <GateKind KIND, bool FAST>
 __device__ __forceinline__ float gate_share(const GroupedArgs& a, float g) {
-    if constexpr (ERF) {
-        return 0.5f * erfcf(g * -0.70710678118654752f);
+    if constexpr (KIND == GateKind::Erf) return 0.5f * erfcf(g * -0.70710678118654752f);
+    float z;
+    if constexpr (KIND == GateKind::Linear) {
+        z = g * a.k0 + a.k2;
     } else {
-        const float x = gate_inner(g), z = x * (a.k0 + a.k1 * x * x) + a.k2;   // (of finite terms)
-        const float s = FAST ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f))
-                             : 1.f / (1.f + expf(-z));
-        return g != g ? g : s;
+        const float x = gate_inner(g);
+        z = g != g ? g : x * (a.k0 + a.k1 * x * x);   // (of finite terms)
     }
+    if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+    return 1.f / (1.f + expf(-z));
 }
 // (where s is 0, -inf gives 0)
 __device__ __forceinline__ float gate_act(float g, float s) { return fmaxf(g, -3.402823466e38f) * s; }
 // act'(g) = s + g s' (far out, where s' has underflowed, s: 0 or 1)
-template <bool ERF, bool FAST>
+template <GateKind KIND, bool FAST>
 __device__ __forceinline__ float gate_slope(const GroupedArgs& a, float g, float s) {
     const float x = gate_inner(g);
-    if constexpr (ERF) {
+    if constexpr (KIND == GateKind::Linear) {
+        return s + x * (s - s * s) * a.k0;
+    } else if constexpr (KIND == GateKind::Erf) {
         const float e = FAST ? __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f) : expf(-0.5f * x * x);
         return s + x * (e * 0.39894228040143268f);
     } else {
         return s + x * (s - s * s) * (a.k0 + 3.f * a.k1 * x * x);
     }
+}
+
+// f(kind as a constant).
+template <typename F>
+__device__ __forceinline__ void with_kind(const GroupedArgs& a, F f) {
+    if (a.kind == GateKind::Linear) f(std::integral_constant<GateKind, GateKind::Linear>{});
+    else if (a.kind == GateKind::Cubic) f(std::integral_constant<GateKind, GateKind::Cubic>{});
+    else f(std::integral_constant<GateKind, GateKind::Erf>{});
 }
 
 // A B of one tile (operands exchanged in the MFMA, so that a lane holds runs of
@@ -505,13 +518,11 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_gated_staged(const Groupe
             if (br >= A.side) continue;
             const f32x16 g = acc[i][0];
             f32x16 h;
-            const auto gate = [&](auto erf) __attribute__((always_inline)) {
+            with_kind(a, [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    h[e] = gate_act(g[e], gate_share<decltype(erf)::value, DT == 0>(a, g[e])) * up[i][e];
-            };
-            if (a.erf) gate(std::true_type{});
-            else gate(std::false_type{});
+                    h[e] = gate_act(g[e], gate_share<decltype(kind)::value, DT == 0>(a, g[e])) * up[i][e];
+            });
             BlockIo<DT>::put(h, scratch, reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0, a.y_ld, A.side, B.side, br, bc);
             if (a.p == nullptr) continue;
             T* P = reinterpret_cast<T*>(a.p) + m0 * a.p_ld + n0;
@@ -554,18 +565,16 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_gated_grad_staged(const G
                 if (owned) {
                     const f32x16 g = BlockIo<DT>::get(scratch, P, a.p_ld, A.side, B.side, br, bc);
                     const f32x16 u = BlockIo<DT>::get(scratch, P + a.ndim, a.p_ld, A.side, B.side, br, bc);
-                    const auto gate = [&](auto erf) __attribute__((always_inline)) {
-                        constexpr bool ERF = decltype(erf)::value;
+                    with_kind(a, [&](auto kind) __attribute__((always_inline)) {
+                        constexpr GateKind KIND = decltype(kind)::value;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float s = gate_share<ERF, DT == 0>(a, g[e]), act = gate_act(g[e], s);
-                            dg[e] = acc[i][j][e] * u[e] * gate_slope<ERF, DT == 0>(a, g[e], s);
+                            const float s = gate_share<KIND, DT == 0>(a, g[e]), act = gate_act(g[e], s);
+                            dg[e] = acc[i][j][e] * u[e] * gate_slope<KIND, DT == 0>(a, g[e], s);
                             du[e] = acc[i][j][e] * act;
                             h[e] = act * u[e];
                         }
-                    };
-                    if (a.erf) gate(std::true_type{});
-                    else gate(std::false_type{});
+                    });
                 }
                 BlockIo<DT>::put(dg, scratch, D, a.y_ld, A.side, B.side, br, bc);
                 BlockIo<DT>::put(du, scratch, D + a.ndim, a.y_ld, A.side, B.side, br, bc);
@@ -935,7 +944,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const void* base, in
 }
 // A gated tile's result: acc[i][0] is the gate's and acc[i][1] the up projection's
 // block of the same rows and columns.  24 stores with [G | U], else 8.
-template <int AM, bool KEEP, bool ERF>
+template <int AM, bool KEEP, GateKind KIND>
 __device__ __forceinline__ void put_gated(const GroupedArgs& a, const f32x16 (&acc)[AM][2], unsigned short* scratch,
                                           int64_t m0, int n0, int rows, int cols, int wm, int wn, int lane) {
     asm volatile("" : "+v"(lane));   // (what follows from it is not kept in registers over the products)
@@ -951,7 +960,7 @@ __device__ __forceinline__ void put_gated(const GroupedArgs& a, const f32x16 (&a
         const f32x16 &g = acc[i < AM ? i : 0][0], &u = acc[i < AM ? i : 0][1];
         f32x16 v;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = gate_act(g[e], gate_share<ERF, true>(a, g[e])) * u[e];
+        for (int e = 0; e < 16; ++e) v[e] = gate_act(g[e], gate_share<KIND, true>(a, g[e])) * u[e];
         const uint32_t hl = (uint32_t)a.y_ld * 2u;
         store_block(packed(v), scratch, tile_rows(a.y, m0 * a.y_ld + n0, a.y_ld, i, rows, cols),
                     in ? r0 * hl + c0 * 2u : kNowhere, hl * 16u, lane);
@@ -967,7 +976,7 @@ __device__ __forceinline__ void put_gated(const GroupedArgs& a, const f32x16 (&a
 // A tile of the gate's gradient, acc the gradient of H.  G and U of kAhead blocks are
 // on their way while one is worked on.  At least 16 loads and stores in all, whatever
 // the tile's size.
-template <int AM, int FN, bool ERF>
+template <int AM, int FN, GateKind KIND>
 __device__ __forceinline__ void put_gate_grad(const GroupedArgs& a, const f32x16 (&acc)[AM][FN], unsigned short* scratch,
                                               int64_t m0, int n0, int rows, int cols, bool owned, int wm, int wn, int lane) {
     asm volatile("" : "+v"(lane));   // (what follows from it is not kept in registers over the products)
@@ -1006,9 +1015,9 @@ __device__ __forceinline__ void put_gate_grad(const GroupedArgs& a, const f32x16
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const float x = o ? hi_f(g.w[m][k]) : lo_f(g.w[m][k]), y = o ? hi_f(u.w[m][k]) : lo_f(u.w[m][k]);
-                    const float d = dh[4 * m + 2 * k + o], s = gate_share<ERF, true>(a, x), act = gate_act(x, s);
+                    const float d = dh[4 * m + 2 * k + o], s = gate_share<KIND, true>(a, x), act = gate_act(x, s);
                     hv[o] = act * y;
-                    dg[o] = d * y * gate_slope<ERF, true>(a, x, s);
+                    dg[o] = d * y * gate_slope<KIND, true>(a, x, s);
                     du[o] = d * act;
                 }
                 v.w[m][k] = pack2(hv[0], hv[1]);
@@ -1183,7 +1192,7 @@ __device__ __forceinline__ int share(const GroupTable& t, int x) {
 }
 
 // GATE: the two passes of a gated block; KEEP: the forward one also stores [G | U].
-template <int MODE, Gate GATE = Gate::None, bool KEEP = false, bool ERF = false>
+template <int MODE, Gate GATE = Gate::None, bool KEEP = false, GateKind KIND = GateKind::Linear>
 __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const int most) {
     constexpr bool AK = MODE != 2, BKK = MODE == 1;   // operands stored along k
     constexpr bool PAIR = GATE == Gate::Forward;
@@ -1268,8 +1277,8 @@ __global__ __launch_bounds__(512) void grouped_big(const GroupedArgs a, const in
         unsigned short* mine = scratch + wave * kScratch;
         const int64_t m0 = (int64_t)(C >> 32);
         const int n0 = (int)(uint32_t)C;
-        if constexpr (PAIR) put_gated<AM, KEEP, ERF>(a, acc, mine, m0, n0, rows, cols, wm, wn, lane);
-        else put_gate_grad<AM, FN, ERF>(a, acc, mine, m0, n0, rows, cols, kd > 0, wm, wn, lane);
+        if constexpr (PAIR) put_gated<AM, KEEP, KIND>(a, acc, mine, m0, n0, rows, cols, wm, wn, lane);
+        else put_gate_grad<AM, FN, KIND>(a, acc, mine, m0, n0, rows, cols, kd > 0, wm, wn, lane);
     };
     int after = 0;   // the tile's first step comes after another tile's
     int p = 0;       // parity of the step
@@ -1394,7 +1403,7 @@ constexpr int kThinRows = 16, kThinCols = 64, kRing = 4, kThinK = 32;
 // projection's, in two panels (one workgroup a CU, as many bytes in flight), or, where
 // those tiles are too few, WIDE = 32 of each as the 64 of one panel (along i: the first
 // and the last four chunks of a row).
-template <bool WT, Gate GATE = Gate::None, bool ERF = false, int WIDE = kThinCols>
+template <bool WT, Gate GATE = Gate::None, GateKind KIND = GateKind::Linear, int WIDE = kThinCols>
 __global__ __launch_bounds__(256) void grouped_mm_thin(const GroupedArgs a) {
     constexpr bool PAIR = GATE == Gate::Forward, MIXED = PAIR && WIDE < kThinCols;
     constexpr int kWide = WIDE;                         // columns of a tile's result
@@ -1517,7 +1526,7 @@ __global__ __launch_bounds__(256) void grouped_mm_thin(const GroupedArgs a) {
         const f32x4 u = sum(c + kWide);
         f32x4 h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = gate_act(v[e], gate_share<ERF, true>(a, v[e])) * u[e];
+        for (int e = 0; e < 4; ++e) h[e] = gate_act(v[e], gate_share<KIND, true>(a, v[e])) * u[e];
         put(a.y, a.y_ld, c, h);
         if (a.p != nullptr) {
             put(a.p, a.p_ld, c, v);
@@ -1531,8 +1540,8 @@ __global__ __launch_bounds__(256) void grouped_mm_thin(const GroupedArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float g = (e & 1) ? hi_f(gw[e >> 1]) : lo_f(gw[e >> 1]), u = (e & 1) ? hi_f(uw[e >> 1]) : lo_f(uw[e >> 1]);
-                const float s = gate_share<ERF, true>(a, g), act = gate_act(g, s);
-                dg[e] = v[e] * u * gate_slope<ERF, true>(a, g, s);
+                const float s = gate_share<KIND, true>(a, g), act = gate_act(g, s);
+                dg[e] = v[e] * u * gate_slope<KIND, true>(a, g, s);
                 du[e] = v[e] * act;
                 h[e] = act * u;
             }
