@@ -185,6 +185,42 @@ struct Staged {
             r[j] = u32x4{(unsigned)w[0], (unsigned)(w[0] >> 32), (unsigned)w[1], (unsigned)(w[1] >> 32)};
         }
     }
+    // The same for steps that k fills, without a branch (the compiler waits for all loads
+    // where ways of control that have loaded differently much meet, so that only one step
+    // could be on its way): chunks outside the tile are loaded from somewhere inside, as
+    // what they hold reaches no result.  Rows have to be a chunk wide.
+    __device__ __forceinline__ bool plain() const { return ALONG_K || before + row_end(0) >= EPC; }
+    struct Plain {
+        const T* q[NCH];
+        int64_t move;
+    };
+    __device__ __forceinline__ Plain plain_start() const {
+        const int row0 = tid() / CPR, c0 = (tid() % CPR) * EPC;
+        Plain f;
+        f.move = ALONG_K ? BK : BK * ld;
+        int64_t c = c0;
+        if (!ALONG_K) {
+            const int end = row_end(0);
+            c = PAIR && in_half(c0) < side ? stored(c0) : PAIR ? 0 : c0;
+            c -= max((int)min(c, (int64_t)end) + EPC - end, 0);   // (from the row's end on: its last chunk)
+            c = min(c, (int64_t)end - EPC);
+        }
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const int row = row0 + j * ROWS;
+            const int in = ALONG_K ? (PAIR ? in_half(row) : row) : 0;
+            const int64_t at = !ALONG_K ? row : in >= side ? 0 : PAIR ? stored(row) : row;
+            f.q[j] = p + at * ld + c;
+        }
+        return f;
+    }
+    __device__ __forceinline__ static void plain_load(Plain& f, u32x4 (&r)[NCH]) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            r[j] = reinterpret_cast<const Loose16*>(f.q[j])->v;
+            f.q[j] += f.move;
+        }
+    }
     // stores the chunks that load(k0, r) has loaded
     __device__ __forceinline__ void put(int k0, T* s, u32x4 (&r)[NCH]) const {
         const int c0 = (tid() % CPR) * EPC, col = PAIR && !ALONG_K ? (int)stored(c0) : c0;
@@ -275,26 +311,50 @@ struct BlockIo {
             }
         }
     }
-    // the other way: a block of C into the lanes that hold its sums (zeros outside)
-    __device__ __forceinline__ static f32x16 get(T* scratch, const T* C, int64_t ldc, int rows, int cols, int br, int bc) {
-        const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+    // The other way, in two parts: a block of C's rows into registers, without a branch
+    // (chunks outside are loaded from somewhere inside) ...
+    struct Fetched {
+        u32x4 w[32 / RPP];
+    };
+    // before, behind: elements of C's rows in memory before column 0, and from there on
+    __device__ __forceinline__ static Fetched fetch(const T* C, int64_t ldc, int64_t before, int64_t behind, int rows,
+                                                    int br, int bc) {
+        const int lane = threadIdx.x & 63;
+        const int64_t col = min((int64_t)(bc + lane % CPR * EPC), behind);
+        const int over = (int)max(col + EPC - behind, (int64_t)0);
+        Fetched f;
 #pragma unroll
         for (int p = 0; p < 32 / RPP; ++p) {
-            const int r = p * RPP + lane / CPR, c = lane % CPR, col = bc + c * EPC;
-            u32x4 w = {0, 0, 0, 0};
-            const T* from = C + (br + r) * ldc + col;
-            if (br + r < rows && col + EPC <= cols) {
-                w = reinterpret_cast<const Loose16*>(from)->v;
-            } else if (br + r < rows) {
+            const T* from = C + min(br + p * RPP + lane / CPR, rows - 1) * ldc + col;
+            if (before + behind >= EPC) {
+                f.w[p] = reinterpret_cast<const Loose16*>(from - over)->v;
+            } else {   // rows narrower than a chunk
+                f.w[p] = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int e = 0; e < EPC - 1; ++e)
-                    if (col + e < cols) {
-                        if constexpr (DT == 0) w[e >> 1] |= (unsigned)from[e] << (16 * (e & 1));
-                        else w[e] = __float_as_uint(from[e]);
+                    if (e < EPC - over) {
+                        if constexpr (DT == 0) f.w[p][e >> 1] |= (unsigned)from[e] << (16 * (e & 1));
+                        else f.w[p][e] = __float_as_uint(from[e]);
                     }
             }
-            *reinterpret_cast<u32x4*>(at(scratch, r, c)) = w;
         }
+        if (over > 0 && over < EPC && before + behind >= EPC) {
+            const int by = over * (int)sizeof(T) * 8;   // 16 .. 112 bits
+#pragma unroll
+            for (int p = 0; p < 32 / RPP; ++p) {
+                const uint64_t lo = f.w[p][0] | (uint64_t)f.w[p][1] << 32, hi = f.w[p][2] | (uint64_t)f.w[p][3] << 32;
+                const uint64_t a = by < 64 ? lo >> by | hi << (64 - by) : hi >> (by - 64), b = by < 64 ? hi >> by : 0;
+                f.w[p] = u32x4{(unsigned)a, (unsigned)(a >> 32), (unsigned)b, (unsigned)(b >> 32)};
+            }
+        }
+        return f;
+    }
+    // ... and from there into the lanes that hold such a block's sums.
+    __device__ __forceinline__ static f32x16 spread(const Fetched& f, T* scratch) {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, gl = lane >> 5;
+#pragma unroll
+        for (int p = 0; p < 32 / RPP; ++p)
+            *reinterpret_cast<u32x4*>(at(scratch, p * RPP + lane / CPR, lane % CPR)) = f.w[p];
         f32x16 v;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -390,43 +450,91 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
     for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < F; ++j) acc[i][j] = f32x16{};
-    if (A.kd > 0) {
+    const auto multiply = [&](int cur) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < BK / SUB; ++kk) {
+            u32x4 av[F], bv[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) av[i] = Staged<DT, AK, EDGE>::frag(sa[cur], wm * WE + i * 32, kk);
+#pragma unroll
+            for (int j = 0; j < F; ++j) bv[j] = Staged<DT, BKK, EDGE>::frag(sb[cur], wn * WE + j * 32, kk);
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int j = 0; j < F; ++j) {
+                    if constexpr (DT == 0) {
+                        acc[i][j] = mfma32w(bv[j], av[i], acc[i][j]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                __uint_as_float(bv[j][e]), __uint_as_float(av[i][e]), acc[i][j], 0, 0, 0);
+                    }
+                }
+        }
+    };
+    int from = 0;   // k that the loop below starts at
+    if constexpr (DT == 0 && EDGE == 128) {
+        // two steps on their way (one expert of 4095 x 4097, 4096 rows 274 -> 251 us, its
+        // weight gradient 275 -> 241; at 5 and 8 steps 15 -> 16.6 and 19.5 -> 21.8, so from 12)
+        const int whole = A.kd / BK;
+        if (whole >= 12 && A.plain() && B.plain()) {
+            auto fa = A.plain_start();
+            auto fb = B.plain_start();
+            u32x4 ra[2][Staged<DT, AK, EDGE>::NCH], rb[2][Staged<DT, BKK, EDGE>::NCH];
+            const auto load = [&](int p) __attribute__((always_inline)) {
+                A.plain_load(fa, ra[p]);
+                B.plain_load(fb, rb[p]);
+            };
+            const auto put = [&](int step, int p) __attribute__((always_inline)) {
+                A.put(step * BK, sa[p], ra[p]);
+                B.put(step * BK, sb[p], rb[p]);
+            };
+            load(0);
+            load(1);
+            put(0, 0);
+            __syncthreads();
+            int i = 0;
+            for (; i + 3 < whole; i += 2) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    load(p);                      // step i + p + 2
+                    if (work) multiply(p);
+                    put(i + p + 1, p ^ 1);
+                    __syncthreads();
+                }
+            }
+            // two or three steps left, of which step i + 2 is not on its way
+            const bool three = i + 2 < whole;
+            if (three) load(0);
+            if (work) multiply(0);
+            put(i + 1, 1);
+            __syncthreads();
+            if (work) multiply(1);
+            if (three) put(i + 2, 0);
+            __syncthreads();
+            if (three) {
+                if (work) multiply(0);
+                __syncthreads();
+            }
+            from = whole * BK;
+        }
+    }
+    if (A.kd > from) {
         u32x4 ra[Staged<DT, AK, EDGE>::NCH], rb[Staged<DT, BKK, EDGE>::NCH];
-        A.load(part * BK, ra);   // past kd: zeros
-        B.load(part * BK, rb);
-        A.put(part * BK, sa[0], ra);
-        B.put(part * BK, sb[0], rb);
+        A.load(from + part * BK, ra);   // past kd: zeros
+        B.load(from + part * BK, rb);
+        A.put(from + part * BK, sa[0], ra);
+        B.put(from + part * BK, sb[0], rb);
         __syncthreads();
-        for (int k0 = 0, cur = 0; k0 < A.kd; k0 += SPLIT * BK, cur ^= 1) {   // the same number of steps in every part
+        for (int k0 = from, cur = 0; k0 < A.kd; k0 += SPLIT * BK, cur ^= 1) {   // the same number of steps in every part
             const int next = k0 + (SPLIT + part) * BK;
             const bool more = next < A.kd;
             if (more) {
                 A.load(next, ra);
                 B.load(next, rb);
             }
-            if (work && k0 + part * BK < A.kd) {
-#pragma unroll
-                for (int kk = 0; kk < BK / SUB; ++kk) {
-                    u32x4 av[F], bv[F];
-#pragma unroll
-                    for (int i = 0; i < F; ++i) av[i] = Staged<DT, AK, EDGE>::frag(sa[cur], wm * WE + i * 32, kk);
-#pragma unroll
-                    for (int j = 0; j < F; ++j) bv[j] = Staged<DT, BKK, EDGE>::frag(sb[cur], wn * WE + j * 32, kk);
-#pragma unroll
-                    for (int i = 0; i < F; ++i)
-#pragma unroll
-                        for (int j = 0; j < F; ++j) {
-                            if constexpr (DT == 0) {
-                                acc[i][j] = mfma32w(bv[j], av[i], acc[i][j]);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                        __uint_as_float(bv[j][e]), __uint_as_float(av[i][e]), acc[i][j], 0, 0, 0);
-                            }
-                        }
-                }
-            }
+            if (work && k0 + part * BK < A.kd) multiply(cur);
             if (more) {
                 A.put(next, sa[cur ^ 1], ra);
                 B.put(next, sb[cur ^ 1], rb);
@@ -555,33 +663,39 @@ __global__ __launch_bounds__(256 * SPLIT) void grouped_gated_grad_staged(const G
     staged_tile<DT, true, WT, EDGE, SPLIT>(A, B, [&](const auto& acc, int wave, T* scratch) __attribute__((always_inline)) {
         const T* P = reinterpret_cast<const T*>(a.p) + m0 * a.p_ld + n0;
         T* D = reinterpret_cast<T*>(a.y) + m0 * a.y_ld + n0;
+        const int r0 = (wave >> 1) * (EDGE / 2), c0 = (wave & 1) * (EDGE / 2);
+        if (r0 >= A.side || c0 >= B.side) return;
+        using Io_ = BlockIo<DT>;
+        typename Io_::Fetched gf[2], uf[2];   // of the block worked on, and of the next one
+        const auto fetch = [&](int b) __attribute__((always_inline)) {
+            const int br = r0 + b / F * 32, bc = c0 + b % F * 32;
+            gf[b & 1] = Io_::fetch(P, a.p_ld, n0, 2 * (int64_t)a.ndim - n0, A.side, br, bc);
+            uf[b & 1] = Io_::fetch(P + a.ndim, a.p_ld, (int64_t)a.ndim + n0, (int64_t)a.ndim - n0, A.side, br, bc);
+        };
+        fetch(0);
 #pragma unroll
-        for (int i = 0; i < F; ++i)
+        for (int b = 0; b < F * F; ++b) {
+            const int i = b / F, j = b % F, br = r0 + i * 32, bc = c0 + j * 32;
+            if (b + 1 < F * F) fetch(b + 1);
+            const f32x16 g = Io_::spread(gf[b & 1], scratch), u = Io_::spread(uf[b & 1], scratch);
+            if (br >= A.side || bc >= B.side) continue;
+            f32x16 dg = {}, du = {}, h = {};
+            if (owned)   // else rows of no expert: zeros for whatever P holds
+                with_kind(a, [&](auto kind) __attribute__((always_inline)) {
+                    constexpr GateKind KIND = decltype(kind)::value;
 #pragma unroll
-            for (int j = 0; j < F; ++j) {
-                const int br = (wave >> 1) * (EDGE / 2) + i * 32, bc = (wave & 1) * (EDGE / 2) + j * 32;
-                if (br >= A.side || bc >= B.side) continue;
-                f32x16 dg = {}, du = {}, h = {};
-                if (owned) {
-                    const f32x16 g = BlockIo<DT>::get(scratch, P, a.p_ld, A.side, B.side, br, bc);
-                    const f32x16 u = BlockIo<DT>::get(scratch, P + a.ndim, a.p_ld, A.side, B.side, br, bc);
-                    with_kind(a, [&](auto kind) __attribute__((always_inline)) {
-                        constexpr GateKind KIND = decltype(kind)::value;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float s = gate_share<KIND, DT == 0>(a, g[e]), act = gate_act(g[e], s);
-                            dg[e] = acc[i][j][e] * u[e] * gate_slope<KIND, DT == 0>(a, g[e], s);
-                            du[e] = acc[i][j][e] * act;
-                            h[e] = act * u[e];
-                        }
-                    });
-                }
-                BlockIo<DT>::put(dg, scratch, D, a.y_ld, A.side, B.side, br, bc);
-                BlockIo<DT>::put(du, scratch, D + a.ndim, a.y_ld, A.side, B.side, br, bc);
-                if (a.h != nullptr)
-                    BlockIo<DT>::put(h, scratch, reinterpret_cast<T*>(a.h) + m0 * a.h_ld + n0, a.h_ld, A.side, B.side, br,
-                                     bc);
-            }
+                    for (int e = 0; e < 16; ++e) {
+                        const float s = gate_share<KIND, DT == 0>(a, g[e]), act = gate_act(g[e], s);
+                        dg[e] = acc[i][j][e] * u[e] * gate_slope<KIND, DT == 0>(a, g[e], s);
+                        du[e] = acc[i][j][e] * act;
+                        h[e] = act * u[e];
+                    }
+                });
+            Io_::put(dg, scratch, D, a.y_ld, A.side, B.side, br, bc);
+            Io_::put(du, scratch, D + a.ndim, a.y_ld, A.side, B.side, br, bc);
+            if (a.h != nullptr)
+                Io_::put(h, scratch, reinterpret_cast<T*>(a.h) + m0 * a.h_ld + n0, a.h_ld, A.side, B.side, br, bc);
+        }
     });
 }
 
