@@ -584,8 +584,8 @@ himuon_status_t himuon_grouped_gated_mm_grad(const himuon_matrix_t* dY, const hi
  *            itself (the same pointer and ld).  N may be 0.
  * weight, bias : device arrays of D elements of type dt, or NULL (1 and 0).
  * eps      : finite, >= 0 (with 0, a row of equal values gives NaN).
- * stats    : device array of N x 2 fp32, written, or NULL: mean and rstd, for
- *            himuon_layer_norm_grad.
+ * stats    : device array of N x 2 fp32, 8-byte aligned, written, or NULL: mean and
+ *            rstd, for himuon_layer_norm_grad.
  * Statistics and sums are fp32 for either type, the variance from the
  * differences to the mean; y is rounded once.  A NaN or infinity makes its row NaN.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (dtype, D above the
