@@ -92,8 +92,9 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int BM, int ntn,
 // Any operand (fp32; bf16 rows and widths that are not whole 16-byte chunks):
 // tiles of 128 x 128 (four waves of 64 x 64 each) or, where those would leave
 // CUs idle, 64 x 64, k in steps of 64 (bf16) or 32 (fp32).  The next step's
-// chunks are loaded into registers while the present one is multiplied from
-// LDS, then stored in the other LDS buffer.  Loads and stores are 16 bytes wide
+// chunks (the next two steps' in products of many) are loaded into registers
+// while the present one is multiplied from LDS, then stored in the other LDS
+// buffer.  Loads and stores are 16 bytes wide
 // at any alignment of the element.  A chunk that reaches past its row's end is
 // loaded from as much further left and shifted (element by element, a load's
 // latency each, the 39 columns of a 4528 x 925 x 39 gradient took 155 instead of
@@ -194,10 +195,11 @@ struct Staged {
         const T* q[NCH];
         int64_t move;
     };
-    __device__ __forceinline__ Plain plain_start() const {
+    // from k0, in steps of `by` k
+    __device__ __forceinline__ Plain plain_start(int k0, int by) const {
         const int row0 = tid() / CPR, c0 = (tid() % CPR) * EPC;
         Plain f;
-        f.move = ALONG_K ? BK : BK * ld;
+        f.move = ALONG_K ? by : by * ld;
         int64_t c = c0;
         if (!ALONG_K) {
             const int end = row_end(0);
@@ -210,7 +212,7 @@ struct Staged {
             const int row = row0 + j * ROWS;
             const int in = ALONG_K ? (PAIR ? in_half(row) : row) : 0;
             const int64_t at = !ALONG_K ? row : in >= side ? 0 : PAIR ? stored(row) : row;
-            f.q[j] = p + at * ld + c;
+            f.q[j] = p + at * ld + c + (ALONG_K ? k0 : k0 * ld);
         }
         return f;
     }
@@ -474,50 +476,49 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
         }
     };
     int from = 0;   // k that the loop below starts at
-    if constexpr (DT == 0 && EDGE == 128) {
-        // two steps on their way (one expert of 4095 x 4097, 4096 rows 274 -> 251 us, its
-        // weight gradient 275 -> 241; at 5 and 8 steps 15 -> 16.6 and 19.5 -> 21.8, so from 12)
-        const int whole = A.kd / BK;
-        if (whole >= 12 && A.plain() && B.plain()) {
-            auto fa = A.plain_start();
-            auto fb = B.plain_start();
-            u32x4 ra[2][Staged<DT, AK, EDGE>::NCH], rb[2][Staged<DT, BKK, EDGE>::NCH];
+    {
+        // Two steps on their way.  In us with one, and with two: one expert of 4095 x 4097, 4096
+        // rows 274 and 251, its weight gradient 275 and 241; 256 rows of 4096 x 1024 23 and 18.5;
+        // 8 experts of 2048 x 1024, 8192 rows in fp32 438 and 400; the weight gradient of 8 of
+        // 512 x 512, 8192 rows 25.0 and 19.9.  (With four in the 64-tiles the same.)  At 5 and 8
+        // steps 15 and 16.6, 19.5 and 21.8, so from 12.
+        constexpr int D = 2;
+        const int whole = A.kd / (SPLIT * BK);   // of each part
+        if (whole * SPLIT >= 12 && whole >= 2 * D && A.plain() && B.plain()) {
+            auto fa = A.plain_start(part * BK, SPLIT * BK);
+            auto fb = B.plain_start(part * BK, SPLIT * BK);
+            u32x4 ra[D][Staged<DT, AK, EDGE>::NCH], rb[D][Staged<DT, BKK, EDGE>::NCH];
             const auto load = [&](int p) __attribute__((always_inline)) {
                 A.plain_load(fa, ra[p]);
                 B.plain_load(fb, rb[p]);
             };
             const auto put = [&](int step, int p) __attribute__((always_inline)) {
-                A.put(step * BK, sa[p], ra[p]);
-                B.put(step * BK, sb[p], rb[p]);
+                A.put((step * SPLIT + part) * BK, sa[p & 1], ra[p % D]);
+                B.put((step * SPLIT + part) * BK, sb[p & 1], rb[p % D]);
             };
-            load(0);
-            load(1);
+#pragma unroll
+            for (int p = 0; p < D; ++p) load(p);
             put(0, 0);
             __syncthreads();
             int i = 0;
-            for (; i + 3 < whole; i += 2) {
+            for (; i + 2 * D - 1 < whole; i += D)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    load(p);                      // step i + p + 2
-                    if (work) multiply(p);
-                    put(i + p + 1, p ^ 1);
+                for (int p = 0; p < D; ++p) {
+                    load(p);                      // step i + p + D
+                    if (work) multiply(p & 1);
+                    put(i + p + 1, p + 1);
                     __syncthreads();
                 }
-            }
-            // two or three steps left, of which step i + 2 is not on its way
-            const bool three = i + 2 < whole;
-            if (three) load(0);
-            if (work) multiply(0);
-            put(i + 1, 1);
-            __syncthreads();
-            if (work) multiply(1);
-            if (three) put(i + 2, 0);
-            __syncthreads();
-            if (three) {
-                if (work) multiply(0);
+            // D to 2 D - 1 steps left, D of them on their way
+#pragma unroll
+            for (int p = 0; p < 2 * D - 1; ++p) {
+                if (i + p >= whole) break;
+                if (i + p + D < whole) load(p % D);
+                if (work) multiply(p & 1);
+                if (i + p + 1 < whole) put(i + p + 1, p + 1);
                 __syncthreads();
             }
-            from = whole * BK;
+            from = whole * SPLIT * BK;
         }
     }
     if (A.kd > from) {
