@@ -476,12 +476,14 @@ __device__ __forceinline__ void staged_tile(const Staged<DT, AK, EDGE>& A, const
         }
     };
     int from = 0;   // k that the loop below starts at
-    {
+    if constexpr (DT == 0 || EDGE == 64 || AK) {
         // Two steps on their way.  In us with one, and with two: one expert of 4095 x 4097, 4096
         // rows 274 and 251, its weight gradient 275 and 241; 256 rows of 4096 x 1024 23 and 18.5;
         // 8 experts of 2048 x 1024, 8192 rows in fp32 438 and 400; the weight gradient of 8 of
         // 512 x 512, 8192 rows 25.0 and 19.9.  (With four in the 64-tiles the same.)  At 5 and 8
-        // steps 15 and 16.6, 19.5 and 21.8, so from 12.
+        // steps 15 and 16.6, 19.5 and 21.8, so from 12.  Not in fp32 weight gradients of 128-tiles:
+        // 8 of 2048 x 2048, 8192 rows 569 and 530, but 23 of 4022 x 968, 50 rows each (two steps,
+        // with nothing but this code in the kernel) 174 and 207.
         constexpr int D = 2;
         const int whole = A.kd / (SPLIT * BK);   // of each part
         if (whole * SPLIT >= 12 && whole >= 2 * D && A.plain() && B.plain()) {
