@@ -204,9 +204,32 @@ __device__ __forceinline__ float largest(const float (&x)[8], bool& odd) {
 // sqrt(v): the hardware's reciprocal root and a Newton step, which leaves nearly every
 // result rounded correctly at two thirds of sqrtf's instructions (arithmetic bounds the
 // step in 8 bits; with the hardware's root alone more codes fell on the wrong side).
+// For v from 2^-96 on: the hardware takes a subnormal v for 0, and further down v - r^2
+// has no bits left.
 __device__ __forceinline__ float root(float v) {
-    const float s = fminf(__builtin_amdgcn_rsqf(v), 1e30f), r = v * s;   // (v = 0: 0, not 0 times infinity)
+    const float s = __builtin_amdgcn_rsqf(v), r = v * s;
     return fmaf(fmaf(-r, r, v), 0.5f * s, r);
+}
+// The same for any v, 0 among them, through a multiple of v.
+__device__ __forceinline__ float root_any(float v) {
+    const bool small = v < 0x1p-96f;
+    const float x = small ? v * 0x1p64f : v, s = fminf(__builtin_amdgcn_rsqf(x), 1e30f), r = x * s;
+    return fmaf(fmaf(-r, r, x), 0.5f * s, r) * (small ? 0x1p-32f : 1.f);
+}
+// r = sqrt(v) of a thread's eight.  A second moment below 2^-96 is rare, but for zeros
+// (weights that no gradient has met), so the way for any v is behind a branch; an
+// element's result is the same bits on either.
+__device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
+    unsigned least = __float_as_uint(v[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) least = min(least, __float_as_uint(v[e]));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = root(v[e]);
+    if (least < 0x0f800000u) {   // 2^-96
+        asm volatile("");   // (not selects that always run)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = root_any(v[e]);
+    }
 }
 
 // 1 / x likewise, for x from 1e-30 to 8e37 (above, where v overflows, 0).
@@ -269,7 +292,11 @@ __device__ __forceinline__ void step_unit(const AdamwArgs& a, const AdamwTensor&
             if constexpr (BITS == 8) v[u][e] = v[u][e] * v[u][e];
             m[u][e] = m[u][e] * a.beta1 + x * a.rest1;
             v[u][e] = v[u][e] * a.beta2 + (x * x) * a.rest2;
-            r[e] = BITS == 8 ? root(v[u][e]) : sqrtf(v[u][e]);
+        }
+        if constexpr (BITS == 8) roots(v[u], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (BITS == 32) r[e] = sqrtf(v[u][e]);
             const float up = m[u][e] * __builtin_amdgcn_rcpf(fmaf(r[e], a.root, a.eps));
             w[u][e] = fmaf(-a.rate, up, w[u][e] * a.keep);
         }
