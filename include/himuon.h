@@ -658,6 +658,10 @@ typedef struct himuon_adamw_state {
  * States and update are computed in fp32 and W is rounded once; the update is
  * taken from m and v before they are rounded to 8 bits.  A NaN or infinity in G
  * stays in its element (a state that is not finite is held as NaN in 8 bits).
+ * A finite g whose square passes fp32's range (|g| above 1.8e19) makes v infinite
+ * and the update 0, then and in later steps (beta2 above 0); in 8 bits sqrt(v) is
+ * held as NaN and read as infinity, and m of such a size takes its block's scale,
+ * beside which ordinary entries of m are lost.
  * No tensor or state of the call may overlap another one, or G.
  * One launch per 256 tensors.  lr, step and the rest are values of the call: a
  * captured one repeats them (grad_scale is read anew).

@@ -133,3 +133,33 @@ def test_one_tiny_gradient_leaves_its_block(cuda, bits):
     keep = torch.arange(B, device=cuda) != 100
     for a, b in zip(*ends):
         assert torch.equal(a, b) if a.numel() == 1 else torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("wdt,gdt", [("float32", "float32"), ("bfloat16", "bfloat16")])
+def test_squares_past_the_range(cuda, wdt, gdt, bits):
+    """Finite gradients whose squares are infinite in fp32: their elements are updated no
+    more, neither then nor later, and stay finite; sqrt(v) and the weights of the
+    elements beside them are what they are beside zeros."""
+    print(f"adamw, squares past fp32's range, {bits} bits {gdt}", flush=True)
+    n, at = 2 * B + 40, torch.tensor([3, 8, 200, 300, 2 * B + 39], device=cuda)
+    w, g = spread(n, 1e-2, 1.0, 8).to(getattr(torch, wdt)), spread(n, 1e-4, 1e-2, 9).to(getattr(torch, gdt))
+    rest = torch.ones(n, dtype=torch.bool, device=cuda)
+    rest[at] = False
+    ends = []
+    for values in (0.0, torch.tensor([1e20, -1e30, 1e25, 3e38, -2e19], device=cuda).to(g.dtype)):
+        one, state = w.clone(), H.adamw_state([w], bits=bits)
+        first = g.clone()
+        first[at] = values
+        H.himuon_adamw_step([one], [first], state, lr=1e-2, step=1)
+        ends.append((one.clone(), held(state)[1][:n].clone()))
+        if isinstance(values, float):
+            continue
+        assert torch.equal(one[at], w[at])
+        r = held(state)[1][at]
+        assert torch.all(torch.isinf(r) if bits == 32 else torch.isnan(r))
+        for step in (2, 3, 4):
+            H.himuon_adamw_step([one], [g], state, lr=1e-2, step=step)
+            assert torch.equal(one[at], w[at]) and torch.isfinite(one).all(), step
+    for a, b in zip(*ends):
+        assert torch.equal(a[rest], b[rest])

@@ -210,22 +210,28 @@ __device__ __forceinline__ float root(float v) {
     const float s = __builtin_amdgcn_rsqf(v), r = v * s;
     return fmaf(fmaf(-r, r, v), 0.5f * s, r);
 }
-// The same for any v, 0 among them, through a multiple of v.
+// The same for any v, 0 among them, through a multiple of v.  Infinite where v is (its
+// update is then 0), and where it is NaN: of a NaN gradient m is NaN too, and else NaN is
+// how codes hold infinity.
 __device__ __forceinline__ float root_any(float v) {
     const bool small = v < 0x1p-96f;
     const float x = small ? v * 0x1p64f : v, s = fminf(__builtin_amdgcn_rsqf(x), 1e30f), r = x * s;
-    return fmaf(fmaf(-r, r, x), 0.5f * s, r) * (small ? 0x1p-32f : 1.f);
+    const float q = fmaf(fmaf(-r, r, x), 0.5f * s, r) * (small ? 0x1p-32f : 1.f);
+    return v < __uint_as_float(kInfinity) ? q : __uint_as_float(kInfinity);
 }
 // r = sqrt(v) of a thread's eight.  A second moment below 2^-96 is rare, but for zeros
-// (weights that no gradient has met), so the way for any v is behind a branch; an
-// element's result is the same bits on either.
+// (weights that no gradient has met), and so is an infinite one, so the way for any v is
+// behind a branch; an element's result is the same bits on either.
 __device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
-    unsigned least = __float_as_uint(v[0]);
+    unsigned least = __float_as_uint(v[0]), most = least;
 #pragma unroll
-    for (int e = 1; e < 8; ++e) least = min(least, __float_as_uint(v[e]));
+    for (int e = 1; e < 8; ++e) {
+        least = min(least, __float_as_uint(v[e]));
+        most = max(most, __float_as_uint(v[e]));
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = root(v[e]);
-    if (least < 0x0f800000u) {   // 2^-96
+    if (least < 0x0f800000u || most >= kInfinity) {   // (2^-96)
         asm volatile("");   // (not selects that always run)
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[e] = root_any(v[e]);
