@@ -233,8 +233,13 @@ __device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
     for (int e = 0; e < 8; ++e) r[e] = root(v[e]);
     if (least < 0x0f800000u || most >= kInfinity) {   // (2^-96)
         asm volatile("");   // (not selects that always run)
+        if (most == 0u) {   // 262 M weights from zero states without gradients: 597 us without this, 590 with
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = root_any(v[e]);
+            for (int e = 0; e < 8; ++e) r[e] = 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = root_any(v[e]);
+        }
     }
 }
 
