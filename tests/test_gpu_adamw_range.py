@@ -163,3 +163,18 @@ def test_squares_past_the_range(cuda, wdt, gdt, bits):
             assert torch.equal(one[at], w[at]) and torch.isfinite(one).all(), step
     for a, b in zip(*ends):
         assert torch.equal(a[rest], b[rest])
+
+
+@pytest.mark.parametrize("size", [7e37, 9e37, 1.2e38, 3.3e38])
+def test_largest_averages(cuda, size):
+    """8 bits: averages m up to the end of fp32's range, where 1 / m is subnormal: codes and
+    scale stand for them, within a gap."""
+    print(f"adamw, m of {size}", flush=True)
+    w, g = torch.zeros(B, device=cuda), spread(B, size * 1e-2, size, 10)
+    state = H.adamw_state([w], bits=8)
+    H.himuon_adamw_step([w], [g], state, lr=1e-2, step=1, betas=(0.0, 0.5))
+    m, unit = held(state)[0], state.m_scale[0].double()
+    most = g.double().abs().max()
+    assert torch.all((unit * 448 - most).abs() <= 4 * U * most)
+    assert torch.all((m - g.double()).abs() <= gap_of(g.double().abs(), unit) * 1.001 + 4 * U * most)
+    assert torch.all(w == 0)

@@ -243,10 +243,12 @@ __device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
     }
 }
 
-// 1 / x likewise, for x from 1e-30 to 8e37 (above, where v overflows, 0).
-__device__ __forceinline__ float reciprocal(float x) {
+// 448 / x likewise, for x from 1e-30 on (through x / 8: above 8.5e37 the reciprocal of x
+// itself would be subnormal, which the hardware's is not).
+__device__ __forceinline__ float codes_per(float x) {
+    x *= 0.125f;
     const float s = __builtin_amdgcn_rcpf(x);
-    return fmaf(fmaf(-x, s, 1.f), s, s);
+    return fmaf(fmaf(-x, s, 1.f), s, s) * 56.f;
 }
 __device__ __forceinline__ unsigned at_most_1(unsigned x) {   // (the compiler makes a test and a select of min)
     unsigned r;
@@ -327,7 +329,7 @@ __device__ __forceinline__ void step_unit(const AdamwArgs& a, const AdamwTensor&
         } else {
             bool m_odd, r_odd;
             const float m_max = largest(m[u], m_odd), r_max = largest(r, r_odd);
-            const float mi = reciprocal(m_max) * 448.f, ri = reciprocal(r_max) * 448.f;
+            const float mi = codes_per(m_max), ri = codes_per(r_max);
             unsigned cm[8], cv[8];
             const unsigned first = (uint32_t)(p.at >> 1) * 0xB890E049u + a.key;
 #pragma unroll
