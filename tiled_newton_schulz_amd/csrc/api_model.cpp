@@ -99,7 +99,7 @@ himuon_status_t activation(himuon_activation_t act, GroupedArgs& a) {
         case HIMUON_SILU: a.kind = GateKind::Linear; a.k0 = 1.f; return HIMUON_OK;
         case HIMUON_GELU: a.kind = GateKind::Erf; return HIMUON_OK;
         case HIMUON_GELU_TANH: a.kind = GateKind::Cubic; a.k0 = slope; a.k1 = slope * 0.044715f; return HIMUON_OK;
-        case HIMUON_RELU: a.kind = GateKind::Linear; a.k0 = 1e30f; a.k2 = -200.f; return HIMUON_OK;   // 0 or 1
+        case HIMUON_RELU: a.kind = GateKind::Step; return HIMUON_OK;
     }
     return HIMUON_ERR_UNSUPPORTED;
 }

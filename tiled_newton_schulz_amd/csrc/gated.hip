@@ -48,7 +48,8 @@ hipError_t launch_grouped_gated(const GroupedArgs& a, hipStream_t s) {
     if (k == GroupedKernel::Thin || k == GroupedKernel::Big) {
         if (a.kind == GateKind::Linear) aligned<GateKind::Linear>(a, k, tiles, s);
         else if (a.kind == GateKind::Cubic) aligned<GateKind::Cubic>(a, k, tiles, s);
-        else aligned<GateKind::Erf>(a, k, tiles, s);
+        else if (a.kind == GateKind::Erf) aligned<GateKind::Erf>(a, k, tiles, s);
+        else aligned<GateKind::Step>(a, k, tiles, s);
     } else if (a.dtype == 0) {
         if (a.nk) staged<0, true>(a, k, grid, s);
         else staged<0, false>(a, k, grid, s);

@@ -21,9 +21,9 @@ enum class Gate : int32_t {
     Grad        // X W_e^T is the gradient of that Y: gradients of G and U
 };
 
-// What s is in act(g) = g s(g): sigmoid(k0 g + k2), sigmoid(k0 g + k1 g^3), or the
-// integral of the normal distribution.
-enum class GateKind : int32_t { Linear, Cubic, Erf };
+// What s is in act(g) = g s(g): sigmoid(k0 g), sigmoid(k0 g + k1 g^3), the integral of
+// the normal distribution, or 1 above 0 and else 0.
+enum class GateKind : int32_t { Linear, Cubic, Erf, Step };
 
 // One launch of Y = X W_e (or X W_e^T) or of G_e = X_e^T D_e.
 struct GroupedArgs {
@@ -47,8 +47,8 @@ struct GroupedArgs {
     void* p;                 // [G | U], M x 2N: written by Forward (or null), read by Grad
     void* h;                 // Grad: H, or null
     int64_t p_ld, h_ld;
-    GateKind kind;           // act(g) = g s(g), with k0, k1, k2
-    float k0, k1, k2;
+    GateKind kind;           // act(g) = g s(g), with k0, k1
+    float k0, k1;
     void* w[kExperts];       // product: weights; weight gradient: results
     int64_t w_ld[kExperts];
 };

@@ -387,19 +387,20 @@ __device__ __forceinline__ void put_blocks(const f32x16 (&acc)[F][F], typename I
 
 // ---- gated block: act(g) = g s(g) -----------------------------------------------
 // silu: s = sigmoid(g); gelu (tanh): (1 + tanh z) / 2 = sigmoid(2 z), so both are
-// sigmoid(k0 g + k1 g^3); relu: s is 0 or 1, as a sigmoid so steep (10^30 g - 200) that
-// only gates below 10^-27 tell the two apart; gelu (erf): the normal distribution's
-// integral.  FAST: the hardware's exp2 and reciprocal, a few 2^-23 of the result (for
-// results rounded to bf16).  The kinds are kernels of their own (told apart for each
-// element, gelu's gradient took 357 instead of 316 us), and silu's and relu's has no
-// branches and no cubic: with both, results of short products took 3 to 8 % longer.
+// sigmoid(k0 g + k1 g^3); gelu (erf): the normal distribution's integral; relu: s is 1
+// for any g above 0, else 0, and NaN for NaN.  FAST: the hardware's exp2 and reciprocal,
+// a few 2^-23 of the result (for results rounded to bf16).  The kinds are kernels of
+// their own (told apart for each element, gelu's gradient took 357 instead of 316 us),
+// and silu's has no branches and no cubic: with both, results of short products took 3
+// to 8 % longer.
 __device__ __forceinline__ float gate_inner(float g) { return __builtin_amdgcn_fmed3f(g, -1e18f, 1e18f); }
 template <GateKind KIND, bool FAST>
 __device__ __forceinline__ float gate_share(const GroupedArgs& a, float g) {
+    if constexpr (KIND == GateKind::Step) return g > 0.f ? 1.f : g == g ? 0.f : g;
     if constexpr (KIND == GateKind::Erf) return 0.5f * erfcf(g * -0.70710678118654752f);
     float z;
     if constexpr (KIND == GateKind::Linear) {
-        z = g * a.k0 + a.k2;
+        z = g * a.k0;
     } else {
         const float x = gate_inner(g);
         z = g != g ? g : x * (a.k0 + a.k1 * x * x);   // (of finite terms)
@@ -413,7 +414,9 @@ __device__ __forceinline__ float gate_act(float g, float s) { return fmaxf(g, -3
 template <GateKind KIND, bool FAST>
 __device__ __forceinline__ float gate_slope(const GroupedArgs& a, float g, float s) {
     const float x = gate_inner(g);
-    if constexpr (KIND == GateKind::Linear) {
+    if constexpr (KIND == GateKind::Step) {
+        return s;
+    } else if constexpr (KIND == GateKind::Linear) {
         return s + x * (s - s * s) * a.k0;
     } else if constexpr (KIND == GateKind::Erf) {
         const float e = FAST ? __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f) : expf(-0.5f * x * x);
@@ -428,7 +431,8 @@ template <typename F>
 __device__ __forceinline__ void with_kind(const GroupedArgs& a, F f) {
     if (a.kind == GateKind::Linear) f(std::integral_constant<GateKind, GateKind::Linear>{});
     else if (a.kind == GateKind::Cubic) f(std::integral_constant<GateKind, GateKind::Cubic>{});
-    else f(std::integral_constant<GateKind, GateKind::Erf>{});
+    else if (a.kind == GateKind::Erf) f(std::integral_constant<GateKind, GateKind::Erf>{});
+    else f(std::integral_constant<GateKind, GateKind::Step>{});
 }
 
 // A B of one tile (operands exchanged in the MFMA, so that a lane holds runs of
