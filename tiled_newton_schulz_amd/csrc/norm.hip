@@ -250,9 +250,14 @@ __global__ __launch_bounds__(kBackward) void norm_backward(const NormArgs a) {
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
+            // past the row's end x_hat is 0: there x is 0, and where -mean rstd is infinite its product
+            // with g, 0 there too, would be NaN
+            const int in = a.cols - (c * L + l) * EPC;
+            const float mean = in > 0 ? p.st.x : 0.f;
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
-                const float g = Elem<DT>::get(p.g[c], e), xh = (Elem<DT>::get(p.x[c], e) - p.st.x) * p.st.y;
+                const float d = Elem<DT>::get(p.x[c], e) - mean;
+                const float g = Elem<DT>::get(p.g[c], e), xh = (WHOLE || e < in ? d : 0.f) * p.st.y;
                 if (SUMS) {
                     db[c][e] += g;
                     dw[c][e] += g * xh;   // (past the row's end g is 0)
