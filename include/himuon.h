@@ -583,11 +583,17 @@ himuon_status_t himuon_grouped_gated_mm_grad(const himuon_matrix_t* dY, const hi
  * X, Y     : N x D, D up to HIMUON_MAX_NORM_COLS; Y is written and may be X
  *            itself (the same pointer and ld).  N may be 0.
  * weight, bias : device arrays of D elements of type dt, or NULL (1 and 0).
- * eps      : finite, >= 0 (with 0, a row of equal values gives NaN).
+ * eps      : finite, >= 0 (with 0, the results of a row of equal values are not
+ *            defined).
  * stats    : device array of N x 2 fp32, 8-byte aligned, written, or NULL: mean and
  *            rstd, for himuon_layer_norm_grad.
  * Statistics and sums are fp32 for either type, the variance from the
- * differences to the mean; y is rounded once.  A NaN or infinity makes its row NaN.
+ * differences to the mean, which in fp32 correct the mean too: y is off by
+ * roundings of the differences, whatever the mean, and is the bias where all values
+ * are equal; y is rounded once.  (The mean in stats is an fp32 number, and so the
+ * gradients' x_hat is off by up to rstd times its rounding.)  A NaN or infinity
+ * makes its row NaN, and so does a sum of finite values past fp32's range;
+ * differences whose mean square is past it (above about 1.8e19) give rstd 0.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (dtype, D above the
  * maximum), HIMUON_ERR_LAYOUT, HIMUON_ERR_OVERLAP, HIMUON_ERR_HIP.
  */

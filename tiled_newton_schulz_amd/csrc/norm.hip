@@ -5,7 +5,9 @@
 // A stream over the rows (HBM bound: one read and one write forward, two reads
 // and one write backward), so a row is read once and held packed in registers by
 // L threads (4 to 1024) in up to eight 16-byte chunks each; mean and variance are
-// taken in two passes over the registers, in fp32, so a large mean costs nothing.
+// taken in two passes over the registers, in fp32: the second, over the differences to
+// the mean, also corrects it in fp32, so a large mean costs y nothing (uncorrected, rows
+// of 12000 values of 3e6 +- 1.5 came out wrong by up to 0.7; the time is the same).
 // Rows may start at any alignment: chunks count from the row's first element.
 //
 // The sums over rows stay in the registers of the threads that own the columns: a
@@ -140,6 +142,8 @@ template <int DT, int L, int CH, bool WHOLE>
 __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int EPC = Elem<DT>::EPC, G = kGroup<L> / L;
+    // (bf16 rows with a mean far above their spread lie in two binades: their sums are exact)
+    constexpr bool CORRECT = DT == 1;
     __shared__ float2 slots[2][16];
     int turn = 0;
     const int l = threadIdx.x % L;
@@ -160,23 +164,34 @@ __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
             for (int e = 0; e < EPC; ++e) sum += Elem<DT>::get(v[c], e);
         stay_packed(v);
         row_sum2<L>(sum, none, slots, turn);
-        const float mean = sum / n;   // (exact where all values are equal)
-        float var = 0.f;
+        const float about = sum / n;
+        float var = 0.f, rest = 0.f;   // sums of squares and of differences
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int in = cols - (c * L + l) * EPC;
             if (in <= 0) continue;
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
-                const float d = Elem<DT>::get(v[c], e) - mean;
+                const float d = Elem<DT>::get(v[c], e) - about;
+                if (CORRECT) rest += WHOLE || e < in ? d : 0.f;
                 var += WHOLE || e < in ? d * d : 0.f;
             }
         }
         stay_packed(v);
-        row_sum2<L>(var, none, slots, turn);
-        const float r = 1.f / sqrtf(var / n + a.eps);
+        row_sum2<L>(var, CORRECT ? rest : none, slots, turn);
+        var /= n;
+        if constexpr (CORRECT) {
+            // `about` is off by its sum's roundings, the more the larger the mean; the mean of the
+            // differences is that error, to their own roundings.  (Where all values are equal, so are the
+            // differences, and all of this is exact: 0.)
+            rest /= n;
+            var = fmaf(-rest, rest, var);
+            var = var < 0.f ? 0.f : var;   // (NaN stays)
+        }
+        const float r = 1.f / sqrtf(var + a.eps);
         if (!live) continue;   // (no barrier below)
-        if (l == 0 && a.stats != nullptr) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, r);
+        if (l == 0 && a.stats != nullptr)
+            *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(CORRECT ? about + rest : about, r);
         T* y = reinterpret_cast<T*>(a.y) + row * a.y_ld;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -184,7 +199,10 @@ __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
             if (at >= cols) continue;
             float f[EPC];
 #pragma unroll
-            for (int e = 0; e < EPC; ++e) f[e] = (Elem<DT>::get(v[c], e) - mean) * r;
+            for (int e = 0; e < EPC; ++e) {
+                const float d = Elem<DT>::get(v[c], e) - about;
+                f[e] = (CORRECT ? d - rest : d) * r;
+            }
             if (a.weight != nullptr) {
                 const u32x4 w = load_chunk<DT, WHOLE>(reinterpret_cast<const T*>(a.weight), at, cols);
 #pragma unroll
