@@ -68,3 +68,21 @@ def test_large_means(cuda, cols, mean):
     s = r.stats.double()
     assert torch.all((s[:, :1] - m).abs() <= off_m + U * m.abs())
     assert torch.all((s[:, 1:] / rstd - 1).abs() <= off_r)
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_equal_values_in_bf16(cuda, cols):
+    """Equal bf16 values have exact sums: up to 2^15 times 8 bits."""
+    print(f"layer norm, equal bf16 values, {cols} columns", flush=True)
+    x = torch.tensor([1.1, 3.3, -1e5 / 3, 2.7e10, 1e-12], device=cuda).bfloat16()[:, None].expand(5, cols).contiguous()
+    w, b = randn((cols,), "bf16", 1), randn((cols,), "bf16", 2)
+    r = H.himuon_layer_norm(x, w, b)
+    assert torch.equal(r.y, b.expand_as(x)) and torch.equal(r.stats[:, 0], x[:, 0].float())
+
+
+def test_the_stats_refusal_names_the_rows(cuda):
+    x = randn((4, 16), "bf16", 1)
+    st = H.himuon_layer_norm(x).stats
+    for bad in (st[:3], st.t().contiguous().t(), st.cpu()):
+        with pytest.raises(ValueError, match="stats must be contiguous with 2 entries per row, on the rows' GPU|tensors must be on one GPU"):
+            H.himuon_layer_norm_grad(x, None, bad, x)

@@ -943,7 +943,8 @@ def _vector(t, n, what, device, width=0):
     if t.dtype != torch.float32:
         raise TypeError(f"{what} must be float32")
     if t.shape != ((n, width) if width else (n,)) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{what} must be contiguous with one entry per row, on the logits' GPU")
+        entry = f"{width} entries" if width else "one entry"
+        raise ValueError(f"{what} must be contiguous with {entry} per row, on the rows' GPU")
     return ctypes.c_void_p(t.data_ptr())
 
 

@@ -28,7 +28,7 @@ struct NormArgs {
     float* part;           // workspace: 2 D sums of each workgroup
 };
 
-// Bytes of workspace a gradient needs (0 where no sums over rows are asked for).
+// Bytes of workspace a gradient needs where dw or db is asked for (else it takes none).
 int64_t norm_grad_bytes(int32_t rows, int32_t cols, int32_t dtype);
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_layer_norm_grad(const NormArgs& a, hipStream_t s);
