@@ -670,7 +670,11 @@ typedef struct himuon_adamw_state {
  * beside which ordinary entries of m are lost.
  * No tensor or state of the call may overlap another one, or G.
  * One launch per 256 tensors.  lr, step and the rest are values of the call: a
- * captured one repeats them (grad_scale is read anew).
+ * captured one repeats them (grad_scale is read anew), step's bias corrections and,
+ * in 8 bits, its random bits among them.  Replayed over and over, 8-bit states are
+ * rounded by the same bits each time, and an average that moves by less than a code
+ * step may stay where it is: training steps on 8-bit states are called for each
+ * step, those on 32-bit ones may be replayed where lr and the corrections may stay.
  * Errors: HIMUON_ERR_INVALID_ARGUMENT, HIMUON_ERR_UNSUPPORTED (types, bits),
  * HIMUON_ERR_LAYOUT, HIMUON_ERR_OVERLAP, HIMUON_ERR_HIP.
  */

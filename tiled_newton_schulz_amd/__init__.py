@@ -897,9 +897,12 @@ def himuon_adamw_step(w, g, state: AdamWState, lr: float, step: int, betas=(0.9,
                       weight_decay: float = 0.0, grad_scale=None, stream=None):
     """One AdamW step on all tensors of w at once, in place, from gradients g and
     the states adamw_state(w) made.  w, g: lists of tensors (bf16 or fp32, each list
-    of one type, which may differ), or what tensors() made of them once.  step: 1 in
-    the first step.  grad_scale: float32 tensor of one element on the GPU that the
-    gradients are multiplied by.  A captured call repeats its lr and step."""
+    of one type, which may differ), or what tensors() made of them once (a list is
+    described anew in each call: 1 us of the host's time a tensor).  step: 1 in the
+    first step.  grad_scale: float32 tensor of one element on the GPU that the
+    gradients are multiplied by.  A captured call repeats its lr and step, and so 8-bit
+    states' random bits: slow averages may not move in its replays, so such steps are
+    to be called, not replayed."""
     import torch
     w, g = tensors(w), tensors(g)
     state.in_place()

@@ -15,9 +15,10 @@
 // A stream (HBM bound: 16 + 2 size(w) + size(g) bytes an element, in 8 bits 4.06 +
 // 2 size(w) + size(g)).  One launch takes 256 tensors: a workgroup takes units of
 // 4096 elements and finds a unit's tensor in the table of the kernel arguments.
-// Measured: 262 M bf16 weights with 8-bit states 566 us (4.7 TB/s; about 65 vector
+// Measured: 262 M bf16 weights with 8-bit states 566 to 590 us (4.6 TB/s; about 65 vector
 // instructions an element, near the rate's share of them), with 32-bit states 1128 us
-// (5.1 TB/s); 96 tensors of 2048 fp32 weights 5.5 us.
+// (5.1 TB/s); 96 tensors of 2048 fp32 weights 5.5 us one launch after the other, 7.5 to 8
+// alone.
 
 #include <algorithm>
 

@@ -1203,7 +1203,8 @@ struct Grid {
     // Height of a slot's tiles.  The two of an expert of 257 to 512 rows of a gated block
     // are of one height, so that they keep in step and read their weights once through the
     // L2 (a full and a ragged one drift apart: 64 experts of 4096 x 2 x 1408 with 16384
-    // rows read 2.33 instead of 1.68 GB).
+    // rows read 2.33 instead of 1.68 GB).  Experts of more rows keep full tiles and a
+    // ragged one: evened out they were not measured.
     __device__ __forceinline__ int height(int rows) const {
         return GATE != Gate::None && rows > kBig && rows <= 2 * kBig ? (rows + 1) / 2 : kBig;
     }
