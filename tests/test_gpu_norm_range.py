@@ -70,6 +70,23 @@ def test_large_means(cuda, cols, mean):
     assert torch.all((s[:, 1:] / rstd - 1).abs() <= off_r)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [8, 64, 100, 513, 4096, 20000])
+def test_squares_past_the_range(cuda, cols, dt):
+    """Differences whose squares are infinite in fp32: rstd is 0 and y the bias, also where
+    sums of the differences pass the range on their way."""
+    print(f"layer norm, squares past fp32's range, {cols} columns {dt}", flush=True)
+    x = torch.zeros((4, cols), device=cuda)
+    x[0, 0], x[0, 1] = 3e38, -3e38
+    x[1] = randn((cols,), "fp32", 1, 1e25)
+    x[2, :2], x[2, 4:6] = 1.6e38, -1.6e38        # 3.2e38 in one thread's sum, 0 in all
+    x[3, :2], x[3, 2:6] = 1.6e38, -1.6e38        # as far, and a mean below 0
+    w, b = randn((cols,), dt, 2), randn((cols,), dt, 3)
+    r = H.himuon_layer_norm(x.to(TYPES[dt]), w, b)
+    assert torch.all(r.stats[:, 1] == 0) and torch.isfinite(r.stats).all()
+    assert torch.equal(r.y, b.expand_as(r.y))
+
+
 @pytest.mark.parametrize("cols", COLS)
 def test_equal_values_in_bf16(cuda, cols):
     """Equal bf16 values have exact sums: up to 2^15 times 8 bits."""

@@ -185,8 +185,9 @@ __global__ __launch_bounds__(kGroup<L>) void norm_forward(const NormArgs a) {
         if constexpr (CORRECT) {
             // `about` is off by its sum's roundings, the more the larger the mean; the mean of the
             // differences is that error, to their own roundings.  (Where all values are equal, so are the
-            // differences, and all of this is exact: 0.)
-            rest /= n;
+            // differences, and all of this is exact: 0.)  Where the squares are infinite, rstd is 0, and
+            // their sum may be infinite or NaN too.
+            rest = var < __uint_as_float(0x7f800000u) ? rest / n : 0.f;
             var = fmaf(-rest, rest, var);
             var = var < 0.f ? 0.f : var;   // (NaN stays)
         }
